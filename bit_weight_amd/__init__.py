@@ -23,6 +23,7 @@ import torch
 __all__ = [
     "SherryError", "lib", "packed_bytes", "workspace_bytes", "plan", "plan_override",
     "quantize_pack", "quantize_act", "gemm", "gemm_i32", "linear", "linear_scratch_bytes", "concat_packed", "quantize_pack2", "gemm2",
+    "gemm_fused", "glu", "layernorm", "layernorm_quantize", "layernorm_backward",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -33,7 +34,7 @@ LIB_PATH = os.environ.get("SHERRY_LIB") or os.path.join(_HERE, "libsherry.so")
 STATUS = {
     0: "SHERRY_OK", -1: "SHERRY_ERR_NULL", -2: "SHERRY_ERR_SHAPE",
     -3: "SHERRY_ERR_ALIGN", -4: "SHERRY_ERR_WORKSPACE", -5: "SHERRY_ERR_HIP",
-    -6: "SHERRY_ERR_DEVICE", -7: "SHERRY_ERR_PARTIAL",
+    -6: "SHERRY_ERR_DEVICE", -7: "SHERRY_ERR_PARTIAL", -8: "SHERRY_ERR_ARG",
 }
 
 
@@ -63,6 +64,7 @@ def lib() -> ctypes.CDLL:
                     "`python -m bit_weight_amd.build` (or __graft_entry__.build())")
             L = ctypes.CDLL(LIB_PATH)
             vp, i64, sz, ci = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
+            cf = ctypes.c_float
             ip = ctypes.POINTER(ctypes.c_int)
             sigs = {
                 "sherry_status_string": ([ci], ctypes.c_char_p),
@@ -82,6 +84,14 @@ def lib() -> ctypes.CDLL:
                 "sherry_gemm2": ([vp, vp, vp, vp, vp, i64, i64, i64, vp, sz, vp], ci),
                 "sherry_linear": ([vp, vp, vp, vp, i64, i64, i64, vp, sz, vp, sz, vp], ci),
                 "sherry_gemm_noalloc": ([vp, vp, vp, vp, vp, i64, i64, i64, vp], ci),
+                "sherry_gemm_fused_workspace_bytes": ([i64, i64, i64], sz),
+                "sherry_gemm_fused": ([vp, vp, vp, vp, vp, ci, vp, vp, ci, i64, i64, i64, vp, sz, vp], ci),
+                "sherry_glu_workspace_bytes": ([i64, i64, i64], sz),
+                "sherry_glu": ([vp, vp, vp, vp, vp, vp, ci, vp, ci, i64, i64, i64, vp, sz, vp], ci),
+                "sherry_layernorm": ([vp, vp, vp, cf, vp, vp, vp, ci, i64, i64, vp], ci),
+                "sherry_layernorm_quantize": ([vp, vp, vp, cf, vp, vp, vp, vp, ci, i64, i64, vp], ci),
+                "sherry_layernorm_backward_scratch_bytes": ([i64, i64], sz),
+                "sherry_layernorm_backward": ([vp, vp, vp, vp, vp, vp, vp, vp, ci, i64, i64, vp, sz, vp], ci),
                 "sherry_probe_read": ([vp, sz, vp, ci, ci, ci, vp], ci),
                 "sherry_probe_empty": ([vp], ci),
                 "sherry_probe_decode": ([ci, vp, ci, ci, vp], ci),
@@ -412,3 +422,190 @@ def gemm2(x: torch.Tensor, s_x: torch.Tensor, packed: torch.Tensor, alpha: torch
     _check(lib().sherry_gemm2(px, s_x.data_ptr(), packed.data_ptr(), alpha.data_ptr(), py, M, N, K,
                               wp, wn, _stream(x.device)), "sherry_gemm2")
     return out
+
+
+# ------------------------------------------------- feed-forward operators
+DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+ACTIVATIONS = {"none": 0, "relu": 1, "relu2": 2, "silu": 3, "gelu": 4, "gelu_tanh": 5}
+
+
+def _act_code(act) -> int:
+    code = ACTIVATIONS.get("none" if act is None else act)
+    if code is None:
+        raise ValueError(f"act must be one of {list(ACTIVATIONS)}, got {act!r}")
+    return code
+
+
+def _dtype_code(dtype) -> int:
+    code = DTYPES.get(dtype)
+    if code is None:
+        raise RuntimeError(f"type must be float32, float16 or bfloat16, got {dtype}")
+    return code
+
+
+def _operand(t, name: str, dtype: torch.dtype, device: torch.device, numel: int):
+    """Pointer of an operand that must be on `device` and hold `numel` values
+    (None -> NULL)."""
+    if t is None:
+        return None
+    p = _dev_tensor(t, name, dtype)
+    if t.device != device:
+        raise RuntimeError(f"{name} must be on {device}, got {t.device}")
+    if t.numel() != numel:
+        raise RuntimeError(f"{name} must hold {numel} values, got {t.numel()}")
+    return p
+
+
+def _matrix(t, name: str, dtype: torch.dtype, device: torch.device, shape):
+    """Pointer of a matrix that must be on `device` with this shape (None -> NULL)."""
+    if t is None:
+        return None
+    if isinstance(t, torch.Tensor) and tuple(t.shape) != tuple(shape):
+        raise RuntimeError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return _operand(t, name, dtype, device, shape[0] * shape[1])
+
+
+def _tokens(x, s_x, K: int):
+    """(M, device, pointers) of int8 tokens and their scales."""
+    px = _dev_tensor(x, "x", torch.int8)
+    if x.dim() != 2 or x.shape[1] != K:
+        raise RuntimeError(f"x must be [M,{K}]")
+    M = x.shape[0]
+    return M, x.device, px, _operand(s_x, "s_x", torch.float32, x.device, M)
+
+
+def _weights(packed, alpha, name: str, N: int, K: int, device):
+    return (_operand(packed, "packed" + name, torch.uint8, device, packed_bytes(N, K)),
+            _operand(alpha, "alpha" + name, torch.float32, device, N))
+
+
+def _zeroed_workspace(workspace, nbytes: int, device):
+    """The split-K workspace: the caller's, the stream's, or, under graph
+    capture, one of the graph's own that each replay zeroes (two graphs
+    captured on one stream may be replayed side by side, and memory that only
+    another graph has zeroed is not zero)."""
+    if workspace is not None:
+        p = _dev_tensor(workspace, "workspace", torch.uint8)
+        if workspace.device != device:
+            raise RuntimeError(f"workspace must be on {device}, got {workspace.device}")
+        return workspace, p, workspace.numel()
+    if nbytes == 0:
+        return None, None, 0
+    if torch.cuda.is_current_stream_capturing():
+        ws = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+    else:
+        ws = _workspaces.get(device, nbytes)
+    return ws, ws.data_ptr(), ws.numel()
+
+
+def _call(device: torch.device, name: str, *args) -> None:
+    """Calls the library with `device` current, on its current stream."""
+    fn = getattr(lib(), name)
+    if torch.cuda.current_device() == device.index:
+        _check(fn(*args, _stream(device)), name)
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, _stream(device)), name)
+
+
+def _output(out, M: int, N: int, dtype: torch.dtype, device: torch.device):
+    if out is None:
+        out = torch.empty((M, N), dtype=dtype, device=device)
+        return out, out.data_ptr()
+    return out, _matrix(out, "out", dtype, device, (M, N))
+
+
+def gemm_fused(x: torch.Tensor, s_x: torch.Tensor, packed: torch.Tensor, alpha: torch.Tensor,
+               N: int, K: int, bias: torch.Tensor | None = None, act: str | None = None,
+               residual: torch.Tensor | None = None, dtype: torch.dtype = torch.float32,
+               out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """y[M,N] = act((x_int8 @ T^T) * s_x[:,None] * alpha + bias) + residual in
+    one kernel (sherry_gemm_fused).  bias is fp32 [N]; residual and y have
+    type `dtype`; out may be the residual (updated in place)."""
+    M, dev, px, ps = _tokens(x, s_x, K)
+    pw, pa = _weights(packed, alpha, "", N, K, dev)
+    code, dt = _act_code(act), _dtype_code(dtype)
+    pb = _operand(bias, "bias", torch.float32, dev, N)
+    pr = _matrix(residual, "residual", dtype, dev, (M, N))
+    out, py = _output(out, M, N, dtype, dev)
+    ws, wp, wn = _zeroed_workspace(workspace, int(lib().sherry_gemm_fused_workspace_bytes(M, N, K)), dev)
+    _call(dev, "sherry_gemm_fused", px, ps, pw, pa, pb, code, pr, py, dt, M, N, K, wp, wn)
+    return out
+
+
+def glu(x: torch.Tensor, s_x: torch.Tensor, packed_gate: torch.Tensor, alpha_gate: torch.Tensor,
+        packed_up: torch.Tensor, alpha_up: torch.Tensor, N: int, K: int, act: str | None = "silu",
+        dtype: torch.dtype = torch.float32, out: torch.Tensor | None = None,
+        workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """h[M,N] = act(g) * u with g and u the products of x with the gate and up
+    matrices, in one kernel (sherry_glu).  A float32 h is what quantize_act
+    takes for the down projection."""
+    M, dev, px, ps = _tokens(x, s_x, K)
+    pg, pag = _weights(packed_gate, alpha_gate, "_gate", N, K, dev)
+    pu, pau = _weights(packed_up, alpha_up, "_up", N, K, dev)
+    code, dt = _act_code(act), _dtype_code(dtype)
+    out, ph = _output(out, M, N, dtype, dev)
+    ws, wp, wn = _zeroed_workspace(workspace, int(lib().sherry_glu_workspace_bytes(M, N, K)), dev)
+    _call(dev, "sherry_glu", px, ps, pg, pag, pu, pau, code, ph, dt, M, N, K, wp, wn)
+    return out
+
+
+def _features(x, weight, bias):
+    """(M, K, device, type code, pointers) of a norm's tokens and vectors."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    if x.dim() != 2:
+        raise RuntimeError("x must be 2-D [M,K]")
+    dt = _dtype_code(x.dtype)
+    px = _dev_tensor(x, "x", x.dtype)
+    M, K = x.shape
+    return (M, K, x.device, dt, px, _operand(weight, "weight", torch.float32, x.device, K),
+            _operand(bias, "bias", torch.float32, x.device, K))
+
+
+def _stats(stats: bool, M: int, device):
+    if not stats:
+        return (), (None, None)
+    mean, rstd = torch.empty((2, M), dtype=torch.float32, device=device)
+    return (mean, rstd), (mean.data_ptr(), rstd.data_ptr())
+
+
+def layernorm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+              eps: float = 1e-5, stats: bool = False, out: torch.Tensor | None = None):
+    """Layer norm of each token of x [M,K] (float32, float16 or bfloat16;
+    weight and bias fp32 [K]) -> y of x's type, or (y, mean, rstd) with
+    `stats` (what layernorm_backward takes).  out may be x."""
+    M, K, dev, dt, px, pw, pb = _features(x, weight, bias)
+    out, py = _output(out, M, K, x.dtype, dev)
+    found, (pm, pr) = _stats(stats, M, dev)
+    _call(dev, "sherry_layernorm", px, pw, pb, eps, py, pm, pr, dt, M, K)
+    return (out, *found) if stats else out
+
+
+def layernorm_quantize(x: torch.Tensor, weight: torch.Tensor | None = None,
+                       bias: torch.Tensor | None = None, eps: float = 1e-5, stats: bool = False):
+    """Layer norm of each token of x [M,K] straight into the int8 tokens the
+    products take -> (q int8 [M,K], s_x fp32 [M]), and mean and rstd with
+    `stats`."""
+    M, K, dev, dt, px, pw, pb = _features(x, weight, bias)
+    q = torch.empty((M, K), dtype=torch.int8, device=dev)
+    s = torch.empty(M, dtype=torch.float32, device=dev)
+    found, (pm, pr) = _stats(stats, M, dev)
+    _call(dev, "sherry_layernorm_quantize", px, pw, pb, eps, q.data_ptr(), s.data_ptr(), pm, pr, dt, M, K)
+    return (q, s, *found)
+
+
+def layernorm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                       weight: torch.Tensor | None = None, out: torch.Tensor | None = None):
+    """Gradients of layernorm -> (dx of x's type, dweight fp32 [K], dbias fp32
+    [K]).  out may be dy."""
+    M, K, dev, dt, px, pw, _ = _features(x, weight, None)
+    pdy = _matrix(dy, "dy", x.dtype, dev, (M, K))
+    pm = _operand(mean, "mean", torch.float32, dev, M)
+    pr = _operand(rstd, "rstd", torch.float32, dev, M)
+    out, pdx = _output(out, M, K, x.dtype, dev)
+    dw, db = torch.empty((2, K), dtype=torch.float32, device=dev)
+    scratch = torch.empty(int(lib().sherry_layernorm_backward_scratch_bytes(M, K)), dtype=torch.uint8, device=dev)
+    _call(dev, "sherry_layernorm_backward", pdy, px, pm, pr, pw, pdx, dw.data_ptr(), db.data_ptr(), dt, M, K,
+          scratch.data_ptr(), scratch.numel())
+    return out, dw, db

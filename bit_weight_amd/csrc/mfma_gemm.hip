@@ -47,7 +47,9 @@
 // each own a slab of weight rows, which then stays in that XCD's L2 for all
 // activation tiles.
 #include "sherry_device.h"
+#include "sherry_grad.h"
 #include "sherry_launch.h"
+#include "sherry_types.h"
 
 namespace sherry {
 namespace {
@@ -183,18 +185,22 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_rsrc(const void* base, 
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, n, 0x00020000);
 }
 
-template <int BM, int KP>
+template <int BM, int KP, int EP>
 __global__ __launch_bounds__(kThreads) void mfma_gemm_kernel(const uint8_t* packed, const int8_t* x,
                                                              const float* xf, int M, int N, int K,
                                                              int n_tiles, int /*unused*/, const float* s_x,
                                                              const float* alpha, float* y, int32_t* acc_out,
-                                                             int32_t* partials) {
+                                                             int32_t* partials, EpilogueOf<EP> e) {
   const GemmArgs a = product_args(packed, x, xf, M, N, K, s_x, alpha, y, acc_out, partials);
   using T = Tiling<BM, KP>;
   constexpr int kBM = BM, kMT = T::kMT, kAStage = T::kAStage, kACopies = T::kACopies;
   constexpr int kLdsBytes = T::kLdsBytes, kNewerLoads = T::kNewerLoads;
   constexpr int kRT = T::kRT, kBN = T::kBN, kOutLd = T::kOutLd, kABufs = T::kABufs;
   constexpr bool kPair = T::kPair;
+  // gated: half of the workgroup's row tiles are the gate's, half the up
+  // matrix's of the same kBNO outputs
+  constexpr bool kGlu = ep_glu(EP);
+  constexpr int kRTO = kGlu ? kRT / 2 : kRT, kBNO = kRTO * kTileRows;
   // the activation buffers [buffer][phase]; after the main loop the
   // epilogue tile reuses them
   // (32-bit words: every view below is a character type or 32-bit lanes)
@@ -219,7 +225,7 @@ __global__ __launch_bounds__(kThreads) void mfma_gemm_kernel(const uint8_t* pack
   const int mt_idx = slot - owned * mt_count;
   const int nt_idx = xcd * per_xcd + owned;
   if (nt_idx >= n_tiles || mt_idx >= mt_count) return;  // padding ids
-  const int m0 = mt_idx * kBM, n0 = nt_idx * kBN;
+  const int m0 = mt_idx * kBM, n0 = nt_idx * kBNO;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wave = wv % kRT, kh = wv / kRT;        // row tile, k-phase
@@ -235,11 +241,13 @@ __global__ __launch_bounds__(kThreads) void mfma_gemm_kernel(const uint8_t* pack
   // row tile (N % 64 != 0) the padding rows decode code 0, the block
   // (0,+1,+1,+1), and form sums of their own: only the n < N mask of the
   // epilogue's stores keeps them out of the output.
-  const int rt_raw = n0 / kTileRows + wave;
+  const int rt_raw = n0 / kTileRows + wave % kRTO;
   const bool n_live = rt_raw < RT;
   const int rt = n_live ? rt_raw : RT - 1;
+  const uint8_t* codes = a.packed;
+  if constexpr (kGlu) codes = wave < kRTO ? a.packed : e.packed2;
   const __amdgpu_buffer_rsrc_t rc =
-      buffer_rsrc(a.packed + tile_offset(rt, 0, KT), (size_t)KT * kTileBytes);
+      buffer_rsrc(codes + tile_offset(rt, 0, KT), (size_t)KT * kTileBytes);
   const __amdgpu_buffer_rsrc_t ra =
       buffer_rsrc(a.x + (size_t)m0 * K, (size_t)(M - m0) * (size_t)K);
 
@@ -433,23 +441,10 @@ __global__ __launch_bounds__(kThreads) void mfma_gemm_kernel(const uint8_t* pack
   // M=512, N=14336, K=4096, where the 29 MB of fp32 output bound it).  Lane
   // (l16, g) of a 16 x 16 MFMA block holds column l16, rows 4g..4g+3.  The
   // scales are read once, before the first barrier.
-  const bool want_y = a.y != nullptr;
-  const int c4 = tid & (kBN / 4 - 1);          // this thread's 4 columns
-  const int n = n0 + 4 * c4;
-  float4 al4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  if (want_y && n < N) al4 = make_float4(a.alpha[n], a.alpha[n + 1], a.alpha[n + 2], a.alpha[n + 3]);
-  if (want_y && tid < kBM) sxs[tid] = a.s_x[min(m0 + tid, M - 1)];
-  // The scale loads complete here, before the first output store.  The
-  // memory counter counts stores as well as loads, so a wait for alpha
-  // placed after a store also waits for that store; left to itself the
-  // compiler puts such a wait before every row's scaling, and the tile's
-  // 16 rows of stores then leave one round trip at a time.
-  __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
+  // The sums of 32 rows (two row blocks qq) into this phase's LDS tile.
   int* ot = reinterpret_cast<int*>(lds);       // [phase][32][kOutLd] sums
   int* mine = ot + kh * 32 * kOutLd;
-#pragma unroll
-  for (int qq = 0; qq < kMT / 2; ++qq) {
-    __syncthreads();  // the previous use of the LDS area is finished
+  auto put_sums = [&](int qq) {
 #pragma unroll
     for (int ii = 0; ii < 2; ++ii)
 #pragma unroll
@@ -457,33 +452,172 @@ __global__ __launch_bounds__(kThreads) void mfma_gemm_kernel(const uint8_t* pack
 #pragma unroll
         for (int t = 0; t < kNT; ++t)
           mine[(16 * ii + 4 * g + r) * kOutLd + wave * kTileRows + 16 * t + l16] = acc[2 * qq + ii][t][r];
-    __syncthreads();
+  };
+  if constexpr (EP == kEpNone) {
+    const bool want_y = a.y != nullptr;
+    const int c4 = tid & (kBN / 4 - 1);          // this thread's 4 columns
+    const int n = n0 + 4 * c4;
+    float4 al4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (want_y && n < N) al4 = make_float4(a.alpha[n], a.alpha[n + 1], a.alpha[n + 2], a.alpha[n + 3]);
+    if (want_y && tid < kBM) sxs[tid] = a.s_x[min(m0 + tid, M - 1)];
+    // The scale loads complete here, before the first output store.  The
+    // memory counter counts stores as well as loads, so a wait for alpha
+    // placed after a store also waits for that store; left to itself the
+    // compiler puts such a wait before every row's scaling, and the tile's
+    // 16 rows of stores then leave one round trip at a time.
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
 #pragma unroll
-    for (int k = 0; k < 32 * (kBN / 4) / kThreads; ++k) {
-      const int ml = tid / (kBN / 4) + (kThreads / (kBN / 4)) * k;   // row within the 32
-      const int m = m0 + 32 * qq + ml;
-      v4i sum = *reinterpret_cast<const v4i*>(&ot[ml * kOutLd + 4 * c4]);
+    for (int qq = 0; qq < kMT / 2; ++qq) {
+      __syncthreads();  // the previous use of the LDS area is finished
+      put_sums(qq);
+      __syncthreads();
 #pragma unroll
-      for (int ph = 1; ph < KP; ++ph) sum += *reinterpret_cast<const v4i*>(&ot[(ph * 32 + ml) * kOutLd + 4 * c4]);
-      if (m < M && n < N) {
-        if (want_y) {
-          const float sx = sxs[32 * qq + ml];
-          const float4 v = make_float4(((float)sum.x * sx) * al4.x, ((float)sum.y * sx) * al4.y,
-                                       ((float)sum.z * sx) * al4.z, ((float)sum.w * sx) * al4.w);
-          __builtin_nontemporal_store(__builtin_bit_cast(v4u, v), reinterpret_cast<v4u*>(a.y + (size_t)m * N + n));
+      for (int k = 0; k < 32 * (kBN / 4) / kThreads; ++k) {
+        const int ml = tid / (kBN / 4) + (kThreads / (kBN / 4)) * k;   // row within the 32
+        const int m = m0 + 32 * qq + ml;
+        v4i sum = *reinterpret_cast<const v4i*>(&ot[ml * kOutLd + 4 * c4]);
+#pragma unroll
+        for (int ph = 1; ph < KP; ++ph) sum += *reinterpret_cast<const v4i*>(&ot[(ph * 32 + ml) * kOutLd + 4 * c4]);
+        if (m < M && n < N) {
+          if (want_y) {
+            const float sx = sxs[32 * qq + ml];
+            const float4 v = make_float4(((float)sum.x * sx) * al4.x, ((float)sum.y * sx) * al4.y,
+                                         ((float)sum.z * sx) * al4.z, ((float)sum.w * sx) * al4.w);
+            __builtin_nontemporal_store(__builtin_bit_cast(v4u, v), reinterpret_cast<v4u*>(a.y + (size_t)m * N + n));
+          } else {
+            __builtin_nontemporal_store(sum, reinterpret_cast<v4i*>(a.acc + (size_t)m * N + n));
+          }
+        }
+      }
+    }
+  } else {
+    constexpr bool kBack = ep_back(EP);
+    constexpr int kCols = kBNO / 4;             // threads across a row: 4 outputs each
+    constexpr int kRowStep = kThreads / kCols;  // rows the workgroup takes at a time
+    static_assert(32 % kRowStep == 0, "whole turns over the 32 rows of a tile");
+    constexpr int kTurns = 32 / kRowStep;
+    __shared__ float inv_rows[kBack ? kBM : 1];
+    const int c4 = tid % kCols, r0 = tid / kCols;
+    const int n = n0 + 4 * c4;
+    const int nl = n < N ? n : 0;               // a valid column for the loads
+    const f4 al{a.alpha[nl], a.alpha[nl + 1], a.alpha[nl + 2], a.alpha[nl + 3]};
+    f4 al2{0.0f, 0.0f, 0.0f, 0.0f}, bias = al2;
+    if constexpr (kGlu) {
+      al2 = f4{e.alpha2[nl], e.alpha2[nl + 1], e.alpha2[nl + 2], e.alpha2[nl + 3]};
+    } else if (e.bias) {
+      bias = f4{e.bias[nl], e.bias[nl + 1], e.bias[nl + 2], e.bias[nl + 3]};
+    }
+    if (tid < kBM) {
+      const int m = min(m0 + tid, M - 1);
+      sxs[tid] = a.s_x[m];
+      if constexpr (kBack)
+        inv_rows[tid] = exp2_of(grad_exponent(e.grad.rows[m], a.s_x[m], e.grad.tops, e.act, kGlu));
+    }
+    f4 sum0{0.0f, 0.0f, 0.0f, 0.0f}, sum1 = sum0;   // this thread's share of dalpha and dalpha2 / dbias
+    const int RT64 = RT * kTileRows;
+    const size_t zrow = (size_t)e.grad.terms * (kGlu ? 2 : 1) * RT64;
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
+#pragma unroll
+    for (int qq = 0; qq < kMT / 2; ++qq) {
+      // this turn's residuals or output gradients, ahead of the barriers
+      f4 io[kTurns];
+#pragma unroll
+      for (int k = 0; k < kTurns; ++k) {
+        const int m = m0 + 32 * qq + r0 + kRowStep * k;
+        io[k] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (m < M && n < N) {
+          if constexpr (kBack) io[k] = load4_as(e.grad.dy, (size_t)m * N + n, e.dtype);
+          else if (!kGlu && e.residual) io[k] = load4_as(e.residual, (size_t)m * N + n, e.dtype);
+        }
+      }
+      __syncthreads();  // the previous use of the LDS area is finished
+      put_sums(qq);
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < kTurns; ++k) {
+        const int ml = r0 + kRowStep * k;
+        const int m = m0 + 32 * qq + ml;
+        if (m >= M || n >= (kBack ? RT64 : N)) continue;
+        v4i s1{0, 0, 0, 0}, s2{0, 0, 0, 0};
+#pragma unroll
+        for (int ph = 0; ph < KP; ++ph) {
+          s1 += *reinterpret_cast<const v4i*>(&ot[(ph * 32 + ml) * kOutLd + 4 * c4]);
+          if constexpr (kGlu) s2 += *reinterpret_cast<const v4i*>(&ot[(ph * 32 + ml) * kOutLd + kBNO + 4 * c4]);
+        }
+        const float sx = sxs[32 * qq + ml];
+        f4 o{0.0f, 0.0f, 0.0f, 0.0f}, o2 = o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float p1 = (float)s1[i] * sx, p2 = (float)s2[i] * sx;
+          const float z = kGlu ? p1 * al[i] : p1 * al[i] + bias[i];
+          if constexpr (EP == kEpFused) {
+            o[i] = act_value(z, e.act) + io[k][i];
+          } else if constexpr (EP == kEpGlu) {
+            o[i] = act_value(z, e.act) * (p2 * al2[i]);
+          } else if constexpr (EP == kEpFusedBack) {
+            const float dz = io[k][i] * act_slope(z, e.act);
+            sum0[i] += dz * p1;
+            sum1[i] += dz;
+            o[i] = dz * al[i];
+          } else {
+            const float dg = io[k][i] * (p2 * al2[i]) * act_slope(z, e.act);
+            const float du = io[k][i] * act_value(z, e.act);
+            sum0[i] += dg * p1;
+            sum1[i] += du * p2;
+            o[i] = dg * al[i];
+            o2[i] = du * al2[i];
+          }
+        }
+        if constexpr (!kBack) {
+          store4_as(e.out, (size_t)m * N + n, e.dtype, o);
         } else {
-          __builtin_nontemporal_store(sum, reinterpret_cast<v4i*>(a.acc + (size_t)m * N + n));
+          // rows past N inside the last row tile: zeros, so the padding adds nothing
+          if (n >= N) o = o2 = f4{0.0f, 0.0f, 0.0f, 0.0f};
+          _Float16* z = reinterpret_cast<_Float16*>(e.grad.z) + (size_t)m * zrow + n;
+          const float scale = inv_rows[32 * qq + ml];
+          store_terms(z, o * scale, e.grad.terms, (kGlu ? 2 : 1) * RT64);
+          if constexpr (kGlu) store_terms(z + RT64, o2 * scale, e.grad.terms, 2 * RT64);
+        }
+      }
+    }
+    if constexpr (kBack) {
+      // the column sums of this token tile, its rows' threads joined in order
+      f4* red = reinterpret_cast<f4*>(lds);
+#pragma unroll
+      for (int which = 0; which < 2; ++which) {
+        __syncthreads();
+        red[tid] = which ? sum1 : sum0;
+        __syncthreads();
+        float* part = which ? e.grad.part1 : e.grad.part0;
+        if (r0 == 0 && n < N && part) {
+          f4 t = red[c4];
+#pragma unroll
+          for (int r = 1; r < kRowStep; ++r) t += red[r * kCols + c4];
+          float* p = part + (size_t)mt_idx * N + n;
+          for (int i = 0; i < 4; ++i) p[i] = t[i];
         }
       }
     }
   }
 }
 
-template <int BM, int KP>
-hipError_t launch_tiles(const GemmPlan& p, const GemmArgs& a, hipStream_t stream) {
-  const int nt = (a.N + Tiling<BM, KP>::kBN - 1) / Tiling<BM, KP>::kBN;
-  launch_product_kernel(mfma_gemm_kernel<BM, KP>, dim3(p.grid), dim3(kThreads), 0, stream, a, nt, 0);
+template <int BM, int KP, int EP>
+hipError_t launch_tiles(const GemmPlan& p, const GemmArgs& a, hipStream_t stream, EpilogueOf<EP> e) {
+  constexpr int kBNO = Tiling<BM, KP>::kBN / (ep_glu(EP) ? 2 : 1);   // outputs per tile
+  const int nt = (a.N + kBNO - 1) / kBNO;
+  launch_product_kernel(mfma_gemm_kernel<BM, KP, EP>, dim3(p.grid), dim3(kThreads), 0, stream, a, nt, 0, e);
   return hipGetLastError();
+}
+
+// plan.rw carries the tile height in units of 64 activation rows (1 or 2),
+// plan.ch the k-phases (2 or 4).
+template <int EP>
+hipError_t launch_ep(const GemmPlan& p, const GemmArgs& a, hipStream_t stream, const EpilogueOf<EP>& e) {
+  if (p.rw == 1 && p.ch == 4) return launch_tiles<64, 4, EP>(p, a, stream, e);
+  if (p.rw == 1 && p.ch == 2) return launch_tiles<64, 2, EP>(p, a, stream, e);
+  if (p.rw == 2 && p.ch == 4) return launch_tiles<128, 4, EP>(p, a, stream, e);
+  if (p.rw == 2 && p.ch == 2) return launch_tiles<128, 2, EP>(p, a, stream, e);
+  return hipErrorInvalidValue;
 }
 
 }  // namespace
@@ -506,14 +640,19 @@ int mfma_gemm_grid(int M, int N, int bm, int kp) {
   return 8 * per_xcd * mt;
 }
 
-// plan.rw carries the tile height in units of 64 activation rows (1 or 2),
-// plan.ch the k-phases (2 or 4).
 hipError_t launch_mfma_gemm(const GemmPlan& p, const GemmArgs& a, hipStream_t stream) {
-  if (p.rw == 1 && p.ch == 4) return launch_tiles<64, 4>(p, a, stream);
-  if (p.rw == 1 && p.ch == 2) return launch_tiles<64, 2>(p, a, stream);
-  if (p.rw == 2 && p.ch == 4) return launch_tiles<128, 4>(p, a, stream);
-  if (p.rw == 2 && p.ch == 2) return launch_tiles<128, 2>(p, a, stream);
-  return hipErrorInvalidValue;
+  return launch_ep<kEpNone>(p, a, stream, NoEpilogueArgs{});
+}
+
+hipError_t launch_mfma_gemm_epilogue(const GemmPlan& p, const GemmArgs& a, int ep, const EpilogueArgs& e,
+                                     hipStream_t stream) {
+  switch (ep) {
+    case kEpFused: return launch_ep<kEpFused>(p, a, stream, e);
+    case kEpGlu: return launch_ep<kEpGlu>(p, a, stream, e);
+    case kEpFusedBack: return launch_ep<kEpFusedBack>(p, a, stream, e);
+    case kEpGluBack: return launch_ep<kEpGluBack>(p, a, stream, e);
+    default: return hipErrorInvalidValue;
+  }
 }
 
 }  // namespace sherry

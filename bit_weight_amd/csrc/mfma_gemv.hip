@@ -51,6 +51,7 @@
 //    with four stages).
 #include "sherry_device.h"
 #include "sherry_launch.h"
+#include "sherry_types.h"
 
 namespace sherry {
 namespace {
@@ -85,6 +86,22 @@ __device__ __forceinline__ float amax4(const float4 v) {
   return fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
 }
 
+// Split-K cells of the gated form: both matrices' sums and the arrivals in
+// one 64-bit cell, so one atomic per output still tells the last split.
+// |sum| <= 128 * 3/4 * 2^20 < 2^27 fits 28 signed bits: the up sum in bits
+// 0..27, the gate sum in 28..55, arrivals (at most kGluMaxSplits) above; a
+// negative field borrows from the one above it, which the decode returns.
+__device__ __forceinline__ unsigned long long glu_addend(int gate, int up) {
+  return (1ull << 56) + ((unsigned long long)(long long)gate << 28) + (unsigned long long)(long long)up;
+}
+__device__ __forceinline__ int glu_cell(unsigned long long c, int& gate, int& up) {
+  up = (int)((uint32_t)c << 4) >> 4;
+  c -= (unsigned long long)(long long)up;
+  gate = (int)((uint32_t)(c >> 28) << 4) >> 4;
+  c -= (unsigned long long)(long long)gate << 28;
+  return (int)(c >> 56);
+}
+
 // Activations of 16-token blocks are loaded four lanes per row (lane
 // 4r + g: token r, inputs 32g..32g+31), so each group of four lanes reads
 // one 128-byte line, and moved to the MFMA layout (lane 16g + r) by LDS
@@ -105,12 +122,15 @@ constexpr bool quad_x(int MT, int MB) { return MT == 16 && MB >= 1; }
 // (>= M*K / (4 * 64 * KW); the launch picks the smallest power of two).
 // SX = staged int8 activations: the split's x copied to LDS once, as in the
 // fused form, instead of loaded per k-tile (the launch uses it at M = 1).
-template <int KW, int MT, int MB, bool FQ, int FMT, int ST, int FS = 1, bool SX = false, bool SL = false>
+// EP = epilogue.  Gated (kEpGlu): the first half of the waves take the gate
+// matrix's row tile, the others the up matrix's of the same outputs.
+template <int KW, int MT, int MB, bool FQ, int FMT, int ST, int FS = 1, bool SX = false, bool SL = false,
+          int EP = kEpNone>
 __global__ __launch_bounds__(64 * KW) void mfma_gemv_kernel(const uint8_t* packed, const int8_t* x,
                                                             const float* xf, int M, int N, int K, int splits,
                                                             int kt_per_split, const float* s_x,
                                                             const float* alpha, float* y, int32_t* acc_out,
-                                                            int32_t* partials) {
+                                                            int32_t* partials, EpilogueOf<EP> e) {
   const GemmArgs a = product_args(packed, x, xf, M, N, K, s_x, alpha, y, acc_out, partials);
   static_assert(MB == 1 || (MT == 16 && !FQ), "several token blocks are whole blocks of 16");
   static_assert(!SX || (!FQ && MB == 1 && MT <= 4), "staged int8 activations: at most 4 tokens");
@@ -118,6 +138,9 @@ __global__ __launch_bounds__(64 * KW) void mfma_gemv_kernel(const uint8_t* packe
   constexpr bool XQ = !FQ && quad_x(MT, MB);
   constexpr int kStages = ST;
   constexpr int NT = 64 * KW;
+  constexpr bool kGlu = ep_glu(EP);
+  constexpr int KS = kGlu ? KW / 2 : KW;   // waves that share one matrix's k-tiles
+  static_assert(EP == kEpNone || (!FQ && FMT == 0), "epilogues: the int8 form of the 5-bit format");
   constexpr int TB = FMT == 0 ? kTileBytes : kTile2Bytes;   // bytes per format tile
   __shared__ __attribute__((aligned(16))) uint32_t tbl2[FMT == 1 ? 256 : 1];
   constexpr int QS = LX ? kFuseMaxSpan * kTileK : 16;   // int8 activations per token in LDS
@@ -134,15 +157,18 @@ __global__ __launch_bounds__(64 * KW) void mfma_gemv_kernel(const uint8_t* packe
   const int tid = threadIdx.x, lane = tid & 63;
   const int q = __builtin_amdgcn_readfirstlane(tid >> 6);   // wave-uniform: scalar offsets
   const int l16 = lane & 15, g = lane >> 4;
+  const int qk = kGlu ? q % KS : q;   // this wave among those of its matrix
 
   const int kt_begin = s * kt_per_split;
   const int kt_end = min(KT, kt_begin + kt_per_split);
   const int span = kt_end - kt_begin;
-  const int nk = span > q ? (span - q + KW - 1) / KW : 0;
+  const int nk = span > qk ? (span - qk + KS - 1) / KS : 0;
 
   // buffer descriptors: this row tile's codes, and the M tokens of x
   const size_t tb = (size_t)rt * KT * TB;
-  const __amdgpu_buffer_rsrc_t rc = gemv_rsrc(a.packed + tb, (size_t)KT * TB);
+  const uint8_t* codes = a.packed;
+  if constexpr (kGlu) codes = q < KS ? a.packed : e.packed2;
+  const __amdgpu_buffer_rsrc_t rc = gemv_rsrc(codes + tb, (size_t)KT * TB);
   const __amdgpu_buffer_rsrc_t rx = gemv_rsrc(a.x, (size_t)M * (size_t)K);
   // an offset the descriptor's range check rejects (the load returns zeros)
   const int x_oob = (size_t)M * (size_t)K > 0x7FFFFFFFull ? 0x7FFFFFFF : M * K;
@@ -160,7 +186,7 @@ __global__ __launch_bounds__(64 * KW) void mfma_gemv_kernel(const uint8_t* packe
   // (unconditional, so no branch merges the stage registers: a wave without
   // k-tiles reads a valid tile of its row tile and never uses it)
   auto load = [&](int i, v4u& w, v4u& h, v4u (&x0)[MB], v4u (&x1)[MB]) {
-    const int kt = min(kt_begin + q + KW * max(min(i, nk - 1), 0), KT - 1);
+    const int kt = min(kt_begin + qk + KS * max(min(i, nk - 1), 0), KT - 1);
     const int ks = kt * TB, ka = kt * kTileK;
     w = __builtin_amdgcn_raw_buffer_load_b128(rc, 16 * lane, ks, 0);
     if constexpr (FMT == 0) {
@@ -323,7 +349,7 @@ __global__ __launch_bounds__(64 * KW) void mfma_gemv_kernel(const uint8_t* packe
     v4i a0[MB], a1[MB];
     if constexpr (LX) {
       // token l16 (zero past M), inputs 32g + 16s of this wave's i-th k-tile
-      const uint32_t* src = &qs[(min(l16, M - 1) * QS + (q + KW * i) * kTileK + 32 * g) / 4];
+      const uint32_t* src = &qs[(min(l16, M - 1) * QS + (qk + KS * i) * kTileK + 32 * g) / 4];
       const v4i v0 = __builtin_bit_cast(v4i, *reinterpret_cast<const v4u*>(src));
       const v4i v1 = __builtin_bit_cast(v4i, *reinterpret_cast<const v4u*>(src + 4));
       const v4i z{0, 0, 0, 0};
@@ -395,7 +421,22 @@ __global__ __launch_bounds__(64 * KW) void mfma_gemv_kernel(const uint8_t* packe
   constexpr int TPW = MT >= KW ? MT / KW : 1;        // tokens per wave and block
   const int n = rt * kTileRows + lane;
   const bool n_ok = n < N;                            // rows past N: padding, never stored
-  const float al = a.y && n_ok ? a.alpha[n] : 0.0f;
+  const bool scaled = EP != kEpNone || a.y;
+  const float al = scaled && n_ok ? a.alpha[n] : 0.0f;
+  // the gated form's second scale, or the fused form's bias and residuals
+  float al2 = 0.0f;
+  float res[EP == kEpFused ? MB : 1][TPW];
+  if constexpr (kGlu) al2 = n_ok ? e.alpha2[n] : 0.0f;
+  if constexpr (EP == kEpFused) {
+    al2 = n_ok && e.bias ? e.bias[n] : 0.0f;
+#pragma unroll
+    for (int b = 0; b < MB; ++b)
+#pragma unroll
+      for (int i = 0; i < TPW; ++i) {
+        const int m = 16 * b + q * TPW + i;
+        res[b][i] = e.residual && n_ok && q * TPW < MT && m < M ? load1_as(e.residual, (size_t)m * N + n, e.dtype) : 0.0f;
+      }
+  }
   // the scales of this wave's tokens, loaded with alpha before any atomic
   // or store (the memory counter counts stores too: a scale loaded after a
   // store would make the next store wait for that one)
@@ -405,7 +446,7 @@ __global__ __launch_bounds__(64 * KW) void mfma_gemv_kernel(const uint8_t* packe
 #pragma unroll
     for (int i = 0; i < TPW; ++i) {
       const int m = 16 * b + q * TPW + i;
-      sxm[b][i] = !FQ && a.y && q * TPW < MT && m < M ? a.s_x[m] : 0.0f;
+      sxm[b][i] = !FQ && scaled && q * TPW < MT && m < M ? a.s_x[m] : 0.0f;
     }
 #pragma unroll
   for (int b = 0; b < MB; ++b) {
@@ -417,18 +458,27 @@ __global__ __launch_bounds__(64 * KW) void mfma_gemv_kernel(const uint8_t* packe
         if (4 * g + j < MT) red[(q * MT + 4 * g + j) * kRedLd + 16 * t + l16] = acc[b][t][j];
     __syncthreads();
     if (q * TPW >= MT) continue;
-    int total[TPW];
+    int total[TPW], total2[TPW];   // total2: the up matrix's sums
 #pragma unroll
     for (int i = 0; i < TPW; ++i) {
       const int m = q * TPW + i;
-      int v = 0;
+      int v = 0, v2 = 0;
 #pragma unroll
-      for (int qq = 0; qq < KW; ++qq) v += red[(qq * MT + m) * kRedLd + lane];
+      for (int qq = 0; qq < KS; ++qq) v += red[(qq * MT + m) * kRedLd + lane];
+#pragma unroll
+      for (int qq = KS; qq < KW; ++qq) v2 += red[(qq * MT + m) * kRedLd + lane];
       total[i] = v;
+      total2[i] = v2;
     }
     bool last[TPW];
 #pragma unroll
     for (int i = 0; i < TPW; ++i) last[i] = true;
+    // one addend of a split-K cell: the sum in the low word and one arrival
+    // above it, or both matrices' sums and the arrival
+    auto cell_of = [](int v, int v2) {
+      if constexpr (kGlu) return glu_addend(v, v2);
+      else return (1ull << 32) + (unsigned long long)(long long)v;
+    };
     if (splits > 1) {
       unsigned long long* cells = reinterpret_cast<unsigned long long*>(a.partials);
       unsigned long long now[TPW];
@@ -439,18 +489,21 @@ __global__ __launch_bounds__(64 * KW) void mfma_gemv_kernel(const uint8_t* packe
         for (int i = 0; i < TPW; ++i) {
           const int m = 16 * b + q * TPW + i;
           if (m < M)
-            now[i] = __hip_atomic_fetch_add(cells + (size_t)m * N + n,
-                                            (1ull << 32) + (unsigned long long)(long long)total[i],
+            now[i] = __hip_atomic_fetch_add(cells + (size_t)m * N + n, cell_of(total[i], total2[i]),
                                             __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
       }
 #pragma unroll
       for (int i = 0; i < TPW; ++i) {
         const int m = 16 * b + q * TPW + i;
-        now[i] += (1ull << 32) + (unsigned long long)(long long)total[i];
-        total[i] = (int)(uint32_t)now[i];
-        // the high word minus the borrow of a negative low word = arrivals
-        last[i] = (((long long)now[i] - (long long)total[i]) >> 32) == (long long)splits;
+        now[i] += cell_of(total[i], total2[i]);
+        if constexpr (kGlu) {
+          last[i] = glu_cell(now[i], total[i], total2[i]) == splits;
+        } else {
+          total[i] = (int)(uint32_t)now[i];
+          // the high word minus the borrow of a negative low word = arrivals
+          last[i] = (((long long)now[i] - (long long)total[i]) >> 32) == (long long)splits;
+        }
         if (m < M && n_ok && last[i])
           __hip_atomic_store(cells + (size_t)m * N + n, 0ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       }
@@ -462,14 +515,19 @@ __global__ __launch_bounds__(64 * KW) void mfma_gemv_kernel(const uint8_t* packe
 #pragma unroll
     for (int i = 0; i < TPW; ++i) {
       const int m = min(16 * b + q * TPW + i, MT - 1);
-      yv[i] = ((float)total[i] * (FQ ? sred[KW * MT + m] : sxm[b][i])) * al;
+      const float sx = FQ ? sred[KW * MT + m] : sxm[b][i];
+      yv[i] = ((float)total[i] * sx) * al;
+      if constexpr (EP == kEpFused) yv[i] = act_value(yv[i] + al2, e.act) + res[b][i];
+      if constexpr (EP == kEpGlu) yv[i] = act_value(yv[i], e.act) * (((float)total2[i] * sx) * al2);
       asm volatile("" : "+v"(yv[i]));
     }
 #pragma unroll
     for (int i = 0; i < TPW; ++i) {
       const int m = 16 * b + q * TPW + i;
       if (m >= M || !n_ok || !last[i]) continue;
-      if (a.y) {
+      if constexpr (EP != kEpNone) {
+        store1_as(e.out, (size_t)m * N + n, e.dtype, yv[i]);
+      } else if (a.y) {
         a.y[(size_t)m * N + n] = yv[i];
       } else {
         a.acc[(size_t)m * N + n] = total[i];
@@ -484,12 +542,12 @@ hipError_t launch_fused_fs(const GemmPlan& p, const GemmArgs& a, hipStream_t str
     if (need > FS) return launch_fused_fs<KW, MT, 2 * FS>(p, a, stream, need);
   }
   if (need > FS) return hipErrorInvalidValue;
-  launch_product_kernel(mfma_gemv_kernel<KW, MT, 1, true, 0, 4, FS>, dim3(p.grid), dim3(64 * KW), 0, stream, a, p.splits, p.kt_per_split);
+  launch_product_kernel(mfma_gemv_kernel<KW, MT, 1, true, 0, 4, FS>, dim3(p.grid), dim3(64 * KW), 0, stream, a, p.splits, p.kt_per_split, NoEpilogueArgs{});
   return hipGetLastError();
 }
 
-template <int KW, bool FQ, int FMT>
-hipError_t launch_kw(const GemmPlan& p, const GemmArgs& a, hipStream_t stream) {
+template <int KW, bool FQ, int FMT, int EP = kEpNone>
+hipError_t launch_kw(const GemmPlan& p, const GemmArgs& a, hipStream_t stream, const EpilogueOf<EP>& e) {
   const dim3 grid(p.grid), block(64 * KW);
   if constexpr (FQ) {
     // fused form: float4 loads per thread for the tokens' rows
@@ -511,10 +569,11 @@ hipError_t launch_kw(const GemmPlan& p, const GemmArgs& a, hipStream_t stream) {
     // under a K-split (the long-K plans split K to reach this form; N=8192,
     // K=28672, 4 splits of 7 k-tiles per wave: M=1 11.4 -> 10.2 us, M=4
     // 11.7 -> 10.8, M=8 11.8 -> 11.4)
-    const int nkw = (p.kt_per_split + KW - 1) / KW;
+    constexpr int KS = ep_glu(EP) ? KW / 2 : KW;
+    const int nkw = (p.kt_per_split + KS - 1) / KS;
     const bool sl4 = nkw >= 4 && nkw <= kSL;
 #define SHERRY_GEMV(MT_, MB_, ST_, SX_, SL_) \
-  launch_product_kernel(mfma_gemv_kernel<KW, MT_, MB_, false, FMT, ST_, 1, SX_, SL_>, grid, block, 0, stream, a, p.splits, p.kt_per_split)
+  launch_product_kernel(mfma_gemv_kernel<KW, MT_, MB_, false, FMT, ST_, 1, SX_, SL_, EP>, grid, block, 0, stream, a, p.splits, p.kt_per_split, e)
     if (a.M <= 1 && p.kt_per_split <= kFuseMaxSpan) {
       if (sl4) SHERRY_GEMV(1, 1, 2, true, true); else SHERRY_GEMV(1, 1, 4, true, false);
     } else if (a.M <= 1) {
@@ -546,9 +605,9 @@ hipError_t launch_kw(const GemmPlan& p, const GemmArgs& a, hipStream_t stream) {
 template <bool FQ, int FMT>
 hipError_t launch_fq(const GemmPlan& p, const GemmArgs& a, hipStream_t stream) {
   switch (p.rw) {
-    case 4: return launch_kw<4, FQ, FMT>(p, a, stream);
-    case 8: return launch_kw<8, FQ, FMT>(p, a, stream);
-    case 16: return launch_kw<16, FQ, FMT>(p, a, stream);
+    case 4: return launch_kw<4, FQ, FMT>(p, a, stream, {});
+    case 8: return launch_kw<8, FQ, FMT>(p, a, stream, {});
+    case 16: return launch_kw<16, FQ, FMT>(p, a, stream, {});
     default: return hipErrorInvalidValue;
   }
 }
@@ -565,6 +624,23 @@ bool mfma_gemv_fusable(const GemmPlan& p, int M, int K) {
 // plan.rw carries the waves per row tile for this path (4, 8 or 16).
 hipError_t launch_mfma_gemv(const GemmPlan& p, const GemmArgs& a, hipStream_t stream) {
   return a.xf ? launch_fq<true, 0>(p, a, stream) : launch_fq<false, 0>(p, a, stream);
+}
+
+hipError_t launch_mfma_gemv_epilogue(const GemmPlan& p, const GemmArgs& a, int ep, const EpilogueArgs& e,
+                                     hipStream_t stream) {
+  if (ep == kEpFused) {
+    switch (p.rw) {
+      case 4: return launch_kw<4, false, 0, kEpFused>(p, a, stream, e);
+      case 8: return launch_kw<8, false, 0, kEpFused>(p, a, stream, e);
+      case 16: return launch_kw<16, false, 0, kEpFused>(p, a, stream, e);
+    }
+  } else if (ep == kEpGlu && p.splits <= kGluMaxSplits) {
+    switch (p.rw) {
+      case 8: return launch_kw<8, false, 0, kEpGlu>(p, a, stream, e);
+      case 16: return launch_kw<16, false, 0, kEpGlu>(p, a, stream, e);
+    }
+  }
+  return hipErrorInvalidValue;
 }
 
 hipError_t launch_mfma_gemv2(const GemmPlan& p, const GemmArgs& a, hipStream_t stream) {

@@ -1,0 +1,488 @@
+// Layer norm over the K features of each token:
+//   mean = sum x / K, var = sum (x - mean)^2 / K, rstd = 1 / sqrt(var + eps),
+//   y = (x - mean) rstd w + b,
+// its form that writes the int8 tokens the products take, and its gradients
+//   g = dy w, xh = (x - mean) rstd,
+//   dx = rstd (g - sum g / K - xh sum(g xh) / K),
+//   dw = sum over tokens of dy xh, db = sum over tokens of dy.
+// All of them stream their inputs once; memory bandwidth bounds them.
+//
+// A group of W waves (1 to 4, or 16 above 16384 features in the forward)
+// holds one token in registers, so the mean and the sum of squared
+// differences from it are taken in two passes without reading x again: the
+// variance has no cancellation.  W is the least that needs at most 64 (fp32
+// sums) values a lane; lane l of the group takes features 4 (l + 64 W j) ..
+// + 3, so every load instruction reads whole lines.
+#include "sherry_device.h"
+#include "sherry_launch.h"
+#include "sherry_types.h"
+
+namespace sherry {
+namespace {
+
+constexpr int kNormThreads = 256;         // forward: 4 waves, 4 / W tokens per workgroup
+constexpr int kLoopThreads = 1024;        // forward above kNormMaxK: one token per workgroup, in loops
+constexpr int kBackThreads = 512;         // backward: 8 waves, 8 / W tokens at a time
+constexpr int kNormMaxK = 16384;          // features held in registers by 4 waves
+constexpr int kBackBlocks = 2 * kCUs;     // most workgroups (rows of partial weight gradients)
+
+// Sum (or maximum) over the W waves that share a token; `slot` is this
+// wave's place in `red`, whose W entries from the token's first on hold the
+// waves' values.  Every wave of the workgroup calls it; two buffers used in
+// turn need one barrier per call.
+template <int W, typename T, typename F>
+__device__ __forceinline__ T group_join(T v, T* red, int wave, F op) {
+  if constexpr (W == 1) {
+    return v;
+  } else {
+    if ((threadIdx.x & 63) == 0) red[wave] = v;
+    __syncthreads();
+    const int first = wave / W * W;
+    T r = red[first];
+#pragma unroll
+    for (int i = 1; i < W; ++i) r = op(r, red[first + i]);
+    return r;
+  }
+}
+
+__device__ __forceinline__ double wave_sum64(double v) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
+  return v;
+}
+
+__device__ __forceinline__ double wave_max64(double v) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) v = fmax(v, __shfl_xor(v, d));
+  return v;
+}
+
+__device__ __forceinline__ double wave_total(double v) { return wave_sum64(v); }
+__device__ __forceinline__ float wave_total(float v) { return wave_sum(v); }
+__device__ __forceinline__ double wave_top(double v) { return wave_max64(v); }
+__device__ __forceinline__ float wave_top(float v) { return wave_max(v); }
+
+struct NormArgs {
+  const void* x;
+  const float* w;     // nullptr: ones
+  const float* b;     // nullptr: zeros
+  void* y;            // the type of x, or
+  int8_t* q;          // int8 with
+  float* s;           //   one scale per token
+  float* mean;        // nullptr: not wanted
+  float* rstd;
+  float eps;
+  int M, K;
+};
+
+// y = (d rstd) w + b of four features, in type S.
+template <typename S>
+__device__ __forceinline__ void normed4(const S (&d)[4], S rstd, const NormArgs& a, int k, S (&v)[4]) {
+  const f4 w = a.w ? load4(a.w + k) : f4{1.0f, 1.0f, 1.0f, 1.0f};
+  const f4 b = a.b ? load4(a.b + k) : f4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = d[i] * rstd * (S)w[i] + (S)b[i];
+}
+
+__device__ __forceinline__ uint32_t quant4_at(const double (&v)[4], double s) {
+  uint32_t r = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    r |= (uint32_t)(uint8_t)(int8_t)fmin(fmax(rint(v[i] / s), -127.0), 127.0) << (8 * i);
+  return r;
+}
+
+// The forward on tokens that fit registers.  Q: int8 output; then everything
+// from the mean on is computed in 64 bits, so that a value next to a border
+// between two int8 steps falls where exact arithmetic puts it (in 32 bits
+// about one value in 1e5 lands on the other side); S is the sums' type.
+template <typename T, int W, int J, bool Q>
+__global__ __launch_bounds__(kNormThreads) void norm_kernel(NormArgs a) {
+  using S = std::conditional_t<Q, double, float>;
+  constexpr int G = kNormThreads / 64 / W;   // tokens per workgroup
+  __shared__ S red[3][kNormThreads / 64];
+  const int wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x % (64 * W);
+  const int m = blockIdx.x * G + wave / W;
+  const bool live = m < a.M;                  // the last workgroup's waves past M only join the barriers
+  const T* x = static_cast<const T*>(a.x) + (size_t)(live ? m : 0) * a.K;
+  const auto add = [](S p, S q) { return p + q; };
+  const auto top = [](S p, S q) { return p > q ? p : q; };
+  f4 xv[J];
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const int k = 4 * (lane + 64 * W * j);
+    xv[j] = live && k < a.K ? load4(x + k) : f4{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  S sum = 0;
+#pragma unroll
+  for (int j = 0; j < J; ++j) sum += ((S)xv[j][0] + (S)xv[j][1]) + ((S)xv[j][2] + (S)xv[j][3]);
+  const S mean = group_join<W>((S)wave_total(sum), red[0], wave, add) / (S)a.K;
+  S sq = 0;
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    if (4 * (lane + 64 * W * j) < a.K) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const S d = (S)xv[j][i] - mean;
+        sq += d * d;
+      }
+    }
+  }
+  const S var = group_join<W>((S)wave_total(sq), red[1], wave, add) / (S)a.K;
+  const S rstd = (S)1 / sqrt(var + (S)a.eps);
+  if (a.mean && live && lane == 0) {
+    a.mean[m] = (float)mean;
+    a.rstd[m] = (float)rstd;
+  }
+  if constexpr (!Q) {
+    if (!live) return;
+    T* y = static_cast<T*>(a.y) + (size_t)m * a.K;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int k = 4 * (lane + 64 * W * j);
+      if (k >= a.K) continue;
+      const S d[4] = {xv[j][0] - mean, xv[j][1] - mean, xv[j][2] - mean, xv[j][3] - mean};
+      S v[4];
+      normed4(d, rstd, a, k, v);
+      store4(y + k, f4{v[0], v[1], v[2], v[3]});
+    }
+  } else {
+    S amax = 0;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int k = 4 * (lane + 64 * W * j);
+      if (k >= a.K) continue;
+      const S d[4] = {xv[j][0] - mean, xv[j][1] - mean, xv[j][2] - mean, xv[j][3] - mean};
+      S v[4];
+      normed4(d, rstd, a, k, v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) amax = fmax(amax, fabs(v[i]));
+    }
+    amax = group_join<W>((S)wave_top(amax), red[2], wave, top);
+    // the scale is the fp32 the product reads; the steps are counted in it
+    const float s = (float)(amax / 127.0) > 0.0f ? (float)(amax / 127.0) : 1.0f;
+    if (!live) return;
+    if (lane == 0) a.s[m] = s;
+    uint32_t* q = reinterpret_cast<uint32_t*>(a.q + (size_t)m * a.K);
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int k = 4 * (lane + 64 * W * j);
+      if (k >= a.K) continue;
+      const S d[4] = {xv[j][0] - mean, xv[j][1] - mean, xv[j][2] - mean, xv[j][3] - mean};
+      S v[4];
+      normed4(d, rstd, a, k, v);
+      q[k / 4] = quant4_at(v, (S)s);
+    }
+  }
+}
+
+// The forward on tokens of more than kNormMaxK features: one workgroup of 16
+// waves per token, which reads the token again for each pass (from L2).
+template <typename T, bool Q>
+__global__ __launch_bounds__(kLoopThreads) void norm_loop_kernel(NormArgs a) {
+  using S = std::conditional_t<Q, double, float>;
+  constexpr int W = kLoopThreads / 64;
+  __shared__ S red[3][W];
+  const int wave = threadIdx.x >> 6;
+  const int m = blockIdx.x;
+  const T* x = static_cast<const T*>(a.x) + (size_t)m * a.K;
+  const auto add = [](S p, S q) { return p + q; };
+  const auto top = [](S p, S q) { return p > q ? p : q; };
+  S sum = 0;
+  for (int k = 4 * threadIdx.x; k < a.K; k += 4 * kLoopThreads) {
+    const f4 v = load4(x + k);
+    sum += ((S)v[0] + (S)v[1]) + ((S)v[2] + (S)v[3]);
+  }
+  const S mean = group_join<W>((S)wave_total(sum), red[0], wave, add) / (S)a.K;
+  S sq = 0;
+  for (int k = 4 * threadIdx.x; k < a.K; k += 4 * kLoopThreads) {
+    const f4 v = load4(x + k);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sq += ((S)v[i] - mean) * ((S)v[i] - mean);
+  }
+  const S var = group_join<W>((S)wave_total(sq), red[1], wave, add) / (S)a.K;
+  const S rstd = (S)1 / sqrt(var + (S)a.eps);
+  if (a.mean && threadIdx.x == 0) {
+    a.mean[m] = (float)mean;
+    a.rstd[m] = (float)rstd;
+  }
+  auto value = [&](int k, S (&v)[4]) {
+    const f4 xv = load4(x + k);
+    const S d[4] = {xv[0] - mean, xv[1] - mean, xv[2] - mean, xv[3] - mean};
+    normed4(d, rstd, a, k, v);
+  };
+  S v[4];
+  if constexpr (!Q) {
+    T* y = static_cast<T*>(a.y) + (size_t)m * a.K;
+    for (int k = 4 * threadIdx.x; k < a.K; k += 4 * kLoopThreads) {
+      value(k, v);
+      store4(y + k, f4{v[0], v[1], v[2], v[3]});
+    }
+  } else {
+    S amax = 0;
+    for (int k = 4 * threadIdx.x; k < a.K; k += 4 * kLoopThreads) {
+      value(k, v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) amax = fmax(amax, fabs(v[i]));
+    }
+    amax = group_join<W>((S)wave_top(amax), red[2], wave, top);
+    const float s = (float)(amax / 127.0) > 0.0f ? (float)(amax / 127.0) : 1.0f;
+    if (threadIdx.x == 0) a.s[m] = s;
+    uint32_t* q = reinterpret_cast<uint32_t*>(a.q + (size_t)m * a.K);
+    for (int k = 4 * threadIdx.x; k < a.K; k += 4 * kLoopThreads) {
+      value(k, v);
+      q[k / 4] = quant4_at(v, (S)s);
+    }
+  }
+}
+
+struct NormBackArgs {
+  const void* dy;
+  const void* x;
+  const float* mean;
+  const float* rstd;
+  const float* w;     // nullptr: ones
+  void* dx;
+  float* part;        // [blocks][2][K] partial dw, db
+  int M, K;
+};
+
+// Gradients on tokens that fit registers.  A group of W waves takes tokens
+// group, group + groups, ... and keeps its sums of dw and db over them in
+// registers; the workgroup adds its groups through LDS at the end and
+// writes one row of partial sums, so no atomics and a fixed order.
+template <typename T, int W, int J>
+__global__ __launch_bounds__(kBackThreads) void norm_backward_kernel(NormBackArgs a) {
+  constexpr int G = kBackThreads / 64 / W;
+  __shared__ float red[2][2][kBackThreads / 64];
+  __shared__ f4 col[kBackThreads];
+  const int wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x % (64 * W);
+  const int group = wave / W;
+  const auto add = [](float p, float q) { return p + q; };
+  const float inv_k = 1.0f / (float)a.K;
+  f4 dw[J], db[J];
+#pragma unroll
+  for (int j = 0; j < J; ++j) dw[j] = db[j] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+  // every wave of the workgroup makes the same number of trips (barriers)
+  int turn = 0;
+  for (int m0 = blockIdx.x * G; m0 < a.M; m0 += gridDim.x * G, turn ^= 1) {
+    const int m = m0 + group;
+    const bool live = m < a.M;
+    const size_t row = (size_t)(live ? m : 0) * a.K;
+    const T* x = static_cast<const T*>(a.x) + row;
+    const T* dy = static_cast<const T*>(a.dy) + row;
+    const float mean = live ? a.mean[m] : 0.0f, rstd = live ? a.rstd[m] : 0.0f;
+    f4 xh[J], g[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int k = 4 * (lane + 64 * W * j);
+      const bool in = live && k < a.K;
+      xh[j] = in ? load4(x + k) : f4{mean, mean, mean, mean};
+      g[j] = in ? load4(dy + k) : f4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int k = 4 * (lane + 64 * W * j);
+      const f4 w = a.w && k < a.K ? load4(a.w + k) : f4{1.0f, 1.0f, 1.0f, 1.0f};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        xh[j][i] = (xh[j][i] - mean) * rstd;
+        dw[j][i] += g[j][i] * xh[j][i];
+        db[j][i] += g[j][i];
+        g[j][i] *= w[i];
+        s1 += g[j][i];
+        s2 += g[j][i] * xh[j][i];
+      }
+    }
+    s1 = group_join<W>(wave_sum(s1), red[turn][0], wave, add) * inv_k;
+    s2 = group_join<W>(wave_sum(s2), red[turn][1], wave, add) * inv_k;
+    if (live) {
+      T* dx = static_cast<T*>(a.dx) + row;
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const int k = 4 * (lane + 64 * W * j);
+        if (k >= a.K) continue;
+        f4 v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = rstd * (g[j][i] - s1 - xh[j][i] * s2);
+        store4(dx + k, v);
+      }
+    }
+  }
+  // the groups' sums of each column, joined through LDS one j at a time
+  float* part = a.part + (size_t)blockIdx.x * 2 * a.K;
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const int k = 4 * (lane + 64 * W * j);
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      __syncthreads();
+      col[threadIdx.x] = which ? db[j] : dw[j];
+      __syncthreads();
+      if (group == 0 && k < a.K) {
+        f4 t = col[lane];
+#pragma unroll
+        for (int gg = 1; gg < G; ++gg) t += col[gg * 64 * W + lane];
+        store4(part + (size_t)which * a.K + k, t);
+      }
+    }
+  }
+}
+
+// Gradients on longer tokens: dx by one workgroup per token that reads it
+// twice, ...
+template <typename T>
+__global__ __launch_bounds__(kLoopThreads) void norm_backward_dx_kernel(NormBackArgs a) {
+  constexpr int W = kLoopThreads / 64;
+  __shared__ float red[2][W];
+  const int wave = threadIdx.x >> 6;
+  const int m = blockIdx.x;
+  const T* x = static_cast<const T*>(a.x) + (size_t)m * a.K;
+  const T* dy = static_cast<const T*>(a.dy) + (size_t)m * a.K;
+  T* dx = static_cast<T*>(a.dx) + (size_t)m * a.K;
+  const auto add = [](float p, float q) { return p + q; };
+  const float mean = a.mean[m], rstd = a.rstd[m];
+  auto load = [&](int k, f4& g, f4& xh) {
+    g = load4(dy + k);
+    if (a.w) g *= load4(a.w + k);
+    xh = (load4(x + k) - mean) * rstd;
+  };
+  float s1 = 0.0f, s2 = 0.0f;
+  f4 g, xh;
+  for (int k = 4 * threadIdx.x; k < a.K; k += 4 * kLoopThreads) {
+    load(k, g, xh);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      s1 += g[i];
+      s2 += g[i] * xh[i];
+    }
+  }
+  s1 = group_join<W>(wave_sum(s1), red[0], wave, add) / (float)a.K;
+  s2 = group_join<W>(wave_sum(s2), red[1], wave, add) / (float)a.K;
+  for (int k = 4 * threadIdx.x; k < a.K; k += 4 * kLoopThreads) {
+    load(k, g, xh);
+    store4(dx + k, (g - s1 - xh * s2) * rstd);
+  }
+}
+
+// ... and partial dw, db by workgroups that each take 1024 columns (grid x)
+// of a share of the tokens (grid y).
+template <typename T>
+__global__ __launch_bounds__(256) void norm_backward_columns_kernel(NormBackArgs a) {
+  const int k = 4 * (blockIdx.x * 256 + threadIdx.x);
+  if (k >= a.K) return;
+  f4 dw{0.0f, 0.0f, 0.0f, 0.0f}, db = dw;
+  for (int m = blockIdx.y; m < a.M; m += gridDim.y) {
+    const f4 g = load4(static_cast<const T*>(a.dy) + (size_t)m * a.K + k);
+    const f4 x = load4(static_cast<const T*>(a.x) + (size_t)m * a.K + k);
+    dw += g * ((x - a.mean[m]) * a.rstd[m]);
+    db += g;
+  }
+  float* part = a.part + (size_t)blockIdx.y * 2 * a.K;
+  store4(part + k, dw);
+  store4(part + a.K + k, db);
+}
+
+// Sums of the partial rows: 64 columns x 4 shares of the rows per workgroup.
+__global__ __launch_bounds__(256) void norm_columns_kernel(const float* part, int rows, int K, float* dw,
+                                                           float* db) {
+  __shared__ float red[4][64];
+  const int lane = threadIdx.x & 63, share = threadIdx.x >> 6;
+  const int k = blockIdx.x * 64 + lane;      // of 2 K: dw's columns, then db's
+  float t = 0.0f;
+  if (k < 2 * K) {
+#pragma unroll 8
+    for (int r = share; r < rows; r += 4) t += part[(size_t)r * 2 * K + k];
+  }
+  red[share][lane] = t;
+  __syncthreads();
+  if (share == 0 && k < 2 * K) {
+    t = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+    if (k < K) {
+      if (dw) dw[k] = t;
+    } else if (db) {
+      db[k - K] = t;
+    }
+  }
+}
+
+template <typename T, bool Q>
+hipError_t launch_norm_as(const NormArgs& a, hipStream_t stream) {
+#define SHERRY_NORM(W_, J_) \
+  hipLaunchKernelGGL((norm_kernel<T, W_, J_, Q>), dim3((a.M + 4 / W_ - 1) / (4 / W_)), dim3(kNormThreads), 0, stream, a)
+  if (a.K <= 256) SHERRY_NORM(1, 1);
+  else if (a.K <= 512) SHERRY_NORM(1, 2);
+  else if (a.K <= 1024) SHERRY_NORM(1, 4);
+  else if (a.K <= 2048) SHERRY_NORM(4, 2);
+  else if (a.K <= 4096) SHERRY_NORM(4, 4);
+  else if (a.K <= 8192) SHERRY_NORM(4, 8);
+  else if (a.K <= kNormMaxK) SHERRY_NORM(4, 16);
+  else hipLaunchKernelGGL((norm_loop_kernel<T, Q>), dim3(a.M), dim3(kLoopThreads), 0, stream, a);
+#undef SHERRY_NORM
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_norm_backward_as(const NormBackArgs& a, int blocks, hipStream_t stream) {
+#define SHERRY_NORM_BACK(W_, J_) \
+  hipLaunchKernelGGL((norm_backward_kernel<T, W_, J_>), dim3(blocks), dim3(kBackThreads), 0, stream, a)
+  if (a.K <= 256) SHERRY_NORM_BACK(1, 1);
+  else if (a.K <= 512) SHERRY_NORM_BACK(1, 2);
+  else if (a.K <= 1024) SHERRY_NORM_BACK(1, 4);
+  else if (a.K <= 2048) SHERRY_NORM_BACK(1, 8);
+  else if (a.K <= 4096) SHERRY_NORM_BACK(2, 8);
+  else if (a.K <= 8192) SHERRY_NORM_BACK(4, 8);
+  else if (a.K <= kNormMaxK) SHERRY_NORM_BACK(8, 8);
+  else {
+    hipLaunchKernelGGL(norm_backward_dx_kernel<T>, dim3(a.M), dim3(kLoopThreads), 0, stream, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(norm_backward_columns_kernel<T>, dim3((a.K + 1023) / 1024, blocks), dim3(256), 0, stream, a);
+  }
+#undef SHERRY_NORM_BACK
+  return hipGetLastError();
+}
+
+int back_waves(int K) { return K <= 2048 ? 1 : K <= 4096 ? 2 : K <= 8192 ? 4 : 8; }
+
+}  // namespace
+
+hipError_t launch_layernorm(const void* x, const float* w, const float* b, float eps, void* y, int8_t* q,
+                            float* s, float* mean, float* rstd, int dtype, int M, int K, hipStream_t stream) {
+  const NormArgs a{x, w, b, y, q, s, mean, rstd, eps, M, K};
+  if (dtype == SHERRY_F32) return q ? launch_norm_as<float, true>(a, stream) : launch_norm_as<float, false>(a, stream);
+  if (dtype == SHERRY_F16)
+    return q ? launch_norm_as<_Float16, true>(a, stream) : launch_norm_as<_Float16, false>(a, stream);
+  return q ? launch_norm_as<__bf16, true>(a, stream) : launch_norm_as<__bf16, false>(a, stream);
+}
+
+// Workgroups of the backward = rows of partial dw, db.
+int layernorm_backward_rows(int M, int K) {
+  if (K > kNormMaxK) return M < 64 ? M : 64;
+  const int per = kBackThreads / 64 / back_waves(K);   // tokens per workgroup and trip
+  const int need = (M + per - 1) / per;
+  return need < kBackBlocks ? need : kBackBlocks;
+}
+
+hipError_t launch_layernorm_backward(const void* dy, const void* x, const float* mean, const float* rstd,
+                                     const float* w, void* dx, float* dw, float* db, int dtype, int M, int K,
+                                     float* part, hipStream_t stream, bool* partial) {
+  const NormBackArgs a{dy, x, mean, rstd, w, dx, part, M, K};
+  const int blocks = layernorm_backward_rows(M, K);
+  *partial = false;
+  hipError_t e = dtype == SHERRY_F32   ? launch_norm_backward_as<float>(a, blocks, stream)
+                 : dtype == SHERRY_F16 ? launch_norm_backward_as<_Float16>(a, blocks, stream)
+                                       : launch_norm_backward_as<__bf16>(a, blocks, stream);
+  if (e != hipSuccess) return e;
+  *partial = true;
+  if (dw || db) {
+    hipLaunchKernelGGL(norm_columns_kernel, dim3((2 * K + 63) / 64), dim3(256), 0, stream, part, blocks, K, dw, db);
+    e = hipGetLastError();
+  }
+  return e;
+}
+
+}  // namespace sherry

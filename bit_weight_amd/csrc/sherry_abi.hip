@@ -1,12 +1,14 @@
 // C ABI of libsherry: host-side validation, launch planning and dispatch.
 // Every argument error is detected here before any HIP call.
 #include <atomic>
+#include <cmath>
 #include <mutex>
 #include <string.h>
 
 #include "../../include/sherry.h"
 #include "sherry_device.h"
 #include "sherry_launch.h"
+#include "sherry_types.h"
 
 namespace sherry {
 
@@ -317,6 +319,50 @@ GemmPlan plan_gemm(int M, int N, int K) {
   return p;
 }
 
+// The plan of a product with an epilogue: the product's, on the matrix-core
+// paths only.
+GemmPlan plan_epilogue(int M, int N, int K) {
+  const GemmPlan p = plan_gemm(M, N, K);
+  return p.path == 0 ? plan_mfma_gemv(M, N, K) : p;
+}
+
+// The gated product's plan: that of one product over both matrices' row
+// tiles, whose workgroups pair a gate tile with the up tile of the same
+// outputs.  On the GEMV the paired workgroup has the waves of both.
+GemmPlan plan_glu(int M, int N, int K) {
+  const int both = 2 * kTileRows * row_tiles(N);
+  const GemmPlan p = plan_epilogue(M, both, K);
+  if (p.path == 1) return p;   // n tiles of kBN / 2 outputs: as many as of kBN rows of both
+  const int m = M < kGemvMaxM ? M : kGemvMaxM;
+  const int kw = 2 * p.rw > 16 || m > 16 ? (m > 16 ? 8 : 16) : 2 * p.rw;
+  GemmPlan q = mfma_gemv_plan_of(m, N, K, kw, p.splits < kGluMaxSplits ? p.splits : kGluMaxSplits);
+  q.chunk = p.chunk;
+  return q;
+}
+
+hipError_t launch_product_epilogue(const GemmPlan& plan, const GemmArgs& args, int ep,
+                                   const EpilogueArgs& e, hipStream_t stream, bool* partial) {
+  *partial = false;
+  if (plan.path == 1) return launch_mfma_gemm_epilogue(plan, args, ep, e, stream);
+  const int chunk = plan.chunk > 0 ? plan.chunk : args.M;
+  const size_t row = (size_t)args.N * dtype_bytes(e.dtype);
+  for (int m0 = 0; m0 < args.M; m0 += chunk) {
+    GemmArgs c = args;
+    EpilogueArgs ec = e;
+    c.M = args.M - m0 < chunk ? args.M - m0 : chunk;
+    c.x = args.x + (size_t)m0 * args.K;
+    c.s_x = args.s_x + m0;
+    ec.out = static_cast<char*>(e.out) + m0 * row;
+    if (e.residual) ec.residual = static_cast<const char*>(e.residual) + m0 * row;
+    const hipError_t err = launch_mfma_gemv_epilogue(plan, c, ep, ec, stream);
+    if (err != hipSuccess) {
+      *partial = m0 > 0;
+      return err;
+    }
+  }
+  return hipSuccess;
+}
+
 }  // namespace sherry
 
 using namespace sherry;
@@ -464,6 +510,7 @@ const char* sherry_status_string(int status) {
     case SHERRY_ERR_PARTIAL:
       return "SHERRY_ERR_PARTIAL: a launch failed after earlier launches of the call were enqueued; "
              "the output is incomplete, the workspace is left zero";
+    case SHERRY_ERR_ARG: return "SHERRY_ERR_ARG: unknown activation or element type, or eps not positive";
     default: return "SHERRY_ERR_UNKNOWN";
   }
 }
@@ -686,6 +733,159 @@ sherry_status sherry_linear(const float* x, const void* packed, const float* alp
     }
   }
   return e == hipSuccess ? SHERRY_OK : (partial ? SHERRY_ERR_PARTIAL : SHERRY_ERR_HIP);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Feed-forward operators.
+namespace {
+
+bool dtype_ok(int dtype) { return dtype == SHERRY_F32 || dtype == SHERRY_F16 || dtype == SHERRY_BF16; }
+bool act_ok(int act) { return act >= SHERRY_ACT_NONE && act <= SHERRY_ACT_GELU_TANH; }
+
+sherry_status status_of(hipError_t e, bool partial) {
+  return e == hipSuccess ? SHERRY_OK : (partial ? SHERRY_ERR_PARTIAL : SHERRY_ERR_HIP);
+}
+
+// Checks and launches a forward product with an epilogue; the matrices and
+// vectors that only one of the two operators has are checked by its caller.
+sherry_status run_epilogue(const GemmPlan& plan, GemmArgs args, int ep, const EpilogueArgs& e,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  if (plan.ws_bytes > 0) {
+    if (!workspace || workspace_bytes < plan.ws_bytes) return SHERRY_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return SHERRY_ERR_ALIGN;
+    args.partials = static_cast<int32_t*>(workspace);
+  }
+  const sherry_status d = check_device();
+  if (d != SHERRY_OK) return d;
+  bool partial = false;
+  const hipError_t err = launch_product_epilogue(plan, args, ep, e, static_cast<hipStream_t>(stream), &partial);
+  return status_of(err, partial);
+}
+
+GemmArgs product_of(const int8_t* x, const float* s_x, const void* packed, const float* alpha, int64_t M,
+                    int64_t N, int64_t K) {
+  GemmArgs a{};
+  a.x = x;
+  a.s_x = s_x;
+  a.packed = static_cast<const uint8_t*>(packed);
+  a.alpha = alpha;
+  a.M = (int)M;
+  a.N = (int)N;
+  a.K = (int)K;
+  return a;
+}
+
+sherry_status check_norm(const void* x, const float* weight, const float* bias, float eps, const float* mean,
+                         const float* rstd, int dtype, int64_t M, int64_t K) {
+  if (!x || (mean == nullptr) != (rstd == nullptr)) return SHERRY_ERR_NULL;
+  if (M < 1 || K < 4 || M > kMaxDim || K > kMaxDim || K % 4 != 0) return SHERRY_ERR_SHAPE;
+  if (!dtype_ok(dtype) || !(eps > 0.0f) || !std::isfinite(eps)) return SHERRY_ERR_ARG;
+  if (!aligned(x, 16) || !aligned(weight, 16) || !aligned(bias, 16) || !aligned(mean, 4) || !aligned(rstd, 4))
+    return SHERRY_ERR_ALIGN;
+  return SHERRY_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t sherry_gemm_fused_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  return shape_ok(M, N, K) ? plan_epilogue((int)M, (int)N, (int)K).ws_bytes : 0;
+}
+
+size_t sherry_glu_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  return shape_ok(M, N, K) ? plan_glu((int)M, (int)N, (int)K).ws_bytes : 0;
+}
+
+sherry_status sherry_gemm_fused(const int8_t* x, const float* s_x, const void* packed, const float* alpha,
+                                const float* bias, int act, const void* residual, void* y, int dtype,
+                                int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes,
+                                void* stream) {
+  if (!x || !s_x || !packed || !alpha || !y) return SHERRY_ERR_NULL;
+  if (!shape_ok(M, N, K)) return SHERRY_ERR_SHAPE;
+  if (!act_ok(act) || !dtype_ok(dtype)) return SHERRY_ERR_ARG;
+  if (!aligned(x, 16) || !aligned(packed, 16) || !aligned(y, 16) || !aligned(residual, 16) ||
+      !aligned(s_x, 4) || !aligned(alpha, 4) || !aligned(bias, 4))
+    return SHERRY_ERR_ALIGN;
+  EpilogueArgs e{};
+  e.bias = bias;
+  e.residual = residual;
+  e.out = y;
+  e.act = act;
+  e.dtype = dtype;
+  return run_epilogue(plan_epilogue((int)M, (int)N, (int)K), product_of(x, s_x, packed, alpha, M, N, K),
+                      kEpFused, e, workspace, workspace_bytes, stream);
+}
+
+sherry_status sherry_glu(const int8_t* x, const float* s_x, const void* packed_gate, const float* alpha_gate,
+                         const void* packed_up, const float* alpha_up, int act, void* h, int dtype, int64_t M,
+                         int64_t N, int64_t K, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!x || !s_x || !packed_gate || !alpha_gate || !packed_up || !alpha_up || !h) return SHERRY_ERR_NULL;
+  if (!shape_ok(M, N, K)) return SHERRY_ERR_SHAPE;
+  if (!act_ok(act) || !dtype_ok(dtype)) return SHERRY_ERR_ARG;
+  if (!aligned(x, 16) || !aligned(packed_gate, 16) || !aligned(packed_up, 16) || !aligned(h, 16) ||
+      !aligned(s_x, 4) || !aligned(alpha_gate, 4) || !aligned(alpha_up, 4))
+    return SHERRY_ERR_ALIGN;
+  EpilogueArgs e{};
+  e.packed2 = static_cast<const uint8_t*>(packed_up);
+  e.alpha2 = alpha_up;
+  e.out = h;
+  e.act = act;
+  e.dtype = dtype;
+  return run_epilogue(plan_glu((int)M, (int)N, (int)K),
+                      product_of(x, s_x, packed_gate, alpha_gate, M, N, K), kEpGlu, e, workspace,
+                      workspace_bytes, stream);
+}
+
+sherry_status sherry_layernorm(const void* x, const float* weight, const float* bias, float eps, void* y,
+                               float* mean, float* rstd, int dtype, int64_t M, int64_t K, void* stream) {
+  if (!y) return SHERRY_ERR_NULL;
+  const sherry_status c = check_norm(x, weight, bias, eps, mean, rstd, dtype, M, K);
+  if (c != SHERRY_OK) return c;
+  if (!aligned(y, 16)) return SHERRY_ERR_ALIGN;
+  const sherry_status d = check_device();
+  if (d != SHERRY_OK) return d;
+  return status_of(launch_layernorm(x, weight, bias, eps, y, nullptr, nullptr, mean, rstd, dtype, (int)M, (int)K,
+                                    static_cast<hipStream_t>(stream)), false);
+}
+
+sherry_status sherry_layernorm_quantize(const void* x, const float* weight, const float* bias, float eps,
+                                        int8_t* q, float* s_x, float* mean, float* rstd, int dtype, int64_t M,
+                                        int64_t K, void* stream) {
+  if (!q || !s_x) return SHERRY_ERR_NULL;
+  const sherry_status c = check_norm(x, weight, bias, eps, mean, rstd, dtype, M, K);
+  if (c != SHERRY_OK) return c;
+  if (!aligned(q, 4) || !aligned(s_x, 4)) return SHERRY_ERR_ALIGN;
+  const sherry_status d = check_device();
+  if (d != SHERRY_OK) return d;
+  return status_of(launch_layernorm(x, weight, bias, eps, nullptr, q, s_x, mean, rstd, dtype, (int)M, (int)K,
+                                    static_cast<hipStream_t>(stream)), false);
+}
+
+size_t sherry_layernorm_backward_scratch_bytes(int64_t M, int64_t K) {
+  if (M < 1 || K < 4 || M > kMaxDim || K > kMaxDim || K % 4 != 0) return 0;
+  return round256((size_t)layernorm_backward_rows((int)M, (int)K) * 2 * K * sizeof(float));
+}
+
+sherry_status sherry_layernorm_backward(const void* dy, const void* x, const float* mean, const float* rstd,
+                                        const float* weight, void* dx, float* dweight, float* dbias, int dtype,
+                                        int64_t M, int64_t K, void* scratch, size_t scratch_bytes,
+                                        void* stream) {
+  if (!dy || !mean || !rstd || !dx) return SHERRY_ERR_NULL;
+  const sherry_status c = check_norm(x, weight, nullptr, 1.0f, mean, rstd, dtype, M, K);
+  if (c != SHERRY_OK) return c;
+  if (!aligned(dy, 16) || !aligned(dx, 16) || !aligned(dweight, 4) || !aligned(dbias, 4)) return SHERRY_ERR_ALIGN;
+  if (!scratch || scratch_bytes < sherry_layernorm_backward_scratch_bytes(M, K)) return SHERRY_ERR_WORKSPACE;
+  if (!aligned(scratch, 256)) return SHERRY_ERR_ALIGN;
+  const sherry_status d = check_device();
+  if (d != SHERRY_OK) return d;
+  bool partial = false;
+  const hipError_t e = launch_layernorm_backward(dy, x, mean, rstd, weight, dx, dweight, dbias, dtype, (int)M,
+                                                 (int)K, static_cast<float*>(scratch),
+                                                 static_cast<hipStream_t>(stream), &partial);
+  return status_of(e, partial);
 }
 
 }  // extern "C"

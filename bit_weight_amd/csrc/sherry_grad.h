@@ -1,0 +1,50 @@
+// The input-gradient product's operands.
+//
+// dx[m,k] = sum over rows n of z[m,n] T[n,k], z the gradient of row n's
+// pre-activation times alpha[n], runs on the fp16 matrix cores: T is exact
+// there and z is written as one fp16 term (relative rounding 2^-12, an
+// eighth of the rounding a bf16 result gets anyway) or, for fp16 and fp32
+// results, as two, high and low, which together keep 22 bits.  fp16 has the
+// digits but not the range, so each token's z is scaled by a power of two
+// (exact) that puts a bound on |z| at 2^15.  The bound needs no pass over z:
+//   |pre-activation| <= P = s_x sum|q| max|alpha| + max|bias|,
+//   |act'| <= 1.25 (2 P for relu2), |act| <= P (P^2 for relu2).
+// It is some 2^4 .. 2^8 above the largest |z| of a row; terms down to 2^-29
+// of the bound stay in fp16's normal range, so the slack costs no digits.
+#pragma once
+
+#include "sherry_launch.h"
+#include "sherry_types.h"
+
+namespace sherry {
+
+// e such that |z| 2^e <= 2^15 for every z of a token: rows = (max |dy|,
+// sum |q|), tops = (max |alpha|, max |alpha2|, max |bias|).  Infinite
+// gradients take the least scale, so that they alone overflow.
+__device__ __forceinline__ int grad_exponent(float2 row, float s_x, const float* tops, int act, bool glu) {
+  const double dy = row.x, sum = (double)row.y * fabs((double)s_x);
+  const double a1 = tops[0], a2 = tops[1], pre = sum * a1 + (glu ? 0.0 : (double)tops[2]);
+  const double slope = act == SHERRY_ACT_RELU2 ? 2.0 * pre : 1.25;
+  const double bound = glu ? dy * slope * a1 * fmax(sum, 1e-300) * a2 : dy * slope * a1;
+  if (!(bound > 0.0)) return 0;
+  if (bound > 1e300) return -120;
+  const int e = 15 - (ilogb(bound) + 1);
+  return e < -120 ? -120 : e > 120 ? 120 : e;
+}
+
+__device__ __forceinline__ float exp2_of(int e) { return __builtin_bit_cast(float, (uint32_t)(e + 127) << 23); }
+
+// v as one fp16 term, or as a high and a low one `stride` elements apart.
+__device__ __forceinline__ void store_terms(_Float16* p, f4 v, int terms, int stride) {
+  const h4 hi = __builtin_convertvector(v, h4);
+  *reinterpret_cast<h4*>(p) = hi;
+  if (terms == 2) {
+    f4 rest = v - __builtin_convertvector(hi, f4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (!(fabsf(rest[i]) < 65536.0f)) rest[i] = 0.0f;   // an infinite or NaN high term stands alone
+    *reinterpret_cast<h4*>(p + stride) = __builtin_convertvector(rest, h4);
+  }
+}
+
+}  // namespace sherry

@@ -4,6 +4,7 @@
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+#include <type_traits>
 
 namespace sherry {
 
@@ -32,6 +33,7 @@ constexpr int kChunkMaxGrid = 64;     //   launches of 64 tokens where the prefi
 constexpr int kGemvWaves = 4;         // waves per GEMV workgroup
 constexpr int kCUs = 256;             // MI355X compute units: one round of one workgroup each
 constexpr int kDefaultSmallMPath = 2;  // M <= 16: 0 = lookup tables, 2 = matrix-core GEMV
+constexpr int kGluMaxSplits = 255;     // gated product: arrivals a split-K cell counts
 constexpr int kFuseMaxM = 4;           // fused quantization: at most 4 tokens,
 constexpr int kFuseMaxMK = 16384;      //   M*K elements read per workgroup for the scales,
 constexpr int kFuseMaxSpan = 32;       //   and k-tiles per K-split held in LDS as int8
@@ -41,6 +43,17 @@ constexpr int kFuseMaxSpan = 32;       //   and k-tiles per K-split held in LDS 
 void set_plan_override(int path, int rw, int ch, int splits);
 
 GemmPlan plan_gemm(int M, int N, int K);
+
+// Backward: what the recomputing product writes and scales by.
+struct GradArgs {
+  const void* dy;          // [M,N] of type dtype
+  const float2* rows;      // per token: max |dy|, sum |q|
+  const float* tops;       // max |alpha|, max |alpha2|, max |bias|
+  uint16_t* z;             // fp16 [M][terms][parts][64 row tiles]: the scaled gradients
+  int terms;               // fp16 terms per gradient: 1, or 2 (high and low parts)
+  float* part0;            // [token tiles][N] partial sums of dalpha
+  float* part1;            // the same of dalpha2 or dbias
+};
 
 struct GemmArgs {
   const int8_t* x;     // int8 activations [M,K], or
@@ -54,19 +67,44 @@ struct GemmArgs {
   int32_t* partials;   // workspace: zero-filled 64-bit accumulators [M,N] for K-splits
 };
 
+// What a product's epilogue does with the exact sums.
+enum Epilogue {
+  kEpNone = 0,       // y = (acc s_x) alpha, or the int32 sums
+  kEpFused = 1,      // out = act((acc s_x) alpha + bias) + residual
+  kEpGlu = 2,        // out = act((acc s_x) alpha) * ((acc2 s_x) alpha2), two weight matrices
+  kEpFusedBack = 3,  // the gradients of kEpFused's pre-activation, for the input-gradient product
+  kEpGluBack = 4     // those of kEpGlu's two
+};
+constexpr bool ep_glu(int ep) { return ep == kEpGlu || ep == kEpGluBack; }
+constexpr bool ep_back(int ep) { return ep == kEpFusedBack || ep == kEpGluBack; }
+
+// Arguments of the epilogues other than kEpNone (kEpNone's kernels take none).
+struct EpilogueArgs {
+  const uint8_t* packed2;   // GLU: the up matrix; packed / alpha are the gate's
+  const float* alpha2;
+  const float* bias;        // fused: nullptr = none
+  const void* residual;     // fused: nullptr = none
+  void* out;                // forward: [M,N] of type dtype
+  int act, dtype;           // SHERRY_ACT_*, SHERRY_F32 / F16 / BF16
+  GradArgs grad;            // backward
+};
+struct NoEpilogueArgs {};
+template <int EP>
+using EpilogueOf = std::conditional_t<EP == kEpNone, NoEpilogueArgs, EpilogueArgs>;
+
 // The product kernels take their arguments as pointers and scalars, not as
 // a GemmArgs struct, with the ones their first instructions need in front:
 // packed, x, xf, M, N, K, two plan integers (the GEMVs: splits and k-tiles
 // per split; the prefill GEMM: n tiles and 0), then s_x, alpha, y, acc,
-// partials.  The build has the leading ones preloaded into SGPRs at
+// partials, and the epilogue's where there is one.  The build has the leading ones preloaded into SGPRs at
 // dispatch (gfx950 kernel-argument preload), which removes a memory round
 // trip from the start of every launch; a struct argument cannot be
 // preloaded.
-template <typename Kernel>
+template <typename Kernel, typename... E>
 inline void launch_product_kernel(Kernel kernel, dim3 grid, dim3 block, size_t lds_bytes,
-                                  hipStream_t stream, const GemmArgs& a, int plan0, int plan1) {
+                                  hipStream_t stream, const GemmArgs& a, int plan0, int plan1, E... e) {
   hipLaunchKernelGGL(kernel, grid, block, lds_bytes, stream, a.packed, a.x, a.xf, a.M, a.N, a.K, plan0,
-                     plan1, a.s_x, a.alpha, a.y, a.acc, a.partials);
+                     plan1, a.s_x, a.alpha, a.y, a.acc, a.partials, e...);
 }
 
 // The GemmArgs a product kernel rebuilds from its arguments.
@@ -110,5 +148,18 @@ hipError_t launch_mfma_gemm(const GemmPlan& plan, const GemmArgs& args, hipStrea
 // whether earlier launches of the same call were already enqueued.
 hipError_t launch_product(const GemmPlan& plan, const GemmArgs& args, hipStream_t stream,
                           bool* partial = nullptr);
+// The same kernels with another epilogue (paths 1 and 2; ep != kEpNone).
+hipError_t launch_mfma_gemv_epilogue(const GemmPlan& plan, const GemmArgs& args, int ep,
+                                     const EpilogueArgs& e, hipStream_t stream);
+hipError_t launch_mfma_gemm_epilogue(const GemmPlan& plan, const GemmArgs& args, int ep,
+                                     const EpilogueArgs& e, hipStream_t stream);
+
+// Layer norm (norm.hip): y in x's type, or q and s (int8 tokens).
+hipError_t launch_layernorm(const void* x, const float* w, const float* b, float eps, void* y, int8_t* q,
+                            float* s, float* mean, float* rstd, int dtype, int M, int K, hipStream_t stream);
+int layernorm_backward_rows(int M, int K);   // rows of 2 K partial sums the backward needs
+hipError_t launch_layernorm_backward(const void* dy, const void* x, const float* mean, const float* rstd,
+                                     const float* w, void* dx, float* dw, float* db, int dtype, int M, int K,
+                                     float* part, hipStream_t stream, bool* partial);
 
 }  // namespace sherry

@@ -1,0 +1,127 @@
+// Element types of the feed-forward operators' inputs and outputs (fp32,
+// fp16, bf16; arithmetic is fp32 everywhere) and the activation functions.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/sherry.h"
+
+namespace sherry {
+
+typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+typedef __bf16 b4 __attribute__((ext_vector_type(4)));
+typedef float f4 __attribute__((ext_vector_type(4)));
+
+__host__ __device__ constexpr int dtype_bytes(int dtype) { return dtype == SHERRY_F32 ? 4 : 2; }
+
+// Four consecutive elements as fp32, and back with one rounding to nearest
+// even.  p is aligned to four elements.
+template <typename T>
+__device__ __forceinline__ f4 load4(const T* p) {
+  if constexpr (sizeof(T) == 4) {
+    return *reinterpret_cast<const f4*>(p);
+  } else {
+    typedef T v4 __attribute__((ext_vector_type(4)));
+    return __builtin_convertvector(*reinterpret_cast<const v4*>(p), f4);
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void store4(T* p, f4 v) {
+  if constexpr (sizeof(T) == 4) {
+    *reinterpret_cast<f4*>(p) = v;
+  } else {
+    typedef T v4 __attribute__((ext_vector_type(4)));
+    *reinterpret_cast<v4*>(p) = __builtin_convertvector(v, v4);
+  }
+}
+
+// The same with the type known at run time (the branch is wave-uniform).
+__device__ __forceinline__ f4 load4_as(const void* p, size_t i, int dtype) {
+  if (dtype == SHERRY_F32) return load4(static_cast<const float*>(p) + i);
+  if (dtype == SHERRY_F16) return load4(static_cast<const _Float16*>(p) + i);
+  return load4(static_cast<const __bf16*>(p) + i);
+}
+
+__device__ __forceinline__ void store4_as(void* p, size_t i, int dtype, f4 v) {
+  if (dtype == SHERRY_F32) store4(static_cast<float*>(p) + i, v);
+  else if (dtype == SHERRY_F16) store4(static_cast<_Float16*>(p) + i, v);
+  else store4(static_cast<__bf16*>(p) + i, v);
+}
+
+__device__ __forceinline__ float load1_as(const void* p, size_t i, int dtype) {
+  if (dtype == SHERRY_F32) return static_cast<const float*>(p)[i];
+  if (dtype == SHERRY_F16) return (float)static_cast<const _Float16*>(p)[i];
+  return (float)static_cast<const __bf16*>(p)[i];
+}
+
+__device__ __forceinline__ void store1_as(void* p, size_t i, int dtype, float v) {
+  if (dtype == SHERRY_F32) static_cast<float*>(p)[i] = v;
+  else if (dtype == SHERRY_F16) static_cast<_Float16*>(p)[i] = (_Float16)v;
+  else static_cast<__bf16*>(p)[i] = (__bf16)v;
+}
+
+// Activation functions and their slopes in fp32 (SHERRY_ACT_*; the switch is
+// wave-uniform).  silu(z) = z / (1 + e^-z); gelu(z) = z Phi(z), Phi the normal
+// distribution function; gelu_tanh replaces Phi by (1 + tanh(c (z + 0.044715
+// z^3))) / 2, c = sqrt(2 / pi); relu2 is relu squared.
+constexpr float kSqrtHalf = 0.70710678118654752f;
+constexpr float kInvSqrt2Pi = 0.39894228040143268f;
+constexpr float kSqrt2OverPi = 0.79788456080286536f;
+constexpr float kGeluCubic = 0.044715f;
+
+__device__ __forceinline__ float act_value(float z, int act) {
+  switch (act) {
+    case SHERRY_ACT_RELU: return z > 0.0f || z != z ? z : 0.0f;
+    case SHERRY_ACT_RELU2: return z > 0.0f || z != z ? z * z : 0.0f;
+    case SHERRY_ACT_SILU: return z / (1.0f + expf(-z));
+    case SHERRY_ACT_GELU: return 0.5f * z * (1.0f + erff(z * kSqrtHalf));
+    case SHERRY_ACT_GELU_TANH:
+      return 0.5f * z * (1.0f + tanhf(kSqrt2OverPi * (z + kGeluCubic * z * z * z)));
+    default: return z;
+  }
+}
+
+__device__ __forceinline__ float act_slope(float z, int act) {
+  switch (act) {
+    case SHERRY_ACT_RELU: return z > 0.0f ? 1.0f : 0.0f;
+    case SHERRY_ACT_RELU2: return z > 0.0f ? 2.0f * z : 0.0f;
+    case SHERRY_ACT_SILU: {
+      const float s = 1.0f / (1.0f + expf(-z));
+      return s * (1.0f + z * (1.0f - s));
+    }
+    case SHERRY_ACT_GELU:
+      return 0.5f * (1.0f + erff(z * kSqrtHalf)) + z * (kInvSqrt2Pi * expf(-0.5f * z * z));
+    case SHERRY_ACT_GELU_TANH: {
+      const float t = tanhf(kSqrt2OverPi * (z + kGeluCubic * z * z * z));
+      return 0.5f * (1.0f + t) +
+             0.5f * z * (1.0f - t * t) * kSqrt2OverPi * (1.0f + 3.0f * kGeluCubic * z * z);
+    }
+    default: return 1.0f;
+  }
+}
+
+// Sum over the 64 lanes of a wave, the same value in every lane (all lanes
+// active), by the DPP steps of wave_max.
+template <int CTRL>
+__device__ __forceinline__ float dpp_shift(float x) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, x),
+                                                               __builtin_bit_cast(int, x), CTRL, 0xF,
+                                                               0xF, false));
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+  v += dpp_shift<0xB1>(v);     // quad_perm [1,0,3,2]
+  v += dpp_shift<0x4E>(v);     // quad_perm [2,3,0,1]
+  v += dpp_shift<0x124>(v);    // row_ror:4
+  v += dpp_shift<0x128>(v);    // row_ror:8
+  const int u = __builtin_bit_cast(int, v);
+  const float r0 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(u, 0));
+  const float r1 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(u, 16));
+  const float r2 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(u, 32));
+  const float r3 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(u, 48));
+  return (r0 + r1) + (r2 + r3);
+}
+
+}  // namespace sherry

@@ -67,14 +67,17 @@ typedef enum {
   SHERRY_ERR_WORKSPACE = -4, /* workspace missing or smaller than required */
   SHERRY_ERR_HIP = -5,       /* a HIP runtime call or launch failed */
   SHERRY_ERR_DEVICE = -6,    /* the current device is not a gfx950 GPU */
-  SHERRY_ERR_PARTIAL = -7    /* a launch failed after earlier launches of the
+  SHERRY_ERR_PARTIAL = -7,   /* a launch failed after earlier launches of the
                                 same call were enqueued (sherry_linear's
-                                quantizer, or the 64-token launches of
-                                64 < M <= 128): those complete, so the output
+                                quantizer, the 64-token launches of
+                                64 < M <= 128, or an earlier step of a
+                                backward pass): those complete, so the output
                                 is partly written; a launch that fails runs
                                 nothing and every launch that runs leaves the
                                 split-K workspace zero, so the workspace needs
                                 no re-zeroing */
+  SHERRY_ERR_ARG = -8        /* an activation, element type or eps that is
+                                none of the listed ones */
 } sherry_status;
 
 /* Human-readable name of a status code (static string; never NULL). */
@@ -230,6 +233,103 @@ sherry_status sherry_gemm2(const int8_t* x, const float* s_x, const void* packed
                            const float* alpha, float* y, int64_t M, int64_t N,
                            int64_t K, void* workspace, size_t workspace_bytes,
                            void* stream);
+
+/* --- Feed-forward operators ------------------------------------------------
+ * What surrounds the product in a decoder layer: bias, activation and
+ * residual in the product's epilogue, the gated block whose two products
+ * share one kernel, and the layer norm that makes the int8 tokens.
+ *
+ * Element types of x / y / residuals / gradients (dtype): arithmetic is fp32
+ * (64-bit where stated), and each output is rounded once, to nearest even. */
+#define SHERRY_F32 0
+#define SHERRY_F16 1
+#define SHERRY_BF16 2
+
+/* Activations (act), Phi = the normal distribution function:
+ *   NONE z;  RELU max(z, 0);  RELU2 max(z, 0)^2;  SILU z / (1 + e^-z);
+ *   GELU z Phi(z);
+ *   GELU_TANH z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2. */
+#define SHERRY_ACT_NONE 0
+#define SHERRY_ACT_RELU 1
+#define SHERRY_ACT_RELU2 2
+#define SHERRY_ACT_SILU 3
+#define SHERRY_ACT_GELU 4
+#define SHERRY_ACT_GELU_TANH 5
+
+/* The product with a bias, an activation and a residual in its epilogue:
+ *   y[m,n] = act((acc[m,n] * s_x[m]) * alpha[n] + bias[n]) + residual[m,n].
+ *   x, s_x, packed, alpha, M, N, K: as sherry_gemm.
+ *   bias     [N] fp32, or NULL.       act: SHERRY_ACT_*.
+ *   residual [M,N] of type dtype, 16-byte aligned, or NULL.  It may be y
+ *            itself (each element is read before it is written, by the same
+ *            thread); it must not overlap y otherwise.
+ *   y        [M,N] of type dtype (written), 16-byte aligned.
+ *   workspace: at least sherry_gemm_fused_workspace_bytes(M,N,K) bytes, by
+ *            the rules of sherry_workspace_bytes (zero before its first use,
+ *            left zero); the two operators' calls may share one buffer on
+ *            one stream with each other and with sherry_gemm.
+ * Runs on sherry_gemm's matrix-core kernels and plan (the lookup-table path,
+ * which only sherry_gemm_plan_override selects, is taken as path 2 here). */
+sherry_status sherry_gemm_fused(const int8_t* x, const float* s_x, const void* packed,
+                                const float* alpha, const float* bias, int act,
+                                const void* residual, void* y, int dtype, int64_t M, int64_t N,
+                                int64_t K, void* workspace, size_t workspace_bytes, void* stream);
+size_t sherry_gemm_fused_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+/* The gated feed-forward block's first half, both products in one kernel:
+ *   h[m,n] = act(g) * u,  g = (acc_gate * s_x[m]) * alpha_gate[n],
+ *                         u = (acc_up * s_x[m]) * alpha_up[n].
+ *   packed_gate, packed_up: two [N,K] matrices in the packed format; the
+ *   other arguments as sherry_gemm_fused.  act(g) * u is formed in fp32. */
+sherry_status sherry_glu(const int8_t* x, const float* s_x, const void* packed_gate,
+                         const float* alpha_gate, const void* packed_up, const float* alpha_up,
+                         int act, void* h, int dtype, int64_t M, int64_t N, int64_t K,
+                         void* workspace, size_t workspace_bytes, void* stream);
+size_t sherry_glu_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+/* Layer norm of each token:
+ *   y = ((x - mean) * rstd) * weight + bias,  mean = sum x / K,
+ *   rstd = 1 / sqrt(sum (x - mean)^2 / K + eps).
+ *   x       [M,K] of type dtype, 16-byte aligned, 1 <= M <= 2^20,
+ *           4 <= K <= 2^20, K % 4 == 0.
+ *   weight, bias  [K] fp32, 16-byte aligned, or NULL (ones, zeros).
+ *   eps     finite and positive.
+ *   y       [M,K] of type dtype (written), 16-byte aligned; may be x.
+ *   mean, rstd  [M] fp32 (written), for the backward pass; both or neither
+ *           NULL. */
+sherry_status sherry_layernorm(const void* x, const float* weight, const float* bias, float eps,
+                               void* y, float* mean, float* rstd, int dtype, int64_t M, int64_t K,
+                               void* stream);
+
+/* The same token as the products take it: the norm's value v, computed in 64
+ * bits, as int8 with one scale,
+ *   s_x = max|v| / 127 rounded to fp32 (1 if that is 0),
+ *   q = clamp(rint(v / s_x), -127, 127), half to even.
+ *   q  [M,K] int8 (written), 4-byte aligned;  s_x [M] fp32 (written).
+ *   x finite; the rest as sherry_layernorm. */
+sherry_status sherry_layernorm_quantize(const void* x, const float* weight, const float* bias,
+                                        float eps, int8_t* q, float* s_x, float* mean, float* rstd,
+                                        int dtype, int64_t M, int64_t K, void* stream);
+
+/* Gradients of sherry_layernorm, with xh = (x - mean) * rstd and
+ * g = dy * weight:
+ *   dx = rstd * (g - sum g / K - xh * sum(g * xh) / K),
+ *   dweight = sum over tokens of dy * xh,  dbias = sum over tokens of dy.
+ *   dy, x   [M,K] of type dtype;  mean, rstd [M] as the forward wrote them.
+ *   weight  as the forward's.
+ *   dx      [M,K] of type dtype (written); may be dy, must not be x.
+ *   dweight, dbias  [K] fp32 (written), 4-byte aligned, each may be NULL.
+ *   scratch at least sherry_layernorm_backward_scratch_bytes(M,K) bytes, any
+ *           content, 256-byte aligned.
+ * For sherry_layernorm_quantize it is the gradient with the rounding to int8
+ * taken as the identity.  The sums run in a fixed order: equal calls give
+ * equal bits. */
+sherry_status sherry_layernorm_backward(const void* dy, const void* x, const float* mean,
+                                        const float* rstd, const float* weight, void* dx,
+                                        float* dweight, float* dbias, int dtype, int64_t M,
+                                        int64_t K, void* scratch, size_t scratch_bytes,
+                                        void* stream);
+size_t sherry_layernorm_backward_scratch_bytes(int64_t M, int64_t K);
 
 /* Launch plan sherry_gemm uses for a shape (host-only, pure; for
  * diagnostics and benchmarks).  Any output pointer may be NULL.

@@ -1,0 +1,228 @@
+"""The feed-forward operators on the GPU against their 64-bit definitions
+(ffn_reference.py), whose bounds count the roundings fp32 arithmetic and the
+output type may add."""
+
+import numpy as np
+import pytest
+import torch
+
+import bit_weight_amd as bw
+import ffn_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    torch.cuda.set_device(0)
+
+
+def _say(*a):
+    print(*a, flush=True)
+
+
+def _gen(seed):
+    g = torch.Generator()
+    g.manual_seed(seed)
+    return g
+
+
+def tokens(M, K, seed):
+    g = _gen(seed)
+    q = torch.randint(-128, 128, (M, K), generator=g, dtype=torch.int16).to(torch.int8)
+    return q, (0.5 + torch.rand(M, generator=g)) / 60
+
+
+def weights(orc, N, K, seed):
+    """(T, packed on the GPU, alpha) of a random 3:4-sparse ternary matrix."""
+    W = torch.randn((N, K), generator=_gen(seed))
+    T, alpha = orc.quantize(W.numpy())
+    packed, galpha = bw.quantize_pack(W.cuda())
+    alpha = torch.from_numpy(alpha) * (0.75 * K) ** -0.5
+    return torch.from_numpy(T), packed, alpha
+
+
+def check(name, got, want, bound):
+    got = got.double().cpu()
+    assert got.shape == want.shape, (name, got.shape, want.shape)
+    off = (got - want).abs()
+    bad = ~(off <= bound)
+    worst = (off / bound.clamp(min=1e-300)).max().item()
+    assert not bad.any(), f"{name}: {int(bad.sum())} of {bad.numel()} outside, worst {worst:.3g} of the bound"
+
+
+# (M, N, K): one token to several tiles; N and K off the 64 x 128 tiles; K split
+# and not; every path and tile shape of the product
+SHAPES = [(1, 4, 16), (1, 4096, 4096), (2, 1100, 2064), (3, 68, 11008), (7, 8192, 1024), (8, 260, 272),
+          (16, 1300, 1040), (17, 4096, 512), (33, 132, 4096), (64, 2052, 784), (65, 300, 8192), (100, 516, 2048),
+          (129, 1028, 400), (300, 640, 1296), (260, 16644, 256), (513, 4100, 144)]
+
+
+@pytest.mark.parametrize("i,shape", list(enumerate(SHAPES)))
+def test_gemm_fused(orc, i, shape):
+    M, N, K = shape
+    name = ref.ACTS[i % 6]
+    dtype = list(ref.TYPES.values())[i % 3]
+    _say(f"gemm_fused {shape} {name} {dtype} {bw.plan(M, N, K)}")
+    q, s = tokens(M, K, 10 + i)
+    T, packed, alpha = weights(orc, N, K, 20 + i)
+    bias = torch.randn(N, generator=_gen(30 + i)) if i % 4 != 1 else None
+    res = torch.randn((M, N), generator=_gen(40 + i)).to(dtype) if i % 4 != 2 else None
+    y = bw.gemm_fused(q.cuda(), s.cuda(), packed, alpha.cuda(), N, K, act=name, dtype=dtype,
+                      bias=None if bias is None else bias.cuda(), residual=None if res is None else res.cuda())
+    torch.cuda.synchronize()
+    assert y.dtype == dtype
+    check("y", y, *ref.gemm_fused(q, s, T, alpha, bias, name, res, dtype))
+
+
+@pytest.mark.parametrize("name", ref.ACTS)
+@pytest.mark.parametrize("t", list(ref.TYPES))
+@pytest.mark.parametrize("M", [3, 140])
+def test_gemm_fused_every_activation_and_type(orc, name, t, M):
+    N, K, dtype = 192, 272, ref.TYPES[t]
+    q, s = tokens(M, K, 1)
+    T, packed, alpha = weights(orc, N, K, 2)
+    alpha = alpha * 3
+    bias = torch.randn(N, generator=_gen(3))
+    res = torch.randn((M, N), generator=_gen(4)).to(dtype)
+    out = res.cuda()
+    y = bw.gemm_fused(q.cuda(), s.cuda(), packed, alpha.cuda(), N, K, bias=bias.cuda(), act=name, residual=out,
+                      dtype=dtype, out=out)      # in place on the residual
+    torch.cuda.synchronize()
+    assert y.data_ptr() == out.data_ptr()
+    check("y", y, *ref.gemm_fused(q, s, T, alpha, bias, name, res, dtype))
+
+
+@pytest.mark.parametrize("i,shape", list(enumerate(SHAPES)))
+def test_glu(orc, i, shape):
+    M, N, K = shape
+    name = ref.ACTS[(i + 3) % 6]
+    dtype = list(ref.TYPES.values())[(i + 1) % 3]
+    _say(f"glu {shape} {name} {dtype}")
+    q, s = tokens(M, K, 110 + i)
+    Tg, pg, ag = weights(orc, N, K, 120 + i)
+    Tu, pu, au = weights(orc, N, K, 130 + i)
+    h = bw.glu(q.cuda(), s.cuda(), pg, ag.cuda(), pu, au.cuda(), N, K, act=name, dtype=dtype)
+    torch.cuda.synchronize()
+    assert h.dtype == dtype
+    check("h", h, *ref.glu(q, s, Tg, ag, Tu, au, name, dtype))
+
+
+def test_glu_cells_hold_the_largest_sums(orc):
+    """Split along K with every sum at its largest magnitude and both signs:
+    the shared 64-bit cells hold the two sums and the arrivals apart."""
+    M, N, K = 2, 64, 65536
+    block = torch.tensor([1, 1, 1, 0], dtype=torch.int8).repeat(K // 4)
+    Tg = torch.stack([block if n % 2 else -block for n in range(N)])
+    Tu = torch.stack([block if n % 3 else -block for n in range(N)])
+    pack = [torch.from_numpy(orc.pack(t.numpy())).cuda() for t in (Tg, Tu)]
+    q = torch.full((M, K), -128, dtype=torch.int8)
+    q[1] = 127
+    s, one = torch.full((M,), 2.0 ** -10), torch.ones(N)
+    assert int(bw.lib().sherry_glu_workspace_bytes(M, N, K)) > 0
+    for _ in range(2):      # the cells are zero again after each call
+        h = bw.glu(q.cuda(), s.cuda(), pack[0], one.cuda(), pack[1], one.cuda(), N, K, act="none")
+        torch.cuda.synchronize()
+        check("h", h, *ref.glu(q, s, Tg, one, Tu, one, "none", torch.float32))
+
+
+def test_rows_and_columns_around_the_output_stay(orc):
+    """Outputs inside a larger buffer: nothing before or behind is written."""
+    for M, N, K in [(5, 68, 272), (200, 132, 144)]:
+        q, s = tokens(M, K, 5)
+        Tg, pg, ag = weights(orc, N, K, 6)
+        for dtype in (torch.float32, torch.bfloat16):
+            buf = torch.full((M + 2, N), 7.0, dtype=dtype, device="cuda")
+            bw.gemm_fused(q.cuda(), s.cuda(), pg, ag.cuda(), N, K, dtype=dtype, out=buf.view(-1)[8:8 + M * N].view(M, N))
+            torch.cuda.synchronize()
+            flat = buf.view(-1)
+            assert bool((flat[:8] == 7).all()) and bool((flat[8 + M * N:] == 7).all())
+
+
+# ------------------------------------------------------------------ layer norm
+def norm_inputs(M, K, dtype, seed):
+    g = _gen(seed)
+    x = torch.randn((M, K), generator=g) * (0.5 + 3 * torch.rand((M, 1), generator=g)) + torch.randn((M, 1), generator=g)
+    return x.to(dtype), 1 + 0.3 * torch.randn(K, generator=g), 0.2 * torch.randn(K, generator=g)
+
+
+NORMS = [(1, 4), (5, 252), (3, 260), (9, 1020), (2, 1028), (6, 2048), (1, 4096), (33, 4100), (3, 8196), (2, 16384),
+         (3, 16388), (1, 40000), (600, 64)]
+
+
+@pytest.mark.parametrize("i,shape", list(enumerate(NORMS)))
+@pytest.mark.parametrize("t", list(ref.TYPES))
+def test_layernorm(i, shape, t):
+    M, K = shape
+    dtype = ref.TYPES[t]
+    x, w, b = norm_inputs(M, K, dtype, i)
+    if i % 3 == 1:
+        w = None
+    if i % 3 == 2:
+        b = None
+    gw, gb = (None if v is None else v.cuda() for v in (w, b))
+    y, mean, rstd = bw.layernorm(x.cuda(), gw, gb, eps=1e-5, stats=True)
+    torch.cuda.synchronize()
+    ry, ty, rm, tm, rr, tr = ref.layernorm(x, w, b, 1e-5, dtype)
+    check("y", y, ry, ty)
+    check("mean", mean, rm, tm + 1e-37)
+    check("rstd", rstd, rr, tr)
+    buf = x.cuda()
+    assert torch.equal(bw.layernorm(buf, gw, gb, eps=1e-5, out=buf), y)      # in place
+    # the int8 form: a step may differ only where 64-bit arithmetic is undecided
+    qv, s = bw.layernorm_quantize(x.cuda(), gw, gb, eps=1e-5)
+    torch.cuda.synchronize()
+    rv, rs = ref.layernorm_quantize(x, w, b, 1e-5)
+    assert torch.equal(s.cpu(), rs)
+    border = (rv - rv.floor() - 0.5).abs() < 1e-9
+    assert bool(((qv.cpu().double() == rv.round().clamp(-127, 127)) | border).all())
+
+
+@pytest.mark.parametrize("i,shape", list(enumerate(NORMS)) + [(20, (3000, 256)), (21, (1100, 1536))])
+@pytest.mark.parametrize("t", list(ref.TYPES))
+def test_layernorm_backward(i, shape, t):
+    M, K = shape
+    dtype = ref.TYPES[t]
+    x, w, _ = norm_inputs(M, K, dtype, i)
+    dy = torch.randn((M, K), generator=_gen(50 + i)).to(dtype)
+    w = None if i % 3 == 1 else w
+    _, mean, rstd = bw.layernorm(x.cuda(), eps=1e-5, stats=True)
+    grads = bw.layernorm_backward(dy.cuda(), x.cuda(), mean, rstd, None if w is None else w.cuda())
+    torch.cuda.synchronize()
+    for name, got, want in zip(("dx", "dw", "db"), grads, ref.layernorm_backward(dy, x, mean.cpu(), rstd.cpu(), w, dtype)):
+        check(name, got, *want)
+    again = bw.layernorm_backward(dy.cuda(), x.cuda(), mean, rstd, None if w is None else w.cuda())
+    assert all(torch.equal(p, q) for p, q in zip(grads, again))
+    buf = dy.cuda()
+    assert torch.equal(bw.layernorm_backward(buf, x.cuda(), mean, rstd, None if w is None else w.cuda(), out=buf)[0],
+                       grads[0])
+
+
+def test_layernorm_rows_without_spread_and_a_far_mean():
+    """Equal features (variance 0), zeros, and a mean far above the spread:
+    rstd = eps^-1/2 of the first two; an all-zero token quantizes to s = 1."""
+    K = 512
+    x = torch.zeros((3, K))
+    x[0] = 3.25
+    x[2] = 1000 + torch.randn(K, generator=_gen(1))
+    y, mean, rstd = bw.layernorm(x.cuda(), eps=1e-5, stats=True)
+    q, s = bw.layernorm_quantize(x.cuda(), eps=1e-5)
+    torch.cuda.synchronize()
+    assert bool((y[:2] == 0).all()) and bool((q[:2] == 0).all()) and bool((s[:2] == 1).all())
+    ry, ty, *_ = ref.layernorm(x, None, None, 1e-5, torch.float32)
+    check("y", y, ry, ty)
+    rv, rs = ref.layernorm_quantize(x, None, None, 1e-5)
+    assert torch.equal(s.cpu(), rs) and torch.equal(q.cpu().double(), rv.round().clamp(-127, 127))
+
+
+def test_layernorm_nan_stays_in_its_row():
+    x = torch.randn((4, 300), generator=_gen(2))
+    x[1, 7] = float("nan")
+    x[2, 3] = float("inf")
+    y = bw.layernorm(x.cuda())
+    torch.cuda.synchronize()
+    assert bool(y[1].isnan().all()) and bool(y[2].isnan().any())
+    ry, ty, *_ = ref.layernorm(x[[0, 3]], None, None, 1e-5, torch.float32)
+    check("y", y[[0, 3]], ry, ty)
