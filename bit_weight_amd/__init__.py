@@ -23,7 +23,7 @@ import torch
 __all__ = [
     "SherryError", "lib", "packed_bytes", "workspace_bytes", "plan", "plan_override",
     "quantize_pack", "quantize_act", "gemm", "gemm_i32", "linear", "linear_scratch_bytes", "concat_packed", "quantize_pack2", "gemm2",
-    "gemm_fused", "glu", "layernorm", "layernorm_quantize", "layernorm_backward",
+    "gemm_fused", "gemm_fused_backward", "glu", "glu_backward", "layernorm", "layernorm_quantize", "layernorm_backward",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -88,6 +88,12 @@ def lib() -> ctypes.CDLL:
                 "sherry_gemm_fused": ([vp, vp, vp, vp, vp, ci, vp, vp, ci, i64, i64, i64, vp, sz, vp], ci),
                 "sherry_glu_workspace_bytes": ([i64, i64, i64], sz),
                 "sherry_glu": ([vp, vp, vp, vp, vp, vp, ci, vp, ci, i64, i64, i64, vp, sz, vp], ci),
+                "sherry_gemm_fused_backward_scratch_bytes": ([i64, i64, i64, ci], sz),
+                "sherry_gemm_fused_backward": ([vp, vp, vp, vp, vp, vp, ci, vp, vp, vp, ci, i64, i64, i64, vp, sz,
+                                                vp], ci),
+                "sherry_glu_backward_scratch_bytes": ([i64, i64, i64, ci], sz),
+                "sherry_glu_backward": ([vp, vp, vp, vp, vp, vp, vp, ci, vp, vp, vp, ci, i64, i64, i64, vp, sz,
+                                         vp], ci),
                 "sherry_layernorm": ([vp, vp, vp, cf, vp, vp, vp, ci, i64, i64, vp], ci),
                 "sherry_layernorm_quantize": ([vp, vp, vp, cf, vp, vp, vp, vp, ci, i64, i64, vp], ci),
                 "sherry_layernorm_backward_scratch_bytes": ([i64, i64], sz),
@@ -548,6 +554,51 @@ def glu(x: torch.Tensor, s_x: torch.Tensor, packed_gate: torch.Tensor, alpha_gat
     ws, wp, wn = _zeroed_workspace(workspace, int(lib().sherry_glu_workspace_bytes(M, N, K)), dev)
     _call(dev, "sherry_glu", px, ps, pg, pag, pu, pau, code, ph, dt, M, N, K, wp, wn)
     return out
+
+
+def _gradient(dy, M: int, N: int, device):
+    """(type code, pointer) of an output gradient [M,N]."""
+    if not isinstance(dy, torch.Tensor):
+        raise TypeError("the output gradient must be a torch.Tensor")
+    return _dtype_code(dy.dtype), _matrix(dy, "the output gradient", dy.dtype, device, (M, N))
+
+
+def gemm_fused_backward(dy: torch.Tensor, x: torch.Tensor, s_x: torch.Tensor, packed: torch.Tensor,
+                        alpha: torch.Tensor, N: int, K: int, bias: torch.Tensor | None = None,
+                        act: str | None = None):
+    """Gradients of gemm_fused from dy [M,N] and its inputs -> (dx of dy's type
+    [M,K], dalpha fp32 [N], dbias fp32 [N]); dx is the gradient of the token
+    x * s_x, the residual's is dy."""
+    M, dev, px, ps = _tokens(x, s_x, K)
+    pw, pa = _weights(packed, alpha, "", N, K, dev)
+    code, pb = _act_code(act), _operand(bias, "bias", torch.float32, dev, N)
+    dt, pdy = _gradient(dy, M, N, dev)
+    dx = torch.empty((M, K), dtype=dy.dtype, device=dev)
+    da, db = torch.empty((2, N), dtype=torch.float32, device=dev)
+    scratch = torch.empty(int(lib().sherry_gemm_fused_backward_scratch_bytes(M, N, K, dt)), dtype=torch.uint8,
+                          device=dev)
+    _call(dev, "sherry_gemm_fused_backward", pdy, px, ps, pw, pa, pb, code, dx.data_ptr(), da.data_ptr(),
+          db.data_ptr(), dt, M, N, K, scratch.data_ptr(), scratch.numel())
+    return dx, da, db
+
+
+def glu_backward(dh: torch.Tensor, x: torch.Tensor, s_x: torch.Tensor, packed_gate: torch.Tensor,
+                 alpha_gate: torch.Tensor, packed_up: torch.Tensor, alpha_up: torch.Tensor, N: int, K: int,
+                 act: str | None = "silu"):
+    """Gradients of glu from dh [M,N] and its inputs -> (dx of dh's type [M,K],
+    dalpha_gate fp32 [N], dalpha_up fp32 [N]); dx is the gradient of the
+    token x * s_x."""
+    M, dev, px, ps = _tokens(x, s_x, K)
+    pg, pag = _weights(packed_gate, alpha_gate, "_gate", N, K, dev)
+    pu, pau = _weights(packed_up, alpha_up, "_up", N, K, dev)
+    code = _act_code(act)
+    dt, pdh = _gradient(dh, M, N, dev)
+    dx = torch.empty((M, K), dtype=dh.dtype, device=dev)
+    dg, du = torch.empty((2, N), dtype=torch.float32, device=dev)
+    scratch = torch.empty(int(lib().sherry_glu_backward_scratch_bytes(M, N, K, dt)), dtype=torch.uint8, device=dev)
+    _call(dev, "sherry_glu_backward", pdh, px, ps, pg, pag, pu, pau, code, dx.data_ptr(), dg.data_ptr(),
+          du.data_ptr(), dt, M, N, K, scratch.data_ptr(), scratch.numel())
+    return dx, dg, du
 
 
 def _features(x, weight, bias):

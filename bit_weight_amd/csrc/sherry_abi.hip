@@ -340,6 +340,11 @@ GemmPlan plan_glu(int M, int N, int K) {
   return q;
 }
 
+// The product that a backward pass recomputes: always the prefill kernel.
+GemmPlan plan_recompute(int M, int N, int K, bool glu) {
+  return plan_prefill(M, glu ? 2 * kTileRows * row_tiles(N) : N, K);
+}
+
 hipError_t launch_product_epilogue(const GemmPlan& plan, const GemmArgs& args, int ep,
                                    const EpilogueArgs& e, hipStream_t stream, bool* partial) {
   *partial = false;
@@ -777,6 +782,21 @@ GemmArgs product_of(const int8_t* x, const float* s_x, const void* packed, const
   return a;
 }
 
+// Backward passes: the recomputing product, then the input-gradient product.
+sherry_status run_backward(const GemmArgs& a, int ep, const EpilogueArgs& e, void* dx, float* d0, float* d1,
+                           void* scratch, size_t scratch_bytes, void* stream) {
+  const GemmPlan product = plan_recompute(a.M, a.N, a.K, ep_glu(ep));
+  const GradPlan plan = plan_grad(product, a.M, a.N, a.K, ep_glu(ep) ? 2 : 1, e.dtype);
+  if (!scratch || scratch_bytes < plan.bytes) return SHERRY_ERR_WORKSPACE;
+  if (!aligned(scratch, 256)) return SHERRY_ERR_ALIGN;
+  const sherry_status d = check_device();
+  if (d != SHERRY_OK) return d;
+  bool partial = false;
+  const hipError_t err = launch_backward(product, plan, a, ep, e, dx, d0, d1, scratch,
+                                         static_cast<hipStream_t>(stream), &partial);
+  return status_of(err, partial);
+}
+
 sherry_status check_norm(const void* x, const float* weight, const float* bias, float eps, const float* mean,
                          const float* rstd, int dtype, int64_t M, int64_t K) {
   if (!x || (mean == nullptr) != (rstd == nullptr)) return SHERRY_ERR_NULL;
@@ -837,6 +857,58 @@ sherry_status sherry_glu(const int8_t* x, const float* s_x, const void* packed_g
   return run_epilogue(plan_glu((int)M, (int)N, (int)K),
                       product_of(x, s_x, packed_gate, alpha_gate, M, N, K), kEpGlu, e, workspace,
                       workspace_bytes, stream);
+}
+
+size_t sherry_gemm_fused_backward_scratch_bytes(int64_t M, int64_t N, int64_t K, int dtype) {
+  if (!shape_ok(M, N, K) || !dtype_ok(dtype)) return 0;
+  const GemmPlan p = plan_recompute((int)M, (int)N, (int)K, false);
+  return plan_grad(p, (int)M, (int)N, (int)K, 1, dtype).bytes;
+}
+
+size_t sherry_glu_backward_scratch_bytes(int64_t M, int64_t N, int64_t K, int dtype) {
+  if (!shape_ok(M, N, K) || !dtype_ok(dtype)) return 0;
+  const GemmPlan p = plan_recompute((int)M, (int)N, (int)K, true);
+  return plan_grad(p, (int)M, (int)N, (int)K, 2, dtype).bytes;
+}
+
+sherry_status sherry_gemm_fused_backward(const void* dy, const int8_t* x, const float* s_x, const void* packed,
+                                         const float* alpha, const float* bias, int act, void* dx, float* dalpha,
+                                         float* dbias, int dtype, int64_t M, int64_t N, int64_t K, void* scratch,
+                                         size_t scratch_bytes, void* stream) {
+  if (!dy || !x || !s_x || !packed || !alpha || !dx) return SHERRY_ERR_NULL;
+  if (!shape_ok(M, N, K)) return SHERRY_ERR_SHAPE;
+  if (!act_ok(act) || !dtype_ok(dtype)) return SHERRY_ERR_ARG;
+  if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(packed, 16) || !aligned(dx, 16) || !aligned(s_x, 4) ||
+      !aligned(alpha, 4) || !aligned(bias, 4) || !aligned(dalpha, 4) || !aligned(dbias, 4))
+    return SHERRY_ERR_ALIGN;
+  EpilogueArgs e{};
+  e.bias = bias;
+  e.act = act;
+  e.dtype = dtype;
+  e.grad.dy = dy;
+  return run_backward(product_of(x, s_x, packed, alpha, M, N, K), kEpFusedBack, e, dx, dalpha, dbias, scratch,
+                      scratch_bytes, stream);
+}
+
+sherry_status sherry_glu_backward(const void* dh, const int8_t* x, const float* s_x, const void* packed_gate,
+                                  const float* alpha_gate, const void* packed_up, const float* alpha_up, int act,
+                                  void* dx, float* dalpha_gate, float* dalpha_up, int dtype, int64_t M, int64_t N,
+                                  int64_t K, void* scratch, size_t scratch_bytes, void* stream) {
+  if (!dh || !x || !s_x || !packed_gate || !alpha_gate || !packed_up || !alpha_up || !dx) return SHERRY_ERR_NULL;
+  if (!shape_ok(M, N, K)) return SHERRY_ERR_SHAPE;
+  if (!act_ok(act) || !dtype_ok(dtype)) return SHERRY_ERR_ARG;
+  if (!aligned(dh, 16) || !aligned(x, 16) || !aligned(packed_gate, 16) || !aligned(packed_up, 16) ||
+      !aligned(dx, 16) || !aligned(s_x, 4) || !aligned(alpha_gate, 4) || !aligned(alpha_up, 4) ||
+      !aligned(dalpha_gate, 4) || !aligned(dalpha_up, 4))
+    return SHERRY_ERR_ALIGN;
+  EpilogueArgs e{};
+  e.packed2 = static_cast<const uint8_t*>(packed_up);
+  e.alpha2 = alpha_up;
+  e.act = act;
+  e.dtype = dtype;
+  e.grad.dy = dh;
+  return run_backward(product_of(x, s_x, packed_gate, alpha_gate, M, N, K), kEpGluBack, e, dx, dalpha_gate,
+                      dalpha_up, scratch, scratch_bytes, stream);
 }
 
 sherry_status sherry_layernorm(const void* x, const float* weight, const float* bias, float eps, void* y,

@@ -154,6 +154,23 @@ hipError_t launch_mfma_gemv_epilogue(const GemmPlan& plan, const GemmArgs& args,
 hipError_t launch_mfma_gemm_epilogue(const GemmPlan& plan, const GemmArgs& args, int ep,
                                      const EpilogueArgs& e, hipStream_t stream);
 
+// Plan of a backward pass: the input-gradient product's tiles and splits and
+// where each array lies in the scratch memory (input_grad.hip).
+struct GradPlan {
+  int terms;          // fp16 terms per gradient
+  int R;              // row tiles of all matrices
+  int mt;             // tokens per workgroup tile / 32
+  int splits, r_per_split;
+  int token_tiles;    // of the recomputing product: rows of partial column sums
+  size_t tops, rows, codes, z, cols, dx_part, bytes;
+};
+GradPlan plan_grad(const GemmPlan& product, int M, int N, int K, int parts, int dtype);
+// `product` is the recomputing product's plan (path 1), ep its epilogue; d0 =
+// dalpha, d1 = dalpha2 or dbias, either may be nullptr.
+hipError_t launch_backward(const GemmPlan& product, const GradPlan& plan, const GemmArgs& args, int ep,
+                           EpilogueArgs e, void* dx, float* d0, float* d1, void* scratch, hipStream_t stream,
+                           bool* partial);
+
 // Layer norm (norm.hip): y in x's type, or q and s (int8 tokens).
 hipError_t launch_layernorm(const void* x, const float* w, const float* b, float eps, void* y, int8_t* q,
                             float* s, float* mean, float* rstd, int dtype, int M, int K, hipStream_t stream);

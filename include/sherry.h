@@ -287,6 +287,41 @@ sherry_status sherry_glu(const int8_t* x, const float* s_x, const void* packed_g
                          void* workspace, size_t workspace_bytes, void* stream);
 size_t sherry_glu_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
+/* Gradients of the two, with the rounding of x to int8 taken as the identity:
+ * dx is the gradient of the token x * s_x, dz that of the value the
+ * activation is applied to.
+ *   gemm_fused:  dz = dy * act'(z);
+ *     dx[m,k] = sum_n dz[m,n] * alpha[n] * T[n,k],
+ *     dalpha[n] = sum_m dz[m,n] * acc[m,n] * s_x[m],  dbias[n] = sum_m dz[m,n]
+ *     (the residual's gradient is dy itself).
+ *   glu:  dg = dh * u * act'(g), du = dh * act(g); dx sums both matrices'
+ *     terms, dalpha_gate and dalpha_up are as dalpha.
+ *   relu' and relu2' are 0 at 0.
+ *   dy, dh   [M,N] of type dtype, 16-byte aligned.
+ *   x, s_x, packed, alpha, bias, act: as the forward call had them; the sums
+ *            are computed again, so the forward saves nothing.
+ *   dx       [M,K] of type dtype (written), 16-byte aligned; overlaps no input.
+ *   dalpha, dbias, ...  [N] fp32 (written), 4-byte aligned, each may be NULL.
+ *   scratch  at least the queried bytes, any content, 256-byte aligned.
+ * dx's terms dz * alpha are rounded to fp16 under one power-of-two scale per
+ * token: one term (relative 2^-12) for bf16 results, a high and a low one
+ * (2^-22) for fp16 and fp32 results.  The sums run in a fixed order: equal
+ * calls give equal bits. */
+sherry_status sherry_gemm_fused_backward(const void* dy, const int8_t* x, const float* s_x,
+                                         const void* packed, const float* alpha,
+                                         const float* bias, int act, void* dx, float* dalpha,
+                                         float* dbias, int dtype, int64_t M, int64_t N, int64_t K,
+                                         void* scratch, size_t scratch_bytes, void* stream);
+size_t sherry_gemm_fused_backward_scratch_bytes(int64_t M, int64_t N, int64_t K, int dtype);
+
+sherry_status sherry_glu_backward(const void* dh, const int8_t* x, const float* s_x,
+                                  const void* packed_gate, const float* alpha_gate,
+                                  const void* packed_up, const float* alpha_up, int act, void* dx,
+                                  float* dalpha_gate, float* dalpha_up, int dtype, int64_t M,
+                                  int64_t N, int64_t K, void* scratch, size_t scratch_bytes,
+                                  void* stream);
+size_t sherry_glu_backward_scratch_bytes(int64_t M, int64_t N, int64_t K, int dtype);
+
 /* Layer norm of each token:
  *   y = ((x - mean) * rstd) * weight + bias,  mean = sum x / K,
  *   rstd = 1 / sqrt(sum (x - mean)^2 / K + eps).

@@ -109,6 +109,73 @@ def glu(q, s, Tg, ag, Tu, au, name, dtype):
     return h, rounded(h, err, dtype)
 
 
+def input_gradient(parts, top, dtype):
+    """dx = sum over parts of c @ T and its bound; parts are (c, error of c, T)
+    with c = dz alpha, top [M] bounds |c| as the library does.  A power of two
+    takes top to (2^14, 2^15]; there one fp16 term is off by 2^-11 of c (two:
+    2^-22) or half a subnormal step, 2^-25, which is 2^-39 of top.  n terms
+    added in fp32 in any order take n roundings of at most sum |c|."""
+    two = dtype != torch.bfloat16
+    term = 2.0 ** -22 if two else 2.0 ** -11
+    dx = sum(c @ T.double() for c, _, T in parts)
+    n = sum(T.shape[0] for _, _, T in parts) * (2 if two else 1)
+    err = sum((e + term * c.abs() + 2.0 ** -39 * top[:, None] + (n + 4) * U * c.abs()) @ T.double().abs()
+              for c, e, T in parts)
+    return dx, rounded(dx, err, dtype)
+
+
+def top_of(dy, q, s, alpha, alpha2, bias, name):
+    """The library's bound on a token's |dz alpha|, from max|dy|, sum|q| s and
+    the largest scales; |act'| <= 1.25, or 2 |z| for relu2."""
+    total = q.double().abs().sum(1) * s.double()
+    a = alpha.abs().max().double()
+    pre = total * a + (0 if bias is None else bias.abs().max().double())
+    top = dy.double().abs().amax(1) * (2 * pre if name == "relu2" else 1.25) * a
+    return top if alpha2 is None else top * total * alpha2.abs().max().double()
+
+
+def gemm_fused_backward(dy, q, s, T, alpha, bias, name, dtype):
+    """((dx, bound), (dalpha, bound), (dbias, bound))."""
+    p, z = product(q, s, T, alpha)
+    ez = 3 * U * z.abs()
+    if bias is not None:
+        z = z + bias.double()
+        ez = ez + U * z.abs()
+    dy = dy.double()
+    dz = dy * slope(z, name)
+    edz = dy.abs() * slope_error(z, ez, name) + U * dz.abs()
+    a = alpha.double()
+    top = top_of(dy, q, s, alpha, None, bias, name)
+    dx = input_gradient([(dz * a, edz * a.abs() + 2 * U * (dz * a).abs(), T)], top, dtype)
+    M = dy.shape[0]
+    da = (dz * p).sum(0)
+    eda = (edz * p.abs()).sum(0) + (M + 6) * U * (dz * p).abs().sum(0)
+    db = dz.sum(0)
+    edb = edz.sum(0) + (M + 2) * U * dz.abs().sum(0)
+    return dx, (da, 1.01 * eda + 1e-37), (db, 1.01 * edb + 1e-37)
+
+
+def glu_backward(dh, q, s, Tg, ag, Tu, au, name, dtype):
+    """((dx, bound), (dalpha_gate, bound), (dalpha_up, bound))."""
+    pg, g = product(q, s, Tg, ag)
+    pu, u = product(q, s, Tu, au)
+    dh, ag, au = dh.double(), ag.double(), au.double()
+    eg, eu = 3 * U * g.abs(), 3 * U * u.abs()
+    sl, a = slope(g, name), act(g, name)
+    dg, du = dh * u * sl, dh * a
+    edg = (dh * u).abs() * slope_error(g, eg, name) + 6 * U * dg.abs()
+    edu = dh.abs() * act_error(g, eg, name) + U * du.abs()
+    top = top_of(dh, q, s, ag, au, None, name)
+    dx = input_gradient([(dg * ag, edg * ag.abs() + 2 * U * (dg * ag).abs(), Tg),
+                         (du * au, edu * au.abs() + 2 * U * (du * au).abs(), Tu)], top, dtype)
+    M = dh.shape[0]
+    found = [dx]
+    for d, e, p in ((dg, edg, pg), (du, edu, pu)):
+        err = (e * p.abs()).sum(0) + (M + 6) * U * (d * p).abs().sum(0)
+        found.append(((d * p).sum(0), 1.01 * err + 1e-37))
+    return found
+
+
 def layernorm(x, w, b, eps, dtype):
     """(y, bound, mean, its bound, rstd, its bound).  A sum over K features
     takes at most `adds` additions on its way: those of one lane (up to 64

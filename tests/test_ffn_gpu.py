@@ -141,6 +141,111 @@ def test_rows_and_columns_around_the_output_stay(orc):
             assert bool((flat[:8] == 7).all()) and bool((flat[8 + M * N:] == 7).all())
 
 
+# ---------------------------------------------------------- backward passes
+# (M, N, K): token tiles of 32 to 256 (one, several, ragged), sums over 1 to
+# many row tiles, split and not, columns past the last half tile
+BACK = [(1, 4, 16), (1, 640, 272), (31, 68, 144), (33, 132, 1040), (64, 1100, 528), (77, 1300, 1040),
+        (130, 516, 2064), (300, 1100, 528), (385, 64, 272), (520, 260, 784), (700, 2112, 336), (140, 4160, 512)]
+
+
+@pytest.mark.parametrize("i,shape", list(enumerate(BACK)))
+@pytest.mark.parametrize("t", list(ref.TYPES))
+def test_gemm_fused_backward(orc, i, shape, t):
+    M, N, K = shape
+    name, dtype = ref.ACTS[(i + 2) % 6], ref.TYPES[t]
+    _say(f"gemm_fused_backward {shape} {name} {dtype}")
+    q, s = tokens(M, K, 210 + i)
+    T, packed, alpha = weights(orc, N, K, 220 + i)
+    bias = torch.randn(N, generator=_gen(230 + i)) if i % 3 else None
+    dy = (torch.randn((M, N), generator=_gen(240 + i)) * 0.01).to(dtype)
+    args = [v.cuda() for v in (dy, q, s)] + [packed, alpha.cuda(), N, K]
+    kw = dict(bias=None if bias is None else bias.cuda(), act=name)
+    got = bw.gemm_fused_backward(*args, **kw)
+    torch.cuda.synchronize()
+    assert got[0].dtype == dtype
+    for what, v, want in zip(("dx", "dalpha", "dbias"), got, ref.gemm_fused_backward(dy, q, s, T, alpha, bias, name, dtype)):
+        check(what, v, *want)
+    assert all(torch.equal(u, v) for u, v in zip(got, bw.gemm_fused_backward(*args, **kw)))   # equal bits
+
+
+@pytest.mark.parametrize("i,shape", list(enumerate(BACK)))
+@pytest.mark.parametrize("t", list(ref.TYPES))
+def test_glu_backward(orc, i, shape, t):
+    M, N, K = shape
+    name, dtype = ref.ACTS[(i + 3) % 6], ref.TYPES[t]
+    _say(f"glu_backward {shape} {name} {dtype}")
+    q, s = tokens(M, K, 310 + i)
+    Tg, pg, ag = weights(orc, N, K, 320 + i)
+    Tu, pu, au = weights(orc, N, K, 330 + i)
+    dh = (torch.randn((M, N), generator=_gen(340 + i)) * 0.01).to(dtype)
+    args = [v.cuda() for v in (dh, q, s)] + [pg, ag.cuda(), pu, au.cuda(), N, K]
+    got = bw.glu_backward(*args, act=name)
+    torch.cuda.synchronize()
+    assert got[0].dtype == dtype
+    want = ref.glu_backward(dh, q, s, Tg, ag, Tu, au, name, dtype)
+    for what, v, w in zip(("dx", "dalpha_gate", "dalpha_up"), got, want):
+        check(what, v, *w)
+    assert all(torch.equal(u, v) for u, v in zip(got, bw.glu_backward(*args, act=name)))      # equal bits
+
+
+@pytest.mark.parametrize("scale", [1e-30, 1e-12, 1.0, 1e12, 1e25])
+def test_backward_gradients_of_any_size(orc, scale):
+    """fp16 terms under a scale per token: gradients far outside fp16's range,
+    tokens of very different sizes, a token without any gradient."""
+    M, N, K = 70, 192, 272
+    q, s = tokens(M, K, 1)
+    T, packed, alpha = weights(orc, N, K, 2)
+    dy = torch.randn((M, N), generator=_gen(3)) * scale * 10.0 ** torch.linspace(-6, 6, M)[:, None]
+    dy[5] = 0
+    q[9] = 0
+    got = bw.gemm_fused_backward(dy.cuda(), q.cuda(), s.cuda(), packed, alpha.cuda(), N, K, act="silu")
+    torch.cuda.synchronize()
+    want = ref.gemm_fused_backward(dy, q, s, T, alpha, None, "silu", torch.float32)
+    for what, v, w in zip(("dx", "dalpha", "dbias"), got, want):
+        check(what, v, *w)
+    assert bool((got[0][5] == 0).all())
+
+
+def test_backward_infinite_and_nan_gradients_stay_in_their_token(orc):
+    M, N, K = 40, 132, 272
+    q, s = tokens(M, K, 1)
+    T, packed, alpha = weights(orc, N, K, 2)
+    dy = torch.randn((M, N), generator=_gen(3))
+    clean = ref.gemm_fused_backward(dy, q, s, T, alpha, None, "none", torch.float32)[0]
+    dy[3, 7], dy[11, 130] = float("inf"), float("nan")
+    dx = bw.gemm_fused_backward(dy.cuda(), q.cuda(), s.cuda(), packed, alpha.cuda(), N, K)[0].cpu()
+    keep = [m for m in range(M) if m not in (3, 11)]
+    check("dx", dx[keep], clean[0][keep], clean[1][keep])
+    # inf x (+-1) keeps its sign, inf x 0 and NaN are NaN
+    want = torch.where(T[7] == 0, float("nan"), float("inf") * T[7].float())
+    assert torch.equal(dx[3].isnan(), want.isnan()) and torch.equal(dx[3][T[7] != 0], want[T[7] != 0])
+    assert bool(dx[11].isnan().all())
+
+
+@pytest.mark.parametrize("name", ref.ACTS[3:])
+def test_backward_against_differences(orc, name):
+    """dalpha and dbias against central differences of the forward in fp32:
+    steps of 2^-7 leave 2^-14 / 6 times the third derivative, below 2 times
+    the value's size here, and the forward's rounding over the step."""
+    M, N, K = 24, 64, 272
+    q, s = tokens(M, K, 1)
+    T, packed, alpha = weights(orc, N, K, 2)
+    bias = torch.randn(N, generator=_gen(3))
+    dy = torch.randn((M, N), generator=_gen(4))
+    d = [v.cuda() for v in (q, s)] + [packed]
+    _, da, db = bw.gemm_fused_backward(dy.cuda(), *d, alpha.cuda(), N, K, bias=bias.cuda(), act=name)
+    forward = lambda a, b: bw.gemm_fused(*d, a.cuda(), N, K, bias=b.cuda(), act=name).double().cpu()
+    h = 2.0 ** -7
+    fd_b = ((forward(alpha, bias + h) - forward(alpha, bias - h)) * dy).sum(0) / (2 * h)
+    size = dy.abs().double().sum(0)
+    tol = size * (2 * h ** 2 / 6 + 64 * ref.U * (2 + bias.abs().max().double()) * 8 / h)
+    check("dbias", db, fd_b, tol)
+    p = (q.double() @ T.double().t()) * s.double()[:, None]
+    step = h / p.abs().max().item()
+    fd_a = ((forward(alpha + step, bias) - forward(alpha - step, bias)) * dy).sum(0) / (2 * step)
+    check("dalpha", da, fd_a, tol * p.abs().max())
+
+
 # ------------------------------------------------------------------ layer norm
 def norm_inputs(M, K, dtype, seed):
     g = _gen(seed)

@@ -25,6 +25,20 @@ def _glu(**kw):
     return bw.lib().sherry_glu(*a.values(), None)
 
 
+def _fused_back(**kw):
+    a = dict(dy=FAKE, x=FAKE, s=FAKE, p=FAKE, al=FAKE, b=None, act=0, dx=FAKE, da=FAKE, db=FAKE, dt=0, M=1, N=64, K=128,
+             ws=FAKE, wsb=BIG)
+    a.update(kw)
+    return bw.lib().sherry_gemm_fused_backward(*a.values(), None)
+
+
+def _glu_back(**kw):
+    a = dict(dy=FAKE, x=FAKE, s=FAKE, pg=FAKE, ag=FAKE, pu=FAKE, au=FAKE, act=3, dx=FAKE, dg=FAKE, du=FAKE, dt=0, M=1,
+             N=64, K=128, ws=FAKE, wsb=BIG)
+    a.update(kw)
+    return bw.lib().sherry_glu_backward(*a.values(), None)
+
+
 def _norm(**kw):
     a = dict(x=FAKE, w=FAKE, b=FAKE, eps=1e-5, y=FAKE, mean=FAKE, rstd=FAKE, dt=0, M=1, K=128)
     a.update(kw)
@@ -67,6 +81,31 @@ def test_product_refusals(call, pointers, aligned16):
     assert call(M=M, N=N, K=K, ws=FAKE + 64) == ALIGN
     for kw in BAD_SHAPES:
         assert query(kw.get("M", 1), kw.get("N", 64), kw.get("K", 128)) == 0
+
+
+@pytest.mark.parametrize("call,pointers,aligned16", [
+    (_fused_back, ("dy", "x", "s", "p", "al", "dx"), ("dy", "x", "p", "dx")),
+    (_glu_back, ("dy", "x", "s", "pg", "ag", "pu", "au", "dx"), ("dy", "x", "pg", "pu", "dx"))])
+def test_backward_refusals(call, pointers, aligned16):
+    for k in pointers:
+        assert call(**{k: None}) == NULL, k
+    for kw in BAD_SHAPES:
+        assert call(**kw) == SHAPE, kw
+    for k in aligned16:
+        assert call(**{k: FAKE + 8}) == ALIGN, k
+    assert call(act=6) == ARG and call(act=-1) == ARG and call(dt=3) == ARG
+    L = bw.lib()
+    query = L.sherry_glu_backward_scratch_bytes if call is _glu_back else L.sherry_gemm_fused_backward_scratch_bytes
+    parts = 2 if call is _glu_back else 1
+    for M, N, K, dt in ((1, 64, 128, 0), (300, 1100, 2064, 2), (2048, 14336, 4096, 1), (7, 4, 1 << 20, 0)):
+        need, rows = query(M, N, K, dt), parts * -(-N // 64)
+        # the fp16 terms and the weights' 2-bit form are the least it holds
+        assert need >= M * rows * 64 * 2 * (1 if dt == 2 else 2) + -(-K // 128) * rows * 2048
+        kw = dict(M=M, N=N, K=K, dt=dt)
+        assert call(ws=None, **kw) == WS and call(wsb=need - 1, **kw) == WS and call(ws=FAKE + 64, **kw) == ALIGN
+    for kw in BAD_SHAPES:
+        assert query(kw.get("M", 1), kw.get("N", 64), kw.get("K", 128), 0) == 0
+    assert query(1, 64, 128, 3) == 0
 
 
 def test_norm_refusals():
