@@ -431,12 +431,15 @@ def gemm2(x: torch.Tensor, s_x: torch.Tensor, packed: torch.Tensor, alpha: torch
 
 
 # ------------------------------------------------- feed-forward operators
+# A small call's kernel takes 5 to 10 us, so the checks and the marshalling
+# here are kept to a few cheap attribute reads per tensor; the error messages
+# are made only once a check has failed.
 DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
-ACTIVATIONS = {"none": 0, "relu": 1, "relu2": 2, "silu": 3, "gelu": 4, "gelu_tanh": 5}
+ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "relu2": 2, "silu": 3, "gelu": 4, "gelu_tanh": 5}
 
 
 def _act_code(act) -> int:
-    code = ACTIVATIONS.get("none" if act is None else act)
+    code = ACTIVATIONS.get(act)
     if code is None:
         raise ValueError(f"act must be one of {list(ACTIVATIONS)}, got {act!r}")
     return code
@@ -449,76 +452,99 @@ def _dtype_code(dtype) -> int:
     return code
 
 
-def _operand(t, name: str, dtype: torch.dtype, device: torch.device, numel: int):
-    """Pointer of an operand that must be on `device` and hold `numel` values
-    (None -> NULL)."""
+def _refuse(t, name: str, dtype: torch.dtype, index: int, shape) -> None:
+    """Raises for an operand that one of the checks below has failed."""
+    _dev_tensor(t, name, dtype)
+    if t.get_device() != index:
+        raise RuntimeError(f"{name} must be on cuda:{index}, got {t.device}")
+    raise RuntimeError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+
+
+def _vector(t, name: str, dtype: torch.dtype, index: int, n: int):
+    """Pointer of an operand of n values on device `index` (None -> NULL)."""
     if t is None:
         return None
-    p = _dev_tensor(t, name, dtype)
-    if t.device != device:
-        raise RuntimeError(f"{name} must be on {device}, got {t.device}")
-    if t.numel() != numel:
-        raise RuntimeError(f"{name} must hold {numel} values, got {t.numel()}")
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.numel() == n
+            and t.is_contiguous()):
+        _refuse(t, name, dtype, index, (n,))
+    return t.data_ptr()
+
+
+def _matrix(t, name: str, dtype: torch.dtype, index: int, M: int, N: int):
+    """Pointer of an [M,N] operand on device `index` (None -> NULL)."""
+    if t is None:
+        return None
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.shape == (M, N)
+            and t.is_contiguous()):
+        _refuse(t, name, dtype, index, (M, N))
+    return t.data_ptr()
+
+
+def _required(p, name: str):
+    if p is None:
+        raise TypeError(f"{name} must be a torch.Tensor")
     return p
 
 
-def _matrix(t, name: str, dtype: torch.dtype, device: torch.device, shape):
-    """Pointer of a matrix that must be on `device` with this shape (None -> NULL)."""
-    if t is None:
-        return None
-    if isinstance(t, torch.Tensor) and tuple(t.shape) != tuple(shape):
-        raise RuntimeError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    return _operand(t, name, dtype, device, shape[0] * shape[1])
-
-
 def _tokens(x, s_x, K: int):
-    """(M, device, pointers) of int8 tokens and their scales."""
+    """(M, device index, pointers) of int8 tokens and their scales."""
     px = _dev_tensor(x, "x", torch.int8)
     if x.dim() != 2 or x.shape[1] != K:
         raise RuntimeError(f"x must be [M,{K}]")
-    M = x.shape[0]
-    return M, x.device, px, _operand(s_x, "s_x", torch.float32, x.device, M)
+    M, index = x.shape[0], x.get_device()
+    return M, index, px, _required(_vector(s_x, "s_x", torch.float32, index, M), "s_x")
 
 
-def _weights(packed, alpha, name: str, N: int, K: int, device):
-    return (_operand(packed, "packed" + name, torch.uint8, device, packed_bytes(N, K)),
-            _operand(alpha, "alpha" + name, torch.float32, device, N))
+def _weights(packed, alpha, name: str, N: int, K: int, index: int):
+    nbytes = packed_bytes(N, K)
+    if nbytes == 0:
+        raise SherryError(-2, "weights [N,K]")
+    return (_required(_vector(packed, "packed" + name, torch.uint8, index, nbytes), "packed" + name),
+            _required(_vector(alpha, "alpha" + name, torch.float32, index, N), "alpha" + name))
 
 
-def _zeroed_workspace(workspace, nbytes: int, device):
-    """The split-K workspace: the caller's, the stream's, or, under graph
-    capture, one of the graph's own that each replay zeroes (two graphs
-    captured on one stream may be replayed side by side, and memory that only
-    another graph has zeroed is not zero)."""
+def _raw_stream(index: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _zeroed_workspace(workspace, nbytes: int, x: torch.Tensor, index: int):
+    """(pointer, bytes) of the split-K workspace, and what keeps it alive: the
+    caller's, the stream's, or, under graph capture, one of the graph's own
+    that each replay zeroes (two graphs captured on one stream may be
+    replayed side by side, and memory that only another graph has zeroed is
+    not zero)."""
     if workspace is not None:
         p = _dev_tensor(workspace, "workspace", torch.uint8)
-        if workspace.device != device:
-            raise RuntimeError(f"workspace must be on {device}, got {workspace.device}")
-        return workspace, p, workspace.numel()
+        if workspace.get_device() != index:
+            raise RuntimeError(f"workspace must be on cuda:{index}, got {workspace.device}")
+        return p, workspace.numel(), workspace
     if nbytes == 0:
-        return None, None, 0
+        return None, 0, None
     if torch.cuda.is_current_stream_capturing():
-        ws = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+        ws = torch.zeros(nbytes, dtype=torch.uint8, device=x.device)
     else:
-        ws = _workspaces.get(device, nbytes)
-    return ws, ws.data_ptr(), ws.numel()
+        ws = _workspaces._bufs.get((index, _raw_stream(index)))
+        if ws is None or ws.numel() < nbytes:
+            ws = _workspaces.get(x.device, nbytes)
+    return ws.data_ptr(), ws.numel(), ws
 
 
-def _call(device: torch.device, name: str, *args) -> None:
-    """Calls the library with `device` current, on its current stream."""
-    fn = getattr(lib(), name)
-    if torch.cuda.current_device() == device.index:
-        _check(fn(*args, _stream(device)), name)
+def _call(name: str, index: int, fn, *args) -> None:
+    """Calls fn(*args, stream) with device `index` current, on its current stream."""
+    if torch.cuda.current_device() == index:
+        status = fn(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(device):
-            _check(fn(*args, _stream(device)), name)
+        with torch.cuda.device(index):
+            status = fn(*args, _raw_stream(index))
+    if status != 0:
+        raise SherryError(status, name)
 
 
-def _output(out, M: int, N: int, dtype: torch.dtype, device: torch.device):
+def _output(out, x: torch.Tensor, index: int, M: int, N: int, dtype: torch.dtype):
     if out is None:
-        out = torch.empty((M, N), dtype=dtype, device=device)
+        out = torch.empty((M, N), dtype=dtype, device=x.device)
         return out, out.data_ptr()
-    return out, _matrix(out, "out", dtype, device, (M, N))
+    return out, _matrix(out, "out", dtype, index, M, N)
 
 
 def gemm_fused(x: torch.Tensor, s_x: torch.Tensor, packed: torch.Tensor, alpha: torch.Tensor,
@@ -528,14 +554,15 @@ def gemm_fused(x: torch.Tensor, s_x: torch.Tensor, packed: torch.Tensor, alpha: 
     """y[M,N] = act((x_int8 @ T^T) * s_x[:,None] * alpha + bias) + residual in
     one kernel (sherry_gemm_fused).  bias is fp32 [N]; residual and y have
     type `dtype`; out may be the residual (updated in place)."""
-    M, dev, px, ps = _tokens(x, s_x, K)
-    pw, pa = _weights(packed, alpha, "", N, K, dev)
+    L = lib()
+    M, index, px, ps = _tokens(x, s_x, K)
+    pw, pa = _weights(packed, alpha, "", N, K, index)
     code, dt = _act_code(act), _dtype_code(dtype)
-    pb = _operand(bias, "bias", torch.float32, dev, N)
-    pr = _matrix(residual, "residual", dtype, dev, (M, N))
-    out, py = _output(out, M, N, dtype, dev)
-    ws, wp, wn = _zeroed_workspace(workspace, int(lib().sherry_gemm_fused_workspace_bytes(M, N, K)), dev)
-    _call(dev, "sherry_gemm_fused", px, ps, pw, pa, pb, code, pr, py, dt, M, N, K, wp, wn)
+    pb = _vector(bias, "bias", torch.float32, index, N)
+    pr = _matrix(residual, "residual", dtype, index, M, N)
+    out, py = _output(out, x, index, M, N, dtype)
+    wp, wn, _ws = _zeroed_workspace(workspace, L.sherry_gemm_fused_workspace_bytes(M, N, K), x, index)
+    _call("sherry_gemm_fused", index, L.sherry_gemm_fused, px, ps, pw, pa, pb, code, pr, py, dt, M, N, K, wp, wn)
     return out
 
 
@@ -546,21 +573,30 @@ def glu(x: torch.Tensor, s_x: torch.Tensor, packed_gate: torch.Tensor, alpha_gat
     """h[M,N] = act(g) * u with g and u the products of x with the gate and up
     matrices, in one kernel (sherry_glu).  A float32 h is what quantize_act
     takes for the down projection."""
-    M, dev, px, ps = _tokens(x, s_x, K)
-    pg, pag = _weights(packed_gate, alpha_gate, "_gate", N, K, dev)
-    pu, pau = _weights(packed_up, alpha_up, "_up", N, K, dev)
+    L = lib()
+    M, index, px, ps = _tokens(x, s_x, K)
+    pg, pag = _weights(packed_gate, alpha_gate, "_gate", N, K, index)
+    pu, pau = _weights(packed_up, alpha_up, "_up", N, K, index)
     code, dt = _act_code(act), _dtype_code(dtype)
-    out, ph = _output(out, M, N, dtype, dev)
-    ws, wp, wn = _zeroed_workspace(workspace, int(lib().sherry_glu_workspace_bytes(M, N, K)), dev)
-    _call(dev, "sherry_glu", px, ps, pg, pag, pu, pau, code, ph, dt, M, N, K, wp, wn)
+    out, ph = _output(out, x, index, M, N, dtype)
+    wp, wn, _ws = _zeroed_workspace(workspace, L.sherry_glu_workspace_bytes(M, N, K), x, index)
+    _call("sherry_glu", index, L.sherry_glu, px, ps, pg, pag, pu, pau, code, ph, dt, M, N, K, wp, wn)
     return out
 
 
-def _gradient(dy, M: int, N: int, device):
+def _gradient(dy, M: int, N: int, index: int):
     """(type code, pointer) of an output gradient [M,N]."""
     if not isinstance(dy, torch.Tensor):
         raise TypeError("the output gradient must be a torch.Tensor")
-    return _dtype_code(dy.dtype), _matrix(dy, "the output gradient", dy.dtype, device, (M, N))
+    return _dtype_code(dy.dtype), _matrix(dy, "the output gradient", dy.dtype, index, M, N)
+
+
+def _gradients(x: torch.Tensor, dtype: torch.dtype, M: int, K: int, N: int, scratch_bytes: int):
+    """dx, two fp32 vectors of N, and the scratch memory of a backward pass."""
+    dev = x.device
+    return (torch.empty((M, K), dtype=dtype, device=dev), torch.empty(N, dtype=torch.float32, device=dev),
+            torch.empty(N, dtype=torch.float32, device=dev),
+            torch.empty(scratch_bytes, dtype=torch.uint8, device=dev))
 
 
 def gemm_fused_backward(dy: torch.Tensor, x: torch.Tensor, s_x: torch.Tensor, packed: torch.Tensor,
@@ -569,16 +605,15 @@ def gemm_fused_backward(dy: torch.Tensor, x: torch.Tensor, s_x: torch.Tensor, pa
     """Gradients of gemm_fused from dy [M,N] and its inputs -> (dx of dy's type
     [M,K], dalpha fp32 [N], dbias fp32 [N]); dx is the gradient of the token
     x * s_x, the residual's is dy."""
-    M, dev, px, ps = _tokens(x, s_x, K)
-    pw, pa = _weights(packed, alpha, "", N, K, dev)
-    code, pb = _act_code(act), _operand(bias, "bias", torch.float32, dev, N)
-    dt, pdy = _gradient(dy, M, N, dev)
-    dx = torch.empty((M, K), dtype=dy.dtype, device=dev)
-    da, db = torch.empty((2, N), dtype=torch.float32, device=dev)
-    scratch = torch.empty(int(lib().sherry_gemm_fused_backward_scratch_bytes(M, N, K, dt)), dtype=torch.uint8,
-                          device=dev)
-    _call(dev, "sherry_gemm_fused_backward", pdy, px, ps, pw, pa, pb, code, dx.data_ptr(), da.data_ptr(),
-          db.data_ptr(), dt, M, N, K, scratch.data_ptr(), scratch.numel())
+    L = lib()
+    M, index, px, ps = _tokens(x, s_x, K)
+    pw, pa = _weights(packed, alpha, "", N, K, index)
+    code, pb = _act_code(act), _vector(bias, "bias", torch.float32, index, N)
+    dt, pdy = _gradient(dy, M, N, index)
+    nbytes = L.sherry_gemm_fused_backward_scratch_bytes(M, N, K, dt)
+    dx, da, db, scratch = _gradients(x, dy.dtype, M, K, N, nbytes)
+    _call("sherry_gemm_fused_backward", index, L.sherry_gemm_fused_backward, pdy, px, ps, pw, pa, pb, code,
+          dx.data_ptr(), da.data_ptr(), db.data_ptr(), dt, M, N, K, scratch.data_ptr(), nbytes)
     return dx, da, db
 
 
@@ -588,37 +623,39 @@ def glu_backward(dh: torch.Tensor, x: torch.Tensor, s_x: torch.Tensor, packed_ga
     """Gradients of glu from dh [M,N] and its inputs -> (dx of dh's type [M,K],
     dalpha_gate fp32 [N], dalpha_up fp32 [N]); dx is the gradient of the
     token x * s_x."""
-    M, dev, px, ps = _tokens(x, s_x, K)
-    pg, pag = _weights(packed_gate, alpha_gate, "_gate", N, K, dev)
-    pu, pau = _weights(packed_up, alpha_up, "_up", N, K, dev)
+    L = lib()
+    M, index, px, ps = _tokens(x, s_x, K)
+    pg, pag = _weights(packed_gate, alpha_gate, "_gate", N, K, index)
+    pu, pau = _weights(packed_up, alpha_up, "_up", N, K, index)
     code = _act_code(act)
-    dt, pdh = _gradient(dh, M, N, dev)
-    dx = torch.empty((M, K), dtype=dh.dtype, device=dev)
-    dg, du = torch.empty((2, N), dtype=torch.float32, device=dev)
-    scratch = torch.empty(int(lib().sherry_glu_backward_scratch_bytes(M, N, K, dt)), dtype=torch.uint8, device=dev)
-    _call(dev, "sherry_glu_backward", pdh, px, ps, pg, pag, pu, pau, code, dx.data_ptr(), dg.data_ptr(),
-          du.data_ptr(), dt, M, N, K, scratch.data_ptr(), scratch.numel())
+    dt, pdh = _gradient(dh, M, N, index)
+    nbytes = L.sherry_glu_backward_scratch_bytes(M, N, K, dt)
+    dx, dg, du, scratch = _gradients(x, dh.dtype, M, K, N, nbytes)
+    _call("sherry_glu_backward", index, L.sherry_glu_backward, pdh, px, ps, pg, pag, pu, pau, code, dx.data_ptr(),
+          dg.data_ptr(), du.data_ptr(), dt, M, N, K, scratch.data_ptr(), nbytes)
     return dx, dg, du
 
 
 def _features(x, weight, bias):
-    """(M, K, device, type code, pointers) of a norm's tokens and vectors."""
+    """(M, K, device index, type code, pointers) of a norm's tokens and vectors."""
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch.Tensor")
-    if x.dim() != 2:
-        raise RuntimeError("x must be 2-D [M,K]")
     dt = _dtype_code(x.dtype)
     px = _dev_tensor(x, "x", x.dtype)
+    if x.dim() != 2:
+        raise RuntimeError("x must be 2-D [M,K]")
     M, K = x.shape
-    return (M, K, x.device, dt, px, _operand(weight, "weight", torch.float32, x.device, K),
-            _operand(bias, "bias", torch.float32, x.device, K))
+    index = x.get_device()
+    return (M, K, index, dt, px, _vector(weight, "weight", torch.float32, index, K),
+            _vector(bias, "bias", torch.float32, index, K))
 
 
-def _stats(stats: bool, M: int, device):
+def _stats(stats: bool, M: int, x: torch.Tensor):
     if not stats:
-        return (), (None, None)
-    mean, rstd = torch.empty((2, M), dtype=torch.float32, device=device)
-    return (mean, rstd), (mean.data_ptr(), rstd.data_ptr())
+        return (), None, None
+    mean = torch.empty(M, dtype=torch.float32, device=x.device)
+    rstd = torch.empty(M, dtype=torch.float32, device=x.device)
+    return (mean, rstd), mean.data_ptr(), rstd.data_ptr()
 
 
 def layernorm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
@@ -626,10 +663,10 @@ def layernorm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.T
     """Layer norm of each token of x [M,K] (float32, float16 or bfloat16;
     weight and bias fp32 [K]) -> y of x's type, or (y, mean, rstd) with
     `stats` (what layernorm_backward takes).  out may be x."""
-    M, K, dev, dt, px, pw, pb = _features(x, weight, bias)
-    out, py = _output(out, M, K, x.dtype, dev)
-    found, (pm, pr) = _stats(stats, M, dev)
-    _call(dev, "sherry_layernorm", px, pw, pb, eps, py, pm, pr, dt, M, K)
+    M, K, index, dt, px, pw, pb = _features(x, weight, bias)
+    out, py = _output(out, x, index, M, K, x.dtype)
+    found, pm, pr = _stats(stats, M, x)
+    _call("sherry_layernorm", index, lib().sherry_layernorm, px, pw, pb, eps, py, pm, pr, dt, M, K)
     return (out, *found) if stats else out
 
 
@@ -638,11 +675,12 @@ def layernorm_quantize(x: torch.Tensor, weight: torch.Tensor | None = None,
     """Layer norm of each token of x [M,K] straight into the int8 tokens the
     products take -> (q int8 [M,K], s_x fp32 [M]), and mean and rstd with
     `stats`."""
-    M, K, dev, dt, px, pw, pb = _features(x, weight, bias)
-    q = torch.empty((M, K), dtype=torch.int8, device=dev)
-    s = torch.empty(M, dtype=torch.float32, device=dev)
-    found, (pm, pr) = _stats(stats, M, dev)
-    _call(dev, "sherry_layernorm_quantize", px, pw, pb, eps, q.data_ptr(), s.data_ptr(), pm, pr, dt, M, K)
+    M, K, index, dt, px, pw, pb = _features(x, weight, bias)
+    q = torch.empty((M, K), dtype=torch.int8, device=x.device)
+    s = torch.empty(M, dtype=torch.float32, device=x.device)
+    found, pm, pr = _stats(stats, M, x)
+    _call("sherry_layernorm_quantize", index, lib().sherry_layernorm_quantize, px, pw, pb, eps, q.data_ptr(),
+          s.data_ptr(), pm, pr, dt, M, K)
     return (q, s, *found)
 
 
@@ -650,13 +688,17 @@ def layernorm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rs
                        weight: torch.Tensor | None = None, out: torch.Tensor | None = None):
     """Gradients of layernorm -> (dx of x's type, dweight fp32 [K], dbias fp32
     [K]).  out may be dy."""
-    M, K, dev, dt, px, pw, _ = _features(x, weight, None)
-    pdy = _matrix(dy, "dy", x.dtype, dev, (M, K))
-    pm = _operand(mean, "mean", torch.float32, dev, M)
-    pr = _operand(rstd, "rstd", torch.float32, dev, M)
-    out, pdx = _output(out, M, K, x.dtype, dev)
-    dw, db = torch.empty((2, K), dtype=torch.float32, device=dev)
-    scratch = torch.empty(int(lib().sherry_layernorm_backward_scratch_bytes(M, K)), dtype=torch.uint8, device=dev)
-    _call(dev, "sherry_layernorm_backward", pdy, px, pm, pr, pw, pdx, dw.data_ptr(), db.data_ptr(), dt, M, K,
-          scratch.data_ptr(), scratch.numel())
+    L = lib()
+    M, K, index, dt, px, pw, _ = _features(x, weight, None)
+    pdy = _required(_matrix(dy, "dy", x.dtype, index, M, K), "dy")
+    pm = _required(_vector(mean, "mean", torch.float32, index, M), "mean")
+    pr = _required(_vector(rstd, "rstd", torch.float32, index, M), "rstd")
+    out, pdx = _output(out, x, index, M, K, x.dtype)
+    dev = x.device
+    dw = torch.empty(K, dtype=torch.float32, device=dev)
+    db = torch.empty(K, dtype=torch.float32, device=dev)
+    nbytes = L.sherry_layernorm_backward_scratch_bytes(M, K)
+    scratch = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    _call("sherry_layernorm_backward", index, L.sherry_layernorm_backward, pdy, px, pm, pr, pw, pdx, dw.data_ptr(),
+          db.data_ptr(), dt, M, K, scratch.data_ptr(), nbytes)
     return out, dw, db

@@ -86,6 +86,7 @@ struct Tiling {
   // 20.5 -> 19.9; M=128 13.7 -> 13.5.)
   static constexpr int kOutLd = kBN + 4;
   static constexpr int kLdsOut = KP * 32 * kOutLd * 4; // epilogue tiles (32 rows, every phase)
+  static constexpr int kLdsTile = KP * 16 * kOutLd * 4;   // 16 rows of them (epilogues other than kEpNone)
   static constexpr int kMT = BM / 16;                  // row blocks per wave (8 or 4)
   static constexpr int kAStage = BM * kBK;             // activation bytes per k-step
   static constexpr int kRowsPerWave = BM / kRT;        // rows each wave of a phase copies
@@ -100,6 +101,9 @@ struct Tiling {
   // and j+2 (2 + 2)
   static constexpr int kNewerLoads = kPair ? 4 : (kABufs == 3 ? 2 + kACopies + 2 : 2);
 };
+
+template <int I>
+using Const = std::integral_constant<int, I>;
 
 // Activation tile in LDS, row-major with 128-byte rows: the 16-byte chunk c
 // of row r sits at chunk position c ^ ((r >> 1) & 7).  A fragment read (16
@@ -195,7 +199,9 @@ __global__ __launch_bounds__(kThreads) void mfma_gemm_kernel(const uint8_t* pack
   using T = Tiling<BM, KP>;
   constexpr int kBM = BM, kMT = T::kMT, kAStage = T::kAStage, kACopies = T::kACopies;
   constexpr int kLdsBytes = T::kLdsBytes, kNewerLoads = T::kNewerLoads;
-  constexpr int kRT = T::kRT, kBN = T::kBN, kOutLd = T::kOutLd, kABufs = T::kABufs;
+  constexpr int kRT = T::kRT, kBN = T::kBN, kOutLd = T::kOutLd;
+  constexpr bool kOwn = EP != kEpNone;
+  constexpr int kABufs = kOwn && T::kABufs == 3 ? 4 : T::kABufs;
   constexpr bool kPair = T::kPair;
   // gated: half of the workgroup's row tiles are the gate's, half the up
   // matrix's of the same kBNO outputs
@@ -204,7 +210,17 @@ __global__ __launch_bounds__(kThreads) void mfma_gemm_kernel(const uint8_t* pack
   // the activation buffers [buffer][phase]; after the main loop the
   // epilogue tile reuses them
   // (32-bit words: every view below is a character type or 32-bit lanes)
-  __shared__ __attribute__((aligned(16))) uint32_t lds[kLdsBytes / 4];
+  // With an epilogue every buffer is an array of its own, picked by a
+  // constant, the first one large enough for the epilogue tile: the compiler
+  // then sees that a step's fragment reads cannot touch what the copies in
+  // flight write.  From one array it waits, before a step's first fragment,
+  // for the copies that step has just issued.  (Measured at M=512, K=4096,
+  // gated N=14336: PLACEHOLDER.)
+  constexpr int kBuf = KP * kAStage / 4, kFirst = kBuf * 4 > T::kLdsTile ? kBuf : T::kLdsTile / 4;
+  __shared__ __attribute__((aligned(16))) uint32_t lds[kOwn ? kFirst : kLdsBytes / 4];
+  __shared__ __attribute__((aligned(16))) uint32_t lds1[kOwn ? kBuf : 4];
+  __shared__ __attribute__((aligned(16))) uint32_t lds2[kOwn && kABufs > 2 ? kBuf : 4];
+  __shared__ __attribute__((aligned(16))) uint32_t lds3[kOwn && kABufs > 3 ? kBuf : 4];
   // the pair table in an array of its own: the compiler then sees that its
   // lookups cannot read what an activation copy in flight is writing.  Its
   // alignment places it first in LDS, below 64 KB, so a lookup's table base
@@ -272,6 +288,10 @@ __global__ __launch_bounds__(kThreads) void mfma_gemm_kernel(const uint8_t* pack
   // an offset the descriptor's range check rejects (the copy writes zeros)
   const int a_oob = (size_t)(M - m0) * (size_t)K > 0x7FFFFFFFull ? 0x7FFFFFFF : (M - m0) * K;
   auto a_buf = [&](int b) { return reinterpret_cast<int8_t*>(lds) + (b * KP + kh) * kAStage; };
+  auto own_buf = [&](auto b) __attribute__((always_inline)) {
+    constexpr int i = decltype(b)::value % kABufs;
+    return reinterpret_cast<int8_t*>(i == 0 ? lds : i == 1 ? lds1 : i == 2 ? lds2 : lds3) + kh * kAStage;
+  };
 
   v4i acc[kMT][kNT];
 #pragma unroll
@@ -284,15 +304,15 @@ __global__ __launch_bounds__(kThreads) void mfma_gemm_kernel(const uint8_t* pack
   const int KJ = (KT + KP - 1) / KP;
   auto ktile = [&](int j) { return min(KP * j + kh, KT - 1); };
   // codes, coalesced (lane = tile row)
-  auto load_codes = [&](int j, v4u& w, uint32_t& h) {
+  auto load_codes = [&](int j, v4u& w, uint32_t& h) __attribute__((always_inline)) {
     const int ks = ktile(j) * kTileBytes;
     w = __builtin_amdgcn_raw_buffer_load_b128(rc, 16 * lane, ks, 0);
     h = __builtin_amdgcn_raw_buffer_load_b32(rc, kTileHiOff + 4 * lane, ks, 0);
   };
   // this wave's share of the activation tile of step j into buffer b
-  auto copy_a = [&](int j, int b) {
+  auto copy_a = [&](int j, int8_t* buf) __attribute__((always_inline)) {
     const int ka = ktile(j) * kBK;
-    int8_t* dst = a_buf(b) + T::kRowsPerWave * wave * kBK;
+    int8_t* dst = buf + T::kRowsPerWave * wave * kBK;
     // (the k-step offset is added to the lane offset, not passed as the
     // scalar offset, so the descriptor's range check sees the whole offset;
     // chunks past K, in a ragged last k-tile whose codes are padding, take
@@ -311,7 +331,7 @@ __global__ __launch_bounds__(kThreads) void mfma_gemm_kernel(const uint8_t* pack
   // follows gets fresh registers and the loop's back edge copies them back
   // after waiting for every load (measured at N=14336, K=4096: M=128 22.9
   // against 20.5 us with them).
-  auto split = [&](const v4u& w, uint32_t h, uint32_t (&f0)[kNT], uint32_t (&f1)[kNT]) {
+  auto split = [&](const v4u& w, uint32_t h, uint32_t (&f0)[kNT], uint32_t (&f1)[kNT]) __attribute__((always_inline)) {
     const uint32_t wt[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int t = 0; t < kNT; ++t) {
@@ -333,10 +353,11 @@ __global__ __launch_bounds__(kThreads) void mfma_gemm_kernel(const uint8_t* pack
   // The arrival and the polls are LDS instructions in asm: as built-ins the
   // compiler cannot tell them from the activation copies in flight and waits
   // for those first.  The poll is bounded (~0.3 s), so a wave always leaves.
-  auto parity_barrier = [&](int j) {   // j: the barrier's index
+  auto parity_barrier = [&](int j) __attribute__((always_inline)) {   // j: the barrier's index
     const uint32_t pa = (uint32_t)(size_t)((__attribute__((address_space(3))) unsigned*)&parity_arrivals[kh]);
     if (lane == 0) asm volatile("ds_add_u32 %0, %1" ::"v"(pa), "v"(1u) : "memory");
     const unsigned target = (unsigned)kRT * (unsigned)(j + 1);
+#pragma unroll 1
     for (int spin = 0; spin < (1 << 22); ++spin) {
       unsigned c;
       asm volatile("ds_read_b32 %0, %1\n\ts_waitcnt lgkmcnt(0)" : "=v"(c) : "v"(pa) : "memory");
@@ -346,8 +367,9 @@ __global__ __launch_bounds__(kThreads) void mfma_gemm_kernel(const uint8_t* pack
   };
   // `even`: j is even (a constant at every call), so with a barrier per two
   // steps the odd steps fold to the decode and the MFMAs.
-  auto step = [&](int j, int b, bool even, v4u& wn, uint32_t& hn, const v4i (&bc0)[kNT],
-                  const v4i (&bc1)[kNT], v4i (&bn0)[kNT], v4i (&bn1)[kNT]) {
+  // `as`: the buffer it reads; `to`, `to2`: those its copies go to.
+  auto step_on = [&](int j, const int8_t* as, int8_t* to, int8_t* to2, bool even, v4u& wn, uint32_t& hn, const v4i (&bc0)[kNT],
+                  const v4i (&bc1)[kNT], v4i (&bn0)[kNT], v4i (&bn1)[kNT]) __attribute__((always_inline)) {
     // every wave's copy of step j (and j+1) has landed and its earlier LDS
     // reads are done; then the buffer of step j-1 is free for the copy of
     // step j+2 (those of j-2, j-1 for j+2, j+3)
@@ -362,12 +384,12 @@ __global__ __launch_bounds__(kThreads) void mfma_gemm_kernel(const uint8_t* pack
       __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
       __builtin_amdgcn_sched_barrier(0);
       if constexpr (kPair) {
-        copy_a(min(j + 2, KJ - 1), (b + 2) & 3);
-        copy_a(min(j + 3, KJ - 1), (b + 3) & 3);
-      } else if constexpr (kABufs == 3) {
-        copy_a(min(j + 2, KJ - 1), b == 0 ? 2 : b - 1);
+        copy_a(min(j + 2, KJ - 1), to);
+        copy_a(min(j + 3, KJ - 1), to2);
+      } else if constexpr (kABufs >= 3) {
+        copy_a(min(j + 2, KJ - 1), to);
       } else {
-        copy_a(min(j + 1, KJ - 1), b ^ 1);
+        copy_a(min(j + 1, KJ - 1), to);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -376,9 +398,14 @@ __global__ __launch_bounds__(kThreads) void mfma_gemm_kernel(const uint8_t* pack
     load_codes(min(j + 3, KJ - 1), wn, hn);
     __builtin_amdgcn_sched_barrier(0);
     if (KP * j + kh < KT)    // KT not a multiple of KP: the last step is short
-      mg_mfma<true, kMT>(acc, bc0, bc1, a_buf(b), l16, g, f0, f1, bn0, bn1, d2);
+      mg_mfma<true, kMT>(acc, bc0, bc1, as, l16, g, f0, f1, bn0, bn1, d2);
     else
-      mg_mfma<false, kMT>(acc, bc0, bc1, a_buf(b), l16, g, f0, f1, bn0, bn1, d2);
+      mg_mfma<false, kMT>(acc, bc0, bc1, as, l16, g, f0, f1, bn0, bn1, d2);
+  };
+  auto step = [&](int j, int b, bool even, v4u& wn, uint32_t& hn, const v4i (&bc0)[kNT],
+                  const v4i (&bc1)[kNT], v4i (&bn0)[kNT], v4i (&bn1)[kNT]) {
+    int8_t* to = a_buf(kPair ? (b + 2) & 3 : kABufs == 3 ? (b == 0 ? 2 : b - 1) : b ^ 1);
+    step_on(j, a_buf(b), to, kPair ? a_buf((b + 3) & 3) : to, even, wn, hn, bc0, bc1, bn0, bn1);
   };
 
   // Two register stages of codes and two sets of B operands, ping-pong.
@@ -393,15 +420,15 @@ __global__ __launch_bounds__(kThreads) void mfma_gemm_kernel(const uint8_t* pack
   v4i bA0[kNT], bA1[kNT], bB0[kNT], bB1[kNT];
   load_codes(0, w0, h0);
   __builtin_amdgcn_sched_barrier(0);
-  copy_a(0, 0);
+  copy_a(0, kOwn ? own_buf(Const<0>{}) : a_buf(0));
   __builtin_amdgcn_sched_barrier(0);
   if constexpr (kPair) {
-    copy_a(min(1, KJ - 1), 1);
+    copy_a(min(1, KJ - 1), kOwn ? own_buf(Const<1>{}) : a_buf(1));
     __builtin_amdgcn_sched_barrier(0);
   }
   load_codes(min(1, KJ - 1), w1, h1);
   __builtin_amdgcn_sched_barrier(0);
-  if constexpr (!kPair && kABufs == 3) copy_a(min(1, KJ - 1), 1);
+  if constexpr (!kPair && kABufs >= 3) copy_a(min(1, KJ - 1), kOwn ? own_buf(Const<1>{}) : a_buf(1));
   __builtin_amdgcn_sched_barrier(0);
   // decode table written (LDS only: the copies stay in flight)
   __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(63));
@@ -420,14 +447,42 @@ __global__ __launch_bounds__(kThreads) void mfma_gemm_kernel(const uint8_t* pack
     __builtin_amdgcn_sched_barrier(0);
   }
 
-  int j = 0, b = 0;
-  for (; j + 2 <= KJ; j += 2) {
-    step(j, b, true, w1, h1, bA0, bA1, bB0, bB1);
-    b = b + 1 == kABufs ? 0 : b + 1;
-    step(j + 1, b, false, w0, h0, bB0, bB1, bA0, bA1);
-    b = b + 1 == kABufs ? 0 : b + 1;
+  if constexpr (kOwn) {
+    // steps in turns of kABufs, a multiple of the 2 register stages (with
+    // 128 x 256 tiles four buffers, not three, for that)
+    static_assert(kABufs % 2 == 0, "a step's register stage follows from its buffer");
+    auto own_step = [&](int j, auto u) __attribute__((always_inline)) {
+      constexpr int i = decltype(u)::value;
+      int8_t* as = own_buf(u);
+      int8_t* to = own_buf(Const<i + (kABufs == 2 ? 1 : 2)>{});
+      int8_t* to2 = own_buf(Const<i + 3>{});
+      if constexpr (i % 2 == 0) step_on(j, as, to, to2, true, w1, h1, bA0, bA1, bB0, bB1);
+      else step_on(j, as, to, to2, false, w0, h0, bB0, bB1, bA0, bA1);
+    };
+    int j = 0;
+    for (; j + kABufs <= KJ; j += kABufs) {
+      own_step(j, Const<0>{});
+      own_step(j + 1, Const<1>{});
+      if constexpr (kABufs > 2) {
+        own_step(j + 2, Const<2>{});
+        own_step(j + 3, Const<3>{});
+      }
+    }
+    if (j < KJ) own_step(j, Const<0>{});
+    if constexpr (kABufs > 2) {
+      if (j + 1 < KJ) own_step(j + 1, Const<1>{});
+      if (j + 2 < KJ) own_step(j + 2, Const<2>{});
+    }
+  } else {
+    int j = 0, b = 0;
+    for (; j + 2 <= KJ; j += 2) {
+      step(j, b, true, w1, h1, bA0, bA1, bB0, bB1);
+      b = b + 1 == kABufs ? 0 : b + 1;
+      step(j + 1, b, false, w0, h0, bB0, bB1, bA0, bA1);
+      b = b + 1 == kABufs ? 0 : b + 1;
+    }
+    if (j < KJ) step(j, b, true, w1, h1, bA0, bA1, bB0, bB1);
   }
-  if (j < KJ) step(j, b, true, w1, h1, bA0, bA1, bB0, bB1);
   // the clamped copies past the end may still be landing in LDS, which the
   // epilogue reuses
   __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
@@ -441,17 +496,18 @@ __global__ __launch_bounds__(kThreads) void mfma_gemm_kernel(const uint8_t* pack
   // M=512, N=14336, K=4096, where the 29 MB of fp32 output bound it).  Lane
   // (l16, g) of a 16 x 16 MFMA block holds column l16, rows 4g..4g+3.  The
   // scales are read once, before the first barrier.
-  // The sums of 32 rows (two row blocks qq) into this phase's LDS tile.
-  int* ot = reinterpret_cast<int*>(lds);       // [phase][32][kOutLd] sums
-  int* mine = ot + kh * 32 * kOutLd;
+  // The sums of the qq-th kTurnRows rows (row blocks) into this phase's LDS tile.
+  constexpr int kTurnRows = kOwn ? 16 : 32, kTurnBlocks = kTurnRows / 16;
+  int* ot = reinterpret_cast<int*>(lds);       // [phase][kTurnRows][kOutLd] sums
+  int* mine = ot + kh * kTurnRows * kOutLd;
   auto put_sums = [&](int qq) {
 #pragma unroll
-    for (int ii = 0; ii < 2; ++ii)
+    for (int ii = 0; ii < kTurnBlocks; ++ii)
 #pragma unroll
       for (int r = 0; r < 4; ++r)
 #pragma unroll
         for (int t = 0; t < kNT; ++t)
-          mine[(16 * ii + 4 * g + r) * kOutLd + wave * kTileRows + 16 * t + l16] = acc[2 * qq + ii][t][r];
+          mine[(16 * ii + 4 * g + r) * kOutLd + wave * kTileRows + 16 * t + l16] = acc[kTurnBlocks * qq + ii][t][r];
   };
   if constexpr (EP == kEpNone) {
     const bool want_y = a.y != nullptr;
@@ -494,8 +550,9 @@ __global__ __launch_bounds__(kThreads) void mfma_gemm_kernel(const uint8_t* pack
     constexpr bool kBack = ep_back(EP);
     constexpr int kCols = kBNO / 4;             // threads across a row: 4 outputs each
     constexpr int kRowStep = kThreads / kCols;  // rows the workgroup takes at a time
-    static_assert(32 % kRowStep == 0, "whole turns over the 32 rows of a tile");
-    constexpr int kTurns = 32 / kRowStep;
+    static_assert(kRowStep <= kTurnRows ? kTurnRows % kRowStep == 0 : kRowStep == 2 * kTurnRows, "rows per turn");
+    // (a row narrower than the workgroup can take in one turn: half the threads rest)
+    constexpr int kTurns = kRowStep <= kTurnRows ? kTurnRows / kRowStep : 1;
     __shared__ float inv_rows[kBack ? kBM : 1];
     const int c4 = tid % kCols, r0 = tid / kCols;
     const int n = n0 + 4 * c4;
@@ -518,14 +575,14 @@ __global__ __launch_bounds__(kThreads) void mfma_gemm_kernel(const uint8_t* pack
     const size_t zrow = (size_t)e.grad.terms * (kGlu ? 2 : 1) * RT64;
     __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
 #pragma unroll
-    for (int qq = 0; qq < kMT / 2; ++qq) {
+    for (int qq = 0; qq < kMT / kTurnBlocks; ++qq) {
       // this turn's residuals or output gradients, ahead of the barriers
       f4 io[kTurns];
 #pragma unroll
       for (int k = 0; k < kTurns; ++k) {
-        const int m = m0 + 32 * qq + r0 + kRowStep * k;
+        const int m = m0 + kTurnRows * qq + r0 + kRowStep * k;
         io[k] = f4{0.0f, 0.0f, 0.0f, 0.0f};
-        if (m < M && n < N) {
+        if (m < M && n < N && r0 < kTurnRows) {
           if constexpr (kBack) io[k] = load4_as(e.grad.dy, (size_t)m * N + n, e.dtype);
           else if (!kGlu && e.residual) io[k] = load4_as(e.residual, (size_t)m * N + n, e.dtype);
         }
@@ -536,15 +593,15 @@ __global__ __launch_bounds__(kThreads) void mfma_gemm_kernel(const uint8_t* pack
 #pragma unroll
       for (int k = 0; k < kTurns; ++k) {
         const int ml = r0 + kRowStep * k;
-        const int m = m0 + 32 * qq + ml;
-        if (m >= M || n >= (kBack ? RT64 : N)) continue;
+        const int m = m0 + kTurnRows * qq + ml;
+        if (m >= M || n >= (kBack ? RT64 : N) || r0 >= kTurnRows) continue;
         v4i s1{0, 0, 0, 0}, s2{0, 0, 0, 0};
 #pragma unroll
         for (int ph = 0; ph < KP; ++ph) {
-          s1 += *reinterpret_cast<const v4i*>(&ot[(ph * 32 + ml) * kOutLd + 4 * c4]);
-          if constexpr (kGlu) s2 += *reinterpret_cast<const v4i*>(&ot[(ph * 32 + ml) * kOutLd + kBNO + 4 * c4]);
+          s1 += *reinterpret_cast<const v4i*>(&ot[(ph * kTurnRows + ml) * kOutLd + 4 * c4]);
+          if constexpr (kGlu) s2 += *reinterpret_cast<const v4i*>(&ot[(ph * kTurnRows + ml) * kOutLd + kBNO + 4 * c4]);
         }
-        const float sx = sxs[32 * qq + ml];
+        const float sx = sxs[kTurnRows * qq + ml];
         f4 o{0.0f, 0.0f, 0.0f, 0.0f}, o2 = o;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -574,7 +631,7 @@ __global__ __launch_bounds__(kThreads) void mfma_gemm_kernel(const uint8_t* pack
           // rows past N inside the last row tile: zeros, so the padding adds nothing
           if (n >= N) o = o2 = f4{0.0f, 0.0f, 0.0f, 0.0f};
           _Float16* z = reinterpret_cast<_Float16*>(e.grad.z) + (size_t)m * zrow + n;
-          const float scale = inv_rows[32 * qq + ml];
+          const float scale = inv_rows[kTurnRows * qq + ml];
           store_terms(z, o * scale, e.grad.terms, (kGlu ? 2 : 1) * RT64);
           if constexpr (kGlu) store_terms(z + RT64, o2 * scale, e.grad.terms, 2 * RT64);
         }
