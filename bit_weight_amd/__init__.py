@@ -431,11 +431,11 @@ def gemm2(x: torch.Tensor, s_x: torch.Tensor, packed: torch.Tensor, alpha: torch
 
 
 # ------------------------------------------------- feed-forward operators
-# A small call's kernel takes 5 to 10 us, so the checks and the marshalling
-# here are kept to a few cheap attribute reads per tensor; the error messages
-# are made only once a check has failed.
+# Their tensors are checked and passed on by a compiled module (csrc/binding.cpp).
 DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "relu2": 2, "silu": 3, "gelu": 4, "gelu_tanh": 5}
+
+_native = None
 
 
 def _act_code(act) -> int:
@@ -452,99 +452,45 @@ def _dtype_code(dtype) -> int:
     return code
 
 
-def _refuse(t, name: str, dtype: torch.dtype, index: int, shape) -> None:
-    """Raises for an operand that one of the checks below has failed."""
-    _dev_tensor(t, name, dtype)
-    if t.get_device() != index:
-        raise RuntimeError(f"{name} must be on cuda:{index}, got {t.device}")
-    raise RuntimeError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
-
-
-def _vector(t, name: str, dtype: torch.dtype, index: int, n: int):
-    """Pointer of an operand of n values on device `index` (None -> NULL)."""
-    if t is None:
-        return None
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.numel() == n
-            and t.is_contiguous()):
-        _refuse(t, name, dtype, index, (n,))
-    return t.data_ptr()
-
-
-def _matrix(t, name: str, dtype: torch.dtype, index: int, M: int, N: int):
-    """Pointer of an [M,N] operand on device `index` (None -> NULL)."""
-    if t is None:
-        return None
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.shape == (M, N)
-            and t.is_contiguous()):
-        _refuse(t, name, dtype, index, (M, N))
-    return t.data_ptr()
-
-
-def _required(p, name: str):
-    if p is None:
-        raise TypeError(f"{name} must be a torch.Tensor")
-    return p
-
-
-def _tokens(x, s_x, K: int):
-    """(M, device index, pointers) of int8 tokens and their scales."""
-    px = _dev_tensor(x, "x", torch.int8)
-    if x.dim() != 2 or x.shape[1] != K:
-        raise RuntimeError(f"x must be [M,{K}]")
-    M, index = x.shape[0], x.get_device()
-    return M, index, px, _required(_vector(s_x, "s_x", torch.float32, index, M), "s_x")
-
-
-def _weights(packed, alpha, name: str, N: int, K: int, index: int):
-    nbytes = packed_bytes(N, K)
-    if nbytes == 0:
-        raise SherryError(-2, "weights [N,K]")
-    return (_required(_vector(packed, "packed" + name, torch.uint8, index, nbytes), "packed" + name),
-            _required(_vector(alpha, "alpha" + name, torch.float32, index, N), "alpha" + name))
-
-
-def _raw_stream(index: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(index)
-
-
-def _zeroed_workspace(workspace, nbytes: int, x: torch.Tensor, index: int):
-    """(pointer, bytes) of the split-K workspace, and what keeps it alive: the
-    caller's, the stream's, or, under graph capture, one of the graph's own
-    that each replay zeroes (two graphs captured on one stream may be
-    replayed side by side, and memory that only another graph has zeroed is
-    not zero)."""
-    if workspace is not None:
-        p = _dev_tensor(workspace, "workspace", torch.uint8)
-        if workspace.get_device() != index:
-            raise RuntimeError(f"workspace must be on cuda:{index}, got {workspace.device}")
-        return p, workspace.numel(), workspace
-    if nbytes == 0:
-        return None, 0, None
-    if torch.cuda.is_current_stream_capturing():
-        ws = torch.zeros(nbytes, dtype=torch.uint8, device=x.device)
-    else:
-        ws = _workspaces._bufs.get((index, _raw_stream(index)))
-        if ws is None or ws.numel() < nbytes:
-            ws = _workspaces.get(x.device, nbytes)
-    return ws.data_ptr(), ws.numel(), ws
-
-
-def _call(name: str, index: int, fn, *args) -> None:
-    """Calls fn(*args, stream) with device `index` current, on its current stream."""
-    if torch.cuda.current_device() == index:
-        status = fn(*args, _raw_stream(index))
-    else:
+def _zeroed_workspace(index: int, nbytes: int) -> torch.Tensor:
+    """The split-K workspace of the current stream of device `index`; under
+    graph capture one of the graph's own, which each replay zeroes (two
+    graphs captured on one stream may be replayed side by side, and memory
+    that only another graph has zeroed is not zero)."""
+    if torch.cuda.current_device() != index:
         with torch.cuda.device(index):
-            status = fn(*args, _raw_stream(index))
-    if status != 0:
-        raise SherryError(status, name)
+            return _zeroed_workspace(index, nbytes)
+    if torch.cuda.is_current_stream_capturing():
+        return torch.zeros(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
+    buf = _workspaces._bufs.get((index, torch._C._cuda_getCurrentRawStream(index)))
+    if buf is None or buf.numel() < nbytes:
+        buf = _workspaces.get(torch.device("cuda", index), nbytes)
+    return buf
 
 
-def _output(out, x: torch.Tensor, index: int, M: int, N: int, dtype: torch.dtype):
-    if out is None:
-        out = torch.empty((M, N), dtype=dtype, device=x.device)
-        return out, out.data_ptr()
-    return out, _matrix(out, "out", dtype, index, M, N)
+def _raise_status(status: int, what: str) -> None:
+    raise SherryError(status, what)
+
+
+def _load_native():
+    global _native
+    L = lib()
+    with _lock:
+        if _native is None:
+            try:
+                from . import _binding
+            except ImportError as e:
+                raise RuntimeError("bit_weight_amd/_binding.so is missing or does not load: build it with "
+                                   "`python -m bit_weight_amd.build` (or __graft_entry__.build())") from e
+            names = [n for n in dir(_binding) if not n.startswith("_") and n != "setup"]
+            entries = {f"sherry_{n}": None for n in names}
+            entries |= {"sherry_packed_bytes": None, "sherry_gemm_fused_workspace_bytes": None,
+                        "sherry_glu_workspace_bytes": None}
+            entries |= {f"sherry_{n}_scratch_bytes": None for n in names if n.endswith("backward")}
+            _binding.setup({n: ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in entries},
+                           _zeroed_workspace, _raise_status)
+            _native = _binding
+    return _native
 
 
 def gemm_fused(x: torch.Tensor, s_x: torch.Tensor, packed: torch.Tensor, alpha: torch.Tensor,
@@ -554,16 +500,17 @@ def gemm_fused(x: torch.Tensor, s_x: torch.Tensor, packed: torch.Tensor, alpha: 
     """y[M,N] = act((x_int8 @ T^T) * s_x[:,None] * alpha + bias) + residual in
     one kernel (sherry_gemm_fused).  bias is fp32 [N]; residual and y have
     type `dtype`; out may be the residual (updated in place)."""
-    L = lib()
-    M, index, px, ps = _tokens(x, s_x, K)
-    pw, pa = _weights(packed, alpha, "", N, K, index)
-    code, dt = _act_code(act), _dtype_code(dtype)
-    pb = _vector(bias, "bias", torch.float32, index, N)
-    pr = _matrix(residual, "residual", dtype, index, M, N)
-    out, py = _output(out, x, index, M, N, dtype)
-    wp, wn, _ws = _zeroed_workspace(workspace, L.sherry_gemm_fused_workspace_bytes(M, N, K), x, index)
-    _call("sherry_gemm_fused", index, L.sherry_gemm_fused, px, ps, pw, pa, pb, code, pr, py, dt, M, N, K, wp, wn)
-    return out
+    return (_native or _load_native()).gemm_fused(x, s_x, packed, alpha, N, K, bias, _act_code(act), residual,
+                                                  _dtype_code(dtype), out, workspace)
+
+
+def gemm_fused_backward(dy: torch.Tensor, x: torch.Tensor, s_x: torch.Tensor, packed: torch.Tensor,
+                        alpha: torch.Tensor, N: int, K: int, bias: torch.Tensor | None = None,
+                        act: str | None = None):
+    """Gradients of gemm_fused from dy [M,N] and its inputs -> (dx of dy's type
+    [M,K], dalpha fp32 [N], dbias fp32 [N]); dx is the gradient of the token
+    x * s_x, the residual's is dy."""
+    return (_native or _load_native()).gemm_fused_backward(dy, x, s_x, packed, alpha, N, K, bias, _act_code(act))
 
 
 def glu(x: torch.Tensor, s_x: torch.Tensor, packed_gate: torch.Tensor, alpha_gate: torch.Tensor,
@@ -573,48 +520,8 @@ def glu(x: torch.Tensor, s_x: torch.Tensor, packed_gate: torch.Tensor, alpha_gat
     """h[M,N] = act(g) * u with g and u the products of x with the gate and up
     matrices, in one kernel (sherry_glu).  A float32 h is what quantize_act
     takes for the down projection."""
-    L = lib()
-    M, index, px, ps = _tokens(x, s_x, K)
-    pg, pag = _weights(packed_gate, alpha_gate, "_gate", N, K, index)
-    pu, pau = _weights(packed_up, alpha_up, "_up", N, K, index)
-    code, dt = _act_code(act), _dtype_code(dtype)
-    out, ph = _output(out, x, index, M, N, dtype)
-    wp, wn, _ws = _zeroed_workspace(workspace, L.sherry_glu_workspace_bytes(M, N, K), x, index)
-    _call("sherry_glu", index, L.sherry_glu, px, ps, pg, pag, pu, pau, code, ph, dt, M, N, K, wp, wn)
-    return out
-
-
-def _gradient(dy, M: int, N: int, index: int):
-    """(type code, pointer) of an output gradient [M,N]."""
-    if not isinstance(dy, torch.Tensor):
-        raise TypeError("the output gradient must be a torch.Tensor")
-    return _dtype_code(dy.dtype), _matrix(dy, "the output gradient", dy.dtype, index, M, N)
-
-
-def _gradients(x: torch.Tensor, dtype: torch.dtype, M: int, K: int, N: int, scratch_bytes: int):
-    """dx, two fp32 vectors of N, and the scratch memory of a backward pass."""
-    dev = x.device
-    return (torch.empty((M, K), dtype=dtype, device=dev), torch.empty(N, dtype=torch.float32, device=dev),
-            torch.empty(N, dtype=torch.float32, device=dev),
-            torch.empty(scratch_bytes, dtype=torch.uint8, device=dev))
-
-
-def gemm_fused_backward(dy: torch.Tensor, x: torch.Tensor, s_x: torch.Tensor, packed: torch.Tensor,
-                        alpha: torch.Tensor, N: int, K: int, bias: torch.Tensor | None = None,
-                        act: str | None = None):
-    """Gradients of gemm_fused from dy [M,N] and its inputs -> (dx of dy's type
-    [M,K], dalpha fp32 [N], dbias fp32 [N]); dx is the gradient of the token
-    x * s_x, the residual's is dy."""
-    L = lib()
-    M, index, px, ps = _tokens(x, s_x, K)
-    pw, pa = _weights(packed, alpha, "", N, K, index)
-    code, pb = _act_code(act), _vector(bias, "bias", torch.float32, index, N)
-    dt, pdy = _gradient(dy, M, N, index)
-    nbytes = L.sherry_gemm_fused_backward_scratch_bytes(M, N, K, dt)
-    dx, da, db, scratch = _gradients(x, dy.dtype, M, K, N, nbytes)
-    _call("sherry_gemm_fused_backward", index, L.sherry_gemm_fused_backward, pdy, px, ps, pw, pa, pb, code,
-          dx.data_ptr(), da.data_ptr(), db.data_ptr(), dt, M, N, K, scratch.data_ptr(), nbytes)
-    return dx, da, db
+    return (_native or _load_native()).glu(x, s_x, packed_gate, alpha_gate, packed_up, alpha_up, N, K,
+                                           _act_code(act), _dtype_code(dtype), out, workspace)
 
 
 def glu_backward(dh: torch.Tensor, x: torch.Tensor, s_x: torch.Tensor, packed_gate: torch.Tensor,
@@ -623,39 +530,8 @@ def glu_backward(dh: torch.Tensor, x: torch.Tensor, s_x: torch.Tensor, packed_ga
     """Gradients of glu from dh [M,N] and its inputs -> (dx of dh's type [M,K],
     dalpha_gate fp32 [N], dalpha_up fp32 [N]); dx is the gradient of the
     token x * s_x."""
-    L = lib()
-    M, index, px, ps = _tokens(x, s_x, K)
-    pg, pag = _weights(packed_gate, alpha_gate, "_gate", N, K, index)
-    pu, pau = _weights(packed_up, alpha_up, "_up", N, K, index)
-    code = _act_code(act)
-    dt, pdh = _gradient(dh, M, N, index)
-    nbytes = L.sherry_glu_backward_scratch_bytes(M, N, K, dt)
-    dx, dg, du, scratch = _gradients(x, dh.dtype, M, K, N, nbytes)
-    _call("sherry_glu_backward", index, L.sherry_glu_backward, pdh, px, ps, pg, pag, pu, pau, code, dx.data_ptr(),
-          dg.data_ptr(), du.data_ptr(), dt, M, N, K, scratch.data_ptr(), nbytes)
-    return dx, dg, du
-
-
-def _features(x, weight, bias):
-    """(M, K, device index, type code, pointers) of a norm's tokens and vectors."""
-    if not isinstance(x, torch.Tensor):
-        raise TypeError("x must be a torch.Tensor")
-    dt = _dtype_code(x.dtype)
-    px = _dev_tensor(x, "x", x.dtype)
-    if x.dim() != 2:
-        raise RuntimeError("x must be 2-D [M,K]")
-    M, K = x.shape
-    index = x.get_device()
-    return (M, K, index, dt, px, _vector(weight, "weight", torch.float32, index, K),
-            _vector(bias, "bias", torch.float32, index, K))
-
-
-def _stats(stats: bool, M: int, x: torch.Tensor):
-    if not stats:
-        return (), None, None
-    mean = torch.empty(M, dtype=torch.float32, device=x.device)
-    rstd = torch.empty(M, dtype=torch.float32, device=x.device)
-    return (mean, rstd), mean.data_ptr(), rstd.data_ptr()
+    return (_native or _load_native()).glu_backward(dh, x, s_x, packed_gate, alpha_gate, packed_up, alpha_up, N, K,
+                                                    _act_code(act))
 
 
 def layernorm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
@@ -663,11 +539,7 @@ def layernorm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.T
     """Layer norm of each token of x [M,K] (float32, float16 or bfloat16;
     weight and bias fp32 [K]) -> y of x's type, or (y, mean, rstd) with
     `stats` (what layernorm_backward takes).  out may be x."""
-    M, K, index, dt, px, pw, pb = _features(x, weight, bias)
-    out, py = _output(out, x, index, M, K, x.dtype)
-    found, pm, pr = _stats(stats, M, x)
-    _call("sherry_layernorm", index, lib().sherry_layernorm, px, pw, pb, eps, py, pm, pr, dt, M, K)
-    return (out, *found) if stats else out
+    return (_native or _load_native()).layernorm(x, weight, bias, eps, stats, out)
 
 
 def layernorm_quantize(x: torch.Tensor, weight: torch.Tensor | None = None,
@@ -675,30 +547,11 @@ def layernorm_quantize(x: torch.Tensor, weight: torch.Tensor | None = None,
     """Layer norm of each token of x [M,K] straight into the int8 tokens the
     products take -> (q int8 [M,K], s_x fp32 [M]), and mean and rstd with
     `stats`."""
-    M, K, index, dt, px, pw, pb = _features(x, weight, bias)
-    q = torch.empty((M, K), dtype=torch.int8, device=x.device)
-    s = torch.empty(M, dtype=torch.float32, device=x.device)
-    found, pm, pr = _stats(stats, M, x)
-    _call("sherry_layernorm_quantize", index, lib().sherry_layernorm_quantize, px, pw, pb, eps, q.data_ptr(),
-          s.data_ptr(), pm, pr, dt, M, K)
-    return (q, s, *found)
+    return (_native or _load_native()).layernorm_quantize(x, weight, bias, eps, stats)
 
 
 def layernorm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
                        weight: torch.Tensor | None = None, out: torch.Tensor | None = None):
     """Gradients of layernorm -> (dx of x's type, dweight fp32 [K], dbias fp32
     [K]).  out may be dy."""
-    L = lib()
-    M, K, index, dt, px, pw, _ = _features(x, weight, None)
-    pdy = _required(_matrix(dy, "dy", x.dtype, index, M, K), "dy")
-    pm = _required(_vector(mean, "mean", torch.float32, index, M), "mean")
-    pr = _required(_vector(rstd, "rstd", torch.float32, index, M), "rstd")
-    out, pdx = _output(out, x, index, M, K, x.dtype)
-    dev = x.device
-    dw = torch.empty(K, dtype=torch.float32, device=dev)
-    db = torch.empty(K, dtype=torch.float32, device=dev)
-    nbytes = L.sherry_layernorm_backward_scratch_bytes(M, K)
-    scratch = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    _call("sherry_layernorm_backward", index, L.sherry_layernorm_backward, pdy, px, pm, pr, pw, pdx, dw.data_ptr(),
-          db.data_ptr(), dt, M, K, scratch.data_ptr(), nbytes)
-    return out, dw, db
+    return (_native or _load_native()).layernorm_backward(dy, x, mean, rstd, weight, out)

@@ -1,4 +1,5 @@
-"""Build libsherry.so (gfx950) in-tree with hipcc.
+"""Build libsherry.so (gfx950) in-tree with hipcc, and with g++ the Python
+module that marshals the feed-forward operators' tensors.
 
     python -m bit_weight_amd.build
 
@@ -14,6 +15,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import sysconfig
 import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -39,12 +41,30 @@ PRELOAD = {"mfma_gemv.hip": ["-mllvm", "-amdgpu-kernarg-preload-count=8"],
            "pack.hip": ["-mllvm", "-amdgpu-kernarg-preload-count=4"]}
 
 
+# The Python module (host code only): torch's headers and libraries, and the
+# library's functions by address
+BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(HERE, "_binding.so")
+
+
+def binding_command(out: str) -> list[str]:
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "include"), sysconfig.get_paths()["include"]]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *[f"-I{d}" for d in include], BINDING_SOURCE, "-o", out, f"-L{os.path.join(root, 'lib')}",
+            "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python"]
+
+
 def _filter(text: str) -> str:
     return "\n".join(l for l in text.splitlines() if "packed-fp32-ops" not in l)
 
 
 def build(verbose: bool = False) -> str:
-    """Compile every source into libsherry.so (always recompiles)."""
+    """Compile every source into libsherry.so and _binding.so (always recompiles)."""
     tmp = LIB + ".tmp"
     with tempfile.TemporaryDirectory(prefix="sherry_build_") as obj_dir:
         procs = []
@@ -55,6 +75,10 @@ def build(verbose: bool = False) -> str:
                 print(" ".join(cmd), flush=True)
             procs.append((src, obj, subprocess.Popen(cmd, stdout=subprocess.PIPE,
                                                      stderr=subprocess.STDOUT, text=True)))
+        cmd = binding_command(BINDING + ".tmp")
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        binding = subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
         objs = []
         for src, obj, proc in procs:
             out = _filter(proc.communicate()[0])
@@ -67,7 +91,11 @@ def build(verbose: bool = False) -> str:
         res = subprocess.run(cmd, capture_output=True, text=True)
         if res.returncode != 0:
             raise RuntimeError(f"link failed ({res.returncode}):\n{_filter(res.stdout + res.stderr)}")
+        out = binding.communicate()[0]
+        if binding.returncode != 0:
+            raise RuntimeError(f"g++ failed on binding.cpp ({binding.returncode}):\n{out}")
     os.replace(tmp, LIB)
+    os.replace(BINDING + ".tmp", BINDING)
     return LIB
 
 

@@ -1,0 +1,429 @@
+// Argument marshalling of the feed-forward operators: checks torch tensors,
+// allocates outputs and scratch memory and calls the library's C ABI on the
+// current stream of the tokens' device.  It holds no arithmetic.  (A CPython
+// module and not ctypes because a decode step's kernel takes 5 to 10 us: the
+// same checks and calls written in Python take 11 us a call on the host.)
+//
+// setup(functions, workspace, error) gives it the library's entry points as
+// addresses, a callable (device index, bytes, device) -> zeroed workspace
+// tensor and one (status, name) that raises.
+#define PY_SSIZE_T_CLEAN
+#include <Python.h>
+
+#include <ATen/ATen.h>
+#include <c10/core/DeviceGuard.h>
+#include <c10/hip/HIPFunctions.h>
+#include <c10/hip/HIPStream.h>
+#include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <cstdarg>
+#include <cstdint>
+#include <cstring>
+
+#include "../../include/sherry.h"
+
+namespace {
+
+PyObject* g_workspace = nullptr;
+PyObject* g_error = nullptr;
+
+decltype(&sherry_packed_bytes) f_packed_bytes;
+decltype(&sherry_gemm_fused) f_gemm_fused;
+decltype(&sherry_gemm_fused_workspace_bytes) f_gemm_fused_workspace_bytes;
+decltype(&sherry_gemm_fused_backward) f_gemm_fused_backward;
+decltype(&sherry_gemm_fused_backward_scratch_bytes) f_gemm_fused_backward_scratch_bytes;
+decltype(&sherry_glu) f_glu;
+decltype(&sherry_glu_workspace_bytes) f_glu_workspace_bytes;
+decltype(&sherry_glu_backward) f_glu_backward;
+decltype(&sherry_glu_backward_scratch_bytes) f_glu_backward_scratch_bytes;
+decltype(&sherry_layernorm) f_layernorm;
+decltype(&sherry_layernorm_quantize) f_layernorm_quantize;
+decltype(&sherry_layernorm_backward) f_layernorm_backward;
+decltype(&sherry_layernorm_backward_scratch_bytes) f_layernorm_backward_scratch_bytes;
+
+struct Entry {
+  const char* name;
+  void* at;
+};
+const Entry kEntries[] = {
+    {"sherry_packed_bytes", &f_packed_bytes},
+    {"sherry_gemm_fused", &f_gemm_fused},
+    {"sherry_gemm_fused_workspace_bytes", &f_gemm_fused_workspace_bytes},
+    {"sherry_gemm_fused_backward", &f_gemm_fused_backward},
+    {"sherry_gemm_fused_backward_scratch_bytes", &f_gemm_fused_backward_scratch_bytes},
+    {"sherry_glu", &f_glu},
+    {"sherry_glu_workspace_bytes", &f_glu_workspace_bytes},
+    {"sherry_glu_backward", &f_glu_backward},
+    {"sherry_glu_backward_scratch_bytes", &f_glu_backward_scratch_bytes},
+    {"sherry_layernorm", &f_layernorm},
+    {"sherry_layernorm_quantize", &f_layernorm_quantize},
+    {"sherry_layernorm_backward", &f_layernorm_backward},
+    {"sherry_layernorm_backward_scratch_bytes", &f_layernorm_backward_scratch_bytes},
+};
+
+// A Python error is set; unwinds to the method's entry.
+struct Raised {};
+
+[[noreturn]] void fail(PyObject* type, const char* format, ...) {
+  va_list args;
+  va_start(args, format);
+  PyErr_FormatV(type, format, args);
+  va_end(args);
+  throw Raised{};
+}
+
+const char* type_name(at::ScalarType t) { return c10::toString(t); }
+
+const at::Tensor& tensor_of(PyObject* o, const char* name) {
+  if (!THPVariable_Check(o)) fail(PyExc_TypeError, "%s must be a torch.Tensor", name);
+  return THPVariable_Unpack(o);
+}
+
+// A contiguous tensor of type t on a GPU; index >= 0: on that one.
+void check_tensor(const at::Tensor& t, const char* name, at::ScalarType type, int index) {
+  if (t.layout() != at::kStrided) fail(PyExc_RuntimeError, "%s must be a dense tensor", name);
+  if (!t.is_cuda()) fail(PyExc_RuntimeError, "%s must be on a GPU device, got %s", name, t.device().str().c_str());
+  if (t.scalar_type() != type)
+    fail(PyExc_RuntimeError, "%s must be %s, got %s", name, type_name(type), type_name(t.scalar_type()));
+  if (!t.is_contiguous()) fail(PyExc_RuntimeError, "%s must be contiguous", name);
+  if (index >= 0 && t.get_device() != index)
+    fail(PyExc_RuntimeError, "%s must be on cuda:%d, got %s", name, index, t.device().str().c_str());
+}
+
+// Pointer of an operand of n values (None: nullptr where it may be missing).
+void* vector_of(PyObject* o, const char* name, at::ScalarType type, int index, int64_t n, bool optional = false) {
+  if (optional && o == Py_None) return nullptr;
+  const at::Tensor& t = tensor_of(o, name);
+  check_tensor(t, name, type, index);
+  if (t.numel() != n)
+    fail(PyExc_RuntimeError, "%s must hold %lld values, got %lld", name, (long long)n, (long long)t.numel());
+  return t.data_ptr();
+}
+
+void* matrix_of(const at::Tensor& t, const char* name, at::ScalarType type, int index, int64_t M, int64_t N) {
+  check_tensor(t, name, type, index);
+  if (t.dim() != 2 || t.size(0) != M || t.size(1) != N)
+    fail(PyExc_RuntimeError, "%s must be [%lld,%lld]", name, (long long)M, (long long)N);
+  return t.data_ptr();
+}
+
+void* matrix_of(PyObject* o, const char* name, at::ScalarType type, int index, int64_t M, int64_t N,
+                bool optional = false) {
+  if (optional && o == Py_None) return nullptr;
+  return matrix_of(tensor_of(o, name), name, type, index, M, N);
+}
+
+int64_t integer(PyObject* o) {
+  const long long v = PyLong_AsLongLong(o);
+  if (v == -1 && PyErr_Occurred()) throw Raised{};
+  return v;
+}
+
+int dtype_of(at::ScalarType t) {
+  switch (t) {
+    case at::kFloat: return SHERRY_F32;
+    case at::kHalf: return SHERRY_F16;
+    case at::kBFloat16: return SHERRY_BF16;
+    default: fail(PyExc_RuntimeError, "type must be float32, float16 or bfloat16, got %s", type_name(t));
+  }
+}
+
+at::ScalarType scalar_of(int64_t dtype) {
+  return dtype == SHERRY_F32 ? at::kFloat : dtype == SHERRY_F16 ? at::kHalf : at::kBFloat16;
+}
+
+// The tokens x [M,K] (int8) and what follows from them.
+struct Tokens {
+  int64_t M, N, K;
+  int index;
+  at::Device device;
+  const int8_t* x;
+  const float* s_x;
+  Tokens(PyObject* px, PyObject* ps, PyObject* pn, PyObject* pk) : device(at::kCPU) {
+    const at::Tensor& t = tensor_of(px, "x");
+    N = integer(pn);
+    K = integer(pk);
+    check_tensor(t, "x", at::kChar, -1);
+    if (t.dim() != 2 || t.size(1) != K) fail(PyExc_RuntimeError, "x must be [M,%lld]", (long long)K);
+    M = t.size(0);
+    index = (int)t.get_device();
+    device = t.device();
+    x = static_cast<const int8_t*>(t.data_ptr());
+    s_x = static_cast<const float*>(vector_of(ps, "s_x", at::kFloat, index, M));
+  }
+};
+
+struct Weights {
+  const void* packed;
+  const float* alpha;
+  Weights(PyObject* pp, PyObject* pa, const char* packed_name, const char* alpha_name, const Tokens& t) {
+    const size_t bytes = f_packed_bytes(t.N, t.K);
+    if (bytes == 0) {
+      Py_XDECREF(PyObject_CallFunction(g_error, "is", SHERRY_ERR_SHAPE, "weights [N,K]"));
+      throw Raised{};
+    }
+    packed = vector_of(pp, packed_name, at::kByte, t.index, (int64_t)bytes);
+    alpha = static_cast<const float*>(vector_of(pa, alpha_name, at::kFloat, t.index, t.N));
+  }
+};
+
+at::Tensor empty(at::IntArrayRef sizes, at::ScalarType type, at::Device device) {
+  return at::empty(sizes, at::TensorOptions().dtype(type).device(device));
+}
+
+// The output: the caller's, or a new one.
+at::Tensor output_of(PyObject* o, int64_t M, int64_t N, at::ScalarType type, int index, at::Device device) {
+  if (o == Py_None) return empty({M, N}, type, device);
+  const at::Tensor& t = tensor_of(o, "out");
+  matrix_of(t, "out", type, index, M, N);
+  return t;
+}
+
+// Runs `call(stream)` with the device current and reports its status.
+template <typename F>
+void launch(const char* name, int index, F call) {
+  const c10::OptionalDeviceGuard guard(at::Device(at::kCUDA, (c10::DeviceIndex)index));
+  const int status = call(static_cast<void*>(c10::hip::getCurrentHIPStream((c10::DeviceIndex)index).stream()));
+  if (status != SHERRY_OK) {
+    Py_XDECREF(PyObject_CallFunction(g_error, "is", status, name));
+    throw Raised{};
+  }
+}
+
+// The split-K workspace: the caller's tensor, none needed, or the module's.
+struct Workspace {
+  void* at = nullptr;
+  size_t bytes = 0;
+  at::Tensor keep;
+  Workspace(PyObject* o, size_t need, const Tokens& t) {
+    if (o != Py_None) {
+      keep = tensor_of(o, "workspace");
+      check_tensor(keep, "workspace", at::kByte, t.index);
+    } else if (need > 0) {
+      PyObject* w = PyObject_CallFunction(g_workspace, "in", t.index, (Py_ssize_t)need);
+      if (!w) throw Raised{};
+      keep = THPVariable_Unpack(w);
+      Py_DECREF(w);
+    } else {
+      return;
+    }
+    at = keep.data_ptr();
+    bytes = (size_t)keep.numel();
+  }
+};
+
+PyObject* wrap(const at::Tensor& t) { return THPVariable_Wrap(t); }
+
+PyObject* wrap_all(std::initializer_list<at::Tensor> ts) {
+  PyObject* r = PyTuple_New((Py_ssize_t)ts.size());
+  if (!r) throw Raised{};
+  Py_ssize_t i = 0;
+  for (const at::Tensor& t : ts) PyTuple_SET_ITEM(r, i++, THPVariable_Wrap(t));
+  return r;
+}
+
+// Every method: a fixed count of arguments, C++ errors (an allocation's) turned
+// into torch's Python ones.
+template <int kCount, PyObject* (*kBody)(PyObject* const*)>
+PyObject* method(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (n != kCount) {
+    PyErr_Format(PyExc_TypeError, "expected %d arguments, got %zd", kCount, n);
+    return nullptr;
+  }
+  HANDLE_TH_ERRORS
+  try {
+    return kBody(args);
+  } catch (const Raised&) {
+    return nullptr;
+  }
+  END_HANDLE_TH_ERRORS
+}
+
+// x, s_x, packed, alpha, N, K, bias, act, residual, dtype, out, workspace
+PyObject* gemm_fused(PyObject* const* a) {
+  const Tokens t(a[0], a[1], a[4], a[5]);
+  const Weights w(a[2], a[3], "packed", "alpha", t);
+  const int act = (int)integer(a[7]), dtype = (int)integer(a[9]);
+  const at::ScalarType type = scalar_of(dtype);
+  const auto* bias = static_cast<const float*>(vector_of(a[6], "bias", at::kFloat, t.index, t.N, true));
+  const void* residual = matrix_of(a[8], "residual", type, t.index, t.M, t.N, true);
+  const at::Tensor y = output_of(a[10], t.M, t.N, type, t.index, t.device);
+  const Workspace ws(a[11], f_gemm_fused_workspace_bytes(t.M, t.N, t.K), t);
+  launch("sherry_gemm_fused", t.index, [&](void* stream) {
+    return f_gemm_fused(t.x, t.s_x, w.packed, w.alpha, bias, act, residual, y.data_ptr(), dtype, t.M, t.N, t.K,
+                        ws.at, ws.bytes, stream);
+  });
+  return wrap(y);
+}
+
+// dy, x, s_x, packed, alpha, N, K, bias, act
+PyObject* gemm_fused_backward(PyObject* const* a) {
+  const Tokens t(a[1], a[2], a[5], a[6]);
+  const Weights w(a[3], a[4], "packed", "alpha", t);
+  const int act = (int)integer(a[8]);
+  const auto* bias = static_cast<const float*>(vector_of(a[7], "bias", at::kFloat, t.index, t.N, true));
+  const at::Tensor& dy = tensor_of(a[0], "dy");
+  const int dtype = dtype_of(dy.scalar_type());
+  const void* pdy = matrix_of(dy, "dy", dy.scalar_type(), t.index, t.M, t.N);
+  const size_t bytes = f_gemm_fused_backward_scratch_bytes(t.M, t.N, t.K, dtype);
+  const at::Tensor dx = empty({t.M, t.K}, dy.scalar_type(), t.device), da = empty({t.N}, at::kFloat, t.device),
+                   db = empty({t.N}, at::kFloat, t.device), scratch = empty({(int64_t)bytes}, at::kByte, t.device);
+  launch("sherry_gemm_fused_backward", t.index, [&](void* stream) {
+    return f_gemm_fused_backward(pdy, t.x, t.s_x, w.packed, w.alpha, bias, act, dx.data_ptr(),
+                                 da.data_ptr<float>(), db.data_ptr<float>(), dtype, t.M, t.N, t.K,
+                                 scratch.data_ptr(), bytes, stream);
+  });
+  return wrap_all({dx, da, db});
+}
+
+// x, s_x, packed_gate, alpha_gate, packed_up, alpha_up, N, K, act, dtype, out, workspace
+PyObject* glu(PyObject* const* a) {
+  const Tokens t(a[0], a[1], a[6], a[7]);
+  const Weights g(a[2], a[3], "packed_gate", "alpha_gate", t), u(a[4], a[5], "packed_up", "alpha_up", t);
+  const int act = (int)integer(a[8]), dtype = (int)integer(a[9]);
+  const at::Tensor h = output_of(a[10], t.M, t.N, scalar_of(dtype), t.index, t.device);
+  const Workspace ws(a[11], f_glu_workspace_bytes(t.M, t.N, t.K), t);
+  launch("sherry_glu", t.index, [&](void* stream) {
+    return f_glu(t.x, t.s_x, g.packed, g.alpha, u.packed, u.alpha, act, h.data_ptr(), dtype, t.M, t.N, t.K, ws.at,
+                 ws.bytes, stream);
+  });
+  return wrap(h);
+}
+
+// dh, x, s_x, packed_gate, alpha_gate, packed_up, alpha_up, N, K, act
+PyObject* glu_backward(PyObject* const* a) {
+  const Tokens t(a[1], a[2], a[7], a[8]);
+  const Weights g(a[3], a[4], "packed_gate", "alpha_gate", t), u(a[5], a[6], "packed_up", "alpha_up", t);
+  const int act = (int)integer(a[9]);
+  const at::Tensor& dh = tensor_of(a[0], "dh");
+  const int dtype = dtype_of(dh.scalar_type());
+  const void* pdh = matrix_of(dh, "dh", dh.scalar_type(), t.index, t.M, t.N);
+  const size_t bytes = f_glu_backward_scratch_bytes(t.M, t.N, t.K, dtype);
+  const at::Tensor dx = empty({t.M, t.K}, dh.scalar_type(), t.device), dg = empty({t.N}, at::kFloat, t.device),
+                   du = empty({t.N}, at::kFloat, t.device), scratch = empty({(int64_t)bytes}, at::kByte, t.device);
+  launch("sherry_glu_backward", t.index, [&](void* stream) {
+    return f_glu_backward(pdh, t.x, t.s_x, g.packed, g.alpha, u.packed, u.alpha, act, dx.data_ptr(),
+                          dg.data_ptr<float>(), du.data_ptr<float>(), dtype, t.M, t.N, t.K, scratch.data_ptr(),
+                          bytes, stream);
+  });
+  return wrap_all({dx, dg, du});
+}
+
+// The tokens x [M,K] of a norm (float32, float16 or bfloat16).
+struct Features {
+  int64_t M, K;
+  int index, dtype;
+  at::ScalarType type;
+  at::Device device;
+  const void* x;
+  explicit Features(PyObject* px) : device(at::kCPU) {
+    const at::Tensor& t = tensor_of(px, "x");
+    type = t.scalar_type();
+    dtype = dtype_of(type);
+    check_tensor(t, "x", type, -1);
+    if (t.dim() != 2) fail(PyExc_RuntimeError, "x must be 2-D [M,K]");
+    M = t.size(0);
+    K = t.size(1);
+    index = (int)t.get_device();
+    device = t.device();
+    x = t.data_ptr();
+  }
+};
+
+struct Stats {
+  at::Tensor mean, rstd;
+  float* pm = nullptr;
+  float* pr = nullptr;
+  Stats(PyObject* wanted, const Features& f) {
+    if (!PyObject_IsTrue(wanted)) return;
+    mean = empty({f.M}, at::kFloat, f.device);
+    rstd = empty({f.M}, at::kFloat, f.device);
+    pm = mean.data_ptr<float>();
+    pr = rstd.data_ptr<float>();
+  }
+};
+
+float number(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw Raised{};
+  return (float)v;
+}
+
+// x, weight, bias, eps, stats, out
+PyObject* layernorm(PyObject* const* a) {
+  const Features f(a[0]);
+  const auto* w = static_cast<const float*>(vector_of(a[1], "weight", at::kFloat, f.index, f.K, true));
+  const auto* b = static_cast<const float*>(vector_of(a[2], "bias", at::kFloat, f.index, f.K, true));
+  const float eps = number(a[3]);
+  const at::Tensor y = output_of(a[5], f.M, f.K, f.type, f.index, f.device);
+  const Stats s(a[4], f);
+  launch("sherry_layernorm", f.index, [&](void* stream) {
+    return f_layernorm(f.x, w, b, eps, y.data_ptr(), s.pm, s.pr, f.dtype, f.M, f.K, stream);
+  });
+  return s.pm ? wrap_all({y, s.mean, s.rstd}) : wrap(y);
+}
+
+// x, weight, bias, eps, stats
+PyObject* layernorm_quantize(PyObject* const* a) {
+  const Features f(a[0]);
+  const auto* w = static_cast<const float*>(vector_of(a[1], "weight", at::kFloat, f.index, f.K, true));
+  const auto* b = static_cast<const float*>(vector_of(a[2], "bias", at::kFloat, f.index, f.K, true));
+  const float eps = number(a[3]);
+  const at::Tensor q = empty({f.M, f.K}, at::kChar, f.device), s_x = empty({f.M}, at::kFloat, f.device);
+  const Stats s(a[4], f);
+  launch("sherry_layernorm_quantize", f.index, [&](void* stream) {
+    return f_layernorm_quantize(f.x, w, b, eps, static_cast<int8_t*>(q.data_ptr()), s_x.data_ptr<float>(), s.pm,
+                                s.pr, f.dtype, f.M, f.K, stream);
+  });
+  return s.pm ? wrap_all({q, s_x, s.mean, s.rstd}) : wrap_all({q, s_x});
+}
+
+// dy, x, mean, rstd, weight, out
+PyObject* layernorm_backward(PyObject* const* a) {
+  const Features f(a[1]);
+  const void* dy = matrix_of(a[0], "dy", f.type, f.index, f.M, f.K);
+  const auto* mean = static_cast<const float*>(vector_of(a[2], "mean", at::kFloat, f.index, f.M));
+  const auto* rstd = static_cast<const float*>(vector_of(a[3], "rstd", at::kFloat, f.index, f.M));
+  const auto* w = static_cast<const float*>(vector_of(a[4], "weight", at::kFloat, f.index, f.K, true));
+  const at::Tensor dx = output_of(a[5], f.M, f.K, f.type, f.index, f.device);
+  const size_t bytes = f_layernorm_backward_scratch_bytes(f.M, f.K);
+  const at::Tensor dw = empty({f.K}, at::kFloat, f.device), db = empty({f.K}, at::kFloat, f.device),
+                   scratch = empty({(int64_t)bytes}, at::kByte, f.device);
+  launch("sherry_layernorm_backward", f.index, [&](void* stream) {
+    return f_layernorm_backward(dy, f.x, mean, rstd, w, dx.data_ptr(), dw.data_ptr<float>(), db.data_ptr<float>(),
+                                f.dtype, f.M, f.K, scratch.data_ptr(), bytes, stream);
+  });
+  return wrap_all({dx, dw, db});
+}
+
+// functions (dict of name -> address), workspace, error
+PyObject* setup(PyObject* const* a) {
+  for (const Entry& e : kEntries) {
+    PyObject* v = PyDict_GetItemString(a[0], e.name);
+    if (!v) fail(PyExc_KeyError, "%s", e.name);
+    void* p = PyLong_AsVoidPtr(v);
+    if (!p) {
+      if (PyErr_Occurred()) throw Raised{};
+      fail(PyExc_ValueError, "%s has no address", e.name);
+    }
+    std::memcpy(e.at, &p, sizeof p);
+  }
+  Py_INCREF(a[1]);
+  Py_XSETREF(g_workspace, a[1]);
+  Py_INCREF(a[2]);
+  Py_XSETREF(g_error, a[2]);
+  Py_RETURN_NONE;
+}
+
+#define SHERRY_METHOD(name, count) \
+  {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&method<count, name>)), METH_FASTCALL, nullptr}
+PyMethodDef kMethods[] = {
+    SHERRY_METHOD(setup, 3),           SHERRY_METHOD(gemm_fused, 12),        SHERRY_METHOD(gemm_fused_backward, 9),
+    SHERRY_METHOD(glu, 12),            SHERRY_METHOD(glu_backward, 10),      SHERRY_METHOD(layernorm, 6),
+    SHERRY_METHOD(layernorm_quantize, 5), SHERRY_METHOD(layernorm_backward, 6), {nullptr, nullptr, 0, nullptr}};
+PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&kModule); }
