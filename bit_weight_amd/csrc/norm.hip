@@ -7,12 +7,13 @@
 //   dw = sum over tokens of dy xh, db = sum over tokens of dy.
 // All of them stream their inputs once; memory bandwidth bounds them.
 //
-// A group of W waves (1 to 4, or 16 above 16384 features in the forward)
-// holds one token in registers, so the mean and the sum of squared
-// differences from it are taken in two passes without reading x again: the
-// variance has no cancellation.  W is the least that needs at most 64 (fp32
-// sums) values a lane; lane l of the group takes features 4 (l + 64 W j) ..
-// + 3, so every load instruction reads whole lines.
+// A group of W waves holds one token in registers, so the mean and the sum of
+// squared differences from it are taken in two passes without reading x
+// again: the variance has no cancellation.  Lane l of the group takes
+// features V (l + 64 W j) .. + V - 1: 16 bytes a load (8 where K is no
+// multiple of 8 in a 16-bit type).  Groups go on to further tokens, the next
+// one's loads in flight, and keep w (and b) in registers: read again for
+// every token they are as many bytes as x and dy together.
 #include "sherry_device.h"
 #include "sherry_launch.h"
 #include "sherry_types.h"
@@ -20,11 +21,11 @@
 namespace sherry {
 namespace {
 
-constexpr int kNormThreads = 256;         // forward: 4 waves, 4 / W tokens per workgroup
-constexpr int kLoopThreads = 1024;        // forward above kNormMaxK: one token per workgroup, in loops
+constexpr int kLoopThreads = 1024;        // above kNormMaxK: one token per workgroup, in loops
 constexpr int kBackThreads = 512;         // backward: 8 waves, 8 / W tokens at a time
-constexpr int kNormMaxK = 16384;          // features held in registers by 4 waves
-constexpr int kBackBlocks = 2 * kCUs;     // most workgroups (rows of partial weight gradients)
+constexpr int kNormMaxK = 16384;          // features held in registers
+constexpr int kNormGroups = 4;            // forward: workgroups of 256 threads per CU before tokens are taken in turns
+constexpr int kBackBlocks = kCUs;         // most workgroups (rows of partial weight gradients)
 
 // Sum (or maximum) over the W waves that share a token; `slot` is this
 // wave's place in `red`, whose W entries from the token's first on hold the
@@ -75,6 +76,31 @@ struct NormArgs {
   int M, K;
 };
 
+// V consecutive features: as loaded, and as fp32.
+template <typename T, int V>
+using Raw = T __attribute__((ext_vector_type(V)));
+template <int V>
+using Vec = float __attribute__((ext_vector_type(V)));
+
+template <typename T, int V>
+__device__ __forceinline__ Raw<T, V> load_raw(const T* p, bool in) {
+  Raw<T, V> r{};
+  if (in) r = *reinterpret_cast<const Raw<T, V>*>(p);
+  return r;
+}
+
+template <int V>
+__device__ __forceinline__ Vec<V> load_vec(const float* p, bool in, float otherwise) {
+  Vec<V> r;
+#pragma unroll
+  for (int i = 0; i < V; i += 4) {
+    const f4 v = in ? load4(p + i) : f4{otherwise, otherwise, otherwise, otherwise};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) r[i + c] = v[c];
+  }
+  return r;
+}
+
 // y = (d rstd) w + b of four features, in type S.
 template <typename S>
 __device__ __forceinline__ void normed4(const S (&d)[4], S rstd, const NormArgs& a, int k, S (&v)[4]) {
@@ -84,95 +110,115 @@ __device__ __forceinline__ void normed4(const S (&d)[4], S rstd, const NormArgs&
   for (int i = 0; i < 4; ++i) v[i] = d[i] * rstd * (S)w[i] + (S)b[i];
 }
 
-__device__ __forceinline__ uint32_t quant4_at(const double (&v)[4], double s) {
-  uint32_t r = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    r |= (uint32_t)(uint8_t)(int8_t)fmin(fmax(rint(v[i] / s), -127.0), 127.0) << (8 * i);
-  return r;
+// One int8 step count; clamped, and a NaN (not accepted) becomes 0.
+__device__ __forceinline__ uint32_t quant_at(double v, double s) {
+  return (uint32_t)(uint8_t)(int8_t)fmin(fmax(rint(v / s), -127.0), 127.0);
 }
 
 // The forward on tokens that fit registers.  Q: int8 output; then everything
 // from the mean on is computed in 64 bits, so that a value next to a border
 // between two int8 steps falls where exact arithmetic puts it (in 32 bits
 // about one value in 1e5 lands on the other side); S is the sums' type.
-template <typename T, int W, int J, bool Q>
-__global__ __launch_bounds__(kNormThreads) void norm_kernel(NormArgs a) {
+template <typename T, int V, int W, int J, bool Q>
+__global__ __launch_bounds__(W == 16 ? 1024 : 256) void norm_kernel(NormArgs a) {
   using S = std::conditional_t<Q, double, float>;
-  constexpr int G = kNormThreads / 64 / W;   // tokens per workgroup
-  __shared__ S red[3][kNormThreads / 64];
+  constexpr int kThreads = W == 16 ? 1024 : 256;
+  constexpr int G = kThreads / 64 / W;   // tokens at a time
+  __shared__ S red[2][3][kThreads / 64];
   const int wave = threadIdx.x >> 6;
   const int lane = threadIdx.x % (64 * W);
-  const int m = blockIdx.x * G + wave / W;
-  const bool live = m < a.M;                  // the last workgroup's waves past M only join the barriers
-  const T* x = static_cast<const T*>(a.x) + (size_t)(live ? m : 0) * a.K;
   const auto add = [](S p, S q) { return p + q; };
   const auto top = [](S p, S q) { return p > q ? p : q; };
-  f4 xv[J];
+  auto feature = [&](int j) { return V * (lane + 64 * W * j); };
+  auto load = [&](int m, Raw<T, V> (&r)[J]) {
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      r[j] = load_raw<T, V>(static_cast<const T*>(a.x) + (size_t)m * a.K + feature(j), m < a.M && feature(j) < a.K);
+  };
+  Raw<T, V> next[J];
+  load(blockIdx.x * G + wave / W, next);
+  Vec<V> w[J], b[J];
 #pragma unroll
   for (int j = 0; j < J; ++j) {
-    const int k = 4 * (lane + 64 * W * j);
-    xv[j] = live && k < a.K ? load4(x + k) : f4{0.0f, 0.0f, 0.0f, 0.0f};
+    w[j] = load_vec<V>(a.w + feature(j), a.w && feature(j) < a.K, 1.0f);
+    b[j] = load_vec<V>(a.b + feature(j), a.b && feature(j) < a.K, 0.0f);
   }
-  S sum = 0;
+  // the same number of trips for every wave of the workgroup (barriers)
+  int turn = 0;
+  for (int m0 = blockIdx.x * G; m0 < a.M; m0 += gridDim.x * G, turn ^= 1) {
+    const int m = m0 + wave / W;
+    const bool live = m < a.M;
+    Vec<V> xv[J];
 #pragma unroll
-  for (int j = 0; j < J; ++j) sum += ((S)xv[j][0] + (S)xv[j][1]) + ((S)xv[j][2] + (S)xv[j][3]);
-  const S mean = group_join<W>((S)wave_total(sum), red[0], wave, add) / (S)a.K;
-  S sq = 0;
+    for (int j = 0; j < J; ++j) xv[j] = __builtin_convertvector(next[j], Vec<V>);
+    if (m0 + (int)gridDim.x * G < a.M) load(m + gridDim.x * G, next);
+    S sum = 0;
 #pragma unroll
-  for (int j = 0; j < J; ++j) {
-    if (4 * (lane + 64 * W * j) < a.K) {
+    for (int j = 0; j < J; ++j) {
+      S part = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const S d = (S)xv[j][i] - mean;
-        sq += d * d;
+      for (int i = 0; i < V; ++i) part += (S)xv[j][i];
+      sum += part;
+    }
+    const S mean = group_join<W>((S)wave_total(sum), red[turn][0], wave, add) / (S)a.K;
+    S sq = 0;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      if (feature(j) < a.K) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const S d = (S)xv[j][i] - mean;
+          sq += d * d;
+        }
       }
     }
-  }
-  const S var = group_join<W>((S)wave_total(sq), red[1], wave, add) / (S)a.K;
-  const S rstd = (S)1 / sqrt(var + (S)a.eps);
-  if (a.mean && live && lane == 0) {
-    a.mean[m] = (float)mean;
-    a.rstd[m] = (float)rstd;
-  }
-  if constexpr (!Q) {
-    if (!live) return;
-    T* y = static_cast<T*>(a.y) + (size_t)m * a.K;
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const int k = 4 * (lane + 64 * W * j);
-      if (k >= a.K) continue;
-      const S d[4] = {xv[j][0] - mean, xv[j][1] - mean, xv[j][2] - mean, xv[j][3] - mean};
-      S v[4];
-      normed4(d, rstd, a, k, v);
-      store4(y + k, f4{v[0], v[1], v[2], v[3]});
+    const S var = group_join<W>((S)wave_total(sq), red[turn][1], wave, add) / (S)a.K;
+    const S rstd = (S)1 / sqrt(var + (S)a.eps);
+    if (a.mean && live && lane == 0) {
+      a.mean[m] = (float)mean;
+      a.rstd[m] = (float)rstd;
     }
-  } else {
-    S amax = 0;
+    S v[J][V];
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const int k = 4 * (lane + 64 * W * j);
-      if (k >= a.K) continue;
-      const S d[4] = {xv[j][0] - mean, xv[j][1] - mean, xv[j][2] - mean, xv[j][3] - mean};
-      S v[4];
-      normed4(d, rstd, a, k, v);
+    for (int j = 0; j < J; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) amax = fmax(amax, fabs(v[i]));
-    }
-    amax = group_join<W>((S)wave_top(amax), red[2], wave, top);
-    // the scale is the fp32 the product reads; the steps are counted in it
-    const float s = (float)(amax / 127.0) > 0.0f ? (float)(amax / 127.0) : 1.0f;
-    if (!live) return;
-    if (lane == 0) a.s[m] = s;
-    uint32_t* q = reinterpret_cast<uint32_t*>(a.q + (size_t)m * a.K);
+      for (int i = 0; i < V; ++i) v[j][i] = ((S)xv[j][i] - mean) * rstd * (S)w[j][i] + (S)b[j][i];
+    if constexpr (!Q) {
+      T* y = static_cast<T*>(a.y) + (size_t)m * a.K;
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const int k = 4 * (lane + 64 * W * j);
-      if (k >= a.K) continue;
-      const S d[4] = {xv[j][0] - mean, xv[j][1] - mean, xv[j][2] - mean, xv[j][3] - mean};
-      S v[4];
-      normed4(d, rstd, a, k, v);
-      q[k / 4] = quant4_at(v, (S)s);
+      for (int j = 0; j < J; ++j) {
+        Vec<V> o;
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] = v[j][i];
+        if (live && feature(j) < a.K)
+          *reinterpret_cast<Raw<T, V>*>(y + feature(j)) = __builtin_convertvector(o, Raw<T, V>);
+      }
+    } else {
+      S amax = 0;
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        if (feature(j) < a.K) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) amax = fmax(amax, fabs(v[j][i]));
+        }
+      }
+      amax = group_join<W>((S)wave_top(amax), red[turn][2], wave, top);
+      // the scale is the fp32 the product reads; the steps are counted in it
+      const float s = (float)(amax / 127.0) > 0.0f ? (float)(amax / 127.0) : 1.0f;
+      if (live && lane == 0) a.s[m] = s;
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        uint32_t q[V / 4];
+#pragma unroll
+        for (int i = 0; i < V; i += 4)
+          q[i / 4] = quant_at(v[j][i], (S)s) | quant_at(v[j][i + 1], (S)s) << 8 | quant_at(v[j][i + 2], (S)s) << 16 |
+                     quant_at(v[j][i + 3], (S)s) << 24;
+        if (live && feature(j) < a.K) {
+          uint32_t* out = reinterpret_cast<uint32_t*>(a.q + (size_t)m * a.K + feature(j));   // 4-byte aligned
+#pragma unroll
+          for (int i = 0; i < V / 4; ++i) out[i] = q[i];
+        }
+      }
     }
   }
 }
@@ -232,7 +278,7 @@ __global__ __launch_bounds__(kLoopThreads) void norm_loop_kernel(NormArgs a) {
     uint32_t* q = reinterpret_cast<uint32_t*>(a.q + (size_t)m * a.K);
     for (int k = 4 * threadIdx.x; k < a.K; k += 4 * kLoopThreads) {
       value(k, v);
-      q[k / 4] = quant4_at(v, (S)s);
+      q[k / 4] = quant_at(v[0], (S)s) | quant_at(v[1], (S)s) << 8 | quant_at(v[2], (S)s) << 16 | quant_at(v[3], (S)s) << 24;
     }
   }
 }
@@ -252,88 +298,114 @@ struct NormBackArgs {
 // group, group + groups, ... and keeps its sums of dw and db over them in
 // registers; the workgroup adds its groups through LDS at the end and
 // writes one row of partial sums, so no atomics and a fixed order.
-template <typename T, int W, int J>
+template <typename T, int V, int W, int J>
 __global__ __launch_bounds__(kBackThreads) void norm_backward_kernel(NormBackArgs a) {
   constexpr int G = kBackThreads / 64 / W;
-  __shared__ float red[2][2][kBackThreads / 64];
-  __shared__ f4 col[kBackThreads];
+  __shared__ float2 red[2][kBackThreads / 64];
+  __shared__ Vec<V> col[kBackThreads];
   const int wave = threadIdx.x >> 6;
   const int lane = threadIdx.x % (64 * W);
   const int group = wave / W;
-  const auto add = [](float p, float q) { return p + q; };
   const float inv_k = 1.0f / (float)a.K;
-  f4 dw[J], db[J];
+  auto feature = [&](int j) { return V * (lane + 64 * W * j); };
+  struct Token {
+    Raw<T, V> x[J], dy[J];
+    float mean, rstd;
+  };
+  auto load = [&](int m, Token& t) {
+    const bool live = m < a.M;
+    const size_t row = (size_t)m * a.K;
 #pragma unroll
-  for (int j = 0; j < J; ++j) dw[j] = db[j] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < J; ++j) {
+      const bool in = live && feature(j) < a.K;
+      t.x[j] = load_raw<T, V>(static_cast<const T*>(a.x) + row + feature(j), in);
+      t.dy[j] = load_raw<T, V>(static_cast<const T*>(a.dy) + row + feature(j), in);
+    }
+    t.mean = live ? a.mean[m] : 0.0f;
+    t.rstd = live ? a.rstd[m] : 0.0f;
+  };
+  Token next;
+  load(blockIdx.x * G + group, next);
+  Vec<V> w[J], dw[J], db[J];
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    w[j] = load_vec<V>(a.w + feature(j), a.w && feature(j) < a.K, 1.0f);
+    dw[j] = db[j] = Vec<V>{};
+  }
   // every wave of the workgroup makes the same number of trips (barriers)
   int turn = 0;
   for (int m0 = blockIdx.x * G; m0 < a.M; m0 += gridDim.x * G, turn ^= 1) {
     const int m = m0 + group;
-    const bool live = m < a.M;
-    const size_t row = (size_t)(live ? m : 0) * a.K;
-    const T* x = static_cast<const T*>(a.x) + row;
-    const T* dy = static_cast<const T*>(a.dy) + row;
-    const float mean = live ? a.mean[m] : 0.0f, rstd = live ? a.rstd[m] : 0.0f;
-    f4 xh[J], g[J];
+    const float mean = next.mean, rstd = next.rstd;
+    Vec<V> xh[J], g[J];
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      const int k = 4 * (lane + 64 * W * j);
-      const bool in = live && k < a.K;
-      xh[j] = in ? load4(x + k) : f4{mean, mean, mean, mean};
-      g[j] = in ? load4(dy + k) : f4{0.0f, 0.0f, 0.0f, 0.0f};
+      xh[j] = __builtin_convertvector(next.x[j], Vec<V>);
+      g[j] = __builtin_convertvector(next.dy[j], Vec<V>);
     }
+    if (m0 + (int)gridDim.x * G < a.M) load(m + gridDim.x * G, next);
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      const int k = 4 * (lane + 64 * W * j);
-      const f4 w = a.w && k < a.K ? load4(a.w + k) : f4{1.0f, 1.0f, 1.0f, 1.0f};
+      const bool in = feature(j) < a.K;   // past K: dy is 0, and xh is made 0
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        xh[j][i] = (xh[j][i] - mean) * rstd;
+      for (int i = 0; i < V; ++i) {
+        xh[j][i] = in ? (xh[j][i] - mean) * rstd : 0.0f;
         dw[j][i] += g[j][i] * xh[j][i];
         db[j][i] += g[j][i];
-        g[j][i] *= w[i];
+        g[j][i] *= w[j][i];
         s1 += g[j][i];
         s2 += g[j][i] * xh[j][i];
       }
     }
-    s1 = group_join<W>(wave_sum(s1), red[turn][0], wave, add) * inv_k;
-    s2 = group_join<W>(wave_sum(s2), red[turn][1], wave, add) * inv_k;
-    if (live) {
-      T* dx = static_cast<T*>(a.dx) + row;
+    s1 = wave_sum(s1);
+    s2 = wave_sum(s2);
+    if constexpr (W > 1) {
+      if ((threadIdx.x & 63) == 0) red[turn][wave] = make_float2(s1, s2);
+      __syncthreads();
+      s1 = s2 = 0.0f;
 #pragma unroll
-      for (int j = 0; j < J; ++j) {
-        const int k = 4 * (lane + 64 * W * j);
-        if (k >= a.K) continue;
-        f4 v;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = rstd * (g[j][i] - s1 - xh[j][i] * s2);
-        store4(dx + k, v);
+      for (int i = 0; i < W; ++i) {
+        const float2 r = red[turn][group * W + i];
+        s1 += r.x;
+        s2 += r.y;
       }
+    }
+    s1 *= inv_k;
+    s2 *= inv_k;
+    T* dx = static_cast<T*>(a.dx) + (size_t)m * a.K;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      Vec<V> v;
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = rstd * (g[j][i] - s1 - xh[j][i] * s2);
+      if (m < a.M && feature(j) < a.K)
+        *reinterpret_cast<Raw<T, V>*>(dx + feature(j)) = __builtin_convertvector(v, Raw<T, V>);
     }
   }
   // the groups' sums of each column, joined through LDS one j at a time
   float* part = a.part + (size_t)blockIdx.x * 2 * a.K;
 #pragma unroll
   for (int j = 0; j < J; ++j) {
-    const int k = 4 * (lane + 64 * W * j);
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
       __syncthreads();
       col[threadIdx.x] = which ? db[j] : dw[j];
       __syncthreads();
-      if (group == 0 && k < a.K) {
-        f4 t = col[lane];
+      if (group == 0 && feature(j) < a.K) {
+        Vec<V> t = col[lane];
 #pragma unroll
         for (int gg = 1; gg < G; ++gg) t += col[gg * 64 * W + lane];
-        store4(part + (size_t)which * a.K + k, t);
+#pragma unroll
+        for (int i = 0; i < V; i += 4)
+          store4(part + (size_t)which * a.K + feature(j) + i, f4{t[i], t[i + 1], t[i + 2], t[i + 3]});
       }
     }
   }
 }
 
 // Gradients on longer tokens: dx by one workgroup per token that reads it
-// twice, ...
+// twice, and before it (it may overwrite dy) ...
 template <typename T>
 __global__ __launch_bounds__(kLoopThreads) void norm_backward_dx_kernel(NormBackArgs a) {
   constexpr int W = kLoopThreads / 64;
@@ -368,7 +440,7 @@ __global__ __launch_bounds__(kLoopThreads) void norm_backward_dx_kernel(NormBack
   }
 }
 
-// ... and partial dw, db by workgroups that each take 1024 columns (grid x)
+// ... partial dw, db by workgroups that each take 1024 columns (grid x)
 // of a share of the tokens (grid y).
 template <typename T>
 __global__ __launch_bounds__(256) void norm_backward_columns_kernel(NormBackArgs a) {
@@ -386,21 +458,21 @@ __global__ __launch_bounds__(256) void norm_backward_columns_kernel(NormBackArgs
   store4(part + a.K + k, db);
 }
 
-// Sums of the partial rows: 64 columns x 4 shares of the rows per workgroup.
-__global__ __launch_bounds__(256) void norm_columns_kernel(const float* part, int rows, int K, float* dw,
-                                                           float* db) {
-  __shared__ float red[4][64];
+// Sums of the partial rows: 64 columns x 16 shares of the rows per workgroup.
+__global__ __launch_bounds__(1024) void norm_columns_kernel(const float* part, int rows, int K, float* dw,
+                                                            float* db) {
+  __shared__ float red[16][64];
   const int lane = threadIdx.x & 63, share = threadIdx.x >> 6;
   const int k = blockIdx.x * 64 + lane;      // of 2 K: dw's columns, then db's
   float t = 0.0f;
   if (k < 2 * K) {
 #pragma unroll 8
-    for (int r = share; r < rows; r += 4) t += part[(size_t)r * 2 * K + k];
+    for (int r = share; r < rows; r += 16) t += part[(size_t)r * 2 * K + k];
   }
   red[share][lane] = t;
   __syncthreads();
   if (share == 0 && k < 2 * K) {
-    t = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+    for (int i = 1; i < 16; ++i) t += red[i][lane];
     if (k < K) {
       if (dw) dw[k] = t;
     } else if (db) {
@@ -409,54 +481,92 @@ __global__ __launch_bounds__(256) void norm_columns_kernel(const float* part, in
   }
 }
 
-template <typename T, bool Q>
+template <typename T, int V, int W, int J, bool Q>
+void launch_norm_tokens(const NormArgs& a, hipStream_t stream) {
+  constexpr int kThreads = W == 16 ? 1024 : 256, G = kThreads / 64 / W;
+  const int need = (a.M + G - 1) / G, most = kNormGroups * kCUs * 256 / kThreads;
+  hipLaunchKernelGGL((norm_kernel<T, V, W, J, Q>), dim3(need < most ? need : most), dim3(kThreads), 0, stream, a);
+}
+
+// W: 1 wave up to 1024 features; above, 4, or 16 where the tokens are too few
+// to fill the GPU with 4 each (at most kCUs of them).
+template <typename T, int V, bool Q>
 hipError_t launch_norm_as(const NormArgs& a, hipStream_t stream) {
-#define SHERRY_NORM(W_, J_) \
-  hipLaunchKernelGGL((norm_kernel<T, W_, J_, Q>), dim3((a.M + 4 / W_ - 1) / (4 / W_)), dim3(kNormThreads), 0, stream, a)
-  if (a.K <= 256) SHERRY_NORM(1, 1);
-  else if (a.K <= 512) SHERRY_NORM(1, 2);
-  else if (a.K <= 1024) SHERRY_NORM(1, 4);
-  else if (a.K <= 2048) SHERRY_NORM(4, 2);
-  else if (a.K <= 4096) SHERRY_NORM(4, 4);
-  else if (a.K <= 8192) SHERRY_NORM(4, 8);
-  else if (a.K <= kNormMaxK) SHERRY_NORM(4, 16);
-  else hipLaunchKernelGGL((norm_loop_kernel<T, Q>), dim3(a.M), dim3(kLoopThreads), 0, stream, a);
-#undef SHERRY_NORM
+  const int chunks = (a.K + V - 1) / V;   // of V features
+  const bool few = a.M <= kCUs;
+  if (a.K <= 1024) {
+    if (chunks <= 64) launch_norm_tokens<T, V, 1, 1, Q>(a, stream);
+    else if (chunks <= 128) launch_norm_tokens<T, V, 1, 2, Q>(a, stream);
+    else if constexpr (V == 4) launch_norm_tokens<T, V, 1, 4, Q>(a, stream);
+  } else if (few && V == 16 / (int)sizeof(T) && a.K <= kNormMaxK) {
+    if constexpr (V == 16 / sizeof(T)) {
+      if (chunks <= 1024) launch_norm_tokens<T, V, 16, 1, Q>(a, stream);
+      else if (chunks <= 2048) launch_norm_tokens<T, V, 16, 2, Q>(a, stream);
+      else if constexpr (V == 4) launch_norm_tokens<T, V, 16, 4, Q>(a, stream);
+    }
+  } else if (a.K <= kNormMaxK) {
+    if (chunks <= 256) launch_norm_tokens<T, V, 4, 1, Q>(a, stream);
+    else if (chunks <= 512) launch_norm_tokens<T, V, 4, 2, Q>(a, stream);
+    else if (chunks <= 1024) launch_norm_tokens<T, V, 4, 4, Q>(a, stream);
+    else if (chunks <= 2048) launch_norm_tokens<T, V, 4, 8, Q>(a, stream);
+    else if constexpr (V == 4) launch_norm_tokens<T, V, 4, 16, Q>(a, stream);
+  } else {
+    hipLaunchKernelGGL((norm_loop_kernel<T, Q>), dim3(a.M), dim3(kLoopThreads), 0, stream, a);
+  }
   return hipGetLastError();
 }
 
-template <typename T>
+// 16 bytes a load where the rows allow it.
+template <typename T, bool Q>
+hipError_t launch_norm_type(const NormArgs& a, hipStream_t stream) {
+  if constexpr (sizeof(T) == 2) {
+    if (a.K % 8 == 0) return launch_norm_as<T, 8, Q>(a, stream);
+  }
+  return launch_norm_as<T, 4, Q>(a, stream);
+}
+
+// Waves per token of the backward.
+int back_waves(int K) { return K <= 2048 ? 1 : K <= 4096 ? 2 : K <= 8192 ? 4 : 8; }
+
+template <typename T, int V>
 hipError_t launch_norm_backward_as(const NormBackArgs& a, int blocks, hipStream_t stream) {
 #define SHERRY_NORM_BACK(W_, J_) \
-  hipLaunchKernelGGL((norm_backward_kernel<T, W_, J_>), dim3(blocks), dim3(kBackThreads), 0, stream, a)
-  if (a.K <= 256) SHERRY_NORM_BACK(1, 1);
-  else if (a.K <= 512) SHERRY_NORM_BACK(1, 2);
+  hipLaunchKernelGGL((norm_backward_kernel<T, V, W_, J_ * 4 / V>), dim3(blocks), dim3(kBackThreads), 0, stream, a)
+  if (a.K <= 512) SHERRY_NORM_BACK(1, 2);
   else if (a.K <= 1024) SHERRY_NORM_BACK(1, 4);
   else if (a.K <= 2048) SHERRY_NORM_BACK(1, 8);
   else if (a.K <= 4096) SHERRY_NORM_BACK(2, 8);
   else if (a.K <= 8192) SHERRY_NORM_BACK(4, 8);
-  else if (a.K <= kNormMaxK) SHERRY_NORM_BACK(8, 8);
-  else {
-    hipLaunchKernelGGL(norm_backward_dx_kernel<T>, dim3(a.M), dim3(kLoopThreads), 0, stream, a);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(norm_backward_columns_kernel<T>, dim3((a.K + 1023) / 1024, blocks), dim3(256), 0, stream, a);
-  }
+  else SHERRY_NORM_BACK(8, 8);
 #undef SHERRY_NORM_BACK
   return hipGetLastError();
 }
 
-int back_waves(int K) { return K <= 2048 ? 1 : K <= 4096 ? 2 : K <= 8192 ? 4 : 8; }
+template <typename T>
+hipError_t launch_norm_backward_type(const NormBackArgs& a, int blocks, hipStream_t stream) {
+  if (a.K > kNormMaxK) {
+    // (the columns first: dx may be dy)
+    hipLaunchKernelGGL(norm_backward_columns_kernel<T>, dim3((a.K + 1023) / 1024, blocks), dim3(256), 0, stream, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(norm_backward_dx_kernel<T>, dim3(a.M), dim3(kLoopThreads), 0, stream, a);
+    return hipGetLastError();
+  }
+  if constexpr (sizeof(T) == 2) {
+    if (a.K % 8 == 0) return launch_norm_backward_as<T, 8>(a, blocks, stream);
+  }
+  return launch_norm_backward_as<T, 4>(a, blocks, stream);
+}
 
 }  // namespace
 
 hipError_t launch_layernorm(const void* x, const float* w, const float* b, float eps, void* y, int8_t* q,
                             float* s, float* mean, float* rstd, int dtype, int M, int K, hipStream_t stream) {
   const NormArgs a{x, w, b, y, q, s, mean, rstd, eps, M, K};
-  if (dtype == SHERRY_F32) return q ? launch_norm_as<float, true>(a, stream) : launch_norm_as<float, false>(a, stream);
+  if (dtype == SHERRY_F32) return q ? launch_norm_type<float, true>(a, stream) : launch_norm_type<float, false>(a, stream);
   if (dtype == SHERRY_F16)
-    return q ? launch_norm_as<_Float16, true>(a, stream) : launch_norm_as<_Float16, false>(a, stream);
-  return q ? launch_norm_as<__bf16, true>(a, stream) : launch_norm_as<__bf16, false>(a, stream);
+    return q ? launch_norm_type<_Float16, true>(a, stream) : launch_norm_type<_Float16, false>(a, stream);
+  return q ? launch_norm_type<__bf16, true>(a, stream) : launch_norm_type<__bf16, false>(a, stream);
 }
 
 // Workgroups of the backward = rows of partial dw, db.
@@ -473,13 +583,13 @@ hipError_t launch_layernorm_backward(const void* dy, const void* x, const float*
   const NormBackArgs a{dy, x, mean, rstd, w, dx, part, M, K};
   const int blocks = layernorm_backward_rows(M, K);
   *partial = false;
-  hipError_t e = dtype == SHERRY_F32   ? launch_norm_backward_as<float>(a, blocks, stream)
-                 : dtype == SHERRY_F16 ? launch_norm_backward_as<_Float16>(a, blocks, stream)
-                                       : launch_norm_backward_as<__bf16>(a, blocks, stream);
+  hipError_t e = dtype == SHERRY_F32   ? launch_norm_backward_type<float>(a, blocks, stream)
+                 : dtype == SHERRY_F16 ? launch_norm_backward_type<_Float16>(a, blocks, stream)
+                                       : launch_norm_backward_type<__bf16>(a, blocks, stream);
   if (e != hipSuccess) return e;
   *partial = true;
   if (dw || db) {
-    hipLaunchKernelGGL(norm_columns_kernel, dim3((2 * K + 63) / 64), dim3(256), 0, stream, part, blocks, K, dw, db);
+    hipLaunchKernelGGL(norm_columns_kernel, dim3((2 * K + 63) / 64), dim3(1024), 0, stream, part, blocks, K, dw, db);
     e = hipGetLastError();
   }
   return e;

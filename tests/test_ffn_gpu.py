@@ -253,7 +253,7 @@ def norm_inputs(M, K, dtype, seed):
     return x.to(dtype), 1 + 0.3 * torch.randn(K, generator=g), 0.2 * torch.randn(K, generator=g)
 
 
-NORMS = [(1, 4), (5, 252), (3, 260), (9, 1020), (2, 1028), (6, 2048), (1, 4096), (33, 4100), (3, 8196), (2, 16384),
+NORMS = [(1, 4), (5, 252), (300, 2052), (700, 1032), (1500, 8200), (260, 16376), (257, 6000), (2, 512), (3, 1032), (3, 260), (9, 1020), (2, 1028), (6, 2048), (1, 4096), (33, 4100), (3, 8196), (2, 16384),
          (3, 16388), (1, 40000), (600, 64)]
 
 
@@ -301,8 +301,8 @@ def test_layernorm_backward(i, shape, t):
     again = bw.layernorm_backward(dy.cuda(), x.cuda(), mean, rstd, None if w is None else w.cuda())
     assert all(torch.equal(p, q) for p, q in zip(grads, again))
     buf = dy.cuda()
-    assert torch.equal(bw.layernorm_backward(buf, x.cuda(), mean, rstd, None if w is None else w.cuda(), out=buf)[0],
-                       grads[0])
+    inplace = bw.layernorm_backward(buf, x.cuda(), mean, rstd, None if w is None else w.cuda(), out=buf)
+    assert inplace[0].data_ptr() == buf.data_ptr() and all(torch.equal(p, q) for p, q in zip(inplace, grads))
 
 
 def test_layernorm_rows_without_spread_and_a_far_mean():
