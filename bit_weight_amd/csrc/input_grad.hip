@@ -59,18 +59,17 @@ __device__ __forceinline__ float block_top(float v, float* red) {
   return r;
 }
 
-// The four weights of code c as 2-bit fields (bit 2j: nonzero, 2j+1: sign).
+// The four weights of code c as 2-bit fields in a byte (two's complement:
+// weight j in bits 2j, 2j + 1, i.e. nonzero and sign).
 __device__ __forceinline__ uint32_t code_fields(uint32_t c) {
-  const uint32_t w = code_word(c);
-  uint32_t f = 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) f |= (((w >> (8 * j)) & 1u) | ((w >> (8 * j + 6)) & 2u)) << (2 * j);
-  return f;
+  const uint32_t w = code_word(c) & 0x03030303u;
+  return (w | w >> 6 | w >> 12 | w >> 18) & 255u;
 }
 
 __global__ __launch_bounds__(kPrepThreads) void grad_prepare_kernel(PrepareArgs a) {
   constexpr int kPitch = 36;   // bytes per row of the staged tile
   __shared__ __attribute__((aligned(16))) uint8_t tile[kPrepThreads / 64][kTileRows * kPitch];
+  __shared__ uint8_t fields[32];
   __shared__ float red[kPrepThreads / 64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   if (blockIdx.x == 0) {
@@ -114,6 +113,8 @@ __global__ __launch_bounds__(kPrepThreads) void grad_prepare_kernel(PrepareArgs 
   const bool live = id < a.parts * RT * KT;
   const int r = live ? id / KT : 0, kt = live ? id - r * KT : 0;   // r: row tile over both matrices
   const int part = r >= RT ? 1 : 0, rt = r - part * RT;
+  if (tid < 32) fields[tid] = (uint8_t)code_fields(tid);
+  __syncthreads();
   {
     const uint8_t* src = a.packed[part] + tile_offset(rt, kt, KT);
     const uint4 lo = *reinterpret_cast<const uint4*>(src + 16 * lane);
@@ -127,8 +128,8 @@ __global__ __launch_bounds__(kPrepThreads) void grad_prepare_kernel(PrepareArgs 
 #pragma unroll
       for (int jj = 0; jj < 8; ++jj) {
         const bool ok = row_ok && kt * kTileK + 4 * (8 * g + jj) < a.K;
-        const uint32_t c = ok ? code_fields(group_code(w[t], (hi >> (8 * t)) & 255u, jj)) : 0u;
-        f[jj >> 2] |= c << (8 * (jj & 3));
+        const uint32_t c = fields[group_code(w[t], (hi >> (8 * t)) & 255u, jj)];
+        f[jj >> 2] |= (ok ? c : 0u) << (8 * (jj & 3));
       }
       uint32_t* dst = reinterpret_cast<uint32_t*>(&tile[wave][(16 * t + i) * kPitch + 8 * g]);
       dst[0] = f[0];
@@ -146,14 +147,14 @@ __global__ __launch_bounds__(kPrepThreads) void grad_prepare_kernel(PrepareArgs 
     for (int s = 0; s < 2; ++s) {
       uint32_t d0 = 0, d1 = 0;   // columns 0, 1 and 2, 3
 #pragma unroll
-      for (int p = 0; p < 4; ++p)
-#pragma unroll
-        for (int o = 0; o < 2; ++o) {
-          const uint32_t f = tile[wave][(32 * s + 8 * g + 2 * p + o) * kPitch + 16 * h + i];
-          // field of column jl at entry e = 4 jl + p: bits 14 - 2 e of this half
-          d0 |= ((f & 3u) << (14 - 2 * p) | ((f >> 2) & 3u) << (6 - 2 * p)) << (16 * o);
-          d1 |= (((f >> 4) & 3u) << (14 - 2 * p) | ((f >> 6) & 3u) << (6 - 2 * p)) << (16 * o);
-        }
+      for (int p = 0; p < 4; ++p) {
+        // rows 2p and 2p + 1 in the two halves; the field of column jl at
+        // entry e = 4 jl + p: bits 14 - 2e of its half
+        const uint8_t* src = &tile[wave][(32 * s + 8 * g + 2 * p) * kPitch + 16 * h + i];
+        const uint32_t f = (uint32_t)src[0] | (uint32_t)src[kPitch] << 16;
+        d0 |= (f & 0x00030003u) << (14 - 2 * p) | ((f >> 2) & 0x00030003u) << (6 - 2 * p);
+        d1 |= ((f >> 4) & 0x00030003u) << (14 - 2 * p) | ((f >> 6) & 0x00030003u) << (6 - 2 * p);
+      }
       out[2 * s] = d0;
       out[2 * s + 1] = d1;
     }

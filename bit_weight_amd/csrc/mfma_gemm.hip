@@ -612,13 +612,16 @@ __global__ __launch_bounds__(kThreads) void mfma_gemm_kernel(const uint8_t* pack
           } else if constexpr (EP == kEpGlu) {
             o[i] = act_value(z, e.act) * (p2 * al2[i]);
           } else if constexpr (EP == kEpFusedBack) {
-            const float dz = io[k][i] * act_slope(z, e.act);
+            float slope;
+            activate<true>(z, e.act, slope);
+            const float dz = io[k][i] * slope;
             sum0[i] += dz * p1;
             sum1[i] += dz;
             o[i] = dz * al[i];
           } else {
-            const float dg = io[k][i] * (p2 * al2[i]) * act_slope(z, e.act);
-            const float du = io[k][i] * act_value(z, e.act);
+            float slope;
+            const float du = io[k][i] * activate<true>(z, e.act, slope);
+            const float dg = io[k][i] * (p2 * al2[i]) * slope;
             sum0[i] += dg * p1;
             sum1[i] += du * p2;
             o[i] = dg * al[i];

@@ -46,16 +46,40 @@ __device__ __forceinline__ T group_join(T v, T* red, int wave, F op) {
   }
 }
 
+// A double from another lane of its 16-lane row by DPP control CTRL, and
+// from one lane of the wave.
+template <int CTRL>
+__device__ __forceinline__ double dpp_shift(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const int lo = (int)(uint32_t)u, hi = (int)(uint32_t)(u >> 32);
+  const uint32_t l = (uint32_t)__builtin_amdgcn_update_dpp(lo, lo, CTRL, 0xF, 0xF, false);
+  const uint32_t h = (uint32_t)__builtin_amdgcn_update_dpp(hi, hi, CTRL, 0xF, 0xF, false);
+  return __builtin_bit_cast(double, (uint64_t)h << 32 | l);
+}
+
+__device__ __forceinline__ double from_lane(double x, int lane) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t l = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, lane);
+  const uint32_t h = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
+  return __builtin_bit_cast(double, (uint64_t)h << 32 | l);
+}
+
+// As wave_sum and wave_max (shuffles, six LDS round trips each, took longer).
+template <typename F>
+__device__ __forceinline__ double wave_join64(double v, F op) {
+  v = op(v, dpp_shift<0xB1>(v));     // quad_perm [1,0,3,2]
+  v = op(v, dpp_shift<0x4E>(v));     // quad_perm [2,3,0,1]
+  v = op(v, dpp_shift<0x124>(v));    // row_ror:4
+  v = op(v, dpp_shift<0x128>(v));    // row_ror:8
+  return op(op(from_lane(v, 0), from_lane(v, 16)), op(from_lane(v, 32), from_lane(v, 48)));
+}
+
 __device__ __forceinline__ double wave_sum64(double v) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
-  return v;
+  return wave_join64(v, [](double a, double b) { return a + b; });
 }
 
 __device__ __forceinline__ double wave_max64(double v) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v = fmax(v, __shfl_xor(v, d));
-  return v;
+  return wave_join64(v, [](double a, double b) { return fmax(a, b); });
 }
 
 __device__ __forceinline__ double wave_total(double v) { return wave_sum64(v); }

@@ -63,43 +63,60 @@ __device__ __forceinline__ void store1_as(void* p, size_t i, int dtype, float v)
 }
 
 // Activation functions and their slopes in fp32 (SHERRY_ACT_*; the switch is
-// wave-uniform).  silu(z) = z / (1 + e^-z); gelu(z) = z Phi(z), Phi the normal
-// distribution function; gelu_tanh replaces Phi by (1 + tanh(c (z + 0.044715
-// z^3))) / 2, c = sqrt(2 / pi); relu2 is relu squared.
+// wave-uniform).  With the logistic function S(t) = 1 / (1 + e^-t):
+// silu(z) = z S(z); gelu(z) = z Phi(z), Phi the normal distribution function;
+// gelu_tanh replaces Phi by (1 + tanh u) / 2 = S(2 u), u = sqrt(2 / pi) (z +
+// 0.044715 z^3); relu2 is relu squared.
 constexpr float kSqrtHalf = 0.70710678118654752f;
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;
-constexpr float kSqrt2OverPi = 0.79788456080286536f;
+constexpr float k2Sqrt2OverPi = 1.5957691216057308f;
 constexpr float kGeluCubic = 0.044715f;
+constexpr float kLog2E = 1.4426950408889634f;
 
-__device__ __forceinline__ float act_value(float z, int act) {
+// S(t) from the hardware's 2^x and reciprocal (each within an ulp).  The
+// rounding of t log2(e) costs |t| / 2 ulp of e^-t, which matters only where
+// S(t) ~ e^t is small: there t S(t), which is what multiplies it, is too.
+// (The library's expf and a division took twice the instructions of the
+// rest of the backward's epilogue.)
+__device__ __forceinline__ float logistic(float t) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2E * t));
+}
+
+// The activation of z and, with kSlope, its slope there.
+template <bool kSlope>
+__device__ __forceinline__ float activate(float z, int act, float& slope) {
   switch (act) {
-    case SHERRY_ACT_RELU: return z > 0.0f || z != z ? z : 0.0f;
-    case SHERRY_ACT_RELU2: return z > 0.0f || z != z ? z * z : 0.0f;
-    case SHERRY_ACT_SILU: return z / (1.0f + expf(-z));
-    case SHERRY_ACT_GELU: return 0.5f * z * (1.0f + erff(z * kSqrtHalf));
-    case SHERRY_ACT_GELU_TANH:
-      return 0.5f * z * (1.0f + tanhf(kSqrt2OverPi * (z + kGeluCubic * z * z * z)));
-    default: return z;
+    case SHERRY_ACT_RELU:
+      if constexpr (kSlope) slope = z > 0.0f ? 1.0f : 0.0f;
+      return z > 0.0f || z != z ? z : 0.0f;
+    case SHERRY_ACT_RELU2:
+      if constexpr (kSlope) slope = z > 0.0f ? 2.0f * z : 0.0f;
+      return z > 0.0f || z != z ? z * z : 0.0f;
+    case SHERRY_ACT_SILU: {
+      const float s = logistic(z);
+      if constexpr (kSlope) slope = s + z * s * (1.0f - s);
+      return z * s;
+    }
+    case SHERRY_ACT_GELU: {
+      const float phi = 0.5f * (1.0f + erff(z * kSqrtHalf));
+      if constexpr (kSlope) slope = phi + z * (kInvSqrt2Pi * __builtin_amdgcn_exp2f(-0.5f * kLog2E * z * z));
+      return z * phi;
+    }
+    case SHERRY_ACT_GELU_TANH: {
+      const float z2 = z * z;
+      const float s = logistic(k2Sqrt2OverPi * (z + kGeluCubic * z2 * z));
+      if constexpr (kSlope) slope = s + z * s * (1.0f - s) * k2Sqrt2OverPi * (1.0f + 3.0f * kGeluCubic * z2);
+      return z * s;
+    }
+    default:
+      if constexpr (kSlope) slope = 1.0f;
+      return z;
   }
 }
 
-__device__ __forceinline__ float act_slope(float z, int act) {
-  switch (act) {
-    case SHERRY_ACT_RELU: return z > 0.0f ? 1.0f : 0.0f;
-    case SHERRY_ACT_RELU2: return z > 0.0f ? 2.0f * z : 0.0f;
-    case SHERRY_ACT_SILU: {
-      const float s = 1.0f / (1.0f + expf(-z));
-      return s * (1.0f + z * (1.0f - s));
-    }
-    case SHERRY_ACT_GELU:
-      return 0.5f * (1.0f + erff(z * kSqrtHalf)) + z * (kInvSqrt2Pi * expf(-0.5f * z * z));
-    case SHERRY_ACT_GELU_TANH: {
-      const float t = tanhf(kSqrt2OverPi * (z + kGeluCubic * z * z * z));
-      return 0.5f * (1.0f + t) +
-             0.5f * z * (1.0f - t * t) * kSqrt2OverPi * (1.0f + 3.0f * kGeluCubic * z * z);
-    }
-    default: return 1.0f;
-  }
+__device__ __forceinline__ float act_value(float z, int act) {
+  float slope;
+  return activate<false>(z, act, slope);
 }
 
 // Sum over the 64 lanes of a wave, the same value in every lane (all lanes
