@@ -228,6 +228,11 @@ __global__ __launch_bounds__(kThreads) void mfma_gemm_kernel(const uint8_t* pack
   // per lookup (measured at M=512, K=4096, N=14336: 32.7 -> 31.9 us)
   __shared__ __attribute__((aligned(1024))) uint2 dec2[1024];
   __shared__ float sxs[kBM];   // s_x of this tile's rows (epilogue)
+  // with an epilogue, also its other factors, loaded ahead of the main loop:
+  // the gradients' scales, and alpha and alpha2 (or the bias) of the outputs
+  constexpr bool kBack = ep_back(EP);
+  __shared__ float inv_rows[kBack ? kBM : 1];
+  __shared__ __attribute__((aligned(16))) float cols[2][kOwn ? kBNO : 4];
   // arrivals at the step barrier of each k-tile parity (128-row tiles)
   __shared__ unsigned parity_arrivals[KP];
 
@@ -418,6 +423,26 @@ __global__ __launch_bounds__(kThreads) void mfma_gemm_kernel(const uint8_t* pack
   v4u w0, w1;
   uint32_t h0, h1;
   v4i bA0[kNT], bA1[kNT], bB0[kNT], bB1[kNT];
+  float sx_in = 0.0f, al_in = 0.0f, al2_in = 0.0f;
+  float2 row_in = make_float2(0.0f, 0.0f);
+  float tops_in[3] = {0.0f, 0.0f, 0.0f};
+  if constexpr (kOwn) {
+    const int mi = min(m0 + tid, M - 1), ni = min(n0 + tid, N - 1);
+    if (tid < kBM) {
+      sx_in = a.s_x[mi];
+      if constexpr (kBack) row_in = e.grad.rows[mi];
+    }
+    if (tid < kBNO) {
+      al_in = a.alpha[ni];
+      if constexpr (kGlu) al2_in = e.alpha2[ni];
+      else if (e.bias) al2_in = e.bias[ni];
+    }
+    if constexpr (kBack) {
+#pragma unroll
+      for (int i = 0; i < 3; ++i) tops_in[i] = e.grad.tops[i];
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
   load_codes(0, w0, h0);
   __builtin_amdgcn_sched_barrier(0);
   copy_a(0, kOwn ? own_buf(Const<0>{}) : a_buf(0));
@@ -430,6 +455,17 @@ __global__ __launch_bounds__(kThreads) void mfma_gemm_kernel(const uint8_t* pack
   __builtin_amdgcn_sched_barrier(0);
   if constexpr (!kPair && kABufs >= 3) copy_a(min(1, KJ - 1), kOwn ? own_buf(Const<1>{}) : a_buf(1));
   __builtin_amdgcn_sched_barrier(0);
+  if constexpr (kOwn) {
+    if (tid < kBM) {
+      sxs[tid] = sx_in;
+      if constexpr (kBack) inv_rows[tid] = exp2_of(grad_exponent(row_in, sx_in, tops_in, e.act, kGlu));
+    }
+    if (tid < kBNO) {
+      cols[0][tid] = al_in;
+      cols[1][tid] = al2_in;
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
   // decode table written (LDS only: the copies stay in flight)
   __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(63));
   __builtin_amdgcn_s_barrier();
@@ -547,45 +583,46 @@ __global__ __launch_bounds__(kThreads) void mfma_gemm_kernel(const uint8_t* pack
       }
     }
   } else {
-    constexpr bool kBack = ep_back(EP);
     constexpr int kCols = kBNO / 4;             // threads across a row: 4 outputs each
     constexpr int kRowStep = kThreads / kCols;  // rows the workgroup takes at a time
     static_assert(kRowStep <= kTurnRows ? kTurnRows % kRowStep == 0 : kRowStep == 2 * kTurnRows, "rows per turn");
     // (a row narrower than the workgroup can take in one turn: half the threads rest)
     constexpr int kTurns = kRowStep <= kTurnRows ? kTurnRows / kRowStep : 1;
-    __shared__ float inv_rows[kBack ? kBM : 1];
+    constexpr int kAll = kBM / kTurnRows * kTurns;   // rows per thread
     const int c4 = tid % kCols, r0 = tid / kCols;
     const int n = n0 + 4 * c4;
-    const int nl = n < N ? n : 0;               // a valid column for the loads
-    const f4 al{a.alpha[nl], a.alpha[nl + 1], a.alpha[nl + 2], a.alpha[nl + 3]};
-    f4 al2{0.0f, 0.0f, 0.0f, 0.0f}, bias = al2;
-    if constexpr (kGlu) {
-      al2 = f4{e.alpha2[nl], e.alpha2[nl + 1], e.alpha2[nl + 2], e.alpha2[nl + 3]};
-    } else if (e.bias) {
-      bias = f4{e.bias[nl], e.bias[nl + 1], e.bias[nl + 2], e.bias[nl + 3]};
-    }
-    if (tid < kBM) {
-      const int m = min(m0 + tid, M - 1);
-      sxs[tid] = a.s_x[m];
-      if constexpr (kBack)
-        inv_rows[tid] = exp2_of(grad_exponent(e.grad.rows[m], a.s_x[m], e.grad.tops, e.act, kGlu));
-    }
+    // this thread's residuals or output gradients, all requested before the
+    // first is used (up to four turns of them in 128 x 256 tiles' registers)
+    constexpr int kAhead = kAll < 8 ? kAll : 8;
+    u4 io[kAhead];
+    const void* in = kBack ? e.grad.dy : e.residual;
+    const bool has_in = !(EP == kEpGlu) && in && n < N && r0 < kTurnRows;
+    const bool wide_in = e.dtype == SHERRY_F32;
+    auto row_of = [&](int i) { return m0 + kTurnRows * (i / kTurns) + r0 + kRowStep * (i % kTurns); };
+    auto load_in = [&](int first) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) io[i] = u4{0u, 0u, 0u, 0u};
+      if (has_in && wide_in) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+          if (row_of(first + i) < M) io[i] = load4_raw(in, (size_t)row_of(first + i) * N + n, SHERRY_F32);
+      } else if (has_in) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+          if (row_of(first + i) < M) io[i] = load4_raw(in, (size_t)row_of(first + i) * N + n, SHERRY_F16);   // (either 16-bit type)
+      }
+    };
+    load_in(0);
+    const f4 al = *reinterpret_cast<const f4*>(&cols[0][4 * c4]);
+    const f4 second = *reinterpret_cast<const f4*>(&cols[1][4 * c4]);   // alpha2, or the bias
+    const f4 al2 = kGlu ? second : f4{0.0f, 0.0f, 0.0f, 0.0f}, bias = second;
     f4 sum0{0.0f, 0.0f, 0.0f, 0.0f}, sum1 = sum0;   // this thread's share of dalpha and dalpha2 / dbias
     const int RT64 = RT * kTileRows;
     const size_t zrow = (size_t)e.grad.terms * (kGlu ? 2 : 1) * RT64;
-    __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
 #pragma unroll
     for (int qq = 0; qq < kMT / kTurnBlocks; ++qq) {
-      // this turn's residuals or output gradients, ahead of the barriers
-      f4 io[kTurns];
-#pragma unroll
-      for (int k = 0; k < kTurns; ++k) {
-        const int m = m0 + kTurnRows * qq + r0 + kRowStep * k;
-        io[k] = f4{0.0f, 0.0f, 0.0f, 0.0f};
-        if (m < M && n < N && r0 < kTurnRows) {
-          if constexpr (kBack) io[k] = load4_as(e.grad.dy, (size_t)m * N + n, e.dtype);
-          else if (!kGlu && e.residual) io[k] = load4_as(e.residual, (size_t)m * N + n, e.dtype);
-        }
+      if constexpr (kAll > kAhead) {
+        if (qq > 0 && qq * kTurns % kAhead == 0) load_in(qq * kTurns);
       }
       __syncthreads();  // the previous use of the LDS area is finished
       put_sums(qq);
@@ -602,26 +639,27 @@ __global__ __launch_bounds__(kThreads) void mfma_gemm_kernel(const uint8_t* pack
           if constexpr (kGlu) s2 += *reinterpret_cast<const v4i*>(&ot[(ph * kTurnRows + ml) * kOutLd + kBNO + 4 * c4]);
         }
         const float sx = sxs[kTurnRows * qq + ml];
+        const f4 in4 = as_f4(io[(qq * kTurns + k) % kAhead], e.dtype);
         f4 o{0.0f, 0.0f, 0.0f, 0.0f}, o2 = o;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float p1 = (float)s1[i] * sx, p2 = (float)s2[i] * sx;
           const float z = kGlu ? p1 * al[i] : p1 * al[i] + bias[i];
           if constexpr (EP == kEpFused) {
-            o[i] = act_value(z, e.act) + io[k][i];
+            o[i] = act_value(z, e.act) + in4[i];
           } else if constexpr (EP == kEpGlu) {
             o[i] = act_value(z, e.act) * (p2 * al2[i]);
           } else if constexpr (EP == kEpFusedBack) {
             float slope;
             activate<true>(z, e.act, slope);
-            const float dz = io[k][i] * slope;
+            const float dz = in4[i] * slope;
             sum0[i] += dz * p1;
             sum1[i] += dz;
             o[i] = dz * al[i];
           } else {
             float slope;
-            const float du = io[k][i] * activate<true>(z, e.act, slope);
-            const float dg = io[k][i] * (p2 * al2[i]) * slope;
+            const float du = in4[i] * activate<true>(z, e.act, slope);
+            const float dg = in4[i] * (p2 * al2[i]) * slope;
             sum0[i] += dg * p1;
             sum1[i] += du * p2;
             o[i] = dg * al[i];

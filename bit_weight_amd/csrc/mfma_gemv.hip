@@ -425,17 +425,33 @@ __global__ __launch_bounds__(64 * KW) void mfma_gemv_kernel(const uint8_t* packe
   const float al = scaled && n_ok ? a.alpha[n] : 0.0f;
   // the gated form's second scale, or the fused form's bias and residuals
   float al2 = 0.0f;
-  float res[EP == kEpFused ? MB : 1][TPW];
+  uint32_t res[EP == kEpFused ? MB : 1][TPW];   // as loaded
   if constexpr (kGlu) al2 = n_ok ? e.alpha2[n] : 0.0f;
   if constexpr (EP == kEpFused) {
     al2 = n_ok && e.bias ? e.bias[n] : 0.0f;
+    const bool wide = e.dtype == SHERRY_F32;
+    const bool any = e.residual && n_ok && q * TPW < MT;
 #pragma unroll
     for (int b = 0; b < MB; ++b)
 #pragma unroll
-      for (int i = 0; i < TPW; ++i) {
-        const int m = 16 * b + q * TPW + i;
-        res[b][i] = e.residual && n_ok && q * TPW < MT && m < M ? load1_as(e.residual, (size_t)m * N + n, e.dtype) : 0.0f;
-      }
+      for (int i = 0; i < TPW; ++i) res[b][i] = 0u;
+    if (any && wide) {
+#pragma unroll
+      for (int b = 0; b < MB; ++b)
+#pragma unroll
+        for (int i = 0; i < TPW; ++i) {
+          const int m = 16 * b + q * TPW + i;
+          if (m < M) res[b][i] = load1_raw(e.residual, (size_t)m * N + n, SHERRY_F32);
+        }
+    } else if (any) {
+#pragma unroll
+      for (int b = 0; b < MB; ++b)
+#pragma unroll
+        for (int i = 0; i < TPW; ++i) {
+          const int m = 16 * b + q * TPW + i;
+          if (m < M) res[b][i] = load1_raw(e.residual, (size_t)m * N + n, SHERRY_F16);   // (either 16-bit type)
+        }
+    }
   }
   // the scales of this wave's tokens, loaded with alpha before any atomic
   // or store (the memory counter counts stores too: a scale loaded after a
@@ -517,7 +533,7 @@ __global__ __launch_bounds__(64 * KW) void mfma_gemv_kernel(const uint8_t* packe
       const int m = min(16 * b + q * TPW + i, MT - 1);
       const float sx = FQ ? sred[KW * MT + m] : sxm[b][i];
       yv[i] = ((float)total[i] * sx) * al;
-      if constexpr (EP == kEpFused) yv[i] = act_value(yv[i] + al2, e.act) + res[b][i];
+      if constexpr (EP == kEpFused) yv[i] = act_value(yv[i] + al2, e.act) + as_f1(res[b][i], e.dtype);
       if constexpr (EP == kEpGlu) yv[i] = act_value(yv[i], e.act) * (((float)total2[i] * sx) * al2);
       asm volatile("" : "+v"(yv[i]));
     }

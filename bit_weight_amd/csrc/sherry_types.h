@@ -37,11 +37,27 @@ __device__ __forceinline__ void store4(T* p, f4 v) {
   }
 }
 
-// The same with the type known at run time (the branch is wave-uniform).
+// The same with the type known at run time (the branches are wave-uniform).
+// Loading and converting are apart, so that several loads can be issued
+// before the first conversion waits for one.
+typedef unsigned int u4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ u4 load4_raw(const void* p, size_t i, int dtype) {
+  if (dtype == SHERRY_F32) return *reinterpret_cast<const u4*>(static_cast<const float*>(p) + i);
+  const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
+  return u4{v.x, v.y, 0u, 0u};
+}
+
+__device__ __forceinline__ f4 as_f4(u4 v, int dtype) {
+  if (dtype == SHERRY_F32) return __builtin_bit_cast(f4, v);
+  const uint2 h = make_uint2(v.x, v.y);
+  if (dtype == SHERRY_F16) return __builtin_convertvector(__builtin_bit_cast(h4, h), f4);
+  return f4{__builtin_bit_cast(float, h.x << 16), __builtin_bit_cast(float, h.x & 0xFFFF0000u),
+            __builtin_bit_cast(float, h.y << 16), __builtin_bit_cast(float, h.y & 0xFFFF0000u)};
+}
+
 __device__ __forceinline__ f4 load4_as(const void* p, size_t i, int dtype) {
-  if (dtype == SHERRY_F32) return load4(static_cast<const float*>(p) + i);
-  if (dtype == SHERRY_F16) return load4(static_cast<const _Float16*>(p) + i);
-  return load4(static_cast<const __bf16*>(p) + i);
+  return as_f4(load4_raw(p, i, dtype), dtype);
 }
 
 __device__ __forceinline__ void store4_as(void* p, size_t i, int dtype, f4 v) {
@@ -50,10 +66,15 @@ __device__ __forceinline__ void store4_as(void* p, size_t i, int dtype, f4 v) {
   else store4(static_cast<__bf16*>(p) + i, v);
 }
 
-__device__ __forceinline__ float load1_as(const void* p, size_t i, int dtype) {
-  if (dtype == SHERRY_F32) return static_cast<const float*>(p)[i];
-  if (dtype == SHERRY_F16) return (float)static_cast<const _Float16*>(p)[i];
-  return (float)static_cast<const __bf16*>(p)[i];
+__device__ __forceinline__ uint32_t load1_raw(const void* p, size_t i, int dtype) {
+  if (dtype == SHERRY_F32) return static_cast<const uint32_t*>(p)[i];
+  return static_cast<const uint16_t*>(p)[i];
+}
+
+__device__ __forceinline__ float as_f1(uint32_t v, int dtype) {
+  if (dtype == SHERRY_F32) return __builtin_bit_cast(float, v);
+  if (dtype == SHERRY_F16) return (float)__builtin_bit_cast(_Float16, (uint16_t)v);
+  return __builtin_bit_cast(float, v << 16);
 }
 
 __device__ __forceinline__ void store1_as(void* p, size_t i, int dtype, float v) {
