@@ -432,40 +432,23 @@ def gemm2(x: torch.Tensor, s_x: torch.Tensor, packed: torch.Tensor, alpha: torch
 
 # ------------------------------------------------- feed-forward operators
 # Their tensors are checked and passed on by a compiled module (csrc/binding.cpp).
-DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "relu2": 2, "silu": 3, "gelu": 4, "gelu_tanh": 5}
 
 _native = None
 
 
-def _act_code(act) -> int:
-    code = ACTIVATIONS.get(act)
-    if code is None:
-        raise ValueError(f"act must be one of {list(ACTIVATIONS)}, got {act!r}")
-    return code
-
-
-def _dtype_code(dtype) -> int:
-    code = DTYPES.get(dtype)
-    if code is None:
-        raise RuntimeError(f"type must be float32, float16 or bfloat16, got {dtype}")
-    return code
-
-
 def _zeroed_workspace(index: int, nbytes: int) -> torch.Tensor:
-    """The split-K workspace of the current stream of device `index`; under
-    graph capture one of the graph's own, which each replay zeroes (two
-    graphs captured on one stream may be replayed side by side, and memory
-    that only another graph has zeroed is not zero)."""
+    """A split-K workspace on the current stream of device `index` (the compiled
+    module asks when the stream has none that is large enough); under graph
+    capture one of the graph's own, which each replay zeroes: two graphs
+    captured on one stream may be replayed side by side, and memory that
+    only another graph has zeroed is not zero."""
     if torch.cuda.current_device() != index:
         with torch.cuda.device(index):
             return _zeroed_workspace(index, nbytes)
     if torch.cuda.is_current_stream_capturing():
         return torch.zeros(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
-    buf = _workspaces._bufs.get((index, torch._C._cuda_getCurrentRawStream(index)))
-    if buf is None or buf.numel() < nbytes:
-        buf = _workspaces.get(torch.device("cuda", index), nbytes)
-    return buf
+    return _workspaces.get(torch.device("cuda", index), nbytes)
 
 
 def _raise_status(status: int, what: str) -> None:
@@ -488,7 +471,7 @@ def _load_native():
                         "sherry_glu_workspace_bytes": None}
             entries |= {f"sherry_{n}_scratch_bytes": None for n in names if n.endswith("backward")}
             _binding.setup({n: ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in entries},
-                           _zeroed_workspace, _raise_status)
+                           _workspaces._bufs, _zeroed_workspace, ACTIVATIONS, _raise_status)
             _native = _binding
     return _native
 
@@ -500,8 +483,8 @@ def gemm_fused(x: torch.Tensor, s_x: torch.Tensor, packed: torch.Tensor, alpha: 
     """y[M,N] = act((x_int8 @ T^T) * s_x[:,None] * alpha + bias) + residual in
     one kernel (sherry_gemm_fused).  bias is fp32 [N]; residual and y have
     type `dtype`; out may be the residual (updated in place)."""
-    return (_native or _load_native()).gemm_fused(x, s_x, packed, alpha, N, K, bias, _act_code(act), residual,
-                                                  _dtype_code(dtype), out, workspace)
+    return (_native or _load_native()).gemm_fused(x, s_x, packed, alpha, N, K, bias, act, residual,
+                                                  dtype, out, workspace)
 
 
 def gemm_fused_backward(dy: torch.Tensor, x: torch.Tensor, s_x: torch.Tensor, packed: torch.Tensor,
@@ -510,7 +493,7 @@ def gemm_fused_backward(dy: torch.Tensor, x: torch.Tensor, s_x: torch.Tensor, pa
     """Gradients of gemm_fused from dy [M,N] and its inputs -> (dx of dy's type
     [M,K], dalpha fp32 [N], dbias fp32 [N]); dx is the gradient of the token
     x * s_x, the residual's is dy."""
-    return (_native or _load_native()).gemm_fused_backward(dy, x, s_x, packed, alpha, N, K, bias, _act_code(act))
+    return (_native or _load_native()).gemm_fused_backward(dy, x, s_x, packed, alpha, N, K, bias, act)
 
 
 def glu(x: torch.Tensor, s_x: torch.Tensor, packed_gate: torch.Tensor, alpha_gate: torch.Tensor,
@@ -521,7 +504,7 @@ def glu(x: torch.Tensor, s_x: torch.Tensor, packed_gate: torch.Tensor, alpha_gat
     matrices, in one kernel (sherry_glu).  A float32 h is what quantize_act
     takes for the down projection."""
     return (_native or _load_native()).glu(x, s_x, packed_gate, alpha_gate, packed_up, alpha_up, N, K,
-                                           _act_code(act), _dtype_code(dtype), out, workspace)
+                                           act, dtype, out, workspace)
 
 
 def glu_backward(dh: torch.Tensor, x: torch.Tensor, s_x: torch.Tensor, packed_gate: torch.Tensor,
@@ -531,7 +514,7 @@ def glu_backward(dh: torch.Tensor, x: torch.Tensor, s_x: torch.Tensor, packed_ga
     dalpha_gate fp32 [N], dalpha_up fp32 [N]); dx is the gradient of the
     token x * s_x."""
     return (_native or _load_native()).glu_backward(dh, x, s_x, packed_gate, alpha_gate, packed_up, alpha_up, N, K,
-                                                    _act_code(act))
+                                                    act)
 
 
 def layernorm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,

@@ -4,17 +4,20 @@
 // module and not ctypes because a decode step's kernel takes 5 to 10 us: the
 // same checks and calls written in Python take 11 us a call on the host.)
 //
-// setup(functions, workspace, error) gives it the library's entry points as
-// addresses, a callable (device index, bytes, device) -> zeroed workspace
-// tensor and one (status, name) that raises.
+// setup() gives it the library's entry points as addresses, the zeroed split-K
+// workspaces by (device index, stream), a callable (device index, bytes) ->
+// workspace for when there is none that serves, the activations' codes by
+// name, and a callable (status, name) that raises.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
 #include <ATen/ATen.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPFunctions.h>
+#include <c10/hip/HIPGraphsC10Utils.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>
+#include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdarg>
@@ -25,7 +28,9 @@
 
 namespace {
 
+PyObject* g_workspaces = nullptr;     // dict
 PyObject* g_workspace = nullptr;
+PyObject* g_activations = nullptr;    // dict
 PyObject* g_error = nullptr;
 
 decltype(&sherry_packed_bytes) f_packed_bytes;
@@ -129,8 +134,18 @@ int dtype_of(at::ScalarType t) {
   }
 }
 
-at::ScalarType scalar_of(int64_t dtype) {
-  return dtype == SHERRY_F32 ? at::kFloat : dtype == SHERRY_F16 ? at::kHalf : at::kBFloat16;
+at::ScalarType scalar_of(PyObject* dtype) {
+  if (!THPDtype_Check(dtype)) fail(PyExc_TypeError, "dtype must be a torch.dtype");
+  return reinterpret_cast<THPDtype*>(dtype)->scalar_type;
+}
+
+int activation_of(PyObject* name) {
+  PyObject* code = PyDict_GetItemWithError(g_activations, name);
+  if (!code) {
+    if (!PyErr_Occurred()) PyErr_Format(PyExc_ValueError, "act must be one of %R, got %R", g_activations, name);
+    throw Raised{};
+  }
+  return (int)integer(code);
 }
 
 // The tokens x [M,K] (int8) and what follows from them.
@@ -201,10 +216,22 @@ struct Workspace {
       keep = tensor_of(o, "workspace");
       check_tensor(keep, "workspace", at::kByte, t.index);
     } else if (need > 0) {
-      PyObject* w = PyObject_CallFunction(g_workspace, "in", t.index, (Py_ssize_t)need);
-      if (!w) throw Raised{};
-      keep = THPVariable_Unpack(w);
-      Py_DECREF(w);
+      const c10::OptionalDeviceGuard guard(t.device);
+      if (c10::hip::currentStreamCaptureStatusMayInitCtx() == c10::hip::CaptureStatus::None) {
+        const auto stream = c10::hip::getCurrentHIPStream((c10::DeviceIndex)t.index).stream();
+        PyObject* key = Py_BuildValue("(iK)", t.index, (unsigned long long)reinterpret_cast<uintptr_t>(stream));
+        if (!key) throw Raised{};
+        PyObject* w = PyDict_GetItemWithError(g_workspaces, key);
+        Py_DECREF(key);
+        if (!w && PyErr_Occurred()) throw Raised{};
+        if (w) keep = tensor_of(w, "workspace");
+      }
+      if (!keep.defined() || (size_t)keep.numel() < need) {
+        PyObject* w = PyObject_CallFunction(g_workspace, "in", t.index, (Py_ssize_t)need);
+        if (!w) throw Raised{};
+        keep = tensor_of(w, "workspace");
+        Py_DECREF(w);
+      }
     } else {
       return;
     }
@@ -244,8 +271,9 @@ PyObject* method(PyObject*, PyObject* const* args, Py_ssize_t n) {
 PyObject* gemm_fused(PyObject* const* a) {
   const Tokens t(a[0], a[1], a[4], a[5]);
   const Weights w(a[2], a[3], "packed", "alpha", t);
-  const int act = (int)integer(a[7]), dtype = (int)integer(a[9]);
-  const at::ScalarType type = scalar_of(dtype);
+  const int act = activation_of(a[7]);
+  const at::ScalarType type = scalar_of(a[9]);
+  const int dtype = dtype_of(type);
   const auto* bias = static_cast<const float*>(vector_of(a[6], "bias", at::kFloat, t.index, t.N, true));
   const void* residual = matrix_of(a[8], "residual", type, t.index, t.M, t.N, true);
   const at::Tensor y = output_of(a[10], t.M, t.N, type, t.index, t.device);
@@ -261,7 +289,7 @@ PyObject* gemm_fused(PyObject* const* a) {
 PyObject* gemm_fused_backward(PyObject* const* a) {
   const Tokens t(a[1], a[2], a[5], a[6]);
   const Weights w(a[3], a[4], "packed", "alpha", t);
-  const int act = (int)integer(a[8]);
+  const int act = activation_of(a[8]);
   const auto* bias = static_cast<const float*>(vector_of(a[7], "bias", at::kFloat, t.index, t.N, true));
   const at::Tensor& dy = tensor_of(a[0], "dy");
   const int dtype = dtype_of(dy.scalar_type());
@@ -281,8 +309,10 @@ PyObject* gemm_fused_backward(PyObject* const* a) {
 PyObject* glu(PyObject* const* a) {
   const Tokens t(a[0], a[1], a[6], a[7]);
   const Weights g(a[2], a[3], "packed_gate", "alpha_gate", t), u(a[4], a[5], "packed_up", "alpha_up", t);
-  const int act = (int)integer(a[8]), dtype = (int)integer(a[9]);
-  const at::Tensor h = output_of(a[10], t.M, t.N, scalar_of(dtype), t.index, t.device);
+  const int act = activation_of(a[8]);
+  const at::ScalarType type = scalar_of(a[9]);
+  const int dtype = dtype_of(type);
+  const at::Tensor h = output_of(a[10], t.M, t.N, type, t.index, t.device);
   const Workspace ws(a[11], f_glu_workspace_bytes(t.M, t.N, t.K), t);
   launch("sherry_glu", t.index, [&](void* stream) {
     return f_glu(t.x, t.s_x, g.packed, g.alpha, u.packed, u.alpha, act, h.data_ptr(), dtype, t.M, t.N, t.K, ws.at,
@@ -295,7 +325,7 @@ PyObject* glu(PyObject* const* a) {
 PyObject* glu_backward(PyObject* const* a) {
   const Tokens t(a[1], a[2], a[7], a[8]);
   const Weights g(a[3], a[4], "packed_gate", "alpha_gate", t), u(a[5], a[6], "packed_up", "alpha_up", t);
-  const int act = (int)integer(a[9]);
+  const int act = activation_of(a[9]);
   const at::Tensor& dh = tensor_of(a[0], "dh");
   const int dtype = dtype_of(dh.scalar_type());
   const void* pdh = matrix_of(dh, "dh", dh.scalar_type(), t.index, t.M, t.N);
@@ -397,8 +427,9 @@ PyObject* layernorm_backward(PyObject* const* a) {
   return wrap_all({dx, dw, db});
 }
 
-// functions (dict of name -> address), workspace, error
+// functions (dict of name -> address), workspaces, workspace, activations, error
 PyObject* setup(PyObject* const* a) {
+  if (!PyDict_Check(a[0]) || !PyDict_Check(a[1]) || !PyDict_Check(a[3])) fail(PyExc_TypeError, "expected a dict");
   for (const Entry& e : kEntries) {
     PyObject* v = PyDict_GetItemString(a[0], e.name);
     if (!v) fail(PyExc_KeyError, "%s", e.name);
@@ -409,17 +440,18 @@ PyObject* setup(PyObject* const* a) {
     }
     std::memcpy(e.at, &p, sizeof p);
   }
-  Py_INCREF(a[1]);
-  Py_XSETREF(g_workspace, a[1]);
-  Py_INCREF(a[2]);
-  Py_XSETREF(g_error, a[2]);
+  PyObject** const to[] = {&g_workspaces, &g_workspace, &g_activations, &g_error};
+  for (int i = 0; i < 4; ++i) {
+    Py_INCREF(a[1 + i]);
+    Py_XSETREF(*to[i], a[1 + i]);
+  }
   Py_RETURN_NONE;
 }
 
 #define SHERRY_METHOD(name, count) \
   {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&method<count, name>)), METH_FASTCALL, nullptr}
 PyMethodDef kMethods[] = {
-    SHERRY_METHOD(setup, 3),           SHERRY_METHOD(gemm_fused, 12),        SHERRY_METHOD(gemm_fused_backward, 9),
+    SHERRY_METHOD(setup, 5),           SHERRY_METHOD(gemm_fused, 12),        SHERRY_METHOD(gemm_fused_backward, 9),
     SHERRY_METHOD(glu, 12),            SHERRY_METHOD(glu_backward, 10),      SHERRY_METHOD(layernorm, 6),
     SHERRY_METHOD(layernorm_quantize, 5), SHERRY_METHOD(layernorm_backward, 6), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};

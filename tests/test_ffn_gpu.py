@@ -331,3 +331,176 @@ def test_layernorm_nan_stays_in_its_row():
     assert bool(y[1].isnan().all()) and bool(y[2].isnan().any())
     ry, ty, *_ = ref.layernorm(x[[0, 3]], None, None, 1e-5, torch.float32)
     check("y", y[[0, 3]], ry, ty)
+
+
+# ------------------------------------------------- the operators as they are used
+class Block:
+    """The feed-forward half of a decoder layer: norm, int8 tokens, gated
+    block, int8 tokens, down projection added to the residual stream."""
+
+    def __init__(self, orc, D, F, seed):
+        self.D, self.F = D, F
+        self.T, self.packed, self.alpha = {}, {}, {}
+        for i, (name, n, k) in enumerate((("gate", F, D), ("up", F, D), ("down", D, F))):
+            self.T[name], self.packed[name], alpha = weights(orc, n, k, seed + i)
+            self.alpha[name] = alpha.cuda()
+        g = _gen(seed + 9)
+        self.w, self.b = (1 + 0.2 * torch.randn(D, generator=g)).cuda(), (0.1 * torch.randn(D, generator=g)).cuda()
+
+    def forward(self, x):
+        q, s = bw.layernorm_quantize(x, self.w, self.b)
+        h = bw.glu(q, s, self.packed["gate"], self.alpha["gate"], self.packed["up"], self.alpha["up"], self.F, self.D)
+        hq, hs = bw.quantize_act(h)
+        y = bw.gemm_fused(hq, hs, self.packed["down"], self.alpha["down"], self.D, self.F, residual=x, dtype=x.dtype)
+        return y, q, s, h, hq, hs
+
+    def backward(self, dy, x, q, s, hq, hs):
+        dh, da, db = bw.gemm_fused_backward(dy, hq, hs, self.packed["down"], self.alpha["down"], self.D, self.F)
+        dxn, dg, du = bw.glu_backward(dh, q, s, self.packed["gate"], self.alpha["gate"], self.packed["up"],
+                                      self.alpha["up"], self.F, self.D)
+        _, mean, rstd = bw.layernorm(x, self.w, self.b, stats=True)
+        dx, dw, dbias = bw.layernorm_backward(dxn, x, mean, rstd, self.w)
+        return dx, da, dg, du, dw, dbias, dh, dxn
+
+
+@pytest.mark.parametrize("M", [1, 5, 16, 40, 100, 200])
+@pytest.mark.parametrize("t", list(ref.TYPES))
+def test_feed_forward_block(orc, M, t):
+    """Each step against its definition on what the step before it gave."""
+    D, F, dtype = 512, 1424, ref.TYPES[t]
+    blk = Block(orc, D, F, 700)
+    x = (2 * torch.randn((M, D), generator=_gen(M))).to(dtype)
+    y, q, s, h, hq, hs = blk.forward(x.cuda())
+    torch.cuda.synchronize()
+    rv, rs = ref.layernorm_quantize(x, blk.w.cpu(), blk.b.cpu(), 1e-5)
+    assert torch.equal(s.cpu(), rs)
+    assert bool(((q.cpu().double() == rv.round()) | ((rv - rv.floor() - 0.5).abs() < 1e-9)).all())
+    a = {k: v.cpu() for k, v in blk.alpha.items()}
+    check("h", h, *ref.glu(q.cpu(), s.cpu(), blk.T["gate"], a["gate"], blk.T["up"], a["up"], "silu", torch.float32))
+    check("y", y, *ref.gemm_fused(hq.cpu(), hs.cpu(), blk.T["down"], a["down"], None, "none", x, dtype))
+    dy = torch.randn((M, D), generator=_gen(M + 1)).to(dtype)
+    dx, da, dg, du, dw, db, dh, dxn = blk.backward(dy.cuda(), x.cuda(), q, s, hq, hs)
+    torch.cuda.synchronize()
+    want = ref.gemm_fused_backward(dy, hq.cpu(), hs.cpu(), blk.T["down"], a["down"], None, "none", dtype)
+    check("dh", dh, *want[0])
+    check("dalpha", da, *want[1])
+    want = ref.glu_backward(dh.cpu(), q.cpu(), s.cpu(), blk.T["gate"], a["gate"], blk.T["up"], a["up"], "silu", dtype)
+    for name, v, w in zip(("dxn", "dgate", "dup"), (dxn, dg, du), want):
+        check(name, v, *w)
+
+
+@pytest.mark.parametrize("M", [1, 7, 200])
+def test_captured_block_replays(orc, M):
+    """Forward and backward in one graph; replayed with new inputs, eager work
+    and synchronizations between the replays."""
+    blk = Block(orc, 256, 2048, 800)      # K = 2048 is split in the down projection at small M
+    x = torch.randn((M, 256), generator=_gen(1)).cuda()
+    dy = torch.randn((M, 256), generator=_gen(2)).cuda()
+
+    def work():
+        y, q, s, h, hq, hs = blk.forward(x)
+        return (y, h, *blk.backward(dy, x, q, s, hq, hs))
+
+    work()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = work()
+    for i in range(4):
+        x.copy_(torch.randn((M, 256), generator=_gen(10 + i)))
+        dy.copy_(torch.randn((M, 256), generator=_gen(20 + i)))
+        eager = [v.clone() for v in work()]
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(eager, held):
+            assert torch.equal(a, b)
+
+
+def test_two_graphs_and_eager_calls_side_by_side(orc):
+    """Split-K products captured into two graphs on one stream, replayed on
+    two streams at once beside eager calls on a third: each has cells of its
+    own, zeroed by itself, whichever is replayed first."""
+    N, K = 1024, 8192
+    T, packed, alpha = weights(orc, N, K, 1)
+    Tu, pu, au = weights(orc, N, K, 2)
+    alpha, au = alpha.cuda(), au.cuda()
+    data = [tokens(4, K, 50 + i) for i in range(3)]
+    dev = [(q.cuda(), s.cuda()) for q, s in data]
+    assert bw.lib().sherry_glu_workspace_bytes(4, N, K) > 0
+    run = lambda i: bw.glu(*dev[i], packed, alpha, pu, au, N, K)
+    want = [run(i).clone() for i in range(3)]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    graphs, held = [], []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            held.append(run(i))
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for order in ((1, 0), (0, 1), (1, 0)):
+        for h in held:
+            h.zero_()
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for i in order:
+                with torch.cuda.stream(streams[i]):
+                    graphs[i].replay()
+            with torch.cuda.stream(streams[2]):
+                eager = run(2)
+        torch.cuda.synchronize()
+        assert torch.equal(held[0], want[0]) and torch.equal(held[1], want[1]) and torch.equal(eager, want[2])
+    check("h", want[0], *ref.glu(*data[0], T, alpha.cpu(), Tu, au.cpu(), "silu", torch.float32))
+
+
+def test_calls_follow_the_current_stream(orc):
+    """Inputs written on a side stream, the operators called on it."""
+    blk = Block(orc, 512, 1024, 900)
+    x = torch.randn((9, 512), generator=_gen(3))
+    want = [v.clone() for v in blk.forward(x.cuda())]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        busy = torch.randn((4096, 4096), device="cuda")
+        for _ in range(4):
+            busy = busy @ busy * 1e-3
+        got = blk.forward(x.cuda() + 0 * busy[:9, :512].nan_to_num(0, 0, 0))
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_refusals_of_device_tensors(orc):
+    N, K = 64, 128
+    q, s = (v.cuda() for v in tokens(3, K, 1))
+    _, packed, alpha = weights(orc, N, K, 1)
+    alpha = alpha.cuda()
+    ok = dict(x=q, s_x=s, packed=packed, alpha=alpha, N=N, K=K)
+    bw.gemm_fused(**ok)
+    for kw in (dict(x=q.float()), dict(x=q[:, ::2]), dict(x=q.t()), dict(s_x=s[:2]), dict(s_x=s.double()),
+               dict(packed=packed[:-1]), dict(packed=packed.cpu()), dict(alpha=alpha[:32]), dict(alpha=alpha.half()),
+               dict(bias=alpha[:32]), dict(bias=alpha.cpu()), dict(residual=torch.zeros(3, N, device="cuda").half()),
+               dict(residual=torch.zeros(N, 3, device="cuda").t()), dict(residual=torch.zeros(2, N, device="cuda")),
+               dict(out=torch.zeros(3, N, device="cuda", dtype=torch.bfloat16)), dict(out=torch.zeros(3, N)),
+               dict(dtype=torch.int8), dict(workspace=torch.zeros(8, device="cuda")), dict(N=128), dict(K=256)):
+        with pytest.raises(RuntimeError):
+            bw.gemm_fused(**(ok | kw))
+    with pytest.raises(ValueError):
+        bw.gemm_fused(**ok, act="swish")
+    with pytest.raises(bw.SherryError):      # an output that is not 16-byte aligned
+        bw.gemm_fused(**ok, out=torch.zeros(3 * N + 1, device="cuda")[1:].view(3, N))
+    with pytest.raises(bw.SherryError):
+        bw.gemm_fused(q[:0], s[:0], packed, alpha, N, K)
+    with pytest.raises(bw.SherryError):      # a workspace of the caller's that is too small
+        T2, p2, a2 = weights(orc, 1024, 8192, 2)
+        bw.gemm_fused(*(v.cuda() for v in tokens(2, 8192, 2)), p2, a2.cuda(), 1024, 8192,
+                      workspace=torch.zeros(256, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(RuntimeError):
+        bw.glu_backward(torch.zeros(3, N, device="cuda", dtype=torch.float64), q, s, packed, alpha, packed, alpha, N, K)
+    x = torch.zeros((2, 130), device="cuda")
+    with pytest.raises(bw.SherryError):      # K % 4
+        bw.layernorm(x)
+    with pytest.raises(bw.SherryError):
+        bw.layernorm(x[:, :128].contiguous(), eps=0.0)
+    with pytest.raises(RuntimeError):
+        bw.layernorm(x[:, :128])
+    torch.cuda.synchronize()

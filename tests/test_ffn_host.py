@@ -158,7 +158,10 @@ def test_python_refusals():
         bw.layernorm(torch.zeros(2, 128))
     with pytest.raises(RuntimeError):
         bw.layernorm(torch.zeros(2, 128, dtype=torch.float64))
-    with pytest.raises(ValueError):
-        bw._act_code("swish")
-    with pytest.raises(RuntimeError):
-        bw._dtype_code(torch.int8)
+    for bad in (None, "x", 3):
+        with pytest.raises(TypeError):
+            bw.gemm_fused(bad, s, packed, alpha, 64, 128)
+        with pytest.raises(TypeError):
+            bw.layernorm(bad)
+    with pytest.raises(TypeError):
+        bw.glu(q, s, packed, alpha, packed, alpha, "64", 128)
