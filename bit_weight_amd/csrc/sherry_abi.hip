@@ -326,16 +326,30 @@ GemmPlan plan_epilogue(int M, int N, int K) {
   return p.path == 0 ? plan_mfma_gemv(M, N, K) : p;
 }
 
-// The gated product's plan: that of one product over both matrices' row
-// tiles, whose workgroups pair a gate tile with the up tile of the same
-// outputs.  On the GEMV the paired workgroup has the waves of both.
+// The gated product's plan.  Path and prefill tiles: those of one product over
+// both matrices' row tiles.  On the GEMV a workgroup pairs a gate row tile
+// with the up row tile of the same outputs and has 4 waves for each, with K
+// split until the grid fills the CUs once (at least one k-tile per wave), and
+// up to 8 tokens until a wave has at most 8 k-tiles (the straight-line form);
+// 8 waves for each where the row tiles fill the CUs without a split and K is
+// longer than that.  Measured against twice the product's waves at its
+// splits (bf16, us): M=1, K=4096, N=11008 7.3 -> 6.1, N=14336 7.2 -> 6.2,
+// N=4096 6.5 -> 5.1; M=8 at N=11008 8.7 -> 6.4, at N=4096, K=11008 9.5 ->
+// 7.0; M=16 at N=8192, K=8192 12.4 -> 9.6; M=64 at N=4096, K=14336 26.1 ->
+// 20.1; 8 waves each against 4 at N=28672, K=8192: M=8 18.6 -> 17.4, M=1
+// 17.3 -> 16.0.
 GemmPlan plan_glu(int M, int N, int K) {
-  const int both = 2 * kTileRows * row_tiles(N);
-  const GemmPlan p = plan_epilogue(M, both, K);
+  const int KT = k_tiles(K), RT = row_tiles(N);
+  const GemmPlan p = plan_epilogue(M, 2 * kTileRows * RT, K);
   if (p.path == 1) return p;   // n tiles of kBN / 2 outputs: as many as of kBN rows of both
   const int m = M < kGemvMaxM ? M : kGemvMaxM;
-  const int kw = 2 * p.rw > 16 || m > 16 ? (m > 16 ? 8 : 16) : 2 * p.rw;
-  GemmPlan q = mfma_gemv_plan_of(m, N, K, kw, p.splits < kGluMaxSplits ? p.splits : kGluMaxSplits);
+  int kw = RT > kCUs && KT > 32 && m <= 16 ? 8 : 4;
+  int splits = RT > kCUs ? 1 : kCUs / RT;
+  if (splits > KT / kw) splits = KT / kw;
+  if (m <= 8 && splits < (KT + 8 * kw - 1) / (8 * kw)) splits = (KT + 8 * kw - 1) / (8 * kw);
+  if (g_ovr_rw.load() > 0) kw = p.rw > 4 && m <= 16 ? 8 : 4;
+  if (g_ovr_splits.load() > 0) splits = p.splits;
+  GemmPlan q = mfma_gemv_plan_of(m, N, K, 2 * kw, splits < kGluMaxSplits ? splits : kGluMaxSplits);
   q.chunk = p.chunk;
   return q;
 }
