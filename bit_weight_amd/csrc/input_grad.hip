@@ -32,6 +32,9 @@ namespace {
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 typedef unsigned int v4u __attribute__((ext_vector_type(4)));
 
+template <int I>
+using Const = std::integral_constant<int, I>;
+
 constexpr int kPrepThreads = 256;
 constexpr int kHalfBytes = 1024;   // a 64-row x 64-column half tile in operand order
 
@@ -181,11 +184,21 @@ __global__ __launch_bounds__(kPrepThreads) void grad_prepare_kernel(PrepareArgs 
 // workgroup BM = 32 MT tokens x 256 columns, over a share of the row tiles
 // (64 contraction indices a step, 128 bytes of z per token).
 //  * z: copied once per workgroup straight into LDS (buffer loads with LDS
-//    return), three buffers, two steps ahead; rows of 128 bytes whose 16-byte
-//    chunks are XOR-swizzled so 16 rows' reads of one chunk hit 16 bank groups.
-//  * T: each wave loads its half tile's 16 bytes a lane two steps ahead and
+//    return), four buffers, up to three steps ahead; rows of 128 bytes whose
+//    16-byte chunks are XOR-swizzled so 16 rows' reads of one chunk hit 16
+//    bank groups.  A buffer is an array of its own, picked by a constant: the
+//    compiler then sees that a step's reads cannot touch what the copies in
+//    flight write (from one array it waits for every copy before the first
+//    read of each step).
+//  * T: each wave loads its half tile's 16 bytes a lane three steps ahead and
 //    makes its operands with shifts and masks between the MFMAs.
-//  * the barrier of a step waits for that step's copies only (counted vmcnt).
+//  * A step is two sub-steps.  Between them a wave waits for its copies of the
+//    next step (counted vmcnt, the newer loads stay in flight) and joins the
+//    barrier; behind it are the copies into the buffer every wave has left by
+//    then, and the next step's first fragments and operands, under the second
+//    sub-step's MFMAs.  A step so starts with MFMAs (with the barrier in front
+//    of the step and three buffers: M=2048, K=4096, 448 row tiles 330 us; so
+//    317, 1.52 PFLOP/s, what the vendor's fp16 product of 8192^3 reaches).
 // Workgroups of one XCD take neighbouring column tiles of the same tokens,
 // so a z tile is read from HBM once and then from that XCD's L2.
 constexpr int kGradThreads = 512;
@@ -207,7 +220,8 @@ struct InputGradArgs {
 
 __device__ __forceinline__ int z_off(int r, int c) { return (r * 8 + (c ^ ((r >> 1) & 7))) * 16; }
 
-constexpr int wait_vm_lgkm0(int vm) { return (vm & 15) | ((vm >> 4) << 14) | 0x70; }
+// s_waitcnt operand: vmcnt(vm) only.
+constexpr int wait_vm(int vm) { return (vm & 15) | ((vm >> 4) << 14) | 0x0F70; }
 
 __device__ __forceinline__ void z_to_lds(__amdgpu_buffer_rsrc_t r, uint8_t* dst, int voffset, int soffset) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 16, voffset, soffset,
@@ -222,22 +236,20 @@ template <int MT>
 __global__ __launch_bounds__(kGradThreads) void input_grad_kernel(InputGradArgs a) {
   constexpr int BM = 32 * MT;
   constexpr int kStage = BM * 128;                       // bytes of z per step
-  constexpr int kCopies = MT >= 2 ? MT / 2 : 1;          // 8-row copies per wave and step
-  // loads a wave issues after a step's copies and before its barrier: the
-  // weights two steps (first: one and two) ahead, the next copies, weights
-  constexpr int kNewer = kCopies + 2;
-  // one array per buffer, picked by constants: the compiler then sees that a
-  // step's reads cannot touch what the copies in flight write (from one
-  // array it waits for every copy before the first read of each step)
-  __shared__ __attribute__((aligned(1024))) uint8_t z0[kStage], z1[kStage], z2[kStage];
+  static_assert(MT % 2 == 0, "fragments are taken in pairs");
+  constexpr int kCopies = MT / 2;                        // 8-row copies per wave and step
+  constexpr int kDecode = MT >= 8 ? 1 : 8 / MT;          // column blocks decoded per pair of fragments
+  __shared__ __attribute__((aligned(1024))) uint8_t z0[kStage], z1[kStage], z2[kStage], z3[kStage];
   __shared__ float back[BM];   // 2^-e / 2 of each token
 
   const int NT = (a.K + kGradBN - 1) / kGradBN, MTiles = (a.M + BM - 1) / BM;
   const int total = NT * MTiles * a.splits, per = (total + 7) / 8;
   const int id = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
   if ((int)(blockIdx.x >> 3) >= per || id >= total) return;
-  const int group = id / NT, nt = id - group * NT;
-  const int mt = group / a.splits, split = group - mt * a.splits;
+  // (quotients come from the vector unit; made scalar, the buffer descriptors
+  // that follow from them stay scalar)
+  const int group = __builtin_amdgcn_readfirstlane(id / NT), nt = id - group * NT;
+  const int mt = __builtin_amdgcn_readfirstlane(group / a.splits), split = group - mt * a.splits;
   const int m0 = mt * BM;
   const int r0 = split * a.r_per_split, r1 = min(a.R, r0 + a.r_per_split);
   const int tid = threadIdx.x, lane = tid & 63;
@@ -263,7 +275,7 @@ __global__ __launch_bounds__(kGradThreads) void input_grad_kernel(InputGradArgs 
   int z_v[kCopies], z_row[kCopies];
 #pragma unroll
   for (int jj = 0; jj < kCopies; ++jj) {
-    z_row[jj] = 8 * ((wave * kCopies + jj) % (BM / 8));
+    z_row[jj] = 8 * (wave * kCopies + jj);
     const int row = z_row[jj] + (lane >> 3);
     const int c = (lane & 7) ^ ((row >> 1) & 7);
     z_v[jj] = min(row, a.M - 1 - m0) * (int)(2 * zrow) + 16 * c;
@@ -287,59 +299,91 @@ __global__ __launch_bounds__(kGradThreads) void input_grad_kernel(InputGradArgs 
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = f4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  // One step on buffer zs: its copies and those of the step before it have
-  // been read, so the copy of step st + 2 may go to `next`; w holds this
-  // step's weights and takes those of step st + 3.
-  auto step = [&](int st, const uint8_t* zs, uint8_t* next, v4u& w) {
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(kNewer));
+  auto frag = [&](const uint8_t* buf, int u) __attribute__((always_inline)) {   // u = MT s + row block
+    return *reinterpret_cast<const h8*>(buf + z_off(16 * (MT * wm + u % MT) + l16, 4 * (u / MT) + g));
+  };
+  auto decode = [&](const v4u& w, int s, int j) __attribute__((always_inline)) {
+    const uint32_t d = w[2 * s + (j >> 1)];
+    v4u o;
+#pragma unroll
+    for (int p = 0; p < 4; ++p) o[p] = (d << (2 * (4 * (j & 1) + p))) & 0xC000C000u;
+    return __builtin_bit_cast(h8, o);
+  };
+  h8 f0, f1, even[4], odd[4];   // fragments; operands of sub-steps 0 and 1
+  // sub-step s on `now`: per pair of fragments its 8 MFMAs, the request of the
+  // fragments two ahead and a share of decoding the sub-step after it
+  auto sub_step = [&](auto sc, const uint8_t* buf, const uint8_t* next, const h8 (&now)[4], h8 (&then)[4],
+                  const v4u& w) __attribute__((always_inline)) {
+    constexpr int s = decltype(sc)::value;
+#pragma unroll
+    for (int i = 0; i < MT; i += 2) {
+      const int u = MT * s + i;
+      const h8 p0 = u + 2 < 2 * MT ? frag(buf, u + 2) : frag(next, u + 2 - 2 * MT);
+      const h8 p1 = u + 3 < 2 * MT ? frag(buf, u + 3) : frag(next, u + 3 - 2 * MT);
+#pragma unroll
+      for (int d = 0; d < kDecode; ++d) {
+        const int j = (i / 2) * kDecode + d;
+        if (j < 4) then[j] = decode(w, 1 - s, j);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f0, now[j], acc[i][j], 0, 0, 0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        acc[i + 1][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f1, now[j], acc[i + 1][j], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+      f0 = p0;
+      f1 = p1;
+    }
+  };
+  // Step st on buffer buf with weights w; next / wn are the next step's, far /
+  // wf those that step st + 3 goes to.
+  auto step = [&](int st, const uint8_t* buf, const uint8_t* next, uint8_t* far, const v4u& w, const v4u& wn,
+                  v4u& wf) __attribute__((always_inline)) {
+    sub_step(Const<0>{}, buf, next, even, odd, w);
+    // newer than the next step's copies: its weights, the copies after them
+    // and theirs
+    __builtin_amdgcn_s_waitcnt(wait_vm(kCopies + 2));
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
     __builtin_amdgcn_sched_barrier(0);
-    copy_z(st + 2, next);
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      h8 bw[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t d = w[2 * s + (j >> 1)];
-        v4u o;
-#pragma unroll
-        for (int p = 0; p < 4; ++p) o[p] = (d << (2 * (4 * (j & 1) + p))) & 0xC000C000u;
-        bw[j] = __builtin_bit_cast(h8, o);
-      }
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        const h8 az = *reinterpret_cast<const h8*>(zs + z_off(16 * (MT * wm + i) + l16, 4 * s + g));
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(az, bw[j], acc[i][j], 0, 0, 0);
-      }
-    }
+    copy_z(st + 3, far);
+    load_w(st + 3, wf);
     __builtin_amdgcn_sched_barrier(0);
-    load_w(st + 3, w);
+    sub_step(Const<1>{}, buf, next, odd, even, wn);
   };
 
-  // issue order: z 0, w 0, z 1, w 1, w 2, then per step: z st + 2, w st + 3
-  v4u w0, w1, w2;
+  v4u w0, w1, w2, w3;
   copy_z(0, z0);
   load_w(0, w0);
   __builtin_amdgcn_sched_barrier(0);
   copy_z(1, z1);
   load_w(1, w1);
   __builtin_amdgcn_sched_barrier(0);
+  copy_z(2, z2);
   load_w(2, w2);
   __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_waitcnt(wait_vm(2 * kCopies + 3));
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+  __builtin_amdgcn_sched_barrier(0);
+  f0 = frag(z0, 0);
+  f1 = frag(z0, 1);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) even[j] = decode(w0, 0, j);
   int st = 0;
-  for (; st + 3 <= steps; st += 3) {
-    step(st, z0, z2, w0);
-    step(st + 1, z1, z0, w1);
-    step(st + 2, z2, z1, w2);
+  for (; st + 4 <= steps; st += 4) {
+    step(st, z0, z1, z3, w0, w1, w3);
+    step(st + 1, z1, z2, z0, w1, w2, w0);
+    step(st + 2, z2, z3, z1, w2, w3, w1);
+    step(st + 3, z3, z0, z2, w3, w0, w2);
   }
-  if (st < steps) step(st, z0, z2, w0);
-  if (st + 1 < steps) step(st + 1, z1, z0, w1);
+  if (st < steps) step(st, z0, z1, z3, w0, w1, w3);
+  if (st + 1 < steps) step(st + 1, z1, z2, z0, w1, w2, w0);
+  if (st + 2 < steps) step(st + 2, z2, z3, z1, w2, w3, w1);
   // the clamped copies past the end land before the workgroup's LDS is freed
-  __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(0));
-  __syncthreads();   // (and `back` is visible where steps is 0)
+  __builtin_amdgcn_s_waitcnt(wait_vm(0));
+  __syncthreads();
 
   // lane (l16, g) of accumulator (i, j): rows 4g .. 4g+3 of row block i,
   // column 4 l16 + j of this wave's 64
@@ -408,7 +452,7 @@ GradPlan plan_grad(const GemmPlan& product, int M, int N, int K, int parts, int 
   GradPlan p{};
   p.terms = dtype == SHERRY_BF16 ? 1 : 2;
   p.R = parts * row_tiles(N);
-  p.mt = M > 384 ? 8 : M > 64 ? 4 : M > 32 ? 2 : 1;
+  p.mt = M > 384 ? 8 : M > 64 ? 4 : 2;
   const int tiles = ((M + 32 * p.mt - 1) / (32 * p.mt)) * ((K + kGradBN - 1) / kGradBN);
   int splits = kCUs / tiles;
   if (splits > p.R / 3) splits = p.R / 3;
@@ -492,7 +536,6 @@ hipError_t launch_backward(const GemmPlan& product, const GradPlan& p, const Gem
   const int total = ((a.K + kGradBN - 1) / kGradBN) * ((a.M + bm - 1) / bm) * p.splits;
   const dim3 grid(8 * ((total + 7) / 8)), block(kGradThreads);
   switch (p.mt) {
-    case 1: hipLaunchKernelGGL(input_grad_kernel<1>, grid, block, 0, stream, g); break;
     case 2: hipLaunchKernelGGL(input_grad_kernel<2>, grid, block, 0, stream, g); break;
     case 4: hipLaunchKernelGGL(input_grad_kernel<4>, grid, block, 0, stream, g); break;
     default: hipLaunchKernelGGL(input_grad_kernel<8>, grid, block, 0, stream, g); break;

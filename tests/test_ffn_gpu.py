@@ -57,7 +57,8 @@ def check(name, got, want, bound):
 # and not; every path and tile shape of the product
 SHAPES = [(1, 4, 16), (1, 4096, 4096), (2, 1100, 2064), (3, 68, 11008), (7, 8192, 1024), (8, 260, 272),
           (16, 1300, 1040), (17, 4096, 512), (33, 132, 4096), (64, 2052, 784), (65, 300, 8192), (100, 516, 2048),
-          (129, 1028, 400), (300, 640, 1296), (260, 16644, 256), (513, 4100, 144)]
+          (129, 1028, 400), (300, 640, 1296), (260, 16644, 256), (513, 4100, 144),
+          (300, 24580, 144), (513, 8196, 272), (256, 16388, 1040)]
 
 
 @pytest.mark.parametrize("i,shape", list(enumerate(SHAPES)))
@@ -145,7 +146,7 @@ def test_rows_and_columns_around_the_output_stay(orc):
 # (M, N, K): token tiles of 32 to 256 (one, several, ragged), sums over 1 to
 # many row tiles, split and not, columns past the last half tile
 BACK = [(1, 4, 16), (1, 640, 272), (31, 68, 144), (33, 132, 1040), (64, 1100, 528), (77, 1300, 1040),
-        (130, 516, 2064), (300, 1100, 528), (385, 64, 272), (520, 260, 784), (700, 2112, 336), (140, 4160, 512)]
+        (130, 516, 2064), (300, 1100, 528), (385, 64, 272), (520, 260, 784), (700, 2112, 336), (140, 4160, 512), (300, 12292, 272), (260, 24580, 144)]
 
 
 @pytest.mark.parametrize("i,shape", list(enumerate(BACK)))
