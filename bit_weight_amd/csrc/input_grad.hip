@@ -204,6 +204,7 @@ __global__ __launch_bounds__(kPrepThreads) void grad_prepare_kernel(PrepareArgs 
 constexpr int kGradThreads = 512;
 constexpr int kGradBN = 256;
 constexpr int kStepK = 64;
+constexpr int kMaxSplits = 64;     // of the contraction
 
 struct InputGradArgs {
   const uint8_t* codes;
@@ -443,22 +444,41 @@ size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace
 
-// Tokens per workgroup tile (32 MT) and contraction splits: tiles of 256
-// tokens read the least z and T per multiply-add, smaller ones waste less of
-// few tokens; splits until the grid fills the CUs once, each of at least 3
-// row tiles (against 8, 4 and 2: M=77, K=1040, N=1300 gated, 42 row tiles, 34.9,
-// 31.1, 31.1 -> 30.3 us; M=300, K=2064, N=1100 38.5, 34.5, 34.2 -> 33.4).
+// Tokens per workgroup tile (32 MT) and contraction splits: the pair with the
+// least estimated time.  A workgroup takes a fixed time and a time per step
+// (us, measured with one workgroup per CU, 56 and 448 steps: MT = 2 36 and
+// 248, MT = 4 52 and 366, MT = 8 90 and 660); larger tiles read less z and T
+// per multiply-add, smaller ones waste less of few tokens and fill the CUs
+// with fewer splits, whose partial results are written and read again at
+// about 6 TB/s.  (Against 256 tokens from 385 on, 128 from 65 on and as many
+// splits as fill the CUs, whole backward pass, bf16: M=512, N=K=4096 55.4 -> 46.2
+// us; M=128 gated there 41.9 -> 39.5; M=512 gated, N=11008 160.9 -> 155.8; fp16
+// M=1500, N=K=2048 63.6 -> 59.6.)
+void plan_tiles(int M, int K, GradPlan& p) {
+  constexpr struct { int mt; double fixed, step; } kTiles[] = {{2, 5.5, 0.54}, {4, 7.0, 0.80}, {8, 9.0, 1.45}};
+  double best = 0.0;
+  for (const auto& t : kTiles) {
+    const double tiles = (double)((M + 32 * t.mt - 1) / (32 * t.mt)) * ((K + kGradBN - 1) / kGradBN);
+    for (int s = 1; s <= kMaxSplits && s <= p.R; ++s) {
+      const int r = (p.R + s - 1) / s;
+      if ((p.R + r - 1) / r != s) continue;   // no empty split
+      double time = ceil(tiles * s / kCUs) * (t.fixed + (double)r * p.terms * t.step);
+      if (s > 1) time += 2.0 + (double)s * M * K * 8.0 / 6.0e6;
+      if (best == 0.0 || time < best) {
+        best = time;
+        p.mt = t.mt;
+        p.splits = s;
+        p.r_per_split = r;
+      }
+    }
+  }
+}
+
 GradPlan plan_grad(const GemmPlan& product, int M, int N, int K, int parts, int dtype) {
   GradPlan p{};
   p.terms = dtype == SHERRY_BF16 ? 1 : 2;
   p.R = parts * row_tiles(N);
-  p.mt = M > 384 ? 8 : M > 64 ? 4 : 2;
-  const int tiles = ((M + 32 * p.mt - 1) / (32 * p.mt)) * ((K + kGradBN - 1) / kGradBN);
-  int splits = kCUs / tiles;
-  if (splits > p.R / 3) splits = p.R / 3;
-  if (splits < 1) splits = 1;
-  p.r_per_split = (p.R + splits - 1) / splits;
-  p.splits = (p.R + p.r_per_split - 1) / p.r_per_split;
+  plan_tiles(M, K, p);
   p.token_tiles = (M + 64 * product.rw - 1) / (64 * product.rw);
   size_t at = 0;
   auto take = [&](size_t bytes) {
