@@ -1,7 +1,7 @@
 // Gradients of the products with an epilogue.  Three steps, the scratch
 // memory between them:
-//  1. grad_prepare_kernel reads what bounds the gradients (per token max|dy|
-//     and sum|q|, per matrix max|alpha|) and lays the weight codes out for
+//  1. grad_prepare_kernel reads what bounds the finite gradients (per token
+//     max|dy| and sum|q|, per matrix max|alpha|) and lays the weight codes out for
 //     step 3;
 //  2. the forward's prefill kernel recomputes the exact sums (1.25 bits per
 //     weight: cheaper than saving M x N fp32 values in the forward) and its
@@ -52,6 +52,12 @@ struct PrepareArgs {
   int parts, dtype, M, N, K;
 };
 
+// |v|, or 0 where v is infinite or NaN: a bound on the finite gradients.
+__device__ __forceinline__ float finite_abs(float v) {
+  const float t = fabsf(v);
+  return t <= 3.402823466e38f ? t : 0.0f;
+}
+
 __device__ __forceinline__ float block_top(float v, float* red) {
   v = wave_max(v);
   __syncthreads();
@@ -86,7 +92,7 @@ __global__ __launch_bounds__(kPrepThreads) void grad_prepare_kernel(PrepareArgs 
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) v[i] = vec[min(n0 + i * kPrepThreads, a.N - 1)];
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) t = fmaxf(t, fabsf(v[i]));
+      for (int i = 0; i < kAhead; ++i) t = fmaxf(t, finite_abs(v[i]));
     }
     t = block_top(t, red);
     if (tid == 0) a.tops[blockIdx.x] = t;
@@ -103,7 +109,8 @@ __global__ __launch_bounds__(kPrepThreads) void grad_prepare_kernel(PrepareArgs 
         v[i] = load4_as(a.dy, (size_t)m * a.N + min(n0 + 4 * i * kPrepThreads, a.N - 4), a.dtype);
 #pragma unroll
       for (int i = 0; i < kAhead / 4; ++i)
-        t = fmaxf(fmaxf(t, fmaxf(fabsf(v[i][0]), fabsf(v[i][1]))), fmaxf(fabsf(v[i][2]), fabsf(v[i][3])));
+        t = fmaxf(fmaxf(t, fmaxf(finite_abs(v[i][0]), finite_abs(v[i][1]))),
+                  fmaxf(finite_abs(v[i][2]), finite_abs(v[i][3])));
     }
     int s = 0;
     const int4* q = reinterpret_cast<const int4*>(a.q + (size_t)m * a.K);

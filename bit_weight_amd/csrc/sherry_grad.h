@@ -19,13 +19,13 @@
 namespace sherry {
 
 // e such that |z| 2^e <= 2^15 for every z of a token: rows = (max |dy|,
-// sum |q|), tops = (max |alpha|, max |alpha2|, max |bias|).  Infinite
-// gradients take the least scale, so that they alone overflow.
+// sum |q|), tops = (max |alpha|, max |alpha2|, max |bias|), the maxima over
+// finite values: an infinite or NaN gradient is one whatever the scale.
 __device__ __forceinline__ int grad_exponent(float2 row, float s_x, const float* tops, int act, bool glu) {
   const double dy = row.x, sum = (double)row.y * fabs((double)s_x);
   const double a1 = tops[0], a2 = tops[1], pre = sum * a1 + (glu ? 0.0 : (double)tops[2]);
   const double slope = act == SHERRY_ACT_RELU2 ? 2.0 * pre : 1.25;
-  const double bound = glu ? dy * slope * a1 * fmax(sum, 1e-300) * a2 : dy * slope * a1;
+  const double bound = glu ? dy * slope * a1 * sum * a2 : dy * slope * a1;
   if (!(bound > 0.0)) return 0;
   if (bound > 1e300) return -120;
   const int e = 15 - (ilogb(bound) + 1);

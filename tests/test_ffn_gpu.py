@@ -223,6 +223,24 @@ def test_backward_infinite_and_nan_gradients_stay_in_their_token(orc):
     assert bool(dx[11].isnan().all())
 
 
+def test_backward_with_outputs_masked_by_their_bias(orc):
+    """A bias of -inf closes an output under relu and relu2: its gradients are
+    0 and the others' are as without it."""
+    M, N, K = 35, 132, 272
+    q, s = tokens(M, K, 1)
+    T, packed, alpha = weights(orc, N, K, 2)
+    bias = torch.randn(N, generator=_gen(5))
+    dy = torch.randn((M, N), generator=_gen(6))
+    open_ = torch.arange(N) % 5 != 2
+    for name in ("relu", "relu2"):
+        masked = torch.where(open_, bias, float("-inf"))
+        got = bw.gemm_fused_backward(dy.cuda(), q.cuda(), s.cuda(), packed, alpha.cuda(), N, K, bias=masked.cuda(), act=name)
+        torch.cuda.synchronize()
+        want = ref.gemm_fused_backward(torch.where(open_, dy, 0.0), q, s, T, alpha, bias, name, torch.float32)
+        for what, v, w in zip(("dx", "dalpha", "dbias"), got, want):
+            check(what, v, *w)
+
+
 @pytest.mark.parametrize("name", ref.ACTS[3:])
 def test_backward_against_differences(orc, name):
     """dalpha and dbias against central differences of the forward in fp32:
