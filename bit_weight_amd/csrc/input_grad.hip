@@ -486,7 +486,8 @@ GradPlan plan_grad(const GemmPlan& product, int M, int N, int K, int parts, int 
   p.terms = dtype == SHERRY_BF16 ? 1 : 2;
   p.R = parts * row_tiles(N);
   plan_tiles(M, K, p);
-  p.token_tiles = (M + 64 * product.rw - 1) / (64 * product.rw);
+  const int bm = product.rw ? 64 * product.rw : 32;   // tokens per tile of the recomputing product
+  p.token_tiles = (M + bm - 1) / bm;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t here = at;

@@ -73,7 +73,7 @@ struct Tiling {
   // buffers (the copy for step j+2 issued in step j), or two with 128-row
   // tiles and 4 phases, whose 4 x 3 x 16 KB would not fit LDS (the copy for
   // step j+1 issued in step j).
-  static constexpr bool kPair = BM == 64;
+  static constexpr bool kPair = BM <= 64;
   static constexpr int kABufs = kPair ? 4 : (BM == 128 && KP == 4 ? 2 : 3);
   static constexpr int kRT = kThreads / 64 / KP;       // row tiles per workgroup (4 or 2)
   static constexpr int kBN = kRT * kTileRows;          // workgroup tile width (256 or 128 weight rows)
@@ -708,10 +708,13 @@ hipError_t launch_tiles(const GemmPlan& p, const GemmArgs& a, hipStream_t stream
   return hipGetLastError();
 }
 
-// plan.rw carries the tile height in units of 64 activation rows (1 or 2),
-// plan.ch the k-phases (2 or 4).
+// plan.rw carries the tile height in units of 64 activation rows (1 or 2; 0: 32
+// rows, the backward epilogues only), plan.ch the k-phases (2 or 4).
 template <int EP>
 hipError_t launch_ep(const GemmPlan& p, const GemmArgs& a, hipStream_t stream, const EpilogueOf<EP>& e) {
+  if constexpr (ep_back(EP)) {
+    if (p.rw == 0 && p.ch == 4) return launch_tiles<32, 4, EP>(p, a, stream, e);
+  }
   if (p.rw == 1 && p.ch == 4) return launch_tiles<64, 4, EP>(p, a, stream, e);
   if (p.rw == 1 && p.ch == 2) return launch_tiles<64, 2, EP>(p, a, stream, e);
   if (p.rw == 2 && p.ch == 4) return launch_tiles<128, 4, EP>(p, a, stream, e);

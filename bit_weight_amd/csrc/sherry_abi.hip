@@ -356,7 +356,15 @@ GemmPlan plan_glu(int M, int N, int K) {
 
 // The product that a backward pass recomputes: always the prefill kernel.
 GemmPlan plan_recompute(int M, int N, int K, bool glu) {
-  return plan_prefill(M, glu ? 2 * kTileRows * row_tiles(N) : N, K);
+  const int rows = glu ? 2 * kTileRows * row_tiles(N) : N;
+  GemmPlan p = plan_prefill(M, rows, K);
+  const long long tiles32 = (long long)((M + 31) / 32) * ((rows + 127) / 128);
+  if (g_ovr_path.load() < 0 && tiles32 <= kCUs) {
+    p.rw = 0;
+    p.ch = 4;
+    p.grid = mfma_gemm_grid(M, rows, 32, 4);
+  }
+  return p;
 }
 
 hipError_t launch_product_epilogue(const GemmPlan& plan, const GemmArgs& args, int ep,
