@@ -427,8 +427,17 @@ __global__ __launch_bounds__(256) void grad_finish_kernel(FinishArgs a) {
   if ((int)blockIdx.x < a.dx_blocks) {
     const size_t n4 = (size_t)a.M * a.K / 4;
     for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += (size_t)a.dx_blocks * 256) {
+      // eight splits' loads in flight at a time, added in order
       f4 t = load4(a.dx_part + 4 * i);
-      for (int s = 1; s < a.splits; ++s) t += load4(a.dx_part + (size_t)s * 4 * n4 + 4 * i);
+      for (int s0 = 1; s0 < a.splits; s0 += 8) {
+        f4 v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (s0 + j < a.splits) v[j] = load4(a.dx_part + (size_t)(s0 + j) * 4 * n4 + 4 * i);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (s0 + j < a.splits) t += v[j];
+      }
       store4_as(a.dx, 4 * i, a.dtype, t);
     }
     return;
@@ -440,8 +449,10 @@ __global__ __launch_bounds__(256) void grad_finish_kernel(FinishArgs a) {
   const int lane = threadIdx.x & 63, share = threadIdx.x >> 6;
   const int n = (c - which * col_blocks) * 64 + lane;
   float t = 0.0f;
-  if (n < a.N)
+  if (n < a.N) {
+#pragma unroll 4
     for (int r = share; r < a.tiles; r += 4) t += part[(size_t)r * a.N + n];
+  }
   red[share][lane] = t;
   __syncthreads();
   if (share == 0 && n < a.N) a.out[which][n] = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
