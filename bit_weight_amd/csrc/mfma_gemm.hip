@@ -536,8 +536,8 @@ __global__ __launch_bounds__(kThreads) void mfma_gemm_kernel(const uint8_t* pack
   // epilogue reuses
   __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
 
-  // Epilogue, 32 rows (two row blocks) at a time: every wave writes its raw
-  // int32 sums into its phase's row-major LDS tile, then each thread adds
+  // Epilogue, 32 rows (two row blocks) at a time, 16 in the forms other than
+  // kEpNone: every wave writes its raw int32 sums into its phase's row-major LDS tile, then each thread adds
   // the KP phases for 4 consecutive columns of one row and stores
   // y = ((float)acc * s_x[m]) * alpha[n] (or the int32 sum), 16 bytes per
   // lane, so each store instruction writes whole 128-byte lines, marked
@@ -622,7 +622,8 @@ __global__ __launch_bounds__(kThreads) void mfma_gemm_kernel(const uint8_t* pack
       } else if (has_in) {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i)
-          if (row_of(first + i) < M) io[i] = load4_raw(in, (size_t)row_of(first + i) * N + n, SHERRY_F16);   // (either 16-bit type)
+          if (row_of(first + i) < M)   // (either 16-bit type)
+            io[i] = load4_raw(in, (size_t)row_of(first + i) * N + n, SHERRY_F16);
       }
     };
     load_in(0);
@@ -649,7 +650,8 @@ __global__ __launch_bounds__(kThreads) void mfma_gemm_kernel(const uint8_t* pack
 #pragma unroll
         for (int ph = 0; ph < KP; ++ph) {
           s1 += *reinterpret_cast<const v4i*>(&ot[(ph * kTurnRows + ml) * kOutLd + 4 * c4]);
-          if constexpr (kGlu) s2 += *reinterpret_cast<const v4i*>(&ot[(ph * kTurnRows + ml) * kOutLd + kBNO + 4 * c4]);
+          if constexpr (kGlu)
+            s2 += *reinterpret_cast<const v4i*>(&ot[(ph * kTurnRows + ml) * kOutLd + kBNO + 4 * c4]);
         }
         const float sx = sxs[kTurnRows * qq + ml];
         const f4 in4 = as_f4(io[(qq * kTurns + k) % kAhead], e.dtype);

@@ -453,7 +453,7 @@ __global__ __launch_bounds__(64 * KW) void mfma_gemv_kernel(const uint8_t* packe
 #pragma unroll
         for (int i = 0; i < TPW; ++i) {
           const int m = 16 * b + q * TPW + i;
-          if (m < M) res[b][i] = load1_raw(e.residual, (size_t)m * N + n, SHERRY_F16);   // (either 16-bit type)
+          if (m < M) res[b][i] = load1_raw(e.residual, (size_t)m * N + n, SHERRY_F16);   // (or bf16)
         }
     }
   }

@@ -78,7 +78,7 @@ enum Epilogue {
 constexpr bool ep_glu(int ep) { return ep == kEpGlu || ep == kEpGluBack; }
 constexpr bool ep_back(int ep) { return ep == kEpFusedBack || ep == kEpGluBack; }
 
-// Arguments of the epilogues other than kEpNone (kEpNone's kernels take none).
+// Arguments of the epilogues other than kEpNone (whose kernels take an empty struct).
 struct EpilogueArgs {
   const uint8_t* packed2;   // GLU: the up matrix; packed / alpha are the gate's
   const float* alpha2;
@@ -96,10 +96,10 @@ using EpilogueOf = std::conditional_t<EP == kEpNone, NoEpilogueArgs, EpilogueArg
 // a GemmArgs struct, with the ones their first instructions need in front:
 // packed, x, xf, M, N, K, two plan integers (the GEMVs: splits and k-tiles
 // per split; the prefill GEMM: n tiles and 0), then s_x, alpha, y, acc,
-// partials, and the epilogue's where there is one.  The build has the leading ones preloaded into SGPRs at
-// dispatch (gfx950 kernel-argument preload), which removes a memory round
-// trip from the start of every launch; a struct argument cannot be
-// preloaded.
+// partials, and last the epilogue's (the matrix-core kernels).  The build
+// has the leading ones preloaded into SGPRs at dispatch (gfx950
+// kernel-argument preload), which removes a memory round trip from the start
+// of every launch; a struct argument cannot be preloaded.
 template <typename Kernel, typename... E>
 inline void launch_product_kernel(Kernel kernel, dim3 grid, dim3 block, size_t lds_bytes,
                                   hipStream_t stream, const GemmArgs& a, int plan0, int plan1, E... e) {

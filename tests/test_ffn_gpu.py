@@ -265,6 +265,77 @@ def test_backward_against_differences(orc, name):
     check("dalpha", da, fd_a, tol * p.abs().max())
 
 
+@pytest.mark.parametrize("name", ref.ACTS[3:])
+@pytest.mark.parametrize("M", [9, 70])
+def test_gated_backward_against_differences(orc, name, M):
+    """Along t, at 1, with h(t) = act(t g) t u (the token's scale), act(t g) u
+    (alpha_gate) and act(g) t u (alpha_up): central differences of the
+    forward in fp32 against the gradients.  A step of d leaves d^2 / 6 times
+    the third derivative, with |act''|, |act'''| <= 1.2 at most 1.2 |u| (3 g^2
+    + |g|^3), and the forward's bound over d."""
+    N, K, d = 132, 272, 2.0 ** -6
+    q, s = tokens(M, K, 1)
+    Tg, pg, ag = weights(orc, N, K, 2)
+    Tu, pu, au = weights(orc, N, K, 3)
+    dh = torch.randn((M, N), generator=_gen(4))
+    dx, dg, du = (t.double().cpu() for t in bw.glu_backward(
+        dh.cuda(), q.cuda(), s.cuda(), pg, ag.cuda(), pu, au.cuda(), N, K, act=name))
+    bounds = ref.glu_backward(dh, q, s, Tg, ag, Tu, au, name, torch.float32)
+
+    def forward(s_, ag_, au_):
+        return bw.glu(q.cuda(), s_.cuda(), pg, ag_.cuda(), pu, au_.cuda(), N, K, act=name).double().cpu()
+
+    _, g = ref.product(q, s, Tg, ag)
+    _, u = ref.product(q, s, Tu, au)
+    _, err = ref.glu(q, s, Tg, ag, Tu, au, name, torch.float32)
+    cut = d ** 2 / 6 * 1.2 * u.abs() * (3 * g ** 2 + g.abs() ** 3) + 1.1 * err / d + 8 * ref.U / d * (g * u).abs()
+    a = dh.double().abs()
+    for along, dim, mine, bound in (
+            ((1, 0, 0), 1, (dx * q.double()).sum(1) * s.double(), (bounds[0][1] * q.double().abs()).sum(1) * s.double()),
+            ((0, 1, 0), 0, dg * ag.double(), bounds[1][1] * ag.double()),
+            ((0, 0, 1), 0, du * au.double(), bounds[2][1] * au.double())):
+        up = forward(*(v * (1 + d * on) for v, on in zip((s, ag, au), along)))
+        down = forward(*(v * (1 - d * on) for v, on in zip((s, ag, au), along)))
+        check(str(along), mine, (dh.double() * (up - down)).sum(dim) / (2 * d), (a * cut).sum(dim) + bound)
+
+
+def test_layernorm_backward_against_differences():
+    """Along random directions of x, w and b: central differences of the
+    definition in 64 bits.  mean and rstd are its own, rounded to fp32 (off by
+    U of themselves), so that only the steps and the gradients' bounds count:
+    steps of 2^-12 leave 2^-24 / 6 times the third derivative in x, which for
+    spreads of 0.5 and more and directions of size one is below 2^6 of the
+    terms' size."""
+    M, K, h = 12, 516, 2.0 ** -12
+    x, w, b = norm_inputs(M, K, torch.float32, 3)
+    g = _gen(5)
+    dy, vx, vw, vb = (torch.randn(sh, generator=g) for sh in ((M, K), (M, K), (K,), (K,)))
+    x64 = x.double()
+    mean = x64.mean(1).float()
+    rstd = (x64.var(1, unbiased=False) + 1e-5).rsqrt().float()
+    dx, dw, db = (t.double().cpu() for t in bw.layernorm_backward(dy.cuda(), x.cuda(), mean.cuda(), rstd.cuda(), w.cuda()))
+    bounds = ref.layernorm_backward(dy, x, mean, rstd, w, torch.float32)
+
+    def loss(t, along):      # per token
+        xx, ww, bb = (p.double() + t * on * v.double() for p, v, on in zip((x, w, b), (vx, vw, vb), along))
+        d = xx - xx.mean(1, keepdim=True)
+        return (dy.double() * (d / torch.sqrt((d * d).mean(1, keepdim=True) + 1e-5) * ww + bb)).sum(1)
+
+    difference = lambda along: (loss(h, along) - loss(-h, along)) / (2 * h)
+    r = rstd.double()[:, None]
+    xh = (x64 - mean.double()[:, None]).abs() * r
+    gw = (dy.double() * w.double()).abs()
+    # what rounding mean and rstd changes of dx . v: each of its three terms by
+    # a few U of rstd and of |mean| rstd in xh
+    terms = r * (gw + gw.mean(1, keepdim=True) + (1 + xh) * (gw * (1 + xh)).mean(1, keepdim=True))
+    moved = 8 * ref.U * (1 + (mean.double().abs()[:, None] * r)) * (terms * vx.double().abs())
+    check("dx", (dx * vx).sum(1), difference((1, 0, 0)),
+          (bounds[0][1] * vx.abs() + moved + 2.0 ** -24 / 6 * 64 * terms * (1 + vx.double().abs())).sum(1))
+    stat = 4 * ref.U * ((xh + mean.double().abs()[:, None] * r) * dy.double().abs() * vw.double().abs()).sum()
+    check("dw", (dw * vw).sum(), difference((0, 1, 0)).sum(), (bounds[1][1] * vw.abs()).sum() + stat + 1e-9 * (xh * dy.abs()).sum())
+    check("db", (db * vb).sum(), difference((0, 0, 1)).sum(), (bounds[2][1] * vb.abs()).sum() + 1e-9 * dy.double().abs().sum())
+
+
 # ------------------------------------------------------------------ layer norm
 def norm_inputs(M, K, dtype, seed):
     g = _gen(seed)
