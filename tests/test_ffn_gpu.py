@@ -207,6 +207,31 @@ def test_backward_gradients_of_any_size(orc, scale):
     assert bool((got[0][5] == 0).all())
 
 
+def test_backward_reads_the_gradients_up_to_two_gibibytes():
+    """The widest outputs, gated, in two fp16 terms: a tile of 256 tokens whose
+    last term ends 2^31 bytes behind its first.  Only the last token's last 64
+    outputs have a gradient, so dx is the sum over them alone (the zeros add
+    without rounding); code 0 is the block (0, 1, 1, 1)."""
+    M, N, K, n = 256, 1 << 20, 1024, 64
+    q, s = tokens(M, K, 1)
+    packed = torch.zeros(N // 64 * (K // 128) * 1280, dtype=torch.uint8, device="cuda")
+    T = torch.tensor([0.0, 1.0, 1.0, 1.0]).repeat(n, K // 4)
+    alpha = (0.5 + torch.rand((2, n), generator=_gen(2))) * (0.75 * K) ** -0.5
+    dh = torch.randn((1, n), generator=_gen(3))
+    wide = torch.zeros((2, N), device="cuda")
+    wide[:, -n:] = alpha
+    grad = torch.zeros((M, N), device="cuda")
+    grad[-1, -n:] = dh[0]
+    got = bw.glu_backward(grad, q.cuda(), s.cuda(), packed, wide[0], packed, wide[1], N, K, act="silu")
+    torch.cuda.synchronize()
+    want = ref.glu_backward(dh, q[-1:], s[-1:], T, alpha[0], T, alpha[1], "silu", torch.float32)
+    check("dx", got[0][-1:], *want[0])
+    assert not got[0][:-1].any()
+    for v, w in zip(got[1:], want[1:]):
+        check("dalpha", v[-n:], *w)
+        assert not v[:-n].any()
+
+
 def test_backward_infinite_and_nan_gradients_stay_in_their_token(orc):
     M, N, K = 40, 132, 272
     q, s = tokens(M, K, 1)
