@@ -56,7 +56,7 @@ def binding_command(out: str) -> list[str]:
     return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
             *[f"-I{d}" for d in include], BINDING_SOURCE, "-o", out, f"-L{os.path.join(root, 'lib')}",
-            "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python"]
+            "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_hip", "-ltorch_python"]
 
 
 def _filter(text: str) -> str:
