@@ -26,7 +26,8 @@ namespace sherry {
 namespace {
 
 constexpr int kLoopThreads = 1024;        // above kNormMaxK: one token per workgroup, in loops
-constexpr int kBackThreads = 512;         // backward: 8 waves, 8 / W tokens at a time
+// backward: 16 waves that share one token or more, or 8 with one each
+constexpr int back_threads(int W) { return W == 1 ? 512 : 1024; }
 constexpr int kNormMaxK = 16384;          // features held in registers
 constexpr int kNormGroups = 4;            // forward: workgroups of 256 threads per CU before tokens are taken in turns
 constexpr int kBackBlocks = kCUs;         // most workgroups (rows of partial weight gradients)
@@ -332,11 +333,12 @@ struct NormBackArgs {
 // against 47.1 us).  Against 8-byte loads, w read again for every token and
 // no token ahead: 109 us.
 template <typename T, int V, int W, int J>
-__global__ __launch_bounds__(kBackThreads) void norm_backward_kernel(NormBackArgs a) {
-  constexpr int G = kBackThreads / 64 / W;
-  __shared__ float2 red[2][kBackThreads / 64];
-  __shared__ Vec<V> col[kBackThreads];
-  const int wave = threadIdx.x >> 6;
+__global__ __launch_bounds__(back_threads(W)) void norm_backward_kernel(NormBackArgs a) {
+  constexpr int kThreads = back_threads(W), G = kThreads / 64 / W;
+  __shared__ float2 red[2][kThreads / 64];
+  __shared__ Vec<V> w[64 * W * J];
+  __shared__ Vec<V> col[G > 1 ? G : 1][G > 1 ? 64 * W * J : 1];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);   // (the rows' addresses: scalar)
   const int lane = threadIdx.x % (64 * W);
   const int group = wave / W;
   const float inv_k = 1.0f / (float)a.K;
@@ -359,12 +361,12 @@ __global__ __launch_bounds__(kBackThreads) void norm_backward_kernel(NormBackArg
   };
   Token next;
   load(blockIdx.x * G + group, next);
-  Vec<V> w[J], dw[J], db[J];
+  Vec<V> dw[J], db[J];
 #pragma unroll
-  for (int j = 0; j < J; ++j) {
-    w[j] = load_vec<V>(a.w + feature(j), a.w && feature(j) < a.K, 1.0f);
-    dw[j] = db[j] = Vec<V>{};
-  }
+  for (int j = 0; j < J; ++j) dw[j] = db[j] = Vec<V>{};
+  for (int i = threadIdx.x; i < 64 * W * J; i += kThreads)
+    w[i] = load_vec<V>(a.w + V * i, a.w && V * i < a.K, 1.0f);
+  __syncthreads();
   // every wave of the workgroup makes the same number of trips (barriers)
   int turn = 0;
   for (int m0 = blockIdx.x * G; m0 < a.M; m0 += gridDim.x * G, turn ^= 1) {
@@ -377,16 +379,18 @@ __global__ __launch_bounds__(kBackThreads) void norm_backward_kernel(NormBackArg
       g[j] = __builtin_convertvector(next.dy[j], Vec<V>);
     }
     if (m0 + (int)gridDim.x * G < a.M) load(m + gridDim.x * G, next);
+    asm volatile("" ::: "memory");   // w stays in LDS
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       const bool in = feature(j) < a.K;   // past K: dy is 0, and xh is made 0
+      const Vec<V> wj = w[lane + 64 * W * j];
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         xh[j][i] = in ? (xh[j][i] - mean) * rstd : 0.0f;
         dw[j][i] += g[j][i] * xh[j][i];
         db[j][i] += g[j][i];
-        g[j][i] *= w[j][i];
+        g[j][i] *= wj[i];
         s1 += g[j][i];
         s2 += g[j][i] * xh[j][i];
       }
@@ -397,7 +401,7 @@ __global__ __launch_bounds__(kBackThreads) void norm_backward_kernel(NormBackArg
       if ((threadIdx.x & 63) == 0) red[turn][wave] = make_float2(s1, s2);
       __syncthreads();
       s1 = s2 = 0.0f;
-#pragma unroll
+#pragma unroll (W < 4 ? W : 4)
       for (int i = 0; i < W; ++i) {
         const float2 r = red[turn][group * W + i];
         s1 += r.x;
@@ -416,22 +420,29 @@ __global__ __launch_bounds__(kBackThreads) void norm_backward_kernel(NormBackArg
         *reinterpret_cast<Raw<T, V>*>(dx + feature(j)) = __builtin_convertvector(v, Raw<T, V>);
     }
   }
-  // the groups' sums of each column, joined through LDS one j at a time
+  // the groups' sums of each column, joined through LDS in the groups' order
   float* part = a.part + (size_t)blockIdx.x * 2 * a.K;
+  auto put = [&](int which, int k, Vec<V> t) {
 #pragma unroll
-  for (int j = 0; j < J; ++j) {
+    for (int i = 0; i < V; i += 4)
+      store4(part + (size_t)which * a.K + k + i, f4{t[i], t[i + 1], t[i + 2], t[i + 3]});
+  };
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
+  for (int which = 0; which < 2; ++which) {
+    if constexpr (G == 1) {
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+        if (feature(j) < a.K) put(which, feature(j), which ? db[j] : dw[j]);
+    } else {
       __syncthreads();
-      col[threadIdx.x] = which ? db[j] : dw[j];
+#pragma unroll
+      for (int j = 0; j < J; ++j) col[group][lane + 64 * W * j] = which ? db[j] : dw[j];
       __syncthreads();
-      if (group == 0 && feature(j) < a.K) {
-        Vec<V> t = col[lane];
-#pragma unroll
-        for (int gg = 1; gg < G; ++gg) t += col[gg * 64 * W + lane];
-#pragma unroll
-        for (int i = 0; i < V; i += 4)
-          store4(part + (size_t)which * a.K + feature(j) + i, f4{t[i], t[i + 1], t[i + 2], t[i + 3]});
+      for (int i = threadIdx.x; i < 64 * W * J && V * i < a.K; i += kThreads) {
+        Vec<V> t = col[0][i];
+#pragma unroll 4
+        for (int gg = 1; gg < G; ++gg) t += col[gg][i];
+        put(which, V * i, t);
       }
     }
   }
@@ -562,18 +573,18 @@ hipError_t launch_norm_type(const NormArgs& a, hipStream_t stream) {
 }
 
 // Waves per token of the backward.
-int back_waves(int K) { return K <= 2048 ? 1 : K <= 4096 ? 2 : K <= 8192 ? 4 : 8; }
+int back_waves(int K) { return K <= 1024 ? 1 : K <= 2048 ? 2 : K <= 4096 ? 4 : K <= 8192 ? 8 : 16; }
 
 template <typename T, int V>
 hipError_t launch_norm_backward_as(const NormBackArgs& a, int blocks, hipStream_t stream) {
 #define SHERRY_NORM_BACK(W_, J_) \
-  hipLaunchKernelGGL((norm_backward_kernel<T, V, W_, J_ * 4 / V>), dim3(blocks), dim3(kBackThreads), 0, stream, a)
+  hipLaunchKernelGGL((norm_backward_kernel<T, V, W_, J_ * 4 / V>), dim3(blocks), dim3(back_threads(W_)), 0, stream, a)
   if (a.K <= 512) SHERRY_NORM_BACK(1, 2);
   else if (a.K <= 1024) SHERRY_NORM_BACK(1, 4);
-  else if (a.K <= 2048) SHERRY_NORM_BACK(1, 8);
-  else if (a.K <= 4096) SHERRY_NORM_BACK(2, 8);
-  else if (a.K <= 8192) SHERRY_NORM_BACK(4, 8);
-  else SHERRY_NORM_BACK(8, 8);
+  else if (a.K <= 2048) SHERRY_NORM_BACK(2, 4);
+  else if (a.K <= 4096) SHERRY_NORM_BACK(4, 4);
+  else if (a.K <= 8192) SHERRY_NORM_BACK(8, 4);
+  else SHERRY_NORM_BACK(16, 4);
 #undef SHERRY_NORM_BACK
   return hipGetLastError();
 }
@@ -608,7 +619,7 @@ hipError_t launch_layernorm(const void* x, const float* w, const float* b, float
 // Workgroups of the backward = rows of partial dw, db.
 int layernorm_backward_rows(int M, int K) {
   if (K > kNormMaxK) return M < 64 ? M : 64;
-  const int per = kBackThreads / 64 / back_waves(K);   // tokens per workgroup and trip
+  const int per = back_threads(back_waves(K)) / 64 / back_waves(K);   // tokens per workgroup and trip
   const int need = (M + per - 1) / per;
   return need < kBackBlocks ? need : kBackBlocks;
 }
