@@ -118,6 +118,27 @@ __device__ __forceinline__ Raw<T, V> load_raw(const T* p, bool in) {
   return r;
 }
 
+// One token's row as a buffer (n bytes; 0 for a token past the last), whose
+// range check stands for the bounds: loads past it give zeros, stores nothing.
+// (The check does not see a scalar offset: the whole offset is the lane's.)
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_of(const void* base, size_t at, int n) {
+  return __builtin_amdgcn_make_buffer_rsrc(static_cast<char*>(const_cast<void*>(base)) + at, 0, n, 0x00020000);
+}
+
+template <typename T, int V>
+__device__ __forceinline__ Raw<T, V> load_row(__amdgpu_buffer_rsrc_t r, int at) {
+  if constexpr (sizeof(T) * V == 16) return __builtin_bit_cast(Raw<T, V>, __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0));
+  else return __builtin_bit_cast(Raw<T, V>, __builtin_amdgcn_raw_buffer_load_b64(r, at, 0, 0));
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void store_row(__amdgpu_buffer_rsrc_t r, int at, Raw<T, V> v) {
+  typedef unsigned int v4u __attribute__((ext_vector_type(4)));
+  typedef unsigned int v2u __attribute__((ext_vector_type(2)));
+  if constexpr (sizeof(T) * V == 16) __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u, v), r, at, 0, 0);
+  else __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(v2u, v), r, at, 0, 0);
+}
+
 template <int V>
 __device__ __forceinline__ Vec<V> load_vec(const float* p, bool in, float otherwise) {
   Vec<V> r;
@@ -325,13 +346,17 @@ struct NormBackArgs {
   int M, K;
 };
 
-// Gradients on tokens that fit registers.  A group of W waves takes tokens
-// group, group + groups, ... and keeps its sums of dw and db over them in
-// registers; the workgroup adds its groups through LDS at the end and
-// writes one row of partial sums, so no atomics and a fixed order.  One
-// workgroup per CU: with two, the partial rows double (8192 x 4096 bf16: 52.3
-// against 47.1 us).  Against 8-byte loads, w read again for every token and
-// no token ahead: 109 us.
+// Gradients on tokens that fit registers, 16 features a lane.  A group of W
+// waves takes tokens group, group + groups, ... and keeps its sums of dw and
+// db over them in registers; the workgroup adds its groups through LDS at the
+// end and writes one row of partial sums, so no atomics and a fixed order.
+// One workgroup per CU: with two, the partial rows double (8192 x 4096 bf16:
+// 52.3 against 47.1 us).  w waits in LDS and the rows are buffers with a scalar
+// base, so 16 waves fit their 128 registers; 8 waves of 32 features a lane
+// with w in registers and a pointer per load spilled (8192 x 4096 bf16 47.1 ->
+// 42.6 us, fp32 4096 x 4096 80.6 -> 47.8, fp16 4096 x 8192 89.9 -> 46.5, fp32
+// 2048 x 16384 182 -> 88.9).  Groups of one wave (K <= 1024) have few features a
+// lane and join more groups: 8 of them (8192 x 1024 fp32 23 us, 16 of them 31).
 template <typename T, int V, int W, int J>
 __global__ __launch_bounds__(back_threads(W)) void norm_backward_kernel(NormBackArgs a) {
   constexpr int kThreads = back_threads(W), G = kThreads / 64 / W;
@@ -343,18 +368,20 @@ __global__ __launch_bounds__(back_threads(W)) void norm_backward_kernel(NormBack
   const int group = wave / W;
   const float inv_k = 1.0f / (float)a.K;
   auto feature = [&](int j) { return V * (lane + 64 * W * j); };
+  constexpr int kChunk = V * (int)sizeof(T);
+  const int bytes = a.K * (int)sizeof(T);   // of a row
   struct Token {
     Raw<T, V> x[J], dy[J];
     float mean, rstd;
   };
   auto load = [&](int m, Token& t) {
     const bool live = m < a.M;
-    const size_t row = (size_t)m * a.K;
+    const size_t row = (size_t)m * bytes;
+    const __amdgpu_buffer_rsrc_t rx = row_of(a.x, row, live ? bytes : 0), rdy = row_of(a.dy, row, live ? bytes : 0);
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      const bool in = live && feature(j) < a.K;
-      t.x[j] = load_raw<T, V>(static_cast<const T*>(a.x) + row + feature(j), in);
-      t.dy[j] = load_raw<T, V>(static_cast<const T*>(a.dy) + row + feature(j), in);
+      t.x[j] = load_row<T, V>(rx, kChunk * (lane + 64 * W * j));
+      t.dy[j] = load_row<T, V>(rdy, kChunk * (lane + 64 * W * j));
     }
     t.mean = live ? a.mean[m] : 0.0f;
     t.rstd = live ? a.rstd[m] : 0.0f;
@@ -410,14 +437,13 @@ __global__ __launch_bounds__(back_threads(W)) void norm_backward_kernel(NormBack
     }
     s1 *= inv_k;
     s2 *= inv_k;
-    T* dx = static_cast<T*>(a.dx) + (size_t)m * a.K;
+    const __amdgpu_buffer_rsrc_t rdx = row_of(a.dx, (size_t)m * bytes, m < a.M ? bytes : 0);
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       Vec<V> v;
 #pragma unroll
       for (int i = 0; i < V; ++i) v[i] = rstd * (g[j][i] - s1 - xh[j][i] * s2);
-      if (m < a.M && feature(j) < a.K)
-        *reinterpret_cast<Raw<T, V>*>(dx + feature(j)) = __builtin_convertvector(v, Raw<T, V>);
+      store_row<T, V>(rdx, kChunk * (lane + 64 * W * j), __builtin_convertvector(v, Raw<T, V>));
     }
   }
   // the groups' sums of each column, joined through LDS in the groups' order

@@ -420,6 +420,23 @@ def test_layernorm_backward(i, shape, t):
     assert inplace[0].data_ptr() == buf.data_ptr() and all(torch.equal(p, q) for p, q in zip(inplace, grads))
 
 
+@pytest.mark.parametrize("t", list(ref.TYPES))
+@pytest.mark.parametrize("M,K", [(1, 4), (5, 260), (7, 1028), (9, 2052), (300, 2056), (3, 4100), (2, 8196), (2, 12300), (2, 16388)])
+def test_layernorm_leaves_what_surrounds_its_output(M, K, t):
+    dtype = ref.TYPES[t]
+    x, w, b = norm_inputs(M, K, dtype, 9)
+    x, w, b = x.cuda(), w.cuda(), b.cuda()
+    pad = 1 << 16
+    whole = torch.full((M * K + 2 * pad,), 7.0, dtype=dtype, device="cuda")
+    out = whole[pad:pad + M * K].view(M, K)
+    y, mean, rstd = bw.layernorm(x, w, b, stats=True)
+    grads = bw.layernorm_backward(y, x, mean, rstd, w)
+    for want, call in ((y, lambda: bw.layernorm(x, w, b, out=out)),
+                       (grads[0], lambda: bw.layernorm_backward(y, x, mean, rstd, w, out=out)[0])):
+        assert torch.equal(call(), want)
+        assert (whole[:pad] == 7).all() and (whole[pad + M * K:] == 7).all()
+
+
 def test_layernorm_rows_without_spread_and_a_far_mean():
     """Equal features (variance 0), zeros, and a mean far above the spread:
     rstd = eps^-1/2 of the first two; an all-zero token quantizes to s = 1."""
