@@ -6,10 +6,10 @@
 //   dx = rstd (g - sum g / K - xh sum(g xh) / K),
 //   dw = sum over tokens of dy xh, db = sum over tokens of dy.
 // All of them stream their inputs once; memory bandwidth bounds them at many
-// tokens (bf16, K = 4096: forward of 2048 tokens 33.6 MB in 8.7 us, 3.9 TB/s
-// with its launch; backward of 8192 tokens 201 MB in 47 us, 4.3 TB/s, 36 us of
-// it the tokens' kernel), the chain of load, reductions and launch at few
-// (16 tokens of 8192 into int8: 6.4 us).
+// tokens (bf16, K = 4096: forward of 2048 tokens 33.6 MB in 8.5 us, 3.9 TB/s
+// with its launch, 8192 tokens 4.9 TB/s; backward of 8192 tokens 201 MB in 42.6
+// us, 4.7 TB/s with its second launch), the chain of load, reductions and
+// launch at few (16 tokens of 8192 into int8: 5.6 us).
 //
 // A group of W waves holds one token in registers, so the mean and the sum of
 // squared differences from it are taken in two passes without reading x
@@ -30,6 +30,7 @@ constexpr int kLoopThreads = 1024;        // above kNormMaxK: one token per work
 constexpr int back_threads(int W) { return W == 1 ? 512 : 1024; }
 constexpr int kNormMaxK = 16384;          // features held in registers
 constexpr int kNormGroups = 4;            // forward: workgroups of 256 threads per CU before tokens are taken in turns
+constexpr int kQuantGroups = 3;           //   of the int8 form
 constexpr int kBackBlocks = kCUs;         // most workgroups (rows of partial weight gradients)
 
 // Sum (or maximum) over the W waves that share a token; `slot` is this
@@ -160,27 +161,52 @@ __device__ __forceinline__ void normed4(const S (&d)[4], S rstd, const NormArgs&
   for (int i = 0; i < 4; ++i) v[i] = d[i] * rstd * (S)w[i] + (S)b[i];
 }
 
-// One int8 step count; clamped, and a NaN (not accepted) becomes 0.
-__device__ __forceinline__ uint32_t quant_at(double v, double s) {
-  return (uint32_t)(uint8_t)(int8_t)fmin(fmax(rint(v / s), -127.0), 127.0);
+// Four int8 step counts in a word: rounded half to even by an addition that
+// leaves no bits behind the point, clamped.
+__device__ __forceinline__ int quant_at(double t) {
+  const int n = (int)(uint32_t)__builtin_bit_cast(uint64_t, t + 0x1.8p52);
+  return n < -127 ? -127 : n > 127 ? 127 : n;
+}
+__device__ __forceinline__ uint32_t quant4(double t0, double t1, double t2, double t3) {
+  const uint32_t lo = __builtin_amdgcn_perm((uint32_t)quant_at(t1), (uint32_t)quant_at(t0), 0x0C0C0400u);
+  const uint32_t hi = __builtin_amdgcn_perm((uint32_t)quant_at(t3), (uint32_t)quant_at(t2), 0x04000C0Cu);
+  return lo | hi;
+}
+
+__device__ __forceinline__ float inverse_root(float v) { return 1.0f / sqrtf(v); }
+// Newton's steps y + y (1 - v y^2) / 2 from the hardware's estimate.
+__device__ __forceinline__ double inverse_root(double v) {
+  double y = __builtin_amdgcn_rsq(v);
+  y += 0.5 * y * (1.0 - v * y * y);
+  y += 0.5 * y * (1.0 - v * y * y);
+  return y;
 }
 
 // The forward on tokens that fit registers.  Q: int8 output; then everything
 // from the mean on is computed in 64 bits, so that a value next to a border
 // between two int8 steps falls where exact arithmetic puts it (in 32 bits
-// about one value in 1e5 lands on the other side); S is the sums' type.  The
-// 64-bit arithmetic costs no time that shows: at 2048 tokens the memory is
-// slower, and a token's 16 waves divide it at few.
+// about one value in 1e5 lands on the other side); S is the sums' type.  A
+// 64-bit operation issues as fast as a 32-bit one, but a division is some 12
+// of them and a rounding with its clamp 6, so the steps are counted by a
+// product with 1 / s, rounded by one addition, and the two divisions by K and
+// the root are products and Newton steps (8192 x 4096 bf16 48.6 -> 31.9 us, 16 x
+// 8192 6.5 -> 5.6; the bytes take 19 and 0.2; with v in 32 bits and only
+// what is next to a border in 64: 43).
 template <typename T, int V, int W, int J, bool Q>
 __global__ __launch_bounds__(W == 16 ? 1024 : 256) void norm_kernel(NormArgs a) {
   using S = std::conditional_t<Q, double, float>;
   constexpr int kThreads = W == 16 ? 1024 : 256;
   constexpr int G = kThreads / 64 / W;   // tokens at a time
+  // w and b beside 16 features in 64 bits do not fit 128 registers
+  constexpr bool kLds = Q && W == 16 && J * V == 16;
+  __shared__ Vec<V> w_lds[kLds ? 64 * W * J : 1], b_lds[kLds ? 64 * W * J : 1];
   __shared__ S red[2][3][kThreads / 64];
   const int wave = threadIdx.x >> 6;
   const int lane = threadIdx.x % (64 * W);
   const auto add = [](S p, S q) { return p + q; };
   const auto top = [](S p, S q) { return p > q ? p : q; };
+  const S inv_k = (S)1 / (S)a.K;
+  auto over_k = [&](S t) { return Q ? t * inv_k : t / (S)a.K; };
   auto feature = [&](int j) { return V * (lane + 64 * W * j); };
   auto load = [&](int m, Raw<T, V> (&r)[J]) {
 #pragma unroll
@@ -189,11 +215,18 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 256) void norm_kernel(NormArgs a) 
   };
   Raw<T, V> next[J];
   load(blockIdx.x * G + wave / W, next);
-  Vec<V> w[J], b[J];
+  Vec<V> w[kLds ? 1 : J], b[kLds ? 1 : J];
 #pragma unroll
   for (int j = 0; j < J; ++j) {
-    w[j] = load_vec<V>(a.w + feature(j), a.w && feature(j) < a.K, 1.0f);
-    b[j] = load_vec<V>(a.b + feature(j), a.b && feature(j) < a.K, 0.0f);
+    const Vec<V> wj = load_vec<V>(a.w + feature(j), a.w && feature(j) < a.K, 1.0f);
+    const Vec<V> bj = load_vec<V>(a.b + feature(j), a.b && feature(j) < a.K, 0.0f);
+    if constexpr (kLds) {
+      w_lds[lane + 64 * W * j] = wj;   // (read by this thread only)
+      b_lds[lane + 64 * W * j] = bj;
+    } else {
+      w[j] = wj;
+      b[j] = bj;
+    }
   }
   // the same number of trips for every wave of the workgroup (barriers)
   int turn = 0;
@@ -212,7 +245,7 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 256) void norm_kernel(NormArgs a) 
       for (int i = 0; i < V; ++i) part += (S)xv[j][i];
       sum += part;
     }
-    const S mean = group_join<W>((S)wave_total(sum), red[turn][0], wave, add) / (S)a.K;
+    const S mean = over_k(group_join<W>((S)wave_total(sum), red[turn][0], wave, add));
     S sq = 0;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
@@ -224,17 +257,20 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 256) void norm_kernel(NormArgs a) 
         }
       }
     }
-    const S var = group_join<W>((S)wave_total(sq), red[turn][1], wave, add) / (S)a.K;
-    const S rstd = (S)1 / sqrt(var + (S)a.eps);
+    const S var = over_k(group_join<W>((S)wave_total(sq), red[turn][1], wave, add));
+    const S rstd = inverse_root(var + (S)a.eps);
     if (a.mean && live && lane == 0) {
       a.mean[m] = (float)mean;
       a.rstd[m] = (float)rstd;
     }
     S v[J][V];
 #pragma unroll
-    for (int j = 0; j < J; ++j)
+    for (int j = 0; j < J; ++j) {
+      const Vec<V> wj = kLds ? w_lds[lane + 64 * W * j] : w[kLds ? 0 : j];
+      const Vec<V> bj = kLds ? b_lds[lane + 64 * W * j] : b[kLds ? 0 : j];
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[j][i] = ((S)xv[j][i] - mean) * rstd * (S)w[j][i] + (S)b[j][i];
+      for (int i = 0; i < V; ++i) v[j][i] = ((S)xv[j][i] - mean) * rstd * (S)wj[i] + (S)bj[i];
+    }
     if constexpr (!Q) {
       T* y = static_cast<T*>(a.y) + (size_t)m * a.K;
 #pragma unroll
@@ -258,13 +294,13 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 256) void norm_kernel(NormArgs a) 
       // the scale is the fp32 the product reads; the steps are counted in it
       const float s = (float)(amax / 127.0) > 0.0f ? (float)(amax / 127.0) : 1.0f;
       if (live && lane == 0) a.s[m] = s;
+      const S inv = (S)1 / (S)s;
 #pragma unroll
       for (int j = 0; j < J; ++j) {
         uint32_t q[V / 4];
 #pragma unroll
         for (int i = 0; i < V; i += 4)
-          q[i / 4] = quant_at(v[j][i], (S)s) | quant_at(v[j][i + 1], (S)s) << 8 | quant_at(v[j][i + 2], (S)s) << 16 |
-                     quant_at(v[j][i + 3], (S)s) << 24;
+          q[i / 4] = quant4(v[j][i] * inv, v[j][i + 1] * inv, v[j][i + 2] * inv, v[j][i + 3] * inv);
         if (live && feature(j) < a.K) {
           uint32_t* out = reinterpret_cast<uint32_t*>(a.q + (size_t)m * a.K + feature(j));   // 4-byte aligned
 #pragma unroll
@@ -327,10 +363,11 @@ __global__ __launch_bounds__(kLoopThreads) void norm_loop_kernel(NormArgs a) {
     amax = group_join<W>((S)wave_top(amax), red[2], wave, top);
     const float s = (float)(amax / 127.0) > 0.0f ? (float)(amax / 127.0) : 1.0f;
     if (threadIdx.x == 0) a.s[m] = s;
+    const S inv = (S)1 / (S)s;
     uint32_t* q = reinterpret_cast<uint32_t*>(a.q + (size_t)m * a.K);
     for (int k = 4 * threadIdx.x; k < a.K; k += 4 * kLoopThreads) {
       value(k, v);
-      q[k / 4] = quant_at(v[0], (S)s) | quant_at(v[1], (S)s) << 8 | quant_at(v[2], (S)s) << 16 | quant_at(v[3], (S)s) << 24;
+      q[k / 4] = quant4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
     }
   }
 }
@@ -554,35 +591,39 @@ __global__ __launch_bounds__(1024) void norm_columns_kernel(const float* part, i
 template <typename T, int V, int W, int J, bool Q>
 void launch_norm_tokens(const NormArgs& a, hipStream_t stream) {
   constexpr int kThreads = W == 16 ? 1024 : 256, G = kThreads / 64 / W;
-  const int need = (a.M + G - 1) / G, most = kNormGroups * kCUs * 256 / kThreads;
+  const int need = (a.M + G - 1) / G, most = W == 16 ? kCUs : (Q ? kQuantGroups : kNormGroups) * kCUs;
   hipLaunchKernelGGL((norm_kernel<T, V, W, J, Q>), dim3(need < most ? need : most), dim3(kThreads), 0, stream, a);
 }
 
 // W: 1 wave up to 1024 features (no barrier); above, 4, or 16 where the tokens
 // are too few to fill the GPU with 4 each (at most kCUs of them; measured at
-// 16 tokens of 8192 bf16 features into int8: 4 waves 9.0 us, 16 waves 7.0).
-// At many tokens kNormGroups = 2, 4 and 8 measured the same within 3 %
-// (2048 x 4096 bf16: 9.1, 8.8, 8.8 us).
+// 16 tokens of 8192 bf16 features into int8: 4 waves 9.0 us, 16 waves 7.0), and
+// for int8 above 8192 features, where 4 waves' registers spill (4096 x 16384
+// fp32 259 us, 16 waves 93.7; 2048 x 12288 bf16 35.3 and 37.6; at 8192 features
+// and below 16 waves are slower, 4096 x 8192 bf16 57.8 against 30.5).  At many
+// tokens kNormGroups = 2, 4 and 8 measured the same within 3 % (2048 x 4096
+// bf16: 9.1, 8.8, 8.8 us); the int8 form's registers hold 3 (2048 x 4096 11.1
+// us with 4, 10.0 with 3).
 template <typename T, int V, bool Q>
 hipError_t launch_norm_as(const NormArgs& a, hipStream_t stream) {
   const int chunks = (a.K + V - 1) / V;   // of V features
-  const bool few = a.M <= kCUs;
+  const bool wide = a.M <= kCUs || (Q && a.K > 8192);
   if (a.K <= 1024) {
     if (chunks <= 64) launch_norm_tokens<T, V, 1, 1, Q>(a, stream);
     else if (chunks <= 128) launch_norm_tokens<T, V, 1, 2, Q>(a, stream);
     else if constexpr (V == 4) launch_norm_tokens<T, V, 1, 4, Q>(a, stream);
-  } else if (few && V == 16 / (int)sizeof(T) && a.K <= kNormMaxK) {
-    if constexpr (V == 16 / sizeof(T)) {
-      if (chunks <= 1024) launch_norm_tokens<T, V, 16, 1, Q>(a, stream);
-      else if (chunks <= 2048) launch_norm_tokens<T, V, 16, 2, Q>(a, stream);
-      else if constexpr (V == 4) launch_norm_tokens<T, V, 16, 4, Q>(a, stream);
-    }
+  } else if (wide && a.K <= kNormMaxK) {
+    if (chunks <= 1024) launch_norm_tokens<T, V, 16, 1, Q>(a, stream);
+    else if (chunks <= 2048) launch_norm_tokens<T, V, 16, 2, Q>(a, stream);
+    else if constexpr (V == 4) launch_norm_tokens<T, V, 16, 4, Q>(a, stream);
   } else if (a.K <= kNormMaxK) {
     if (chunks <= 256) launch_norm_tokens<T, V, 4, 1, Q>(a, stream);
     else if (chunks <= 512) launch_norm_tokens<T, V, 4, 2, Q>(a, stream);
     else if (chunks <= 1024) launch_norm_tokens<T, V, 4, 4, Q>(a, stream);
-    else if (chunks <= 2048) launch_norm_tokens<T, V, 4, 8, Q>(a, stream);
-    else if constexpr (V == 4) launch_norm_tokens<T, V, 4, 16, Q>(a, stream);
+    else if constexpr (V == 4 || !Q) {
+      if (chunks <= 2048) launch_norm_tokens<T, V, 4, 8, Q>(a, stream);
+      else if constexpr (!Q) launch_norm_tokens<T, V, 4, 16, Q>(a, stream);
+    }
   } else {
     hipLaunchKernelGGL((norm_loop_kernel<T, Q>), dim3(a.M), dim3(kLoopThreads), 0, stream, a);
   }
