@@ -454,6 +454,21 @@ def test_layernorm_rows_without_spread_and_a_far_mean():
     assert torch.equal(s.cpu(), rs) and torch.equal(q.cpu().double(), rv.round().clamp(-127, 127))
 
 
+@pytest.mark.parametrize("K", [512, 4096, 8192, 16384, 16388])
+@pytest.mark.parametrize("size,weight", [(1e-30, 1.0), (1e30, 1.0), (1.0, 1e-43), (1.0, 1e30), (1e-3, 1e-40)])
+def test_layernorm_quantize_of_any_size(K, size, weight):
+    """Values and scales far from 1, scales among the subnormal numbers (a
+    rounded one may leave more than 127 steps: clamped)."""
+    x, w, b = norm_inputs(6, K, torch.float32, 5)
+    x, w = x * size, w * weight
+    q, s = bw.layernorm_quantize(x.cuda(), w.cuda(), eps=1e-5)
+    torch.cuda.synchronize()
+    rv, rs = ref.layernorm_quantize(x, w, None, float(np.float32(1e-5)))
+    assert torch.equal(s.cpu(), rs)
+    border = (rv - rv.floor() - 0.5).abs() < 1e-9
+    assert bool(((q.cpu().double() == rv.round().clamp(-127, 127)) | border).all())
+
+
 def test_layernorm_nan_stays_in_its_row():
     x = torch.randn((4, 300), generator=_gen(2))
     x[1, 7] = float("nan")
