@@ -6,7 +6,7 @@
 //   dx = rstd (g - sum g / K - xh sum(g xh) / K),
 //   dw = sum over tokens of dy xh, db = sum over tokens of dy.
 // All of them stream their inputs once; memory bandwidth bounds them at many
-// tokens (bf16, K = 4096: forward of 2048 tokens 33.6 MB in 8.5 us, 3.9 TB/s
+// tokens (bf16, K = 4096: forward of 2048 tokens 33.6 MB in 8.1 us, 4.1 TB/s
 // with its launch, 8192 tokens 4.9 TB/s; backward of 8192 tokens 201 MB in 42.6
 // us, 4.7 TB/s with its second launch), the chain of load, reductions and
 // launch at few (16 tokens of 8192 into int8: 5.6 us).
@@ -29,8 +29,6 @@ constexpr int kLoopThreads = 1024;        // above kNormMaxK: one token per work
 // backward: 16 waves that share one token or more, or 8 with one each
 constexpr int back_threads(int W) { return W == 1 ? 512 : 1024; }
 constexpr int kNormMaxK = 16384;          // features held in registers
-constexpr int kNormGroups = 4;            // forward: workgroups of 256 threads per CU before tokens are taken in turns
-constexpr int kQuantGroups = 3;           //   of the int8 form
 constexpr int kBackBlocks = kCUs;         // most workgroups (rows of partial weight gradients)
 
 // Sum (or maximum) over the W waves that share a token; `slot` is this
@@ -588,10 +586,14 @@ __global__ __launch_bounds__(1024) void norm_columns_kernel(const float* part, i
   }
 }
 
+// As many workgroups as the registers hold at once, which then take further
+// tokens in turns with w and b at hand (bf16, us, against 4 per CU: 2048 x 4096
+// 8.6 -> 8.1, into int8 11.1 -> 10.0; 4096 x 8192 29.6 -> 26.5, 2048 x 12288 27.4
+// -> 24.8; but 4096 x 2048 9.7 -> 10.1).
 template <typename T, int V, int W, int J, bool Q>
 void launch_norm_tokens(const NormArgs& a, hipStream_t stream) {
   constexpr int kThreads = W == 16 ? 1024 : 256, G = kThreads / 64 / W;
-  const int need = (a.M + G - 1) / G, most = W == 16 ? kCUs : (Q ? kQuantGroups : kNormGroups) * kCUs;
+  const int need = (a.M + G - 1) / G, most = (W == 16 ? 1 : J * V > 16 ? 2 : 3) * kCUs;
   hipLaunchKernelGGL((norm_kernel<T, V, W, J, Q>), dim3(need < most ? need : most), dim3(kThreads), 0, stream, a);
 }
 
@@ -600,10 +602,7 @@ void launch_norm_tokens(const NormArgs& a, hipStream_t stream) {
 // 16 tokens of 8192 bf16 features into int8: 4 waves 9.0 us, 16 waves 7.0), and
 // for int8 above 8192 features, where 4 waves' registers spill (4096 x 16384
 // fp32 259 us, 16 waves 93.7; 2048 x 12288 bf16 35.3 and 37.6; at 8192 features
-// and below 16 waves are slower, 4096 x 8192 bf16 57.8 against 30.5).  At many
-// tokens kNormGroups = 2, 4 and 8 measured the same within 3 % (2048 x 4096
-// bf16: 9.1, 8.8, 8.8 us); the int8 form's registers hold 3 (2048 x 4096 11.1
-// us with 4, 10.0 with 3).
+// and below 16 waves are slower, 4096 x 8192 bf16 57.8 against 30.5).
 template <typename T, int V, bool Q>
 hipError_t launch_norm_as(const NormArgs& a, hipStream_t stream) {
   const int chunks = (a.K + V - 1) / V;   // of V features
