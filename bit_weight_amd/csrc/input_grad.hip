@@ -1,8 +1,8 @@
 // Gradients of the products with an epilogue.  Three steps, the scratch
 // memory between them:
 //  1. grad_prepare_kernel reads what bounds the finite gradients (per token
-//     max|dy| and sum|q|, per matrix max|alpha|) and lays the weight codes out for
-//     step 3;
+//     max|dy| and sum|q|, per matrix max|alpha|, the largest positive bias) and
+//     lays the weight codes out for step 3;
 //  2. the forward's prefill kernel recomputes the exact sums (1.25 bits per
 //     weight: cheaper than saving M x N fp32 values in the forward) and its
 //     epilogue writes z = dz alpha in scaled fp16 (sherry_grad.h) and partial
@@ -95,7 +95,7 @@ __global__ __launch_bounds__(kPrepThreads) void grad_prepare_kernel(PrepareArgs 
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) v[i] = vec[min(n0 + i * kPrepThreads, a.N - 1)];
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) t = fmaxf(t, finite_abs(v[i]));
+      for (int i = 0; i < kAhead; ++i) t = fmaxf(t, blockIdx.x == 2 && v[i] < 0.0f ? 0.0f : finite_abs(v[i]));
     }
     t = block_top(t, red);
     if (tid == 0) a.tops[blockIdx.x] = t;

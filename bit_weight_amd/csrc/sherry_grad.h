@@ -7,8 +7,10 @@
 // results, as two, high and low, which together keep 22 bits.  fp16 has the
 // digits but not the range, so each token's z is scaled by a power of two
 // (exact) that puts a bound on |z| at 2^15.  The bound needs no pass over z:
-//   |pre-activation| <= P = s_x sum|q| max|alpha| + max|bias|,
-//   |act'| <= 1.25 (2 P for relu2), |act| <= P (P^2 for relu2).
+//   pre-activation <= P = s_x sum|q| max|alpha| + max(bias, 0),
+//   |act'| <= 1.25 (2 P for relu2, where it is not 0), |act| <= P (P^2 for
+//   relu2).  A bias that closes its output, however far below 0, so leaves
+//   the others' scale alone.
 // It is some 2^4 .. 2^8 above the largest |z| of a row; terms down to 2^-29
 // of the bound stay in fp16's normal range, so the slack costs no digits.
 #pragma once
@@ -19,7 +21,7 @@
 namespace sherry {
 
 // e such that |z| 2^e <= 2^15 for every z of a token: rows = (max |dy|,
-// sum |q|), tops = (max |alpha|, max |alpha2|, max |bias|), the maxima over
+// sum |q|), tops = (max |alpha|, max |alpha2|, max(bias, 0)), the maxima over
 // finite values: an infinite or NaN gradient is one whatever the scale.
 __device__ __forceinline__ int grad_exponent(float2 row, float s_x, const float* tops, int act, bool glu) {
   const double dy = row.x, sum = (double)row.y * fabs((double)s_x);

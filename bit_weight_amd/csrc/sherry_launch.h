@@ -48,7 +48,7 @@ GemmPlan plan_gemm(int M, int N, int K);
 struct GradArgs {
   const void* dy;          // [M,N] of type dtype
   const float2* rows;      // per token: max |dy|, sum |q|
-  const float* tops;       // max |alpha|, max |alpha2|, max |bias|
+  const float* tops;       // max |alpha|, max |alpha2|, max(bias, 0)
   uint16_t* z;             // fp16 [M][terms][parts][64 row tiles]: the scaled gradients
   int terms;               // fp16 terms per gradient: 1, or 2 (high and low parts)
   float* part0;            // [token tiles][N] partial sums of dalpha
