@@ -6,13 +6,14 @@
 //  2. the forward's prefill kernel recomputes the exact sums (1.25 bits per
 //     weight: cheaper than saving M x N fp32 values in the forward) and its
 //     epilogue writes z = dz alpha in scaled fp16 (sherry_grad.h) and partial
-//     sums of dalpha, dbias;
+//     sums of dalpha, dbias; gradients_again_kernel then writes z again for
+//     tokens whose scale came out too small, and every token's factor back;
 //  3. input_grad_kernel forms dx = sum over rows n of z[m,n] T[n,k] on the
 //     fp16 matrix cores, both matrices of the gated block in one sum;
 // and grad_finish_kernel adds partial sums where a step left some.
 // Matrix-core time bounds the sum at many tokens (bf16, K = 4096, N = 14336,
-// gated, M=2048: 25 + 250 + 318 + 14 us, 1.9 POP/s int8 and 1.52 PFLOP/s fp16 in
-// steps 2 and 3), the four launches at few (M=77, K=1040, N=1300: 24 us).
+// gated, M=2048: 26 + 254 + 5 + 300 + 14 us, 1.9 POP/s int8 and 1.6 PFLOP/s fp16
+// in steps 2 and 3), the five launches at few (M=77, K=1040, N=1300: 29 us).
 //
 // Step 3's weights.  The product contracts over weight rows, but a 5-bit
 // code covers 4 columns of one row, so no operand of the matrix instruction
@@ -52,6 +53,7 @@ struct PrepareArgs {
   uint8_t* codes;         // [2 k tiles][parts x row tiles][kHalfBytes]
   float2* rows;
   float* tops;
+  uint32_t* largest;
   int parts, dtype, M, N, K;
 };
 
@@ -131,7 +133,10 @@ __global__ __launch_bounds__(kPrepThreads) void grad_prepare_kernel(PrepareArgs 
     __syncthreads();
     if (lane == 0) red[wave] = total;
     __syncthreads();
-    if (tid == 0) a.rows[m] = make_float2(t, (red[0] + red[1]) + (red[2] + red[3]));
+    if (tid == 0) {
+      a.rows[m] = make_float2(t, (red[0] + red[1]) + (red[2] + red[3]));
+      a.largest[m] = 0u;
+    }
     return;
   }
   const int KT = k_tiles(a.K), RT = row_tiles(a.N);
@@ -219,12 +224,10 @@ constexpr int kMaxSplits = 64;     // of the contraction
 struct InputGradArgs {
   const uint8_t* codes;
   const _Float16* z;
-  const float2* rows;
-  const float* tops;
-  const float* s_x;
+  const float* back;
   void* dx;          // [M,K] of type dtype (one split), or
   float* part;       // [splits][M][K]
-  int act, glu, dtype, terms;
+  int dtype, terms;
   int M, K, R;       // R: row tiles of all matrices
   int splits, r_per_split;
 };
@@ -271,7 +274,7 @@ __global__ __launch_bounds__(kGradThreads) void input_grad_kernel(InputGradArgs 
 
   for (int t = tid; t < BM; t += kGradThreads) {
     const int m = min(m0 + t, a.M - 1);
-    back[t] = 0.5f * exp2_of(-grad_exponent(a.rows[m], a.s_x[m], a.tops, a.act, a.glu));
+    back[t] = a.back[m];
   }
 
   // this wave's 64 columns (past the last k tile: the last half again, not stored)
@@ -511,6 +514,8 @@ GradPlan plan_grad(const GemmPlan& product, int M, int N, int K, int parts, int 
   };
   p.tops = take(3 * sizeof(float));
   p.rows = take((size_t)M * sizeof(float2));
+  p.largest = take((size_t)M * sizeof(uint32_t));
+  p.back = take((size_t)M * sizeof(float));
   p.codes = take(2 * (size_t)k_tiles(K) * p.R * kHalfBytes);
   p.z = take((size_t)M * p.terms * p.R * kStepK * sizeof(uint16_t));
   p.cols = take(p.token_tiles > 1 ? 2 * (size_t)p.token_tiles * N * sizeof(float) : 0);
@@ -536,6 +541,7 @@ hipError_t launch_backward(const GemmPlan& product, const GradPlan& p, const Gem
   pa.codes = reinterpret_cast<uint8_t*>(base + p.codes);
   pa.rows = reinterpret_cast<float2*>(base + p.rows);
   pa.tops = reinterpret_cast<float*>(base + p.tops);
+  pa.largest = reinterpret_cast<uint32_t*>(base + p.largest);
   pa.parts = parts;
   pa.dtype = e.dtype;
   pa.M = a.M;
@@ -551,23 +557,23 @@ hipError_t launch_backward(const GemmPlan& product, const GradPlan& p, const Gem
   float* cols = reinterpret_cast<float*>(base + p.cols);
   e.grad.rows = pa.rows;
   e.grad.tops = pa.tops;
+  e.grad.largest = pa.largest;
+  e.grad.back = reinterpret_cast<float*>(base + p.back);
   e.grad.z = reinterpret_cast<uint16_t*>(base + p.z);
   e.grad.terms = p.terms;
   e.grad.part0 = !d0 ? nullptr : direct ? d0 : cols;
   e.grad.part1 = !d1 ? nullptr : direct ? d1 : cols + (size_t)p.token_tiles * a.N;
   err = launch_mfma_gemm_epilogue(product, a, ep, e, stream);
   if (err != hipSuccess) return err;
+  err = launch_gradients_again(a, ep, e, stream);
+  if (err != hipSuccess) return err;
 
   InputGradArgs g{};
   g.codes = pa.codes;
   g.z = reinterpret_cast<const _Float16*>(base + p.z);
-  g.rows = pa.rows;
-  g.tops = pa.tops;
-  g.s_x = a.s_x;
+  g.back = e.grad.back;
   g.dx = dx;
   g.part = p.splits > 1 ? reinterpret_cast<float*>(base + p.dx_part) : nullptr;
-  g.act = e.act;
-  g.glu = glu;
   g.dtype = e.dtype;
   g.terms = p.terms;
   g.M = a.M;

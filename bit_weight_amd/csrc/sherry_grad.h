@@ -2,17 +2,25 @@
 //
 // dx[m,k] = sum over rows n of z[m,n] T[n,k], z the gradient of row n's
 // pre-activation times alpha[n], runs on the fp16 matrix cores: T is exact
-// there and z is written as one fp16 term (relative rounding 2^-12, an
+// there and z is written as one fp16 term (relative rounding 2^-11, an
 // eighth of the rounding a bf16 result gets anyway) or, for fp16 and fp32
 // results, as two, high and low, which together keep 22 bits.  fp16 has the
 // digits but not the range, so each token's z is scaled by a power of two
-// (exact) that puts a bound on |z| at 2^15.  The bound needs no pass over z:
+// (exact) that puts a bound on |z| at 2^15.  The bound is known before any z:
 //   pre-activation <= P = s_x sum|q| max|alpha| + max(bias, 0),
 //   |act'| <= 1.25 (2 P for relu2, where it is not 0), |act| <= P (P^2 for
 //   relu2).  A bias that closes its output, however far below 0, so leaves
 //   the others' scale alone.
-// It is some 2^4 .. 2^8 above the largest |z| of a row; terms down to 2^-29
-// of the bound stay in fp16's normal range, so the slack costs no digits.
+// What the bound cannot know is which of its factors meet: the largest |z| of a
+// token lies 2^4 .. 2^14 below it where scales and gradients are of one size
+// (K up to 16384),
+// and any number of powers of two where a row scale or a column of gradients
+// far above the others belongs to an output whose gradient is 0.  A value is
+// off by up to 2^-25 after scaling (half of fp16's least step), so S powers of
+// two of slack make that 2^(S - 39) of the token's largest |z|.  The first pass
+// therefore also finds each token's largest |z|, and where S is above
+// kMostSlack, which leaves 2^-16 (one term) or 2^-24 (two), a second pass
+// writes the token's z again under the scale that its largest asks for.
 #pragma once
 
 #include "sherry_launch.h"
@@ -32,6 +40,16 @@ __device__ __forceinline__ int grad_exponent(float2 row, float s_x, const float*
   if (bound > 1e300) return -120;
   const int e = 15 - (ilogb(bound) + 1);
   return e < -120 ? -120 : e > 120 ? 120 : e;
+}
+
+// The same, given the bits of the largest |z| (0: none known; infinite: the
+// token's dx has no finite value): the exponent that z is left under.
+constexpr int kMostSlack[2] = {23, 15};   // with one term, with two
+__device__ __forceinline__ int exponent_used(int bound, uint32_t largest, int terms) {
+  if (largest == 0u || largest >= 0x7F800000u) return bound;
+  const int own = 14 - ilogbf(__builtin_bit_cast(float, largest));   // |z| 2^own < 2^15
+  if (own - bound <= (terms == 2 ? kMostSlack[1] : kMostSlack[0])) return bound;
+  return own > 120 ? 120 : own;
 }
 
 __device__ __forceinline__ float exp2_of(int e) { return __builtin_bit_cast(float, (uint32_t)(e + 127) << 23); }

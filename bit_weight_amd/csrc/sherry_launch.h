@@ -50,6 +50,8 @@ struct GradArgs {
   const float2* rows;      // per token: max |dy|, sum |q|
   const float* tops;       // max |alpha|, max |alpha2|, max(bias, 0)
   uint16_t* z;             // fp16 [M][terms][parts][64 row tiles]: the scaled gradients
+  uint32_t* largest;       // per token: bits of the largest |dz alpha| (0 before the product)
+  float* back;             // per token: what takes its sums of 2 T z back (written by the second pass)
   int terms;               // fp16 terms per gradient: 1, or 2 (high and low parts)
   float* part0;            // [token tiles][N] partial sums of dalpha
   float* part1;            // the same of dalpha2 or dbias
@@ -154,6 +156,10 @@ hipError_t launch_mfma_gemv_epilogue(const GemmPlan& plan, const GemmArgs& args,
 hipError_t launch_mfma_gemm_epilogue(const GemmPlan& plan, const GemmArgs& args, int ep,
                                      const EpilogueArgs& e, hipStream_t stream);
 
+// The backward product once more for the tokens whose gradients lie far below
+// their scale's bound (writes z, and `back` of every token; `largest` is complete).
+hipError_t launch_gradients_again(const GemmArgs& args, int ep, const EpilogueArgs& e, hipStream_t stream);
+
 // Plan of a backward pass: the input-gradient product's tiles and splits and
 // where each array lies in the scratch memory (input_grad.hip).
 struct GradPlan {
@@ -162,7 +168,7 @@ struct GradPlan {
   int mt;             // tokens per workgroup tile / 32
   int splits, r_per_split;
   int token_tiles;    // of the recomputing product: rows of partial column sums
-  size_t tops, rows, codes, z, cols, dx_part, bytes;
+  size_t tops, rows, largest, back, codes, z, cols, dx_part, bytes;
 };
 GradPlan plan_grad(const GemmPlan& product, int M, int N, int K, int parts, int dtype);
 // `product` is the recomputing product's plan (path 1), ep its epilogue; d0 =

@@ -165,6 +165,14 @@ __device__ __forceinline__ float dpp_shift(float x) {
                                                                0xF, false));
 }
 
+// Maximum over the 16 lanes of a row, in every lane.
+__device__ __forceinline__ float row16_max(float v) {
+  v = fmaxf(v, dpp_shift<0xB1>(v));
+  v = fmaxf(v, dpp_shift<0x4E>(v));
+  v = fmaxf(v, dpp_shift<0x124>(v));
+  return fmaxf(v, dpp_shift<0x128>(v));
+}
+
 __device__ __forceinline__ float wave_sum(float v) {
   v += dpp_shift<0xB1>(v);     // quad_perm [1,0,3,2]
   v += dpp_shift<0x4E>(v);     // quad_perm [2,3,0,1]

@@ -304,9 +304,11 @@ size_t sherry_glu_workspace_bytes(int64_t M, int64_t N, int64_t K);
  *   dalpha, dbias, ...  [N] fp32 (written), 4-byte aligned, each may be NULL.
  *   scratch  at least the queried bytes, any content, 256-byte aligned.
  * dx's terms dz * alpha are rounded to fp16 under one power-of-two scale per
- * token: one term (relative 2^-12) for bf16 results, a high and a low one
- * (2^-22) for fp16 and fp32 results.  The sums run in a fixed order: equal
- * calls give equal bits. */
+ * token: one term for bf16 results, off by at most 2^-11 of itself or 2^-16 of
+ * the token's largest, a high and a low one for fp16 and fp32 results (2^-22
+ * or 2^-24), whatever the sizes of the scales and gradients they come from
+ * (and 2^-145, where all of a token's are near fp32's least numbers).
+ * The sums run in a fixed order: equal calls give equal bits. */
 sherry_status sherry_gemm_fused_backward(const void* dy, const int8_t* x, const float* s_x,
                                          const void* packed, const float* alpha,
                                          const float* bias, int act, void* dx, float* dalpha,

@@ -42,3 +42,143 @@ def closed_by_bias(orc, name, t, closing):
 @pytest.mark.parametrize("name", ["relu", "relu2"])
 def test_backward_with_outputs_closed_by_a_finite_bias(orc, name, t, closing):
     closed_by_bias(orc, name, t, closing)
+
+
+# dx's terms are off by 2^-11 (one fp16 term, bf16 results) or 2^-22 (two) of
+# themselves and by FLOOR of the largest |dz alpha| of their token, however
+# large the factors are that no gradient passes.
+TERM = {torch.bfloat16: 2.0 ** -11, torch.float16: 2.0 ** -22, torch.float32: 2.0 ** -22}
+FLOOR = {torch.bfloat16: 2.0 ** -16, torch.float16: 2.0 ** -24, torch.float32: 2.0 ** -24}
+
+
+def dx_and_bound(parts, dtype):
+    """As ffn_reference.input_gradient, with the floor from the exact terms."""
+    top = torch.stack([c.abs().amax(1) for c, _, _ in parts]).amax(0)
+    return ref.input_gradient(parts, top * FLOOR[dtype] * 2.0 ** 39, dtype)
+
+
+def gated_terms(dh, q, s, Tg, ag, Tu, au, name):
+    """[(dz alpha, its error in fp32, T)] of both matrices, as in
+    ffn_reference.glu_backward."""
+    _, g = ref.product(q, s, Tg, ag)
+    _, u = ref.product(q, s, Tu, au)
+    dh, ag, au = dh.double(), ag.double(), au.double()
+    sl, a = ref.slope(g, name), ref.act(g, name)
+    dg, du = dh * u * sl, dh * a
+    eg = 3 * ref.U * g.abs()
+    edg = (dh * u).abs() * ref.slope_error(g, eg, name) + 6 * ref.U * dg.abs()
+    edu = dh.abs() * ref.act_error(g, eg, name) + ref.U * du.abs()
+    if name in ("relu", "relu2"):       # (a negative gate's sign is exact, and so are its zeros)
+        edg, edu = (torch.where(g < 0, 0.0, e) for e in (edg, edu))
+    return [(dg * ag, edg * ag.abs() + 2 * ref.U * (dg * ag).abs(), Tg),
+            (du * au, edu * au.abs() + 2 * ref.U * (du * au).abs(), Tu)]
+
+
+def closed_outlier(orc, M, N, K, factor, seed):
+    """A gated block whose output 7 has scales `factor` times the others' and,
+    in two tokens of three, a gradient `factor` times the others', but a gate
+    that is closed (negative) for every token."""
+    q, s = tokens(M, K, seed)
+    q = q.clamp(min=-127)
+    Tg, pg, ag = weights(orc, N, K, seed + 1)
+    Tu, pu, au = weights(orc, N, K, seed + 2)
+    acc = q.double() @ Tg[7].double()
+    q = torch.where(acc[:, None] > 0, -q, q)
+    q[acc == 0] = 0
+    dh = torch.randn((M, N), generator=_gen(seed + 3)) * 0.01
+    dh[:, 7] *= torch.where(torch.arange(M) % 3 < 2, factor, 1.0)
+    ag[7] *= factor
+    au[7] *= factor
+    return q, s, Tg, pg, ag, Tu, pu, au, dh
+
+
+@pytest.mark.parametrize("t", list(ref.TYPES))
+@pytest.mark.parametrize("factor", [2.0 ** 3, 2.0 ** 5, 2.0 ** 12])
+@pytest.mark.parametrize("M,N", [(1, 132), (40, 132), (77, 1300), (140, 4160), (300, 24580)])
+def test_gated_backward_beside_a_closed_outlier(orc, M, N, factor, t):
+    dtype = ref.TYPES[t]
+    q, s, Tg, pg, ag, Tu, pu, au, dh = closed_outlier(orc, M, N, 272, factor, 41)
+    dh = dh.to(dtype)
+    args = [v.cuda() for v in (dh, q, s)] + [pg, ag.cuda(), pu, au.cuda(), N, 272]
+    got = bw.glu_backward(*args, act="relu2")
+    torch.cuda.synchronize()
+    check("dx", got[0], *dx_and_bound(gated_terms(dh, q, s, Tg, ag, Tu, au, "relu2"), dtype))
+    for v, w in zip(got[1:], ref.glu_backward(dh, q, s, Tg, ag, Tu, au, "relu2", dtype)[1:]):
+        check("dalpha", v, *w)
+    assert all(torch.equal(u, v) for u, v in zip(got, bw.glu_backward(*args, act="relu2")))      # equal bits
+
+
+@pytest.mark.parametrize("t", ["fp32", "fp16"])
+@pytest.mark.parametrize("name", ["relu", "relu2"])
+@pytest.mark.parametrize("factor", [1.0, 2.0 ** 4, 2.0 ** 8, 2.0 ** 15])
+def test_gated_backward_keeps_the_digits_of_one_open_output(orc, name, factor, t):
+    """Gradients at the closed outlier and one other output only: dx is one
+    term of each matrix, so no sum's rounding hides its digits (the high and
+    low parts and the two matrices' terms: 4 additions)."""
+    M, N, K, dtype = 60, 132, 1040, ref.TYPES[t]
+    q, s, Tg, pg, ag, Tu, pu, au, dh = closed_outlier(orc, M, N, K, factor, 51)
+    dh = torch.where((torch.arange(N) == 7) | (torch.arange(N) == 20), dh, 0.0)
+    if t == "fp16":
+        dh = dh.clamp(-60000, 60000)
+    dh = dh.to(dtype)
+    got = bw.glu_backward(*[v.cuda() for v in (dh, q, s)], pg, ag.cuda(), pu, au.cuda(), N, K, act=name)[0]
+    torch.cuda.synchronize()
+    parts = gated_terms(dh, q, s, Tg, ag, Tu, au, name)
+    dx = sum(c @ T.double() for c, _, T in parts)
+    top = torch.stack([c.abs().amax(1) for c, _, _ in parts]).amax(0)
+    size = sum(c.abs().sum(1) for c, _, _ in parts)
+    err = sum(e.sum(1) for _, e, _ in parts) + (TERM[dtype] + 5 * ref.U) * size + 2 * FLOOR[dtype] * top
+    check("dx", got, dx, ref.rounded(dx, err[:, None].expand_as(dx), dtype))
+
+
+@pytest.mark.parametrize("t", list(ref.TYPES))
+@pytest.mark.parametrize("name", ["relu", "relu2", "silu"])
+def test_product_backward_beside_a_closed_outlier(orc, name, t):
+    """Ungated: a row scale and a gradient column far above the others', closed
+    by the sign of its sums (relu, relu2) or far in silu's tail."""
+    M, N, K, dtype = 70, 196, 528, ref.TYPES[t]
+    q, s, T, packed, alpha, _, _, _, dy = closed_outlier(orc, M, N, K, 2.0 ** 14, 61)
+    if name == "silu":
+        q[(q.double() @ T[7].double()).abs() < 64] = 0
+    dy = dy.to(dtype)
+    got = bw.gemm_fused_backward(dy.cuda(), q.cuda(), s.cuda(), packed, alpha.cuda(), N, K, act=name)
+    torch.cuda.synchronize()
+    _, z = ref.product(q, s, T, alpha)
+    dyd, a = dy.double(), alpha.double()
+    dz = dyd * ref.slope(z, name)
+    e = dyd.abs() * torch.where(dz == 0, 0.0, ref.slope_error(z, 3 * ref.U * z.abs(), name)) + ref.U * dz.abs()
+    e = torch.where(z < -100, dz.abs(), e)        # (silu's tail: the slope may as well be 0)
+    dx, bound = dx_and_bound([(dz * a, e * a.abs() + 2 * ref.U * (dz * a).abs(), T)], dtype)
+    # where the outlier is open (silu, all sums 0) its gradients pass 65520,
+    # from where on fp16 rounds to infinity
+    most = 65520.0 if dtype == torch.float16 else float("inf")
+    over, near = dx.abs() - bound >= most, dx.abs() + bound >= most
+    v = got[0].cpu().double()
+    assert torch.equal(v[over], dx[over].sign() * float("inf"))
+    check("dx", torch.where(near, dx, v), dx, bound)
+
+
+def test_captured_backward_beside_outliers_that_come_and_go(orc):
+    """One graph replayed with tokens that need another scale and with tokens
+    that do not, eager work between the replays."""
+    M, N, K = 77, 1300, 272
+    sets = [closed_outlier(orc, M, N, K, f, 41) for f in (2.0 ** 12, 1.0, 2.0 ** 30, 1.0, 2.0 ** 5)]
+    _, s, _, pg, _, _, pu, _, _ = sets[0]
+    live = [v.cuda().clone() for v in (sets[0][8], sets[0][0], s, sets[0][4], sets[0][7])]
+
+    def work():
+        dh, q, sx, ag, au = live
+        return bw.glu_backward(dh, q, sx, pg, ag, pu, au, N, K, act="relu2")
+
+    work()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = work()
+    for q, sx, _, _, ag, _, _, au, dh in sets:
+        for v, new in zip(live, (dh, q, sx, ag, au)):
+            v.copy_(new)
+        eager = [v.clone() for v in work()]
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(eager, held))
