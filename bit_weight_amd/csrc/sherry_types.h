@@ -140,7 +140,9 @@ __device__ __forceinline__ float activate(float z, int act, float& slope) {
       return z * phi;
     }
     case SHERRY_ACT_GELU_TANH: {
-      const float z2 = z * z;
+      // (beyond 11 S is 0, or 1 and 1 - S 0, in fp32, whatever z^2 is, so long as
+      // it stays finite: 0 times an infinite z^2 is none)
+      const float z2 = fminf(z * z, 1e6f);
       const float s = logistic(k2Sqrt2OverPi * (z + kGeluCubic * z2 * z));
       if constexpr (kSlope) slope = s + z * s * (1.0f - s) * k2Sqrt2OverPi * (1.0f + 3.0f * kGeluCubic * z2);
       return z * s;

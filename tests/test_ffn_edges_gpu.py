@@ -182,3 +182,33 @@ def test_captured_backward_beside_outliers_that_come_and_go(orc):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(eager, held))
+
+
+@pytest.mark.parametrize("t", list(ref.TYPES))
+@pytest.mark.parametrize("closing", [-1e6, -1e12, LOWEST])
+@pytest.mark.parametrize("name", ["silu", "gelu", "gelu_tanh"])
+def test_backward_of_the_smooth_activations_far_below_zero(orc, name, t, closing):
+    closed_by_bias(orc, name, t, closing)
+
+
+@pytest.mark.parametrize("name", ref.ACTS[1:])
+@pytest.mark.parametrize("M", [3, 140])
+def test_activations_far_above_zero(orc, name, M):
+    """Biases up to 1e30: act(z) = z (z^2), off by at most 4 roundings of z and 12 of
+    the activation, and slope 1 (2 z, times a gradient
+    that keeps the product finite)."""
+    N, K = 132, 272
+    q, s = tokens(M, K, 1)
+    T, packed, alpha = weights(orc, N, K, 2)
+    bias = 10.0 ** torch.linspace(3, 15 if name == "relu2" else 30, N)
+    dy = torch.randn((M, N), generator=_gen(6)) / bias
+    d = [v.cuda() for v in (q, s)] + [packed, alpha.cuda(), N, K]
+    y = bw.gemm_fused(*d, bias=bias.cuda(), act=name)
+    _, _, db = bw.gemm_fused_backward(dy.cuda(), *d, bias=bias.cuda(), act=name)
+    torch.cuda.synchronize()
+    _, z = ref.product(q, s, T, alpha)
+    z = z + bias.double()
+    want = z * z if name == "relu2" else z
+    check("y", y, want, 16 * ref.U * want.abs())
+    dz = dy.double() * (2 * z if name == "relu2" else 1.0)
+    check("dbias", db, dz.sum(0), (M + 40) * ref.U * dz.abs().sum(0))
