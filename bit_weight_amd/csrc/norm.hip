@@ -205,6 +205,13 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 256) void norm_kernel(NormArgs a) 
   const auto top = [](S p, S q) { return p > q ? p : q; };
   const S inv_k = (S)1 / (S)a.K;
   auto over_k = [&](S t) { return Q ? t * inv_k : t / (S)a.K; };
+  // the mean to the last bit, by one step on what the product leaves of the
+  // sum: equal features then have no spread (K = 196: all ones were 2^-53 off
+  // their mean, and that became the scale)
+  auto mean_of = [&](S t) {
+    const S m = over_k(t);
+    return Q ? (S)fma(fma(-m, (S)a.K, t), inv_k, m) : m;
+  };
   auto feature = [&](int j) { return V * (lane + 64 * W * j); };
   auto load = [&](int m, Raw<T, V> (&r)[J]) {
 #pragma unroll
@@ -243,7 +250,7 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 256) void norm_kernel(NormArgs a) 
       for (int i = 0; i < V; ++i) part += (S)xv[j][i];
       sum += part;
     }
-    const S mean = over_k(group_join<W>((S)wave_total(sum), red[turn][0], wave, add));
+    const S mean = mean_of(group_join<W>((S)wave_total(sum), red[turn][0], wave, add));
     S sq = 0;
 #pragma unroll
     for (int j = 0; j < J; ++j) {

@@ -212,3 +212,15 @@ def test_activations_far_above_zero(orc, name, M):
     check("y", y, want, 16 * ref.U * want.abs())
     dz = dy.double() * (2 * z if name == "relu2" else 1.0)
     check("dbias", db, dz.sum(0), (M + 40) * ref.U * dz.abs().sum(0))
+
+
+@pytest.mark.parametrize("t", list(ref.TYPES))
+@pytest.mark.parametrize("K", [12, 196, 300, 308, 364, 396, 1100, 3136, 4900, 9900, 16380, 16388, 19600])
+def test_int8_norm_of_equal_features(K, t):
+    """No spread, so v = 0 whatever the features' value: s = 1 and q = 0.  (In
+    64 bits the sum of K equal fp32 values is exact, and so is its K-th.)"""
+    x = torch.tensor([1.0, -3.25, 0.1, 1000.7, 1e-30, 60000.0, 0.0])[:, None].expand(-1, K).contiguous().to(ref.TYPES[t])
+    for M in (1, 7, 700):       # 16 and 4 waves a token
+        q, s = bw.layernorm_quantize(x.repeat(M // 7 + 1, 1)[:M].cuda())
+        torch.cuda.synchronize()
+        assert bool((s == 1).all()) and not q.any()
