@@ -159,6 +159,18 @@ __device__ __forceinline__ void normed4(const S (&d)[4], S rstd, const NormArgs&
   for (int i = 0; i < 4; ++i) v[i] = d[i] * rstd * (S)w[i] + (S)b[i];
 }
 
+// A token with a value that is not finite has no scale: s = NaN, so that every
+// product of it is NaN, and steps without a meaning.  Its largest |v| is made
+// infinite here (a maximum passes over NaN): a feature that is not finite leaves
+// no finite spread, which is looked at once a token, and a lane with a weight
+// or bias that is not takes 0 and infinity for its first ones.
+constexpr double kNoScale = __builtin_inf();
+__device__ __forceinline__ float scale_of(double amax) {
+  if (amax == kNoScale) return __builtin_nanf("");
+  const float s = (float)(amax / 127.0);
+  return s > 0.0f ? s : 1.0f;
+}
+
 // Four int8 step counts in a word: rounded half to even by an addition that
 // leaves no bits behind the point, clamped.
 __device__ __forceinline__ int quant_at(double t) {
@@ -221,10 +233,15 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 256) void norm_kernel(NormArgs a) 
   Raw<T, V> next[J];
   load(blockIdx.x * G + wave / W, next);
   Vec<V> w[kLds ? 1 : J], b[kLds ? 1 : J];
+  float odd = 0.0f;   // NaN where a weight or bias is not finite
 #pragma unroll
   for (int j = 0; j < J; ++j) {
     const Vec<V> wj = load_vec<V>(a.w + feature(j), a.w && feature(j) < a.K, 1.0f);
     const Vec<V> bj = load_vec<V>(a.b + feature(j), a.b && feature(j) < a.K, 0.0f);
+    if constexpr (Q) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) odd = fmaf(bj[i], 0.0f, fmaf(wj[i], 0.0f, odd));
+    }
     if constexpr (kLds) {
       w_lds[lane + 64 * W * j] = wj;   // (read by this thread only)
       b_lds[lane + 64 * W * j] = bj;
@@ -232,6 +249,12 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 256) void norm_kernel(NormArgs a) 
       w[j] = wj;
       b[j] = bj;
     }
+  }
+  if (Q && odd != 0.0f) {
+    Vec<V>& w0 = kLds ? w_lds[lane] : w[0];
+    Vec<V>& b0 = kLds ? b_lds[lane] : b[0];
+    w0[0] = 0.0f;
+    b0[0] = __builtin_inff();
   }
   // the same number of trips for every wave of the workgroup (barriers)
   int turn = 0;
@@ -295,9 +318,10 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 256) void norm_kernel(NormArgs a) 
           for (int i = 0; i < V; ++i) amax = fmax(amax, fabs(v[j][i]));
         }
       }
+      if (!(var < kNoScale)) amax = kNoScale;   // a feature that is not finite: no finite spread
       amax = group_join<W>((S)wave_top(amax), red[turn][2], wave, top);
       // the scale is the fp32 the product reads; the steps are counted in it
-      const float s = (float)(amax / 127.0) > 0.0f ? (float)(amax / 127.0) : 1.0f;
+      const float s = scale_of(amax);
       if (live && lane == 0) a.s[m] = s;
       const S inv = (S)1 / (S)s;
 #pragma unroll
@@ -360,13 +384,18 @@ __global__ __launch_bounds__(kLoopThreads) void norm_loop_kernel(NormArgs a) {
     }
   } else {
     S amax = 0;
+    bool none = false;
     for (int k = 4 * threadIdx.x; k < a.K; k += 4 * kLoopThreads) {
       value(k, v);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) amax = fmax(amax, fabs(v[i]));
+      for (int i = 0; i < 4; ++i) {
+        amax = fmax(amax, fabs(v[i]));
+        none |= v[i] != v[i];
+      }
     }
+    if (none) amax = kNoScale;
     amax = group_join<W>((S)wave_top(amax), red[2], wave, top);
-    const float s = (float)(amax / 127.0) > 0.0f ? (float)(amax / 127.0) : 1.0f;
+    const float s = scale_of(amax);
     if (threadIdx.x == 0) a.s[m] = s;
     const S inv = (S)1 / (S)s;
     uint32_t* q = reinterpret_cast<uint32_t*>(a.q + (size_t)m * a.K);

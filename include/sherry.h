@@ -343,7 +343,9 @@ sherry_status sherry_layernorm(const void* x, const float* weight, const float* 
  *   s_x = max|v| / 127 rounded to fp32 (1 if that is 0),
  *   q = clamp(rint(v / s_x), -127, 127), half to even.
  *   q  [M,K] int8 (written), 4-byte aligned;  s_x [M] fp32 (written).
- *   x finite; the rest as sherry_layernorm. */
+ *   A token with a value v that is not finite (one feature of it, or a weight
+ *   or bias, is infinite or NaN) gets s_x = NaN, so that its products are NaN;
+ *   its q then has no meaning.  The rest as sherry_layernorm. */
 sherry_status sherry_layernorm_quantize(const void* x, const float* weight, const float* bias,
                                         float eps, int8_t* q, float* s_x, float* mean, float* rstd,
                                         int dtype, int64_t M, int64_t K, void* stream);

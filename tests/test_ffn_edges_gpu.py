@@ -224,3 +224,36 @@ def test_int8_norm_of_equal_features(K, t):
         q, s = bw.layernorm_quantize(x.repeat(M // 7 + 1, 1)[:M].cuda())
         torch.cuda.synchronize()
         assert bool((s == 1).all()) and not q.any()
+
+
+@pytest.mark.parametrize("t", list(ref.TYPES))
+@pytest.mark.parametrize("K", [64, 1028, 2048, 8192, 8200, 16384, 16388])
+@pytest.mark.parametrize("M", [5, 300])
+def test_int8_norm_passes_on_what_is_not_finite(M, K, t):
+    """A NaN or an infinity in a token: no scale (NaN), so every product of the
+    token is NaN; the other tokens are as without it."""
+    x = torch.randn((M, K), generator=_gen(M + K)).to(ref.TYPES[t])
+    clean = bw.layernorm_quantize(x.cuda())
+    bad = {1: float("nan"), 2: float("inf"), 4: -float("inf"), M - 2: float("nan")}
+    for i, (m, v) in enumerate(bad.items()):
+        x[m, (K - 1) * i // 3] = v
+    q, s = bw.layernorm_quantize(x.cuda())
+    torch.cuda.synchronize()
+    lost = torch.zeros(M, dtype=torch.bool)
+    lost[list(bad)] = True
+    assert torch.equal(s.isnan().cpu(), lost)
+    assert torch.equal(s.cpu()[~lost], clean[1].cpu()[~lost]) and torch.equal(q.cpu()[~lost], clean[0].cpu()[~lost])
+
+
+@pytest.mark.parametrize("which", ["weight", "bias"])
+@pytest.mark.parametrize("K", [64, 1028, 8192, 16384, 16388])
+@pytest.mark.parametrize("M", [5, 300])
+def test_int8_norm_passes_on_a_weight_that_is_not_finite(M, K, which):
+    x = torch.randn((M, K), generator=_gen(K)).cuda()
+    for v in (float("nan"), float("inf")):
+        for k in (0, K // 2 + 1, K - 1):
+            w = torch.ones(K, device="cuda")
+            w[k] = v
+            q, s = bw.layernorm_quantize(x, **{which: w})
+            torch.cuda.synchronize()
+            assert bool(s.isnan().all())
