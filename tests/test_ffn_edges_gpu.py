@@ -257,3 +257,26 @@ def test_int8_norm_passes_on_a_weight_that_is_not_finite(M, K, which):
             q, s = bw.layernorm_quantize(x, **{which: w})
             torch.cuda.synchronize()
             assert bool(s.isnan().all())
+
+
+def test_gated_cells_hold_the_largest_sums_and_the_most_splits(orc):
+    """K = 2^20, where the shared 64-bit cells are fullest: |sum| = 128 * 3/4 *
+    2^20, between 2^26 and 2^27, in both 28-bit fields and with both signs,
+    and as many splits as 8 bits count (of the 256 that the CUs ask for at
+    most 255: 249 of 33 k tiles)."""
+    M, N, K = 2, 64, 1 << 20
+    assert int(bw.lib().sherry_glu_workspace_bytes(M, N, K)) > 0
+    block = torch.tensor([1, 1, 1, 0], dtype=torch.int8).repeat(K // 4)
+    flip = torch.arange(N)
+    Tg = torch.where(flip % 2 == 0, -1, 1)[:, None].to(torch.int8) * block
+    Tu = torch.where(flip % 3 == 0, -1, 1)[:, None].to(torch.int8) * block
+    pack = [torch.from_numpy(orc.pack(t.numpy())).cuda() for t in (Tg, Tu)]
+    q = torch.full((M, K), -128, dtype=torch.int8)
+    q[1] = 127
+    s, one = torch.full((M,), 2.0 ** -14), torch.ones(N)
+    top = 0.75 * K * q[:, 0].double()[:, None] * 2.0 ** -14
+    want = top * torch.where(flip % 2 == 0, -1.0, 1.0) * top * torch.where(flip % 3 == 0, -1.0, 1.0)
+    for _ in range(2):      # the cells are zero again after each call
+        h = bw.glu(q.cuda(), s.cuda(), pack[0], one.cuda(), pack[1], one.cuda(), N, K, act="none")
+        torch.cuda.synchronize()
+        check("h", h, want, 8 * ref.U * want.abs())
