@@ -204,11 +204,22 @@ def quantize_act(x: torch.Tensor):
     return q, s
 
 
+def _capturing(device: torch.device) -> bool:
+    """Whether the current stream of `device` is being captured into a graph."""
+    if torch.cuda.current_device() == device.index:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.device(device):
+        return torch.cuda.is_current_stream_capturing()
+
+
 class _Workspaces:
     """Zero-filled scratch per (device, stream), grown on demand.
 
     The library leaves a workspace zero-ready after every call, so one buffer
-    serves every call issued on its stream."""
+    serves every call issued on its stream.  Under graph capture each call gets
+    one of the graph's own, which every replay zeroes: a buffer of the stream's
+    would be shared by whatever runs beside a replay and freed under the graph
+    when it grows, and one made under capture is not zero before a replay."""
 
     def __init__(self):
         self._bufs = {}
@@ -216,6 +227,8 @@ class _Workspaces:
     def get(self, device: torch.device, nbytes: int):
         if nbytes == 0:
             return None
+        if _capturing(device):
+            return torch.zeros(nbytes, dtype=torch.uint8, device=device)
         key = (device.index, torch.cuda.current_stream(device).cuda_stream)
         buf = self._bufs.get(key)
         if buf is None or buf.numel() < nbytes:
@@ -227,7 +240,7 @@ class _Workspaces:
 _workspaces = _Workspaces()
 
 
-def _gemm_args(x, packed, N, K):
+def _gemm_args(x, packed, N, K, workspace):
     px = _dev_tensor(x, "x", torch.int8)
     _dev_tensor(packed, "packed", torch.uint8)
     if x.dim() != 2 or x.shape[1] != K:
@@ -235,22 +248,21 @@ def _gemm_args(x, packed, N, K):
     if packed.numel() != packed_bytes(N, K):
         raise RuntimeError("packed has the wrong size for [N,K]")
     M = x.shape[0]
-    ws = _workspaces.get(x.device, workspace_bytes(M, N, K))
-    return px, M, ws
+    if workspace is None:
+        workspace = _workspaces.get(x.device, workspace_bytes(M, N, K))
+    return px, M, workspace
 
 
 def gemm(x: torch.Tensor, s_x: torch.Tensor, packed: torch.Tensor, alpha: torch.Tensor,
          N: int, K: int, out: torch.Tensor | None = None,
          workspace: torch.Tensor | None = None) -> torch.Tensor:
     """y[M,N] = ((float)(x_int8 @ T^T) * s_x[:,None]) * alpha[None,:]."""
-    px, M, ws = _gemm_args(x, packed, N, K)
+    px, M, ws = _gemm_args(x, packed, N, K, workspace)
     _dev_tensor(s_x, "s_x", torch.float32)
     _dev_tensor(alpha, "alpha", torch.float32)
     if out is None:
         out = torch.empty((M, N), dtype=torch.float32, device=x.device)
     py = _dev_tensor(out, "out", torch.float32)
-    if workspace is not None:
-        ws = workspace
     wp = ws.data_ptr() if ws is not None else None
     wn = ws.numel() if ws is not None else 0
     _check(lib().sherry_gemm(px, s_x.data_ptr(), packed.data_ptr(), alpha.data_ptr(), py, M, N, K,
@@ -262,12 +274,10 @@ def gemm_i32(x: torch.Tensor, packed: torch.Tensor, N: int, K: int,
              out: torch.Tensor | None = None,
              workspace: torch.Tensor | None = None) -> torch.Tensor:
     """acc[M,N] = x_int8 @ T^T in int32 (exact)."""
-    px, M, ws = _gemm_args(x, packed, N, K)
+    px, M, ws = _gemm_args(x, packed, N, K, workspace)
     if out is None:
         out = torch.empty((M, N), dtype=torch.int32, device=x.device)
     pa = _dev_tensor(out, "out", torch.int32)
-    if workspace is not None:
-        ws = workspace
     wp = ws.data_ptr() if ws is not None else None
     wn = ws.numel() if ws is not None else 0
     _check(lib().sherry_gemm_i32(px, packed.data_ptr(), pa, M, N, K, wp, wn, _stream(x.device)),
@@ -352,7 +362,9 @@ def linear(x: torch.Tensor, packed: torch.Tensor, alpha: torch.Tensor, N: int, K
     py = _dev_tensor(out, "out", torch.float32)
     ws = workspace if workspace is not None else _workspaces.get(x.device, workspace_bytes(M, N, K))
     nsc = linear_scratch_bytes(M, N, K)
-    if scratch is None and nsc > 0:
+    if scratch is None and nsc > 0 and _capturing(x.device):
+        scratch = torch.empty(nsc, dtype=torch.uint8, device=x.device)      # the graph's own
+    elif scratch is None and nsc > 0:
         key = (x.device.index, torch.cuda.current_stream(x.device).cuda_stream)
         scratch = _scratch.get(key)
         if scratch is None or scratch.numel() < nsc:
@@ -439,15 +451,7 @@ _native = None
 
 def _zeroed_workspace(index: int, nbytes: int) -> torch.Tensor:
     """A split-K workspace on the current stream of device `index` (the compiled
-    module asks when the stream has none that is large enough); under graph
-    capture one of the graph's own, which each replay zeroes: two graphs
-    captured on one stream may be replayed side by side, and memory that
-    only another graph has zeroed is not zero."""
-    if torch.cuda.current_device() != index:
-        with torch.cuda.device(index):
-            return _zeroed_workspace(index, nbytes)
-    if torch.cuda.is_current_stream_capturing():
-        return torch.zeros(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
+    module asks when the stream has none that is large enough)."""
     return _workspaces.get(torch.device("cuda", index), nbytes)
 
 

@@ -280,3 +280,44 @@ def test_gated_cells_hold_the_largest_sums_and_the_most_splits(orc):
         h = bw.glu(q.cuda(), s.cuda(), pack[0], one.cuda(), pack[1], one.cuda(), N, K, act="none")
         torch.cuda.synchronize()
         check("h", h, want, 8 * ref.U * want.abs())
+
+
+def test_capture_leaves_the_eager_workspaces_alone(orc):
+    """Split-K products first called under capture: what they take belongs to
+    the graph, so eager calls on that stream, before the first replay and
+    beside later ones, find cells of their own."""
+    N, K, M = 1024, 8192, 4
+    T, packed, alpha = weights(orc, N, K, 1)
+    alpha = alpha.cuda()
+    q, s = tokens(M, K, 50)
+    dq, ds = q.cuda(), s.cuda()
+    x = (q.float() * s[:, None]).cuda()
+    p2, a2 = bw.quantize_pack2(torch.randn((N, K), generator=_gen(2)).cuda())
+    assert bw.workspace_bytes(M, N, K) > 0 and bw.linear_scratch_bytes(M, N, K) > 0
+    calls = [lambda: bw.gemm(dq, ds, packed, alpha, N, K), lambda: bw.gemm_i32(dq, packed, N, K),
+             lambda: bw.linear(x, packed, alpha, N, K), lambda: bw.gemm2(dq, ds, p2, a2, N, K),
+             lambda: bw.gemm_fused(dq, ds, packed, alpha, N, K)]
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        warm = [c() for c in calls]
+    torch.cuda.synchronize()
+    for i, call in enumerate(calls):
+        for known in (False, True):        # the stream has no workspace yet, or one
+            fresh = torch.cuda.Stream()
+            with torch.cuda.stream(fresh):
+                if known:
+                    call()
+            torch.cuda.synchronize()
+            before = {k: v.data_ptr() for d in (bw._workspaces._bufs, bw._scratch) for k, v in d.items()}
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=fresh):
+                held = call()
+            after = {k: v.data_ptr() for d in (bw._workspaces._bufs, bw._scratch) for k, v in d.items()}
+            assert before == after
+            for _ in range(3):
+                with torch.cuda.stream(side):
+                    graph.replay()
+                with torch.cuda.stream(fresh):
+                    eager = call()
+                torch.cuda.synchronize()
+                assert torch.equal(held, warm[i]) and torch.equal(eager, warm[i])
