@@ -444,6 +444,9 @@ def gemm2(x: torch.Tensor, s_x: torch.Tensor, packed: torch.Tensor, alpha: torch
 
 # ------------------------------------------------- feed-forward operators
 # Their tensors are checked and passed on by a compiled module (csrc/binding.cpp).
+# They have no autograd formula: with a tensor that requires a gradient the
+# outputs require one too, and a backward pass through them raises.  To train
+# through them, call them and their *_backward in a torch.autograd.Function.
 ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "relu2": 2, "silu": 3, "gelu": 4, "gelu_tanh": 5}
 
 _native = None

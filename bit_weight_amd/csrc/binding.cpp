@@ -14,16 +14,21 @@
 #include <ATen/ATen.h>
 #include <ATen/hip/EmptyTensor.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/core/GradMode.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPGraphsC10Utils.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/Dtype.h>
+#include <torch/csrc/autograd/functions/basic_ops.h>
+#include <torch/csrc/autograd/functions/utils.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdarg>
 #include <cstdint>
 #include <cstring>
+#include <memory>
+#include <string>
 
 #include "../../include/sherry.h"
 
@@ -243,6 +248,38 @@ struct Workspace {
   }
 };
 
+// Autograd: the operators have backward passes of their own and no grad_fn.
+// Where one of the tensors requires a gradient the outputs are made to say
+// so, and a backward pass through them fails by the operator's name instead
+// of leaving that gradient out.  A caller's output cannot carry this: refused,
+// as torch's functions do.
+class Gradients {
+ public:
+  Gradients(const char* name, std::initializer_list<PyObject*> inputs, PyObject* out = Py_None) : name_(name) {
+    if (!c10::GradMode::is_enabled()) return;
+    for (PyObject* o : inputs)
+      if (o != Py_None && THPVariable_Unpack(o).requires_grad())
+        edges_.push_back(torch::autograd::impl::gradient_edge(THPVariable_Unpack(o)));
+    if (out != Py_None && (!edges_.empty() || THPVariable_Unpack(out).requires_grad()))
+      fail(PyExc_RuntimeError, "%s with out= cannot carry gradients, but a tensor requires one: call it in torch.no_grad()",
+           name);
+  }
+  void mark(std::initializer_list<at::Tensor> outputs) {
+    if (edges_.empty()) return;
+    const std::shared_ptr<torch::autograd::Node> node(
+        new torch::autograd::NotImplemented(
+            std::string("bit_weight_amd.") + name_ + " (put it and its backward pass into a torch.autograd.Function)",
+            std::move(edges_)),
+        torch::autograd::deleteNode);
+    for (const at::Tensor& t : outputs)
+      if (t.defined() && at::isFloatingType(t.scalar_type())) torch::autograd::set_history(t, node);
+  }
+
+ private:
+  const char* name_;
+  torch::autograd::edge_list edges_;
+};
+
 PyObject* wrap(const at::Tensor& t) { return THPVariable_Wrap(t); }
 
 PyObject* wrap_all(std::initializer_list<at::Tensor> ts) {
@@ -281,10 +318,12 @@ PyObject* gemm_fused(PyObject* const* a) {
   const void* residual = matrix_of(a[8], "residual", type, t.index, t.M, t.N, true);
   const at::Tensor y = output_of(a[10], t.M, t.N, type, t.index, t.device);
   const Workspace ws(a[11], f_gemm_fused_workspace_bytes(t.M, t.N, t.K), t);
+  Gradients gradients("gemm_fused", {a[1], a[3], a[6], a[8]}, a[10]);
   launch("sherry_gemm_fused", t.index, [&](void* stream) {
     return f_gemm_fused(t.x, t.s_x, w.packed, w.alpha, bias, act, residual, y.data_ptr(), dtype, t.M, t.N, t.K,
                         ws.at, ws.bytes, stream);
   });
+  gradients.mark({y});
   return wrap(y);
 }
 
@@ -300,11 +339,13 @@ PyObject* gemm_fused_backward(PyObject* const* a) {
   const size_t bytes = f_gemm_fused_backward_scratch_bytes(t.M, t.N, t.K, dtype);
   const at::Tensor dx = empty({t.M, t.K}, dy.scalar_type(), t.device), da = empty({t.N}, at::kFloat, t.device),
                    db = empty({t.N}, at::kFloat, t.device), scratch = empty({(int64_t)bytes}, at::kByte, t.device);
+  Gradients gradients("gemm_fused_backward", {a[0], a[2], a[4], a[7]});
   launch("sherry_gemm_fused_backward", t.index, [&](void* stream) {
     return f_gemm_fused_backward(pdy, t.x, t.s_x, w.packed, w.alpha, bias, act, dx.data_ptr(),
                                  da.data_ptr<float>(), db.data_ptr<float>(), dtype, t.M, t.N, t.K,
                                  scratch.data_ptr(), bytes, stream);
   });
+  gradients.mark({dx, da, db});
   return wrap_all({dx, da, db});
 }
 
@@ -317,10 +358,12 @@ PyObject* glu(PyObject* const* a) {
   const int dtype = dtype_of(type);
   const at::Tensor h = output_of(a[10], t.M, t.N, type, t.index, t.device);
   const Workspace ws(a[11], f_glu_workspace_bytes(t.M, t.N, t.K), t);
+  Gradients gradients("glu", {a[1], a[3], a[5]}, a[10]);
   launch("sherry_glu", t.index, [&](void* stream) {
     return f_glu(t.x, t.s_x, g.packed, g.alpha, u.packed, u.alpha, act, h.data_ptr(), dtype, t.M, t.N, t.K, ws.at,
                  ws.bytes, stream);
   });
+  gradients.mark({h});
   return wrap(h);
 }
 
@@ -335,11 +378,13 @@ PyObject* glu_backward(PyObject* const* a) {
   const size_t bytes = f_glu_backward_scratch_bytes(t.M, t.N, t.K, dtype);
   const at::Tensor dx = empty({t.M, t.K}, dh.scalar_type(), t.device), dg = empty({t.N}, at::kFloat, t.device),
                    du = empty({t.N}, at::kFloat, t.device), scratch = empty({(int64_t)bytes}, at::kByte, t.device);
+  Gradients gradients("glu_backward", {a[0], a[2], a[4], a[6]});
   launch("sherry_glu_backward", t.index, [&](void* stream) {
     return f_glu_backward(pdh, t.x, t.s_x, g.packed, g.alpha, u.packed, u.alpha, act, dx.data_ptr(),
                           dg.data_ptr<float>(), du.data_ptr<float>(), dtype, t.M, t.N, t.K, scratch.data_ptr(),
                           bytes, stream);
   });
+  gradients.mark({dx, dg, du});
   return wrap_all({dx, dg, du});
 }
 
@@ -391,9 +436,11 @@ PyObject* layernorm(PyObject* const* a) {
   const float eps = number(a[3]);
   const at::Tensor y = output_of(a[5], f.M, f.K, f.type, f.index, f.device);
   const Stats s(a[4], f);
+  Gradients gradients("layernorm", {a[0], a[1], a[2]}, a[5]);
   launch("sherry_layernorm", f.index, [&](void* stream) {
     return f_layernorm(f.x, w, b, eps, y.data_ptr(), s.pm, s.pr, f.dtype, f.M, f.K, stream);
   });
+  gradients.mark({y, s.mean, s.rstd});
   return s.pm ? wrap_all({y, s.mean, s.rstd}) : wrap(y);
 }
 
@@ -405,10 +452,12 @@ PyObject* layernorm_quantize(PyObject* const* a) {
   const float eps = number(a[3]);
   const at::Tensor q = empty({f.M, f.K}, at::kChar, f.device), s_x = empty({f.M}, at::kFloat, f.device);
   const Stats s(a[4], f);
+  Gradients gradients("layernorm_quantize", {a[0], a[1], a[2]});
   launch("sherry_layernorm_quantize", f.index, [&](void* stream) {
     return f_layernorm_quantize(f.x, w, b, eps, static_cast<int8_t*>(q.data_ptr()), s_x.data_ptr<float>(), s.pm,
                                 s.pr, f.dtype, f.M, f.K, stream);
   });
+  gradients.mark({s_x, s.mean, s.rstd});
   return s.pm ? wrap_all({q, s_x, s.mean, s.rstd}) : wrap_all({q, s_x});
 }
 
@@ -423,10 +472,12 @@ PyObject* layernorm_backward(PyObject* const* a) {
   const size_t bytes = f_layernorm_backward_scratch_bytes(f.M, f.K);
   const at::Tensor dw = empty({f.K}, at::kFloat, f.device), db = empty({f.K}, at::kFloat, f.device),
                    scratch = empty({(int64_t)bytes}, at::kByte, f.device);
+  Gradients gradients("layernorm_backward", {a[0], a[1], a[2], a[3], a[4]}, a[5]);
   launch("sherry_layernorm_backward", f.index, [&](void* stream) {
     return f_layernorm_backward(dy, f.x, mean, rstd, w, dx.data_ptr(), dw.data_ptr<float>(), db.data_ptr<float>(),
                                 f.dtype, f.M, f.K, scratch.data_ptr(), bytes, stream);
   });
+  gradients.mark({dx, dw, db});
   return wrap_all({dx, dw, db});
 }
 

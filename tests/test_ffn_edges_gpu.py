@@ -321,3 +321,83 @@ def test_capture_leaves_the_eager_workspaces_alone(orc):
                     eager = call()
                 torch.cuda.synchronize()
                 assert torch.equal(held, warm[i]) and torch.equal(eager, warm[i])
+
+
+def test_outputs_do_not_lose_gradients_silently(orc):
+    """With a tensor that requires a gradient the output says so, and a
+    backward pass through it fails by the operator's name; without grad mode,
+    or without such a tensor, outputs are plain."""
+    M, N, K = 3, 64, 128
+    q, s = (v.cuda() for v in tokens(M, K, 1))
+    _, packed, alpha = weights(orc, N, K, 2)
+    alpha = alpha.cuda()
+    x, w = torch.randn((M, K), device="cuda"), torch.ones(K, device="cuda")
+    dy = torch.randn((M, N), device="cuda")
+    res = torch.randn((M, N), device="cuda")
+    on = lambda t: t.clone().requires_grad_()
+    mean, rstd = bw.layernorm(x, stats=True)[1:]
+    cases = {
+        "gemm_fused": [lambda f: bw.gemm_fused(q, s, packed, f(alpha), N, K),
+                       lambda f: bw.gemm_fused(q, f(s), packed, alpha, N, K),
+                       lambda f: bw.gemm_fused(q, s, packed, alpha, N, K, bias=f(alpha)),
+                       lambda f: bw.gemm_fused(q, s, packed, alpha, N, K, residual=f(res))],
+        "glu": [lambda f: bw.glu(q, s, packed, f(alpha), packed, alpha, N, K),
+                lambda f: bw.glu(q, s, packed, alpha, packed, f(alpha), N, K)],
+        "layernorm": [lambda f: bw.layernorm(f(x), w), lambda f: bw.layernorm(x, f(w)),
+                      lambda f: bw.layernorm(x, w, f(w)), lambda f: bw.layernorm(x, f(w), stats=True)],
+        "layernorm_quantize": [lambda f: bw.layernorm_quantize(f(x), w), lambda f: bw.layernorm_quantize(x, w, f(w))],
+        "gemm_fused_backward": [lambda f: bw.gemm_fused_backward(f(dy), q, s, packed, alpha, N, K)],
+        "glu_backward": [lambda f: bw.glu_backward(dy, q, s, packed, f(alpha), packed, alpha, N, K)],
+        "layernorm_backward": [lambda f: bw.layernorm_backward(f(x), x, mean, rstd, w)],
+    }
+    for name, calls in cases.items():
+        for call in calls:
+            plain, tracked = call(lambda t: t), call(on)
+            with torch.no_grad():
+                without = call(on)
+            plain, tracked, without = (v if isinstance(v, tuple) else (v,) for v in (plain, tracked, without))
+            for a, b, c in zip(plain, tracked, without):
+                assert torch.equal(a, b) and torch.equal(a, c) and not a.requires_grad and not c.requires_grad
+                assert b.requires_grad == b.is_floating_point()
+                if b.requires_grad:
+                    with pytest.raises(RuntimeError, match=f"bit_weight_amd.{name} .*not implemented"):
+                        b.sum().backward()
+    # a given output cannot carry it: refused, as torch's own functions do
+    out = torch.empty((M, N), device="cuda")
+    for call in (lambda: bw.gemm_fused(q, s, packed, on(alpha), N, K, out=out),
+                 lambda: bw.glu(q, s, packed, on(alpha), packed, alpha, N, K, out=out),
+                 lambda: bw.gemm_fused(q, s, packed, alpha, N, K, out=on(out)),
+                 lambda: bw.layernorm(on(x), out=torch.empty_like(x)),
+                 lambda: bw.layernorm_backward(x, x, mean, rstd, on(w), out=torch.empty_like(x))):
+        with pytest.raises(RuntimeError, match="out="):
+            call()
+        with torch.no_grad():
+            call()
+
+
+def test_a_hand_written_autograd_function(orc):
+    """The way to train through the operators: a torch.autograd.Function of
+    their forward and backward."""
+    M, N, K = 5, 64, 128
+    q, s = (v.cuda() for v in tokens(M, K, 1))
+    _, pg, ag = weights(orc, N, K, 2)
+    _, pu, au = weights(orc, N, K, 3)
+    ag, au = ag.cuda().requires_grad_(), au.cuda().requires_grad_()
+
+    class Glu(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, ag, au):
+            ctx.save_for_backward(ag, au)
+            return bw.glu(q, s, pg, ag, pu, au, N, K)
+
+        @staticmethod
+        def backward(ctx, dh):
+            ag, au = ctx.saved_tensors
+            return bw.glu_backward(dh, q, s, pg, ag, pu, au, N, K)[1:]
+
+    h = Glu.apply(ag, au)
+    dh = torch.randn_like(h)
+    h.backward(dh)
+    with torch.no_grad():
+        _, dg, du = bw.glu_backward(dh, q, s, pg, ag, pu, au, N, K)
+    assert torch.equal(ag.grad, dg) and torch.equal(au.grad, du)
