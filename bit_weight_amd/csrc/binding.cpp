@@ -414,7 +414,9 @@ struct Stats {
   float* pm = nullptr;
   float* pr = nullptr;
   Stats(PyObject* wanted, const Features& f) {
-    if (!PyObject_IsTrue(wanted)) return;
+    const int truth = PyObject_IsTrue(wanted);
+    if (truth < 0) throw Raised{};
+    if (!truth) return;
     mean = empty({f.M}, at::kFloat, f.device);
     rstd = empty({f.M}, at::kFloat, f.device);
     pm = mean.data_ptr<float>();

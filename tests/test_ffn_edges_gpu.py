@@ -401,3 +401,10 @@ def test_a_hand_written_autograd_function(orc):
     with torch.no_grad():
         _, dg, du = bw.glu_backward(dh, q, s, pg, ag, pu, au, N, K)
     assert torch.equal(ag.grad, dg) and torch.equal(au.grad, du)
+
+
+def test_stats_that_have_no_truth_value_are_refused():
+    x = torch.randn((2, 128), device="cuda")
+    for call in (bw.layernorm, bw.layernorm_quantize):
+        with pytest.raises(RuntimeError, match="ambiguous"):
+            call(x, stats=torch.ones(2))
