@@ -341,7 +341,8 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 256) void norm_kernel(NormArgs a) 
 }
 
 // The forward on tokens of more than kNormMaxK features: one workgroup of 16
-// waves per token, which reads the token again for each pass (from L2).
+// waves per token, which reads the token again for each pass: from L2 while the
+// tokens in work fit it (an XCD's 32 tokens in 4 MB: 64K features in 16 bits).
 template <typename T, bool Q>
 __global__ __launch_bounds__(kLoopThreads) void norm_loop_kernel(NormArgs a) {
   using S = std::conditional_t<Q, double, float>;
@@ -625,11 +626,13 @@ __global__ __launch_bounds__(1024) void norm_columns_kernel(const float* part, i
 // As many workgroups as the registers hold at once, which then take further
 // tokens in turns with w and b at hand (bf16, us, against 4 per CU: 2048 x 4096
 // 8.6 -> 8.1, into int8 11.1 -> 10.0; 4096 x 8192 29.6 -> 26.5, 2048 x 12288 27.4
-// -> 24.8; but 4096 x 2048 9.7 -> 10.1).
+// -> 24.8).  With up to 8 features a lane that is 4 (16384 x 2048 29.9 -> 27.6
+// against 3, 4096 x 2048 9.40 -> 9.33), but 3 into int8 (2048 x 2048 8.1 -> 7.8
+// against 4, though 16384 x 2048 42.1 -> 44.3).
 template <typename T, int V, int W, int J, bool Q>
 void launch_norm_tokens(const NormArgs& a, hipStream_t stream) {
   constexpr int kThreads = W == 16 ? 1024 : 256, G = kThreads / 64 / W;
-  const int need = (a.M + G - 1) / G, most = (W == 16 ? 1 : J * V > 16 ? 2 : 3) * kCUs;
+  const int need = (a.M + G - 1) / G, most = (W == 16 ? 1 : J * V > 16 ? 2 : J * V > 8 || Q ? 3 : 4) * kCUs;
   hipLaunchKernelGGL((norm_kernel<T, V, W, J, Q>), dim3(need < most ? need : most), dim3(kThreads), 0, stream, a);
 }
 
