@@ -242,7 +242,9 @@ __device__ __forceinline__ void z_to_lds(__amdgpu_buffer_rsrc_t r, uint8_t* dst,
                                            0, 0);
 }
 
-// 2^31 bytes from base on: what 256 tokens' z at most takes.
+// 2^31 bytes from base on.  The range check sees the lanes' offsets, here below
+// 2^31, and not the scalar one added to them: 256 tokens' z, whose last bytes
+// lie 2^31 behind the first, is within it either way.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t all_of(const void* base) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)0x80000000u, 0x00020000);
 }
