@@ -408,3 +408,55 @@ def test_stats_that_have_no_truth_value_are_refused():
     for call in (bw.layernorm, bw.layernorm_quantize):
         with pytest.raises(RuntimeError, match="ambiguous"):
             call(x, stats=torch.ones(2))
+
+
+# The ends of the ranges: 2^20 tokens, outputs or inputs, one block of the others
+@pytest.mark.parametrize("t", list(ref.TYPES))
+@pytest.mark.parametrize("M,N,K", [(1 << 20, 4, 16), (1, 1 << 20, 16), (70, 1 << 18, 16), (3, 4, 1 << 20), (140, 4, 1 << 18)])
+def test_products_at_the_ends_of_their_range(orc, M, N, K, t):
+    dtype = ref.TYPES[t]
+    q, s = tokens(M, K, 71)
+    Tg, pg, ag = weights(orc, N, K, 72)
+    Tu, pu, au = weights(orc, N, K, 73)
+    bias, res = torch.randn(N, generator=_gen(74)), torch.randn((M, N), generator=_gen(75)).to(dtype)
+    dy = (torch.randn((M, N), generator=_gen(76)) * 0.01).to(dtype)
+    d = [v.cuda() for v in (q, s)]
+    y = bw.gemm_fused(*d, pg, ag.cuda(), N, K, bias=bias.cuda(), act="gelu", residual=res.cuda(), dtype=dtype)
+    check("y", y, *ref.gemm_fused(q, s, Tg, ag, bias, "gelu", res, dtype))
+    h = bw.glu(*d, pg, ag.cuda(), pu, au.cuda(), N, K, dtype=dtype)
+    check("h", h, *ref.glu(q, s, Tg, ag, Tu, au, "silu", dtype))
+    for name, v, w in zip(("dx", "dalpha", "dbias"),
+                          bw.gemm_fused_backward(dy.cuda(), *d, pg, ag.cuda(), N, K, bias=bias.cuda(), act="gelu"),
+                          ref.gemm_fused_backward(dy, q, s, Tg, ag, bias, "gelu", dtype)):
+        check(name, v, *w)
+    for name, v, w in zip(("dx", "dgate", "dup"), bw.glu_backward(dy.cuda(), *d, pg, ag.cuda(), pu, au.cuda(), N, K),
+                          ref.glu_backward(dy, q, s, Tg, ag, Tu, au, "silu", dtype)):
+        check(name, v, *w)
+
+
+EPS = torch.tensor(1e-5).item()     # the default, as fp32 holds it
+
+
+@pytest.mark.parametrize("t", list(ref.TYPES))
+@pytest.mark.parametrize("M,K", [(1 << 20, 4), (2, 1 << 20)])
+def test_norms_at_the_ends_of_their_range(M, K, t):
+    dtype = ref.TYPES[t]
+    g = _gen(81)
+    x, w, b = torch.randn((M, K), generator=g).to(dtype), 1 + 0.3 * torch.randn(K, generator=g), 0.2 * torch.randn(K, generator=g)
+    dy = torch.randn((M, K), generator=g).to(dtype)
+    y, mean, rstd = bw.layernorm(x.cuda(), w.cuda(), b.cuda(), stats=True)
+    check("y", y, *ref.layernorm(x, w, b, EPS, dtype)[:2])
+    q, s = bw.layernorm_quantize(x.cuda(), w.cuda(), b.cuda())
+    rv, rs = ref.layernorm_quantize(x, w, b, EPS)
+    # equal but where 64-bit arithmetic (within 1e-12 here) does not decide a
+    # rounding: of the scale to fp32, of a value between two steps
+    d = x.double() - x.double().mean(1, keepdim=True)
+    s64 = (d / torch.sqrt((d * d).mean(1, keepdim=True) + EPS) * w.double() + b.double()).abs().amax(1) / 127
+    open_ = (s64 * (1 + 1e-12)).float() != (s64 * (1 - 1e-12)).float()
+    # (undecided: 2e-12 of steps of 2^-24 to 2^-23, so up to M 2^-14.8 on average)
+    assert bool(((s.cpu() == rs) | open_).all()) and int(open_.sum()) <= 2 + M * 2.0 ** -13
+    border = (rv - rv.floor() - 0.5).abs() < 1e-9
+    assert bool(((q.cpu().double() == rv.round().clamp(-127, 127)) | border | open_[:, None]).all())
+    for name, v, want in zip(("dx", "dw", "db"), bw.layernorm_backward(dy.cuda(), x.cuda(), mean, rstd, w.cuda()),
+                             ref.layernorm_backward(dy, x, mean.cpu(), rstd.cpu(), w, dtype)):
+        check(name, v, *want)
