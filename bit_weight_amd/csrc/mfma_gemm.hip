@@ -52,7 +52,7 @@
 // epilogue takes its sums through LDS 16 rows at a time, its other inputs
 // requested together ahead of it.  The main loop bounds all of them (bf16,
 // K = 4096, N = 14336: gated M=512 59.5 us, 2.02 POP/s; its backward sums at
-// M=2048 250 us, 1.92 POP/s with the epilogue; K = 14336, N = 4096, M=512
+// M=2048 254 us, 1.89 POP/s with the epilogue; K = 14336, N = 4096, M=512
 // 33 us, 1.8 POP/s; the vendor's int8 product reaches 2.70 POP/s at 8192^3,
 // and 1.54 and 2.26 on the two gated shapes).
 // Tiles are numbered so that the 8 XCDs (workgroups are dealt round-robin)
