@@ -1,8 +1,8 @@
 // Gradients of the products with an epilogue.  Three steps, the scratch
 // memory between them:
-//  1. grad_prepare_kernel reads what bounds the finite gradients (per token
-//     max|dy| and sum|q|, per matrix max|alpha|, the largest positive bias) and
-//     lays the weight codes out for step 3;
+//  1. grad_prepare_kernel reads what the size of the finite gradients follows
+//     from (per token max|dy|, sum|q| and sum q^2, per matrix max|alpha|, the
+//     largest positive bias) and lays the weight codes out for step 3;
 //  2. the forward's prefill kernel recomputes the exact sums (1.25 bits per
 //     weight: cheaper than saving M x N fp32 values in the forward) and its
 //     epilogue writes z = dz alpha in scaled fp16 (sherry_grad.h) and partial
@@ -51,13 +51,13 @@ struct PrepareArgs {
   const void* dy;
   const int8_t* q;
   uint8_t* codes;         // [2 k tiles][parts x row tiles][kHalfBytes]
-  float2* rows;
+  GradRow* rows;
   float* tops;
   uint32_t* largest;
   int parts, dtype, M, N, K;
 };
 
-// |v|, or 0 where v is infinite or NaN: a bound on the finite gradients.
+// |v|, or 0 where v is infinite or NaN.
 __device__ __forceinline__ float finite_abs(float v) {
   const float t = fabsf(v);
   return t <= 3.402823466e38f ? t : 0.0f;
@@ -85,6 +85,7 @@ __global__ __launch_bounds__(kPrepThreads) void grad_prepare_kernel(PrepareArgs 
   __shared__ __attribute__((aligned(16))) uint8_t tile[kPrepThreads / 64][kTileRows * kPitch];
   __shared__ uint8_t fields[32];
   __shared__ float red[kPrepThreads / 64];
+  __shared__ float2 sums[kPrepThreads / 64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   // maxima: kAhead loads in flight per thread (a load a turn, waited for,
   // made block 0 the launch's last: 54 us at N = 14336)
@@ -117,7 +118,7 @@ __global__ __launch_bounds__(kPrepThreads) void grad_prepare_kernel(PrepareArgs 
         t = fmaxf(fmaxf(t, fmaxf(finite_abs(v[i][0]), finite_abs(v[i][1]))),
                   fmaxf(finite_abs(v[i][2]), finite_abs(v[i][3])));
     }
-    int s = 0;
+    int s = 0, squares = 0;
     const int4* q = reinterpret_cast<const int4*>(a.q + (size_t)m * a.K);
     for (int k = tid; k < a.K / 16; k += kPrepThreads) {
       const int4 v = q[k];
@@ -125,16 +126,22 @@ __global__ __launch_bounds__(kPrepThreads) void grad_prepare_kernel(PrepareArgs 
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int b = 0; b < 4; ++b) s += abs((w[i] << (24 - 8 * b)) >> 24);
+        for (int b = 0; b < 4; ++b) {
+          const int x = (w[i] << (24 - 8 * b)) >> 24;
+          s += abs(x);
+          squares += x * x;
+        }
     }
     t = block_top(t, red);
-    // (a lane's sum is below 2^24: 128 K / kPrepThreads)
-    const float total = wave_sum((float)s);
+    // (a lane's sums stay below 2^19 and 2^26: K / kPrepThreads values)
+    const float2 total = make_float2(wave_sum((float)s), wave_sum((float)squares));
     __syncthreads();
-    if (lane == 0) red[wave] = total;
+    if (lane == 0) sums[wave] = total;
     __syncthreads();
     if (tid == 0) {
-      a.rows[m] = make_float2(t, (red[0] + red[1]) + (red[2] + red[3]));
+      const float sum = (sums[0].x + sums[1].x) + (sums[2].x + sums[3].x);
+      const float square = (sums[0].y + sums[1].y) + (sums[2].y + sums[3].y);
+      a.rows[m] = GradRow{t, sum, fminf(sum, kSpread * sqrtf(0.75f * square)), 0.0f};
       a.largest[m] = 0u;
     }
     return;
@@ -515,7 +522,7 @@ GradPlan plan_grad(const GemmPlan& product, int M, int N, int K, int parts, int 
     return here;
   };
   p.tops = take(3 * sizeof(float));
-  p.rows = take((size_t)M * sizeof(float2));
+  p.rows = take((size_t)M * sizeof(GradRow));
   p.largest = take((size_t)M * sizeof(uint32_t));
   p.back = take((size_t)M * sizeof(float));
   p.codes = take(2 * (size_t)k_tiles(K) * p.R * kHalfBytes);
@@ -541,7 +548,7 @@ hipError_t launch_backward(const GemmPlan& product, const GradPlan& p, const Gem
   pa.dy = e.grad.dy;
   pa.q = a.x;
   pa.codes = reinterpret_cast<uint8_t*>(base + p.codes);
-  pa.rows = reinterpret_cast<float2*>(base + p.rows);
+  pa.rows = reinterpret_cast<GradRow*>(base + p.rows);
   pa.tops = reinterpret_cast<float*>(base + p.tops);
   pa.largest = reinterpret_cast<uint32_t*>(base + p.largest);
   pa.parts = parts;

@@ -431,7 +431,7 @@ __device__ __forceinline__ void product_tile(GemmArgs a, EpilogueOf<EP> e, int M
   uint32_t h0, h1;
   v4i bA0[kNT], bA1[kNT], bB0[kNT], bB1[kNT];
   float sx_in = 0.0f, al_in = 0.0f, al2_in = 0.0f;
-  float2 row_in = make_float2(0.0f, 0.0f);
+  GradRow row_in{};
   float tops_in[3] = {0.0f, 0.0f, 0.0f};
   uint32_t largest_in = 0u;
   if constexpr (kOwn) {
@@ -468,8 +468,10 @@ __device__ __forceinline__ void product_tile(GemmArgs a, EpilogueOf<EP> e, int M
     if (tid < kBM) {
       sxs[tid] = sx_in;
       if constexpr (kBack) {
-        const int bound = grad_exponent(row_in, sx_in, tops_in, e.act, kGlu);
-        inv_rows[tid] = exp2_of(kAgain ? exponent_used(bound, largest_in, e.grad.terms) : bound);
+        int exponent = first_exponent(row_in, sx_in, tops_in, e.act, kGlu);
+        if constexpr (kAgain)
+          exponent = last_exponent(exponent, largest_in, row_in, sx_in, tops_in, e.act, kGlu, e.grad.terms);
+        inv_rows[tid] = exp2_of(exponent);
       }
     }
     if (tid < kBNO) {
@@ -747,8 +749,8 @@ __global__ __launch_bounds__(kThreads) void mfma_gemm_kernel(const uint8_t* pack
 }
 
 // The backward's gradients once more, for the token tiles with a token whose
-// largest |z| lies so far below the bound that fp16's range would cost it
-// digits (sherry_grad.h): now under a scale of its own.  The others, as a rule
+// largest |z| passes fp16's range under its first scale, or lies so far below
+// that the range costs it digits (sherry_grad.h): now under a scale of its own.  The others, as a rule
 // all of them, are left after a look at their tokens; so that this look costs
 // little, a grid of one round walks the tiles, `share` workgroups to a token
 // tile: 4.7 us at M=2048, N=14336 gated, of 599, and 3.8 at M=77, N=1300, of 29.
@@ -764,10 +766,12 @@ __global__ __launch_bounds__(kThreads) void gradients_again_kernel(GemmArgs a, i
   for (int mt = blockIdx.x / share; mt < mt_count; mt += at_once) {
     if (tid < 64) {
       const int m = min(kAgainBM * mt + tid, a.M - 1);
-      const int bound = grad_exponent(e.grad.rows[m], a.s_x[m], e.grad.tops, e.act, ep_glu(EP));
-      const int used = exponent_used(bound, e.grad.largest[m], e.grad.terms);
-      if (blockIdx.x % share == 0) e.grad.back[m] = 0.5f * exp2_of(-used);   // (the last token's by several, alike)
-      const unsigned long long any = __ballot(used != bound);
+      const GradRow row = e.grad.rows[m];
+      const int first = first_exponent(row, a.s_x[m], e.grad.tops, e.act, ep_glu(EP));
+      const int last =
+          last_exponent(first, e.grad.largest[m], row, a.s_x[m], e.grad.tops, e.act, ep_glu(EP), e.grad.terms);
+      if (blockIdx.x % share == 0) e.grad.back[m] = 0.5f * exp2_of(-last);   // (the last token's by several, alike)
+      const unsigned long long any = __ballot(first != last);
       if (tid == 0) wanted = any != 0;
     }
     __syncthreads();

@@ -6,21 +6,24 @@
 // eighth of the rounding a bf16 result gets anyway) or, for fp16 and fp32
 // results, as two, high and low, which together keep 22 bits.  fp16 has the
 // digits but not the range, so each token's z is scaled by a power of two
-// (exact) that puts a bound on |z| at 2^15.  The bound is known before any z:
-//   pre-activation <= P = s_x sum|q| max|alpha| + max(bias, 0),
+// (exact) that puts its size at 2^15 at most.  That size is known before any z:
+//   pre-activation <= P = s_x S max|alpha| + max(bias, 0),
 //   |act'| <= 1.25 (2 P for relu2, where it is not 0), |act| <= P (P^2 for
 //   relu2).  A bias that closes its output, however far below 0, so leaves
 //   the others' scale alone.
-// What the bound cannot know is which of its factors meet: the largest |z| of a
-// token lies 2^4 .. 2^14 below it where scales and gradients are of one size
-// (K up to 16384),
-// and any number of powers of two where a row scale or a column of gradients
-// far above the others belongs to an output whose gradient is 0.  A value is
-// off by up to 2^-25 after scaling (half of fp16's least step), so S powers of
-// two of slack make that 2^(S - 39) of the token's largest |z|.  The first pass
-// therefore also finds each token's largest |z|, and where S is above
-// kMostSlack, which leaves 2^-16 (one term) or 2^-24 (two), a second pass
-// writes the token's z again under the scale that its largest asks for.
+// With S = sum|q| this is a bound, but one that lies sqrt(K) / 4 above what sums
+// of K terms reach, twice over in the gated relu2.  S is therefore kSpread
+// standard deviations of a sum with signs at random, sqrt(3/4 sum q^2), where
+// that is less.  Nor can it know which of its factors meet: the largest |z| of a
+// token lies 2 to 2^9 below it where scales and gradients are of one size, and
+// any number of powers of two where a row scale or a column of gradients far
+// above the others belongs to an output whose gradient is 0.  A value is off by
+// up to 2^-25 after scaling (half of fp16's least step), so S powers of two of
+// slack make that 2^(S - 39) of the token's largest |z|.  The first pass
+// therefore also finds each token's largest |z|.  Where that passes 2^15, or
+// where S is above kMostSlack, which leaves 2^-16 (one term) or 2^-24 (two), a
+// second pass writes the token's z again under the scale that its largest
+// asks for.
 #pragma once
 
 #include "sherry_launch.h"
@@ -28,11 +31,14 @@
 
 namespace sherry {
 
-// e such that |z| 2^e <= 2^15 for every z of a token: rows = (max |dy|,
-// sum |q|), tops = (max |alpha|, max |alpha2|, max(bias, 0)), the maxima over
-// finite values: an infinite or NaN gradient is one whatever the scale.
-__device__ __forceinline__ int grad_exponent(float2 row, float s_x, const float* tops, int act, bool glu) {
-  const double dy = row.x, sum = (double)row.y * fabs((double)s_x);
+constexpr float kSpread = 8.0f;
+
+// e such that |z| 2^e <= 2^15 for every z of a token if S bounds its sums: tops =
+// (max |alpha|, max |alpha2|, max(bias, 0)), the maxima over finite values: an
+// infinite or NaN gradient is one whatever the scale.
+__device__ __forceinline__ int grad_exponent(const GradRow& row, float S, float s_x, const float* tops, int act,
+                                             bool glu) {
+  const double dy = row.dy, sum = (double)S * fabs((double)s_x);
   const double a1 = tops[0], a2 = tops[1], pre = sum * a1 + (glu ? 0.0 : (double)tops[2]);
   const double slope = act == SHERRY_ACT_RELU2 ? 2.0 * pre : 1.25;
   const double bound = glu ? dy * slope * a1 * sum * a2 : dy * slope * a1;
@@ -42,13 +48,21 @@ __device__ __forceinline__ int grad_exponent(float2 row, float s_x, const float*
   return e < -120 ? -120 : e > 120 ? 120 : e;
 }
 
-// The same, given the bits of the largest |z| (0: none known; infinite: the
-// token's dx has no finite value): the exponent that z is left under.
+// That of the first pass.
+__device__ __forceinline__ int first_exponent(const GradRow& row, float s_x, const float* tops, int act, bool glu) {
+  return grad_exponent(row, row.likely, s_x, tops, act, glu);
+}
+
+// The exponent that z is left under, given the first pass's and the bits of the
+// largest |z| it found.  An infinite one leaves the token's dx without a finite
+// value; the bound then keeps the finite z from becoming infinite too.
 constexpr int kMostSlack[2] = {23, 15};   // with one term, with two
-__device__ __forceinline__ int exponent_used(int bound, uint32_t largest, int terms) {
-  if (largest == 0u || largest >= 0x7F800000u) return bound;
+__device__ __forceinline__ int last_exponent(int first, uint32_t largest, const GradRow& row, float s_x,
+                                             const float* tops, int act, bool glu, int terms) {
+  if (largest == 0u) return first;
+  if (largest >= 0x7F800000u) return grad_exponent(row, row.sum, s_x, tops, act, glu);
   const int own = 14 - ilogbf(__builtin_bit_cast(float, largest));   // |z| 2^own < 2^15
-  if (own - bound <= (terms == 2 ? kMostSlack[1] : kMostSlack[0])) return bound;
+  if (own >= first && own - first <= (terms == 2 ? kMostSlack[1] : kMostSlack[0])) return first;
   return own > 120 ? 120 : own;
 }
 

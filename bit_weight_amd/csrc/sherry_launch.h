@@ -44,10 +44,18 @@ void set_plan_override(int path, int rw, int ch, int splits);
 
 GemmPlan plan_gemm(int M, int N, int K);
 
+// Backward: what the size of a token's gradients follows from.
+struct GradRow {
+  float dy;        // max |dy|
+  float sum;       // sum |q|: no product of the token and a weight row is larger
+  float likely;    // what none of them passes unless the row takes the token's signs
+  float unused;
+};
+
 // Backward: what the recomputing product writes and scales by.
 struct GradArgs {
   const void* dy;          // [M,N] of type dtype
-  const float2* rows;      // per token: max |dy|, sum |q|
+  const GradRow* rows;     // per token
   const float* tops;       // max |alpha|, max |alpha2|, max(bias, 0)
   uint16_t* z;             // fp16 [M][terms][parts][64 row tiles]: the scaled gradients
   uint32_t* largest;       // per token: bits of the largest |dz alpha| (0 before the product)
@@ -156,8 +164,8 @@ hipError_t launch_mfma_gemv_epilogue(const GemmPlan& plan, const GemmArgs& args,
 hipError_t launch_mfma_gemm_epilogue(const GemmPlan& plan, const GemmArgs& args, int ep,
                                      const EpilogueArgs& e, hipStream_t stream);
 
-// The backward product once more for the tokens whose gradients lie far below
-// their scale's bound (writes z, and `back` of every token; `largest` is complete).
+// The backward product once more for the tokens whose gradients do not fit
+// their scale (writes z, and `back` of every token; `largest` is complete).
 hipError_t launch_gradients_again(const GemmArgs& args, int ep, const EpilogueArgs& e, hipStream_t stream);
 
 // Plan of a backward pass: the input-gradient product's tiles and splits and

@@ -184,6 +184,58 @@ def test_captured_backward_beside_outliers_that_come_and_go(orc):
         assert all(torch.equal(a, b) for a, b in zip(eager, held))
 
 
+def aligned_tokens(M, K, T, rows, seed):
+    """Tokens of which every third takes the signs of a row of T, so that its
+    sum there is sqrt(K) / 8 times what tokens of their size reach elsewhere."""
+    q, s = tokens(M, K, seed)
+    for i, m in enumerate(range(0, M, 3)):
+        q[m] = 127 * T[rows[i % len(rows)]]
+    return q, s
+
+
+@pytest.mark.parametrize("t", list(ref.TYPES))
+@pytest.mark.parametrize("name", ["relu2", "silu", "gelu"])
+@pytest.mark.parametrize("M,N,K", [(1, 132, 4096), (70, 196, 4096), (300, 1100, 1040), (5, 68, 65536)])
+def test_backward_of_tokens_aligned_with_a_row(orc, M, N, K, name, t):
+    """Gradients above what the first scale allows for, gated (both matrices
+    alike) and not."""
+    dtype = ref.TYPES[t]
+    T, packed, alpha = weights(orc, N, K, 91)
+    q, s = aligned_tokens(M, K, T, (20, 3, 64), 92)
+    dh = (torch.randn((M, N), generator=_gen(93)) * 1e-4).to(dtype)
+    d = [v.cuda() for v in (dh, q, s)] + [packed, alpha.cuda()]
+    got = bw.glu_backward(*d, packed, alpha.cuda(), N, K, act=name)
+    torch.cuda.synchronize()
+    check("dx", got[0], *dx_and_bound(gated_terms(dh, q, s, T, alpha, T, alpha, name), dtype))
+    for v, w in zip(got[1:], ref.glu_backward(dh, q, s, T, alpha, T, alpha, name, dtype)[1:]):
+        check("dalpha", v, *w)
+    got = bw.gemm_fused_backward(*d, N, K, act=name)
+    torch.cuda.synchronize()
+    _, z = ref.product(q, s, T, alpha)
+    a, dz = alpha.double(), dh.double() * ref.slope(z, name)
+    e = dh.double().abs() * ref.slope_error(z, 3 * ref.U * z.abs(), name) + ref.U * dz.abs()
+    check("dx", got[0], *dx_and_bound([(dz * a, e * a.abs() + 2 * ref.U * (dz * a).abs(), T)], dtype))
+    for v, w in zip(got[1:], ref.gemm_fused_backward(dh, q, s, T, alpha, None, name, dtype)[1:]):
+        check("dalpha", v, *w)
+
+
+def test_infinite_gradient_beside_one_above_its_scale(orc):
+    """An infinite gradient at one output and a finite one at another that the
+    first scale would make infinite: only the first is."""
+    M, N, K = 6, 132, 4096
+    T, packed, alpha = weights(orc, N, K, 91)
+    q, s = aligned_tokens(M, K, T, (20,), 92)
+    acc = q[3].double() @ T.double().t()
+    acc[20] = 0
+    n = int(acc.argmax())
+    dy = torch.randn((M, N), generator=_gen(94))
+    dy[3, n], dy[3, 20] = float("inf"), -1e3
+    dx = bw.gemm_fused_backward(dy.cuda(), q.cuda(), s.cuda(), packed, alpha.cuda(), N, K, act="relu2")[0].cpu()
+    want = torch.where(T[n] == 0, float("nan"), float("inf") * T[n].float())
+    assert torch.equal(dx[3].isnan(), want.isnan()) and torch.equal(dx[3][T[n] != 0], want[T[n] != 0])
+    assert bool(dx[[0, 1, 2, 4, 5]].isfinite().all())
+
+
 @pytest.mark.parametrize("t", list(ref.TYPES))
 @pytest.mark.parametrize("closing", [-1e6, -1e12, LOWEST])
 @pytest.mark.parametrize("name", ["silu", "gelu", "gelu_tanh"])
