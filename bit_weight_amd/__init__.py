@@ -17,6 +17,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -24,6 +25,7 @@ __all__ = [
     "SherryError", "lib", "packed_bytes", "workspace_bytes", "plan", "plan_override",
     "quantize_pack", "quantize_act", "gemm", "gemm_i32", "linear", "linear_scratch_bytes", "concat_packed", "quantize_pack2", "gemm2",
     "gemm_fused", "gemm_fused_backward", "glu", "glu_backward", "layernorm", "layernorm_quantize", "layernorm_backward",
+    "qk_norm_rope", "qk_norm_rope_backward", "KVCache", "kv_cache", "cache_write", "cache_read", "cache_attention",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -98,6 +100,15 @@ def lib() -> ctypes.CDLL:
                 "sherry_layernorm_quantize": ([vp, vp, vp, cf, vp, vp, vp, vp, ci, i64, i64, vp], ci),
                 "sherry_layernorm_backward_scratch_bytes": ([i64, i64], sz),
                 "sherry_layernorm_backward": ([vp, vp, vp, vp, vp, vp, vp, vp, ci, i64, i64, vp, sz, vp], ci),
+                "sherry_qk_norm_rope": ([vp, i64, vp, vp, cf, ci, vp, i64, ci, vp, vp, vp, ci, i64, i64, i64, i64, vp], ci),
+                "sherry_qk_norm_rope_backward_scratch_bytes": ([i64, i64, i64, i64], sz),
+                "sherry_qk_norm_rope_backward": ([vp, vp, vp, i64, vp, vp, cf, ci, vp, i64, ci, vp, vp, i64, vp, vp, ci,
+                                                  i64, i64, i64, i64, vp, sz, vp], ci),
+                "sherry_cache_write": ([vp, vp, i64, vp, i64, ci, vp, i64, vp, vp, i64, i64, vp], ci),
+                "sherry_cache_read": ([vp, vp, vp, ci, vp, i64, vp, vp, i64, i64, vp], ci),
+                "sherry_cache_attention_scratch_bytes": ([i64, i64, i64, i64, i64], sz),
+                "sherry_cache_attention": ([vp, i64, i64, vp, vp, i64, vp, vp, i64, i64, cf, i64, i64, vp, vp, ci, vp, sz,
+                                            vp], ci),
                 "sherry_probe_read": ([vp, sz, vp, ci, ci, ci, vp], ci),
                 "sherry_probe_empty": ([vp], ci),
                 "sherry_probe_decode": ([ci, vp, ci, ci, vp], ci),
@@ -476,7 +487,7 @@ def _load_native():
             entries = {f"sherry_{n}": None for n in names}
             entries |= {"sherry_packed_bytes": None, "sherry_gemm_fused_workspace_bytes": None,
                         "sherry_glu_workspace_bytes": None}
-            entries |= {f"sherry_{n}_scratch_bytes": None for n in names if n.endswith("backward")}
+            entries |= {f"sherry_{n}_scratch_bytes": None for n in names if n.endswith(("backward", "attention"))}
             _binding.setup({n: ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in entries},
                            _workspaces._bufs, _zeroed_workspace, ACTIVATIONS, _raise_status)
             _native = _binding
@@ -545,3 +556,80 @@ def layernorm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rs
     """Gradients of layernorm -> (dx of x's type, dweight fp32 [K], dbias fp32
     [K]).  out may be dy."""
     return (_native or _load_native()).layernorm_backward(dy, x, mean, rstd, weight, out)
+
+
+# ------------------------------------------------------ attention operators
+class KVCache(NamedTuple):
+    """A paged cache of keys and values in 8 bits, blocks of 16 tokens of one
+    head with one scale each (see include/sherry.h for the layout)."""
+
+    k: torch.Tensor          # int8 [pages, heads, page_size / 16, dim / 16, 16 tokens, 16 features]
+    v: torch.Tensor          # int8 [pages, heads, page_size / 16, dim / 16, 16 features, 16 tokens]
+    k_scale: torch.Tensor    # fp32 [pages, heads, page_size / 16]
+    v_scale: torch.Tensor
+
+
+def kv_cache(pages: int, page_size: int, heads: int, dim: int, device="cuda") -> KVCache:
+    """An empty cache: page_size a power of two from 16 to 1024, dim a multiple
+    of 16 up to 256."""
+    if pages < 1 or not 16 <= page_size <= 1024 or page_size & (page_size - 1) or heads < 1 or dim % 16 or not 16 <= dim <= 256:
+        raise ValueError("kv_cache needs pages >= 1, page_size a power of two from 16 to 1024, heads >= 1 and dim a "
+                         "multiple of 16 up to 256")
+    shape = (pages, heads, page_size // 16)
+    k, v = (torch.zeros((*shape, dim // 16, 16, 16), dtype=torch.int8, device=device) for _ in range(2))
+    return KVCache(k, v, torch.zeros(shape, device=device), torch.zeros(shape, device=device))
+
+
+def qk_norm_rope(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, q_heads: int, k_heads: int, dim: int,
+                 q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None, eps: float = 1e-6,
+                 norm: bool = True, interleaved: bool = False):
+    """Norm of each query and key head of x [T, >= (q_heads + k_heads) dim] (a
+    stacked q/k/v product; float32, float16 or bfloat16, rows may be a slice's)
+    and its rotation by positions (int32 [T]) -> (q [T, q_heads, dim],
+    k [T, k_heads, dim]) of x's type.  freqs: float64 [rotary_dim / 2], radians a
+    position; the first rotary_dim features turn, as pairs of halves or of
+    neighbours (`interleaved`).  Weights are fp32 [dim]; norm=False rotates only."""
+    return (_native or _load_native()).qk_norm_rope(x, positions, freqs, q_heads, k_heads, dim, q_weight, k_weight, eps,
+                                                    norm, interleaved)
+
+
+def qk_norm_rope_backward(dq: torch.Tensor, dk: torch.Tensor, x: torch.Tensor, positions: torch.Tensor,
+                          freqs: torch.Tensor, q_weight: torch.Tensor | None = None,
+                          k_weight: torch.Tensor | None = None, eps: float = 1e-6, norm: bool = True,
+                          interleaved: bool = False, out: torch.Tensor | None = None):
+    """Gradients of qk_norm_rope from dq, dk and its inputs -> (dx, dq_weight fp32
+    [dim], dk_weight fp32 [dim]; both None with norm=False).  dx is
+    [T, (q_heads + k_heads) dim], or out, whose rows may be longer (the rest is
+    left as it was, for the values' gradient); out may be x."""
+    return (_native or _load_native()).qk_norm_rope_backward(dq, dk, x, positions, freqs, q_weight, k_weight, eps, norm,
+                                                             interleaved, out)
+
+
+def cache_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, starts: torch.Tensor,
+                lens: torch.Tensor) -> KVCache:
+    """Writes new tokens' k and v [T, heads, dim] (rows may be slices of a stacked
+    product) into the cache: rows starts[i] .. starts[i+1] - 1 are the last of the
+    lens[i] tokens of sequence i, whose pages are table[i] (all int32).  Each
+    block of 16 tokens and head has one power of two as its scale, which grows
+    with its tokens.  Returns the cache."""
+    (_native or _load_native()).cache_write(*cache, k, v, table, starts, lens)
+    return cache
+
+
+def cache_read(cache: KVCache, table: torch.Tensor, starts: torch.Tensor, lens: torch.Tensor, tokens: int,
+               dtype: torch.dtype = torch.float32):
+    """The last starts[i+1] - starts[i] tokens of each sequence back as `dtype` ->
+    (k, v), each [tokens, heads, dim]."""
+    return (_native or _load_native()).cache_read(*cache, table, starts, lens, tokens, dtype)
+
+
+def cache_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, starts: torch.Tensor, lens: torch.Tensor,
+                    scale: float | None = None, window: int | None = None, sinks: int = 0,
+                    out: torch.Tensor | None = None, lse: bool = False):
+    """Causal attention of each sequence's newest tokens, q [T, q_heads, dim] (rows
+    may be slices), over its lens[i] tokens in the cache, theirs included -> y
+    [T, q_heads, dim] of q's type, or (y, lse fp32 [T, q_heads]) with `lse`.
+    scale is 1 / sqrt(dim) unless given.  With a window a query sees its last
+    `window` tokens and the first `sinks` ones.  starts, lens and table are as
+    cache_write's."""
+    return (_native or _load_native()).cache_attention(q, *cache, table, starts, lens, scale, window, sinks, out, lse)

@@ -1,4 +1,4 @@
-// Argument marshalling of the feed-forward operators: checks torch tensors,
+// Argument marshalling of the feed-forward and attention operators: checks torch tensors,
 // allocates outputs and scratch memory and calls the library's C ABI on the
 // current stream of the tokens' device.  It holds no arithmetic.  (A CPython
 // module and not ctypes because a decode step's kernel takes 5 to 10 us: the
@@ -24,6 +24,7 @@
 #include <torch/csrc/autograd/functions/utils.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <cstdarg>
 #include <cstdint>
 #include <cstring>
@@ -52,6 +53,13 @@ decltype(&sherry_layernorm) f_layernorm;
 decltype(&sherry_layernorm_quantize) f_layernorm_quantize;
 decltype(&sherry_layernorm_backward) f_layernorm_backward;
 decltype(&sherry_layernorm_backward_scratch_bytes) f_layernorm_backward_scratch_bytes;
+decltype(&sherry_qk_norm_rope) f_qk_norm_rope;
+decltype(&sherry_qk_norm_rope_backward) f_qk_norm_rope_backward;
+decltype(&sherry_qk_norm_rope_backward_scratch_bytes) f_qk_norm_rope_backward_scratch_bytes;
+decltype(&sherry_cache_write) f_cache_write;
+decltype(&sherry_cache_read) f_cache_read;
+decltype(&sherry_cache_attention) f_cache_attention;
+decltype(&sherry_cache_attention_scratch_bytes) f_cache_attention_scratch_bytes;
 
 struct Entry {
   const char* name;
@@ -71,6 +79,13 @@ const Entry kEntries[] = {
     {"sherry_layernorm_quantize", &f_layernorm_quantize},
     {"sherry_layernorm_backward", &f_layernorm_backward},
     {"sherry_layernorm_backward_scratch_bytes", &f_layernorm_backward_scratch_bytes},
+    {"sherry_qk_norm_rope", &f_qk_norm_rope},
+    {"sherry_qk_norm_rope_backward", &f_qk_norm_rope_backward},
+    {"sherry_qk_norm_rope_backward_scratch_bytes", &f_qk_norm_rope_backward_scratch_bytes},
+    {"sherry_cache_write", &f_cache_write},
+    {"sherry_cache_read", &f_cache_read},
+    {"sherry_cache_attention", &f_cache_attention},
+    {"sherry_cache_attention_scratch_bytes", &f_cache_attention_scratch_bytes},
 };
 
 // A Python error is set; unwinds to the method's entry.
@@ -483,6 +498,248 @@ PyObject* layernorm_backward(PyObject* const* a) {
   return wrap_all({dx, dw, db});
 }
 
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Raised{};
+  return v;
+}
+
+// A matrix whose rows may lie further apart than they are long (a slice of a
+// stacked product): its rows' distance.
+void check_rows(const at::Tensor& t, const char* name, at::ScalarType type, int index) {
+  if (t.layout() != at::kStrided) fail(PyExc_RuntimeError, "%s must be a dense tensor", name);
+  if (!t.is_cuda()) fail(PyExc_RuntimeError, "%s must be on a GPU device, got %s", name, t.device().str().c_str());
+  if (t.scalar_type() != type)
+    fail(PyExc_RuntimeError, "%s must be %s, got %s", name, type_name(type), type_name(t.scalar_type()));
+  if (index >= 0 && t.get_device() != index)
+    fail(PyExc_RuntimeError, "%s must be on cuda:%d, got %s", name, index, t.device().str().c_str());
+}
+
+int64_t stride_of(const at::Tensor& t, int64_t width) { return t.size(0) > 1 ? t.stride(0) : (width + 7) / 8 * 8; }
+
+// [T, heads, dim], a row's heads one after another.
+int64_t heads_of(const at::Tensor& t, const char* name, at::ScalarType type, int index, int64_t T, int64_t heads,
+                 int64_t dim) {
+  check_rows(t, name, type, index);
+  if (t.dim() != 3 || t.size(0) != T || t.size(1) != heads || t.size(2) != dim)
+    fail(PyExc_RuntimeError, "%s must be [%lld,%lld,%lld]", name, (long long)T, (long long)heads, (long long)dim);
+  if ((dim > 1 && t.stride(2) != 1) || (heads > 1 && t.stride(1) != dim))
+    fail(PyExc_RuntimeError, "%s must have its rows' %lld values one after another", name, (long long)(heads * dim));
+  return stride_of(t, heads * dim);
+}
+
+// What qk_norm_rope and its backward share: x [T, width], positions, freqs, weights.
+struct Stacked {
+  int64_t T, width, stride;
+  int index, dtype;
+  at::ScalarType type;
+  at::Device device;
+  const void* x;
+  const int32_t* positions;
+  const double* freqs;
+  int64_t rotary;
+  float eps;
+  bool norm;
+  const float *wq, *wk;
+  Stacked(PyObject* px, PyObject* pp, PyObject* pf, PyObject* pwq, PyObject* pwk, PyObject* pe, PyObject* pn,
+          int64_t dim)
+      : device(at::kCPU) {
+    const at::Tensor& t = tensor_of(px, "x");
+    type = t.scalar_type();
+    dtype = dtype_of(type);
+    check_rows(t, "x", type, -1);
+    if (t.dim() != 2 || (t.size(1) > 1 && t.stride(1) != 1)) fail(PyExc_RuntimeError, "x must be 2-D with contiguous rows");
+    T = t.size(0);
+    width = t.size(1);
+    stride = stride_of(t, width);
+    index = (int)t.get_device();
+    device = t.device();
+    x = t.data_ptr();
+    positions = static_cast<const int32_t*>(vector_of(pp, "positions", at::kInt, index, T));
+    const at::Tensor& f = tensor_of(pf, "freqs");
+    check_tensor(f, "freqs", at::kDouble, index);
+    rotary = 2 * f.numel();
+    freqs = rotary ? f.data_ptr<double>() : nullptr;
+    norm = truth(pn);
+    eps = number(pe);
+    wq = static_cast<const float*>(vector_of(pwq, "q_weight", at::kFloat, index, dim, true));
+    wk = static_cast<const float*>(vector_of(pwk, "k_weight", at::kFloat, index, dim, true));
+    if (!norm && (wq || wk)) fail(PyExc_ValueError, "norm=False takes no weights");
+  }
+};
+
+// x, positions, freqs, q_heads, k_heads, dim, q_weight, k_weight, eps, norm, interleaved
+PyObject* qk_norm_rope(PyObject* const* a) {
+  const int64_t hq = integer(a[3]), hk = integer(a[4]), dim = integer(a[5]);
+  const Stacked s(a[0], a[1], a[2], a[6], a[7], a[8], a[9], dim);
+  if (hq < 1 || hk < 1 || dim < 1 || hq > 1024 || hk > 1024 || dim > 256 || s.width < (hq + hk) * dim)
+    fail(PyExc_RuntimeError, "x must hold (q_heads + k_heads) * dim values a row, at most 1024 heads of 256");
+  const bool interleaved = truth(a[10]);
+  const at::Tensor q = empty({s.T, hq, dim}, s.type, s.device), k = empty({s.T, hk, dim}, s.type, s.device);
+  Gradients gradients("qk_norm_rope", {a[0], a[6], a[7]});
+  launch("sherry_qk_norm_rope", s.index, [&](void* stream) {
+    return f_qk_norm_rope(s.x, s.stride, s.wq, s.wk, s.eps, s.norm, s.freqs, s.rotary, interleaved, s.positions,
+                          q.data_ptr(), k.data_ptr(), s.dtype, s.T, hq, hk, dim, stream);
+  });
+  gradients.mark({q, k});
+  return wrap_all({q, k});
+}
+
+// dq, dk, x, positions, freqs, q_weight, k_weight, eps, norm, interleaved, out
+PyObject* qk_norm_rope_backward(PyObject* const* a) {
+  const at::Tensor &dq = tensor_of(a[0], "dq"), &dk = tensor_of(a[1], "dk");
+  if (dq.dim() != 3 || dk.dim() != 3 || dq.size(2) != dk.size(2))
+    fail(PyExc_RuntimeError, "dq and dk must be [T,heads,dim]");
+  const int64_t hq = dq.size(1), hk = dk.size(1), dim = dq.size(2), width = (hq + hk) * dim;
+  const Stacked s(a[2], a[3], a[4], a[5], a[6], a[7], a[8], dim);
+  if (s.width < width) fail(PyExc_RuntimeError, "x must hold dq's and dk's heads, %lld values a row", (long long)width);
+  check_tensor(dq, "dq", s.type, s.index);
+  check_tensor(dk, "dk", s.type, s.index);
+  if (dq.size(0) != s.T || dk.size(0) != s.T) fail(PyExc_RuntimeError, "dq and dk must have x's %lld rows", (long long)s.T);
+  const bool interleaved = truth(a[9]);
+  at::Tensor dx;
+  int64_t stride = width;
+  if (a[10] == Py_None) {
+    dx = empty({s.T, width}, s.type, s.device);
+  } else {
+    dx = tensor_of(a[10], "out");
+    check_rows(dx, "out", s.type, s.index);
+    if (dx.dim() != 2 || dx.size(0) != s.T || dx.size(1) < width || (dx.size(1) > 1 && dx.stride(1) != 1))
+      fail(PyExc_RuntimeError, "out must be [%lld,at least %lld] with contiguous rows", (long long)s.T, (long long)width);
+    stride = stride_of(dx, dx.size(1));
+  }
+  at::Tensor dwq, dwk, scratch;
+  size_t bytes = 0;
+  if (s.norm) {
+    bytes = f_qk_norm_rope_backward_scratch_bytes(s.T, hq, hk, dim);
+    dwq = empty({dim}, at::kFloat, s.device);
+    dwk = empty({dim}, at::kFloat, s.device);
+    scratch = empty({(int64_t)bytes}, at::kByte, s.device);
+  }
+  Gradients gradients("qk_norm_rope_backward", {a[0], a[1], a[2], a[5], a[6]}, a[10]);
+  launch("sherry_qk_norm_rope_backward", s.index, [&](void* stream) {
+    return f_qk_norm_rope_backward(dq.data_ptr(), dk.data_ptr(), s.x, s.stride, s.wq, s.wk, s.eps, s.norm, s.freqs,
+                                   s.rotary, interleaved, s.positions, dx.data_ptr(), stride,
+                                   s.norm ? dwq.data_ptr<float>() : nullptr, s.norm ? dwk.data_ptr<float>() : nullptr,
+                                   s.dtype, s.T, hq, hk, dim, s.norm ? scratch.data_ptr() : nullptr, bytes, stream);
+  });
+  gradients.mark({dx, dwq, dwk});
+  return wrap_all({dx, dwq, dwk});      // (an undefined tensor becomes None)
+}
+
+// The cache's tensors and the sequences of a call.
+struct Cache {
+  sherry_kv_cache c;
+  int index;
+  at::Device device;
+  int64_t S, table_width;
+  const int32_t *table, *starts, *lens;
+  // k, v, k_scale, v_scale and table, starts, lens
+  Cache(PyObject* const* a, PyObject* const* b) : device(at::kCPU) {
+    const at::Tensor& k = tensor_of(a[0], "cache.k");
+    check_tensor(k, "cache.k", at::kChar, -1);
+    if (k.dim() != 6 || k.size(4) != 16 || k.size(5) != 16)
+      fail(PyExc_RuntimeError, "cache.k must be [pages,heads,page_size/16,dim/16,16,16]");
+    index = (int)k.get_device();
+    device = k.device();
+    const at::Tensor& v = tensor_of(a[1], "cache.v");
+    check_tensor(v, "cache.v", at::kChar, index);
+    if (v.sizes() != k.sizes()) fail(PyExc_RuntimeError, "cache.v must have cache.k's shape");
+    c.k = k.data_ptr();
+    c.v = v.data_ptr();
+    c.pages = k.size(0);
+    c.heads = k.size(1);
+    c.page_size = 16 * k.size(2);
+    c.dim = 16 * k.size(3);
+    float* scales[2];
+    const char* names[2] = {"cache.k_scale", "cache.v_scale"};
+    for (int i = 0; i < 2; ++i) {
+      const at::Tensor& s = tensor_of(a[2 + i], names[i]);
+      check_tensor(s, names[i], at::kFloat, index);
+      if (s.dim() != 3 || s.size(0) != k.size(0) || s.size(1) != k.size(1) || s.size(2) != k.size(2))
+        fail(PyExc_RuntimeError, "%s must be [pages,heads,page_size/16]", names[i]);
+      scales[i] = s.data_ptr<float>();
+    }
+    c.k_scale = scales[0];
+    c.v_scale = scales[1];
+    const at::Tensor& t = tensor_of(b[0], "table");
+    check_tensor(t, "table", at::kInt, index);
+    if (t.dim() != 2) fail(PyExc_RuntimeError, "table must be 2-D [sequences,pages of one]");
+    S = t.size(0);
+    table_width = t.size(1);
+    table = t.data_ptr<int32_t>();
+    starts = static_cast<const int32_t*>(vector_of(b[1], "starts", at::kInt, index, S + 1));
+    lens = static_cast<const int32_t*>(vector_of(b[2], "lens", at::kInt, index, S));
+  }
+};
+
+// k, v, k_scale, v_scale of the cache; k, v, table, starts, lens
+PyObject* cache_write(PyObject* const* a) {
+  const Cache c(a, a + 6);
+  const at::Tensor &k = tensor_of(a[4], "k"), &v = tensor_of(a[5], "v");
+  const int dtype = dtype_of(k.scalar_type());
+  if (k.dim() != 3) fail(PyExc_RuntimeError, "k must be [T,heads,dim]");
+  const int64_t T = k.size(0);
+  const int64_t ks = heads_of(k, "k", k.scalar_type(), c.index, T, c.c.heads, c.c.dim);
+  const int64_t vs = heads_of(v, "v", k.scalar_type(), c.index, T, c.c.heads, c.c.dim);
+  if (c10::GradMode::is_enabled() && (k.requires_grad() || v.requires_grad()))
+    fail(PyExc_RuntimeError, "cache_write cannot carry gradients, but a tensor requires one: call it in torch.no_grad()");
+  launch("sherry_cache_write", c.index, [&](void* stream) {
+    return f_cache_write(&c.c, k.data_ptr(), ks, v.data_ptr(), vs, dtype, c.table, c.table_width, c.starts, c.lens,
+                         c.S, T, stream);
+  });
+  Py_RETURN_NONE;
+}
+
+// k, v, k_scale, v_scale of the cache; table, starts, lens, tokens, dtype
+PyObject* cache_read(PyObject* const* a) {
+  const Cache c(a, a + 4);
+  const int64_t T = integer(a[7]);
+  const at::ScalarType type = scalar_of(a[8]);
+  const int dtype = dtype_of(type);
+  if (T < 1 || T > (1 << 20)) fail(PyExc_RuntimeError, "tokens must be from 1 to 2^20, got %lld", (long long)T);
+  const at::Tensor k = empty({T, c.c.heads, c.c.dim}, type, c.device), v = empty({T, c.c.heads, c.c.dim}, type, c.device);
+  launch("sherry_cache_read", c.index, [&](void* stream) {
+    return f_cache_read(&c.c, k.data_ptr(), v.data_ptr(), dtype, c.table, c.table_width, c.starts, c.lens, c.S, T,
+                        stream);
+  });
+  return wrap_all({k, v});
+}
+
+// q; k, v, k_scale, v_scale of the cache; table, starts, lens, scale, window, sinks, out, lse
+PyObject* cache_attention(PyObject* const* a) {
+  const Cache c(a + 1, a + 5);
+  const at::Tensor& q = tensor_of(a[0], "q");
+  const at::ScalarType type = q.scalar_type();
+  const int dtype = dtype_of(type);
+  if (q.dim() != 3) fail(PyExc_RuntimeError, "q must be [T,q_heads,dim]");
+  const int64_t T = q.size(0), heads = q.size(1);
+  const int64_t stride = heads_of(q, "q", type, c.index, T, heads, c.c.dim);
+  const float scale = a[8] == Py_None ? (float)(1.0 / std::sqrt((double)c.c.dim)) : number(a[8]);
+  const int64_t window = a[9] == Py_None ? 0 : integer(a[9]), sinks = integer(a[10]);
+  if (a[9] != Py_None && window < 1) fail(PyExc_ValueError, "window must be at least 1, or None");
+  at::Tensor y;
+  if (a[11] == Py_None) {
+    y = empty({T, heads, c.c.dim}, type, c.device);
+  } else {
+    y = tensor_of(a[11], "out");
+    check_tensor(y, "out", type, c.index);
+    if (y.sizes() != q.sizes()) fail(PyExc_RuntimeError, "out must have q's shape");
+  }
+  at::Tensor lse;
+  if (truth(a[12])) lse = empty({T, heads}, at::kFloat, c.device);
+  const size_t bytes = f_cache_attention_scratch_bytes(T, c.S, heads, c.c.heads, c.c.dim);
+  const at::Tensor scratch = empty({(int64_t)bytes}, at::kByte, c.device);
+  Gradients gradients("cache_attention", {a[0]}, a[11]);
+  launch("sherry_cache_attention", c.index, [&](void* stream) {
+    return f_cache_attention(q.data_ptr(), stride, heads, &c.c, c.table, c.table_width, c.starts, c.lens, c.S, T,
+                             scale, window, sinks, y.data_ptr(), lse.defined() ? lse.data_ptr<float>() : nullptr,
+                             dtype, scratch.data_ptr(), bytes, stream);
+  });
+  gradients.mark({y, lse});
+  return lse.defined() ? wrap_all({y, lse}) : wrap(y);
+}
+
 // functions (dict of name -> address), workspaces, workspace, activations, error
 PyObject* setup(PyObject* const* a) {
   if (!PyDict_Check(a[0]) || !PyDict_Check(a[1]) || !PyDict_Check(a[3])) fail(PyExc_TypeError, "expected a dict");
@@ -509,7 +766,9 @@ PyObject* setup(PyObject* const* a) {
 PyMethodDef kMethods[] = {
     SHERRY_METHOD(setup, 5),           SHERRY_METHOD(gemm_fused, 12),        SHERRY_METHOD(gemm_fused_backward, 9),
     SHERRY_METHOD(glu, 12),            SHERRY_METHOD(glu_backward, 10),      SHERRY_METHOD(layernorm, 6),
-    SHERRY_METHOD(layernorm_quantize, 5), SHERRY_METHOD(layernorm_backward, 6), {nullptr, nullptr, 0, nullptr}};
+    SHERRY_METHOD(layernorm_quantize, 5), SHERRY_METHOD(layernorm_backward, 6),
+    SHERRY_METHOD(qk_norm_rope, 11),   SHERRY_METHOD(qk_norm_rope_backward, 11), SHERRY_METHOD(cache_write, 9),
+    SHERRY_METHOD(cache_read, 9),      SHERRY_METHOD(cache_attention, 13),   {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -983,3 +983,208 @@ sherry_status sherry_layernorm_backward(const void* dy, const void* x, const flo
 }
 
 }  // extern "C"
+
+// --- attention operators ----------------------------------------------------
+namespace {
+
+constexpr int64_t kMaxHeads = 1024;
+constexpr int64_t kMaxTokens = int64_t(1) << 30;      // of a sequence
+
+bool head_ok(int64_t dim) { return dim >= 16 && dim <= 256 && dim % 16 == 0; }
+
+// Rows of `width` values, 16 bytes aligned each.
+bool rows_ok(int64_t stride, int64_t width) { return stride >= width && stride % 8 == 0 && stride <= kMaxTokens; }
+
+// What the forward and the backward of the head norms share.
+sherry_status head_norm_args(const void* x, int64_t x_stride, const float* q_weight, const float* k_weight, float eps,
+                             int norm, const double* freqs, int64_t rotary_dim, int interleaved,
+                             const int32_t* positions, const void* q, const void* k, int dtype, int64_t T,
+                             int64_t q_heads, int64_t k_heads, int64_t dim, HeadNormArgs& g) {
+  if (!positions || !q || !k || (rotary_dim > 0 && !freqs)) return SHERRY_ERR_NULL;
+  if (T < 1 || T > kMaxDim || q_heads < 1 || q_heads > kMaxHeads || k_heads < 1 || k_heads > kMaxHeads ||
+      !head_ok(dim) || rotary_dim < 0 || rotary_dim > dim || rotary_dim % 8 != 0)
+    return SHERRY_ERR_SHAPE;
+  if (x && !rows_ok(x_stride, (q_heads + k_heads) * dim)) return SHERRY_ERR_SHAPE;
+  if (!dtype_ok(dtype) || (norm && (!(eps > 0.0f) || !std::isfinite(eps))) || (!norm && (q_weight || k_weight)))
+    return SHERRY_ERR_ARG;
+  if (!aligned(x, 16) || !aligned(q, 16) || !aligned(k, 16) || !aligned(q_weight, 16) || !aligned(k_weight, 16) ||
+      !aligned(freqs, 8) || !aligned(positions, 4))
+    return SHERRY_ERR_ALIGN;
+  g.x = x;
+  g.x_stride = x_stride;
+  g.wq = q_weight;
+  g.wk = k_weight;
+  g.eps = eps;
+  g.freqs = freqs;
+  g.positions = positions;
+  g.T = (int)T;
+  g.Hq = (int)q_heads;
+  g.Hk = (int)k_heads;
+  g.D = (int)dim;
+  g.R = (int)rotary_dim;
+  g.interleaved = interleaved != 0;
+  g.norm = norm != 0;
+  g.dtype = dtype;
+  g.q = const_cast<void*>(q);
+  g.k = const_cast<void*>(k);
+  return SHERRY_OK;
+}
+
+sherry_status cache_args(const sherry_kv_cache* cache, const int32_t* table, int64_t table_width,
+                         const int32_t* starts, const int32_t* lens, int64_t S, int64_t T, int dtype, CacheArgs& c) {
+  if (!cache || !cache->k || !cache->v || !cache->k_scale || !cache->v_scale || !table || !starts || !lens)
+    return SHERRY_ERR_NULL;
+  const int64_t page = cache->page_size;
+  if (cache->pages < 1 || cache->pages > kMaxTokens || page < 16 || page > 1024 || (page & (page - 1)) != 0 ||
+      cache->heads < 1 || cache->heads > kMaxHeads / 2 || !head_ok(cache->dim) || table_width < 1 ||
+      table_width > kMaxTokens / page || S < 1 || S > kMaxDim || T < 1 || T > kMaxDim)
+    return SHERRY_ERR_SHAPE;
+  if (!dtype_ok(dtype)) return SHERRY_ERR_ARG;
+  if (!aligned(cache->k, 16) || !aligned(cache->v, 16) || !aligned(cache->k_scale, 4) || !aligned(cache->v_scale, 4) ||
+      !aligned(table, 4) || !aligned(starts, 4) || !aligned(lens, 4))
+    return SHERRY_ERR_ALIGN;
+  c.k = static_cast<uint8_t*>(cache->k);
+  c.v = static_cast<uint8_t*>(cache->v);
+  c.k_scale = cache->k_scale;
+  c.v_scale = cache->v_scale;
+  c.pages = (int)cache->pages;
+  c.block_shift = __builtin_ctz((unsigned)page) - 4;
+  c.H = (int)cache->heads;
+  c.D = (int)cache->dim;
+  c.table = table;
+  c.table_width = (int)table_width;
+  c.starts = starts;
+  c.lens = lens;
+  c.S = (int)S;
+  c.T = (int)T;
+  c.dtype = dtype;
+  return SHERRY_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+sherry_status sherry_qk_norm_rope(const void* x, int64_t x_stride, const float* q_weight, const float* k_weight,
+                                  float eps, int norm, const double* freqs, int64_t rotary_dim, int interleaved,
+                                  const int32_t* positions, void* q, void* k, int dtype, int64_t T, int64_t q_heads,
+                                  int64_t k_heads, int64_t dim, void* stream) {
+  if (!x) return SHERRY_ERR_NULL;
+  HeadNormArgs g{};
+  const sherry_status c = head_norm_args(x, x_stride, q_weight, k_weight, eps, norm, freqs, rotary_dim, interleaved,
+                                         positions, q, k, dtype, T, q_heads, k_heads, dim, g);
+  if (c != SHERRY_OK) return c;
+  const sherry_status d = check_device();
+  if (d != SHERRY_OK) return d;
+  return status_of(launch_head_norm(g, static_cast<hipStream_t>(stream)), false);
+}
+
+size_t sherry_qk_norm_rope_backward_scratch_bytes(int64_t T, int64_t q_heads, int64_t k_heads, int64_t dim) {
+  if (T < 1 || T > kMaxDim || q_heads < 1 || q_heads > kMaxHeads || k_heads < 1 || k_heads > kMaxHeads ||
+      !head_ok(dim))
+    return 0;
+  return round256((size_t)head_norm_backward_rows((int)T, (int)(q_heads + k_heads), (int)dim) * 2 * dim *
+                  sizeof(float));
+}
+
+sherry_status sherry_qk_norm_rope_backward(const void* dq, const void* dk, const void* x, int64_t x_stride,
+                                           const float* q_weight, const float* k_weight, float eps, int norm,
+                                           const double* freqs, int64_t rotary_dim, int interleaved,
+                                           const int32_t* positions, void* dx, int64_t dx_stride, float* dq_weight,
+                                           float* dk_weight, int dtype, int64_t T, int64_t q_heads, int64_t k_heads,
+                                           int64_t dim, void* scratch, size_t scratch_bytes, void* stream) {
+  if ((norm && !x) || !dx) return SHERRY_ERR_NULL;
+  HeadNormArgs g{};
+  const sherry_status c = head_norm_args(norm ? x : nullptr, x_stride, q_weight, k_weight, eps, norm, freqs,
+                                         rotary_dim, interleaved, positions, dq, dk, dtype, T, q_heads, k_heads, dim, g);
+  if (c != SHERRY_OK) return c;
+  if (!rows_ok(dx_stride, (q_heads + k_heads) * dim)) return SHERRY_ERR_SHAPE;
+  if (!norm && (dq_weight || dk_weight)) return SHERRY_ERR_ARG;
+  if (!aligned(dx, 16) || !aligned(dq_weight, 4) || !aligned(dk_weight, 4)) return SHERRY_ERR_ALIGN;
+  if (norm) {
+    if (!scratch || scratch_bytes < sherry_qk_norm_rope_backward_scratch_bytes(T, q_heads, k_heads, dim))
+      return SHERRY_ERR_WORKSPACE;
+    if (!aligned(scratch, 256)) return SHERRY_ERR_ALIGN;
+  }
+  const sherry_status d = check_device();
+  if (d != SHERRY_OK) return d;
+  g.dx = dx;
+  g.dx_stride = dx_stride;
+  g.part = static_cast<float*>(scratch);
+  bool partial = false;
+  const hipError_t e = launch_head_norm_backward(g, dq_weight, dk_weight, static_cast<hipStream_t>(stream), &partial);
+  return status_of(e, partial);
+}
+
+sherry_status sherry_cache_write(const sherry_kv_cache* cache, const void* k, int64_t k_stride, const void* v,
+                                 int64_t v_stride, int dtype, const int32_t* table, int64_t table_width,
+                                 const int32_t* starts, const int32_t* lens, int64_t S, int64_t T, void* stream) {
+  if (!k || !v) return SHERRY_ERR_NULL;
+  CacheArgs c{};
+  const sherry_status s = cache_args(cache, table, table_width, starts, lens, S, T, dtype, c);
+  if (s != SHERRY_OK) return s;
+  if (!rows_ok(k_stride, cache->heads * cache->dim) || !rows_ok(v_stride, cache->heads * cache->dim))
+    return SHERRY_ERR_SHAPE;
+  if (!aligned(k, 16) || !aligned(v, 16)) return SHERRY_ERR_ALIGN;
+  const sherry_status d = check_device();
+  if (d != SHERRY_OK) return d;
+  c.x_k = k;
+  c.x_v = v;
+  c.k_stride = k_stride;
+  c.v_stride = v_stride;
+  return status_of(launch_cache_write(c, static_cast<hipStream_t>(stream)), false);
+}
+
+sherry_status sherry_cache_read(const sherry_kv_cache* cache, void* k, void* v, int dtype, const int32_t* table,
+                                int64_t table_width, const int32_t* starts, const int32_t* lens, int64_t S, int64_t T,
+                                void* stream) {
+  if (!k || !v) return SHERRY_ERR_NULL;
+  CacheArgs c{};
+  const sherry_status s = cache_args(cache, table, table_width, starts, lens, S, T, dtype, c);
+  if (s != SHERRY_OK) return s;
+  if (!aligned(k, 16) || !aligned(v, 16)) return SHERRY_ERR_ALIGN;
+  const sherry_status d = check_device();
+  if (d != SHERRY_OK) return d;
+  return status_of(launch_cache_read(c, k, v, static_cast<hipStream_t>(stream)), false);
+}
+
+size_t sherry_cache_attention_scratch_bytes(int64_t T, int64_t S, int64_t q_heads, int64_t heads, int64_t dim) {
+  if (T < 1 || T > kMaxDim || S < 1 || S > kMaxDim || heads < 1 || heads > kMaxHeads / 2 || q_heads < 1 ||
+      q_heads > kMaxHeads || q_heads % heads != 0 || !head_ok(dim))
+    return 0;
+  return round256(cache_attention_scratch_bytes((int)T, (int)S, (int)q_heads, (int)heads, (int)dim));
+}
+
+sherry_status sherry_cache_attention(const void* q, int64_t q_stride, int64_t q_heads, const sherry_kv_cache* cache,
+                                     const int32_t* table, int64_t table_width, const int32_t* starts,
+                                     const int32_t* lens, int64_t S, int64_t T, float scale, int64_t window,
+                                     int64_t sinks, void* y, float* lse, int dtype, void* scratch,
+                                     size_t scratch_bytes, void* stream) {
+  if (!q || !y) return SHERRY_ERR_NULL;
+  AttentionArgs a{};
+  const sherry_status s = cache_args(cache, table, table_width, starts, lens, S, T, dtype, a.c);
+  if (s != SHERRY_OK) return s;
+  if (q_heads < 1 || q_heads > kMaxHeads || q_heads % cache->heads != 0 || !rows_ok(q_stride, q_heads * cache->dim))
+    return SHERRY_ERR_SHAPE;
+  if (!std::isfinite(scale) || window < 0 || sinks < 0) return SHERRY_ERR_ARG;
+  if (!aligned(q, 16) || !aligned(y, 16) || !aligned(lse, 4)) return SHERRY_ERR_ALIGN;
+  if (!scratch || scratch_bytes < sherry_cache_attention_scratch_bytes(T, S, q_heads, cache->heads, cache->dim))
+    return SHERRY_ERR_WORKSPACE;
+  if (!aligned(scratch, 256)) return SHERRY_ERR_ALIGN;
+  const sherry_status d = check_device();
+  if (d != SHERRY_OK) return d;
+  a.q = q;
+  a.q_stride = q_stride;
+  a.Hq = (int)q_heads;
+  a.scale = scale;
+  a.window = window >= kMaxTokens ? 0 : (int)window;      // (a window of every token is none)
+  a.sinks = (int)(sinks < kMaxTokens ? sinks : kMaxTokens);
+  a.y = y;
+  a.lse = lse;
+  a.scratch = static_cast<float*>(scratch);
+  bool partial = false;
+  const hipError_t e = launch_cache_attention(a, static_cast<hipStream_t>(stream), &partial);
+  return status_of(e, partial);
+}
+
+}  // extern "C"

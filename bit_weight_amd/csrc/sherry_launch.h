@@ -193,4 +193,56 @@ hipError_t launch_layernorm_backward(const void* dy, const void* x, const float*
                                      const float* w, void* dx, float* dw, float* db, int dtype, int M, int K,
                                      float* part, hipStream_t stream, bool* partial);
 
+// Norm and rotation of each head (head_norm.hip).  Forward: q, k are written;
+// backward: q, k hold dz and dx is written (its first (Hq + Hk) D columns).
+struct HeadNormArgs {
+  const void* x;            // [T, x_stride]: Hq heads of queries, then Hk of keys
+  int64_t x_stride, dx_stride;
+  const float *wq, *wk;     // nullptr: ones
+  float eps;
+  const double* freqs;      // [R / 2]
+  const int32_t* positions;
+  int T, Hq, Hk, D, R;
+  bool interleaved, norm;
+  int dtype;
+  void *q, *k, *dx;
+  float* part;              // backward: rows of 2 D partial weight gradients
+};
+hipError_t launch_head_norm(const HeadNormArgs& g, hipStream_t stream);
+int head_norm_backward_rows(int T, int heads, int D);
+hipError_t launch_head_norm_backward(const HeadNormArgs& g, float* dwq, float* dwk, hipStream_t stream,
+                                     bool* partial);
+
+// The 8-bit cache (sherry_cache.h) and what a call brings to it.
+struct CacheArgs {
+  uint8_t *k, *v;
+  float *k_scale, *v_scale;
+  int pages, block_shift;   // a page is 2^block_shift blocks of 16 tokens
+  int H, D;
+  const int32_t* table;     // [S, table_width]
+  int table_width;
+  const int32_t *starts, *lens;
+  int S, T;
+  int dtype;                // of rows
+  const void *x_k, *x_v;    // cache_write's rows
+  int64_t k_stride, v_stride;
+};
+hipError_t launch_cache_write(const CacheArgs& c, hipStream_t stream);
+hipError_t launch_cache_read(const CacheArgs& c, void* k, void* v, hipStream_t stream);
+
+// Attention over it (cache_attention.hip).
+struct AttentionArgs {
+  CacheArgs c;
+  const void* q;
+  int64_t q_stride;
+  int Hq;
+  float scale;
+  int window, sinks;        // window 0: none
+  void* y;                  // [T, Hq, D] of type c.dtype
+  float* lse;               // [T, Hq], or nullptr
+  float* scratch;
+};
+size_t cache_attention_scratch_bytes(int T, int S, int Hq, int H, int D);
+hipError_t launch_cache_attention(const AttentionArgs& a, hipStream_t stream, bool* partial);
+
 }  // namespace sherry

@@ -370,6 +370,132 @@ sherry_status sherry_layernorm_backward(const void* dy, const void* x, const flo
                                         void* stream);
 size_t sherry_layernorm_backward_scratch_bytes(int64_t M, int64_t K);
 
+/* --- Attention operators ----------------------------------------------------
+ * What lies between a layer's stacked q/k/v product and its output product:
+ * the norm and rotation of each head, a paged cache of keys and values in 8
+ * bits, and attention over it.  dim is a head's features: a multiple of 16
+ * from 16 to 256.  At most 1024 query heads and 512 key heads, 2^20 rows T.
+ * Rows are T rows of heads * dim values of type dtype (SHERRY_F32 ...), a
+ * `stride` of values apart (a multiple of 8, so that slices of a stacked row
+ * serve), 16-byte aligned. */
+
+/* Norm of each query and key head and the rotation by its token's position:
+ *   r = 1 / sqrt(sum x^2 / dim + eps),  y = x * r * weight (norm != 0) or x,
+ *   z = y with the pairs (a, b) among its first rotary_dim features turned:
+ *       (a cos t - b sin t, b cos t + a sin t),  t = positions[row] * freqs[i];
+ *   pair i is features i and i + rotary_dim / 2, or 2 i and 2 i + 1 with
+ *   `interleaved`.
+ *   x        [T, x_stride]: q_heads heads of queries, then k_heads of keys
+ *            (what follows them in a row, the values, is not looked at).
+ *   q_weight, k_weight  [dim] fp32, 16-byte aligned, or NULL (ones); NULL
+ *            without the norm.
+ *   eps      finite and positive (not looked at without the norm).
+ *   freqs    [rotary_dim / 2] in 64 bits, radians a position (NULL where
+ *            rotary_dim is 0); rotary_dim a multiple of 8, at most dim.
+ *            Angles are taken in 64 bits.
+ *   positions [T] int32.
+ *   q [T, q_heads, dim], k [T, k_heads, dim]  (written), 16-byte aligned; they
+ *            overlap no input. */
+sherry_status sherry_qk_norm_rope(const void* x, int64_t x_stride, const float* q_weight,
+                                  const float* k_weight, float eps, int norm, const double* freqs,
+                                  int64_t rotary_dim, int interleaved, const int32_t* positions,
+                                  void* q, void* k, int dtype, int64_t T, int64_t q_heads,
+                                  int64_t k_heads, int64_t dim, void* stream);
+
+/* Its gradients, from those of q and k and the same x:
+ *   dy = dz turned back,  dweight = sum over tokens and heads of dy * x * r,
+ *   dx = r * (g - x * r * mean(g * x * r)),  g = dy * weight.
+ *   dq [T, q_heads, dim], dk [T, k_heads, dim].
+ *   dx       the first (q_heads + k_heads) * dim values of rows dx_stride
+ *            apart (written; what follows them is left as it was); may be x
+ *            with the same stride, overlaps no input otherwise.
+ *   dq_weight, dk_weight  [dim] fp32 (written), each may be NULL; NULL without
+ *            the norm (x and scratch may be NULL then too).
+ *   scratch  at least the queried bytes, any content, 256-byte aligned.
+ * The sums run in a fixed order: equal calls give equal bits. */
+sherry_status sherry_qk_norm_rope_backward(const void* dq, const void* dk, const void* x,
+                                           int64_t x_stride, const float* q_weight,
+                                           const float* k_weight, float eps, int norm,
+                                           const double* freqs, int64_t rotary_dim, int interleaved,
+                                           const int32_t* positions, void* dx, int64_t dx_stride,
+                                           float* dq_weight, float* dk_weight, int dtype, int64_t T,
+                                           int64_t q_heads, int64_t k_heads, int64_t dim,
+                                           void* scratch, size_t scratch_bytes, void* stream);
+size_t sherry_qk_norm_rope_backward_scratch_bytes(int64_t T, int64_t q_heads, int64_t k_heads,
+                                                  int64_t dim);
+
+/* The cache: pages of page_size tokens (a power of two from 16 to 1024) of
+ * every head, in blocks of 16 tokens of one head with one scale each:
+ *   k  int8 [pages, heads, page_size / 16, dim / 16, 16 tokens, 16 features],
+ *   v  int8 [pages, heads, page_size / 16, dim / 16, 16 features, 16 tokens],
+ *   k_scale, v_scale  fp32 [pages, heads, page_size / 16]; value = int8 * scale.
+ * k and v 16-byte aligned device pointers; the struct itself is host memory. */
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int64_t pages, page_size, heads, dim;
+} sherry_kv_cache;
+
+/* The calls below take S sequences at once:
+ *   table    [S, table_width] int32: position t of sequence i lies in page
+ *            table[i][t / page_size] (table_width * page_size <= 2^30).
+ *   starts   [S + 1] int32, ascending from 0 to at most T: rows starts[i] ..
+ *            starts[i + 1] - 1 of the call are sequence i's (rows behind the
+ *            last sequence's are neither read nor written).
+ *   lens     [S] int32: tokens sequence i has; the call's rows are its last.
+ * They are device memory and checked there: a position without a page (slot
+ * past the table, page number out of range) is not written, reads as NaN, and
+ * makes the queries that see it, or all of a sequence longer than its table,
+ * NaN.  Entries past a sequence's last page are not looked at. */
+
+/* Writes new tokens' keys and values: rows of k and v (heads * dim values) go
+ * to the positions lens[i] - n .. lens[i] - 1.  A block's scale is the least
+ * power of two 2^e, e >= -126, with max|x| <= 127 * 2^e over its tokens so far,
+ * and q = rint(x / 2^e), half to even.  Where a block has earlier tokens (the
+ * position of the first new one is no multiple of 16) its scale can only grow,
+ * and the earlier values are rounded again, rint(q * old / new).  A value that
+ * is not finite makes its block's scale NaN, and so the block's values.
+ * A block is written by one sequence of a call only, and a block's first
+ * position first; earlier positions may be written again (drafts that were
+ * refused), later ones are then forgotten. */
+sherry_status sherry_cache_write(const sherry_kv_cache* cache, const void* k, int64_t k_stride,
+                                 const void* v, int64_t v_stride, int dtype, const int32_t* table,
+                                 int64_t table_width, const int32_t* starts, const int32_t* lens,
+                                 int64_t S, int64_t T, void* stream);
+
+/* Reads the last starts[i + 1] - starts[i] tokens of each sequence back:
+ *   k, v  [T, heads, dim] of type dtype (written), 16-byte aligned. */
+sherry_status sherry_cache_read(const sherry_kv_cache* cache, void* k, void* v, int dtype,
+                                const int32_t* table, int64_t table_width, const int32_t* starts,
+                                const int32_t* lens, int64_t S, int64_t T, void* stream);
+
+/* Causal attention of each sequence's newest tokens (which the cache holds
+ * already) over the cache: query row j of n in sequence i is at position
+ * p = lens[i] - n + j and sees positions t <= p, and with a window (> 0) only
+ * those with p - t < window or t < sinks;
+ *   s_t = scale * q . k_t,  y = sum e^(s_t - lse) v_t,  lse = log sum e^(s_t).
+ * Query head h reads key head h / (q_heads / heads).  A query that sees nothing
+ * gives y = 0 and lse = -infinity.
+ *   q        rows of q_heads * dim values;  q_heads a multiple of heads.
+ *   window   0: none.        sinks: looked at with a window only.
+ *   y        [T, q_heads, dim] of type dtype (written), 16-byte aligned.
+ *   lse      [T, q_heads] fp32 (written), or NULL.
+ *   scratch  at least the queried bytes, any content, 256-byte aligned.
+ * Products run in fp16 with fp32 sums: 16-bit queries are exact (bf16 down to
+ * 2^-38 of the row's largest) and the weights e^(s - m) are rounded to 11 bits,
+ * fp32 queries and their weights to 22; weights times scales below 2^-31 of the
+ * largest are lost.  The sums run in a fixed order: equal calls give equal bits. */
+sherry_status sherry_cache_attention(const void* q, int64_t q_stride, int64_t q_heads,
+                                     const sherry_kv_cache* cache, const int32_t* table,
+                                     int64_t table_width, const int32_t* starts,
+                                     const int32_t* lens, int64_t S, int64_t T, float scale,
+                                     int64_t window, int64_t sinks, void* y, float* lse, int dtype,
+                                     void* scratch, size_t scratch_bytes, void* stream);
+size_t sherry_cache_attention_scratch_bytes(int64_t T, int64_t S, int64_t q_heads, int64_t heads,
+                                            int64_t dim);
+
 /* Launch plan sherry_gemm uses for a shape (host-only, pure; for
  * diagnostics and benchmarks).  Any output pointer may be NULL.
  *   path: 0 = lookup-table GEMV (per-segment tables in LDS, §2.2; M <= 16),
