@@ -17,45 +17,27 @@
 // largest one so far (a power of two too) times 2^7.  One fp16 term of each
 // for 16-bit queries (q is exact, the weights off by 2^-12), a high and a low
 // one for fp32 queries (2^-23).
-#include "sherry_cache.h"
+#include "sherry_attention.h"
 
 namespace sherry {
 namespace {
 
-typedef _Float16 h8 __attribute__((ext_vector_type(8)));
-typedef _Float16 h2 __attribute__((ext_vector_type(2)));
-
-constexpr int kStep = 64;                // tokens
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kRows = 16;                // queries of a unit
 constexpr int kBlocks = 2 * kCUs;        // workgroups
 constexpr int kLeast = 2 * kWaves;       // steps that a workgroup takes at least
-constexpr float kWeight = 128.0f;        // of e^(s - m) as an operand: with the slack of the maximum below 2^15
-constexpr float kSlack = 8.0f;           // a maximum is kept until it is passed by this (of base 2)
-
-// What a sequence's queries see: the steps of its first tokens, then those from
-// the window's on.
-struct Steps {
-  int head, from, to;
-  __device__ __forceinline__ int count() const { return head + to - from; }
-  __device__ __forceinline__ int at(int s) const { return s < head ? s : from + s - head; }
-};
-
-__device__ __forceinline__ Steps steps_of(const AttentionArgs& a, const Rows& r) {
-  const int room = min(r.len, a.c.table_width << (a.c.block_shift + 4));     // (what has no page gives NaN, once)
-  Steps s{0, 0, max((room + kStep - 1) / kStep, 1)};
-  if (a.window > 0) {
-    s.from = min(max(r.len - r.n - a.window + 1, 0) / kStep, s.to - 1);
-    s.head = min((a.sinks + kStep - 1) / kStep, s.from);
-  }
-  return s;
-}
+constexpr float kWeight = 128.0f;        // 2^kWeightExponent
 
 // Units of a sequence: each head's tiles of 16 rows; a row is a token and one of
 // the query heads that share the head.
 __device__ __forceinline__ int tiles_of(const AttentionArgs& a, const Rows& r) {
   return (r.n * (a.Hq / a.c.H) + kRows - 1) / kRows;
+}
+
+// All of a sequence's units look at the same steps.
+__device__ __forceinline__ Steps steps_of(const AttentionArgs& a, const Rows& r) {
+  return Steps(a, r.len - r.n, r.len - 1);
 }
 
 __device__ __forceinline__ int64_t cost_of(const AttentionArgs& a, int i) {
@@ -81,48 +63,6 @@ struct Deal {
   }
 };
 
-__device__ __forceinline__ int64_t shfl_up64(int64_t v, int d) {
-  const int lo = __shfl_up((int)(uint32_t)v, d), hi = __shfl_up((int)(v >> 32), d);
-  return ((int64_t)hi << 32) | (uint32_t)lo;
-}
-
-// Sum over the workgroup of v, with the sum over the threads before this one.
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t& before, int64_t* parts) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int64_t sum = v;
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const int64_t u = shfl_up64(sum, d);
-    if (lane >= d) sum += u;
-  }
-  __syncthreads();
-  if (lane == 63) parts[wave] = sum;
-  __syncthreads();
-  int64_t total = 0;
-  before = sum - v;
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    if (w < wave) before += parts[w];
-    total += parts[w];
-  }
-  return total;
-}
-
-// Four 8-bit values as fp16: 1024 + (q + 128) is 0x6400 with the byte in its low half.
-__device__ __forceinline__ void halves4(uint32_t w, h2& a, h2& b) {
-  const h2 off = {(_Float16)-1152.0f, (_Float16)-1152.0f};
-  w ^= 0x80808080u;
-  a = __builtin_bit_cast(h2, __builtin_amdgcn_perm(0x64646464u, w, 0x04010400u)) + off;
-  b = __builtin_bit_cast(h2, __builtin_amdgcn_perm(0x64646464u, w, 0x04030402u)) + off;
-}
-
-__device__ __forceinline__ h8 halves8(uint32_t x, uint32_t y) {
-  h2 a, b, c, d;
-  halves4(x, a, b);
-  halves4(y, c, d);
-  return h8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
-}
-
 __device__ __forceinline__ float max_of_groups(float v) {
   v = fmaxf(v, __shfl_xor(v, 16));
   return fmaxf(v, __shfl_xor(v, 32));
@@ -133,8 +73,6 @@ __device__ __forceinline__ float sum_of_groups(float v) {
   return v + __shfl_xor(v, 32);
 }
 
-__device__ __forceinline__ float above(float m) { return m == -__builtin_inff() ? 0.0f : m; }
-
 // kC: D / 64 rounded up.  kTerms: fp16 terms of q and of the weights.
 template <int kC, int kTerms>
 struct Wave {
@@ -143,7 +81,6 @@ struct Wave {
   int lane, i, g;
   int seq, h, pieces;
   Rows r;
-  Steps steps;
   int pos;              // of this lane's query
   int low, high;        // of the tile's queries
   float factor;         // of q's power of two and the scale, for base 2
@@ -181,11 +118,9 @@ struct Wave {
         for (int b = 0; b < 4; ++b) top = fmaxf(top, fabsf(raw[c][j][b]));
       }
     top = max_of_groups(top);
-    const int e = (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127;      // 2^e <= top < 2^(e + 1)
-    const int up = top > 0.0f && top < __builtin_inff() ? min(13 - e, 126) : 0;
-    const float times = __builtin_bit_cast(float, (uint32_t)(max(up, -126) + 127) << 23);
+    const float times = row_scale(top);
     factor = a.scale * kLog2E / times;
-    if (r.len > a.c.table_width << (a.c.block_shift + 4)) factor = __builtin_nanf("");     // tokens without pages
+    if (r.len > room_of(a)) factor = __builtin_nanf("");     // tokens without pages
 #pragma unroll
     for (int c = 0; c < kC; ++c)
 #pragma unroll
@@ -224,7 +159,7 @@ struct Wave {
 #pragma unroll
     for (int t = 0; t < kTiles; ++t)
       if (t < pieces) vw[t] = *reinterpret_cast<const uint4*>(values + 256 * t);
-    if (page < 0) ks = vs = __builtin_nanf("");
+    if (page < 0 || vs != vs) ks = __builtin_nanf("");      // whoever sees it gives NaN
 
     f4 s[4];
 #pragma unroll
@@ -243,7 +178,7 @@ struct Wave {
     // (the pieces past D that the keys' loads repeat meet zeros of q)
     const float f = factor * ks;
     const int t0 = kStep * ts;
-    const bool all = t0 + kStep - 1 <= low && (a.window == 0 || high - t0 < a.window || t0 + kStep <= a.sinks);
+    const bool all = sees_all(a, t0, low, high);
     float top = -__builtin_inff();
 #pragma unroll
     for (int n = 0; n < 4; ++n)
@@ -252,8 +187,7 @@ struct Wave {
         s[n][b] *= f;
         if (!all) {
           const int j = t0 + 16 * g + 4 * n + b;
-          const bool seen = j <= pos && (a.window == 0 || pos - j < a.window || j < a.sinks);
-          s[n][b] = seen ? s[n][b] : -__builtin_inff();
+          s[n][b] = sees(a, j, pos) ? s[n][b] : -__builtin_inff();
         }
         top = fmaxf(top, s[n][b]);
       }
@@ -286,12 +220,12 @@ struct Wave {
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
       if (t < pieces) {
-      const h8 v0 = halves8(vw[t].x, vw[t].y), v1 = halves8(vw[t].z, vw[t].w);
+        const h8 v0 = halves8(vw[t].x, vw[t].y), v1 = halves8(vw[t].z, vw[t].w);
 #pragma unroll
-      for (int u = 0; u < kTerms; ++u) {
-        o[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, p[u][0], o[t], 0, 0, 0);
-        o[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, p[u][1], o[t], 0, 0, 0);
-      }
+        for (int u = 0; u < kTerms; ++u) {
+          o[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, p[u][0], o[t], 0, 0, 0);
+          o[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, p[u][1], o[t], 0, 0, 0);
+        }
       }
     }
   }
@@ -313,7 +247,7 @@ __global__ __launch_bounds__(kThreads) void attention_kernel(AttentionArgs a) {
   int64_t total = 0, before;
   for (int base = 0; base < a.c.S; base += kThreads) {
     const int i = base + threadIdx.x;
-    total += block_scan(i < a.c.S ? cost_of(a, i) : 0, before, parts);
+    total += block_scan<kWaves>(i < a.c.S ? cost_of(a, i) : 0, before, parts);
   }
   if (total == 0) return;
   const Deal deal(total);
@@ -322,7 +256,7 @@ __global__ __launch_bounds__(kThreads) void attention_kernel(AttentionArgs a) {
   int64_t left = deal.first(block + 1) - begin, past = 0;
   for (int base = 0;; base += kThreads) {       // (begin < total, so a sequence has it)
     const int i = base + threadIdx.x;
-    const int64_t own = i < a.c.S ? cost_of(a, i) : 0, all = block_scan(own, before, parts);
+    const int64_t own = i < a.c.S ? cost_of(a, i) : 0, all = block_scan<kWaves>(own, before, parts);
     before += past;
     if (begin >= before && begin < before + own) {
       found_seq = i;
@@ -340,15 +274,15 @@ __global__ __launch_bounds__(kThreads) void attention_kernel(AttentionArgs a) {
   while (left > 0) {
     w.seq = seq;
     w.r = rows_of(a.c, seq);
-    w.steps = steps_of(a, w.r);
-    const int count = w.steps.count(), tiles = tiles_of(a, w.r), units = w.r.n == 0 ? 0 : a.c.H * tiles;
+    const Steps steps = steps_of(a, w.r);
+    const int count = steps.count(), tiles = tiles_of(a, w.r), units = w.r.n == 0 ? 0 : a.c.H * tiles;
     for (int u = (int)(rest / count); u < units && left > 0; ++u) {
       const int s0 = (int)(rest - (int64_t)u * count), s1 = (int)min((int64_t)count, s0 + left);
       const int tile = u % tiles;
       w.h = u / tiles;
       w.load_queries(tile);
       w.reset();
-      for (int s = s0 + wave; s < s1; s += kWaves) w.step(w.steps.at(s));
+      for (int s = s0 + wave; s < s1; s += kWaves) w.step(steps.at(s));
       // the waves' parts
       const float sum = sum_of_groups(w.l);
       __syncthreads();
@@ -382,7 +316,7 @@ __global__ __launch_bounds__(kThreads) void attention_kernel(AttentionArgs a) {
           if (token < w.r.n) {
             const size_t at = (size_t)(w.r.row0 + token) * a.Hq + w.h * group + line - token * group;
             store4_as(a.y, at * a.c.D + d, a.c.dtype, y);
-            if (a.lse && d == 0) a.lse[at] = (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f;
+            if (a.lse && d == 0) a.lse[at] = (m + __builtin_amdgcn_logf(l)) * kLn2;
           }
         } else {
           *reinterpret_cast<f4*>(part + (size_t)row * a.c.D + d) = y;
@@ -411,7 +345,7 @@ __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttentionArgs 
   int64_t total = 0, before;
   for (int base = 0; base < a.c.S; base += kThreads) {
     const int i = base + threadIdx.x;
-    const int64_t own = i < a.c.S ? cost_of(a, i) : 0, all = block_scan(own, before, parts);
+    const int64_t own = i < a.c.S ? cost_of(a, i) : 0, all = block_scan<kWaves>(own, before, parts);
     if (own > 0) {
       const Rows r = rows_of(a.c, i);
       if (t >= r.row0 && t < r.row0 + r.n) {
@@ -448,7 +382,7 @@ __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttentionArgs 
     y = l == 0.0f ? f4{} : y / l;
     const size_t at = (size_t)t * a.Hq + h * group + head;
     store4_as(a.y, at * a.c.D + d, a.c.dtype, y);
-    if (a.lse && d == 0) a.lse[at] = (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f;
+    if (a.lse && d == 0) a.lse[at] = (m + __builtin_amdgcn_logf(l)) * kLn2;
   }
 }
 
@@ -464,12 +398,16 @@ void launch_terms(const AttentionArgs& a, hipStream_t stream) {
 
 }  // namespace
 
+// Many rows a sequence: the kernel that shares a step's keys and values between 128 rows.
+static bool tiles_pay(int T, int S, int Hq, int H) { return (int64_t)T * (Hq / H) >= 64 * (int64_t)S; }
+
 size_t cache_attention_scratch_bytes(int T, int S, int Hq, int H, int D) {
-  (void)T, (void)S, (void)Hq, (void)H;
+  if (tiles_pay(T, S, Hq, H)) return attention_tiles_scratch_bytes(S, D);
   return (size_t)2 * kBlocks * part_floats(D) * sizeof(float);
 }
 
 hipError_t launch_cache_attention(const AttentionArgs& a, hipStream_t stream, bool* partial) {
+  if (tiles_pay(a.c.T, a.c.S, a.Hq, a.c.H)) return launch_attention_tiles(a, stream, partial);
   if (a.c.dtype == SHERRY_F32) launch_terms<2>(a, stream);
   else launch_terms<1>(a, stream);
   const hipError_t e = hipGetLastError();

@@ -243,6 +243,8 @@ struct AttentionArgs {
   float* scratch;
 };
 size_t cache_attention_scratch_bytes(int T, int S, int Hq, int H, int D);
+size_t attention_tiles_scratch_bytes(int S, int D);      // cache_attention_tiles.hip: many queries a sequence
+hipError_t launch_attention_tiles(const AttentionArgs& a, hipStream_t stream, bool* partial);
 hipError_t launch_cache_attention(const AttentionArgs& a, hipStream_t stream, bool* partial);
 
 }  // namespace sherry

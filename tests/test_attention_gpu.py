@@ -359,3 +359,18 @@ def test_attention(lens, new, page, Hq, H, D, window, sinks, t):
         check("lse", lse[at:at + m], *want_lse)
         at += m
     assert torch.equal(y, bw.cache_attention(on, cache, table, starts, tl, window=window, sinks=sinks))      # equal bits
+
+
+PROMPTS = [
+    # lens, new, page, Hq, H, D, window, sinks: many queries a sequence
+    ([64], [64], 16, 1, 1, 64, None, 0), ([200], [200], 16, 4, 1, 128, None, 0), ([700, 65, 300], [300, 65, 100], 32, 4, 2, 128, None, 0),
+    ([500], [140], 64, 3, 3, 80, None, 0), ([330, 0, 90], [130, 0, 90], 16, 7, 1, 48, None, 0), ([257], [257], 128, 2, 1, 256, None, 0),
+    ([400, 128], [129, 128], 16, 6, 2, 192, None, 0), ([600], [400], 16, 2, 1, 64, 70, 5), ([1000], [100], 32, 8, 4, 96, 200, 90),
+    ([300], [300], 16, 2, 2, 32, 1, 0), ([150, 1, 500], [150, 1, 200], 16, 16, 1, 112, None, 0), ([90] * 5, [80] * 5, 16, 4, 4, 16, 33, 3),
+]
+
+
+@pytest.mark.parametrize("t", list(ref.TYPES))
+@pytest.mark.parametrize("lens,new,page,Hq,H,D,window,sinks", PROMPTS)
+def test_attention_of_prompts(lens, new, page, Hq, H, D, window, sinks, t):
+    test_attention(lens, new, page, Hq, H, D, window, sinks, t)
