@@ -135,9 +135,10 @@ __global__ __launch_bounds__(kPlanThreads) void attention_plan_kernel(AttentionA
 // kC: D / 64 rounded up.
 template <int kC>
 struct Layout {
-  static constexpr int kChunks = 8 * kC;                  // of 8 features, in a key's row
-  static constexpr int kKeys = kStep * 64 * kC * 2;       // bytes of 64 tokens' keys as fp16 (and of values)
-  static constexpr int kBuffer = 2 * kKeys;
+  // of 8 features, in a key's row: a power of two, so that chunks differ in an exclusive or
+  static constexpr int kChunks = kC == 3 ? 32 : 8 * kC;
+  static constexpr int kKeys = kStep * kChunks * 16;      // bytes of 64 tokens' keys as fp16
+  static constexpr int kBuffer = kKeys + kStep * 64 * kC * 2;
   // 16 bytes `chunk` of key row `row`: sixteen rows of the same chunk lie in different banks
   static __device__ __forceinline__ int key(int row, int chunk) {
     return 16 * (row * kChunks + (kChunks % 16 == 0 ? chunk ^ (row & 15) : chunk ^ ((row >> 1) & 7)));
@@ -159,22 +160,136 @@ __global__ __launch_bounds__(kThreads, kC <= 2 ? 2 : 1) void attention_tiles_ker
   const int block = (blockIdx.x & 7) * (blocks / 8) + (blockIdx.x >> 3);
   const Plan plan = *scratch.plan;
   if (block >= plan.used) return;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, i = lane & 31, f = lane >> 5;
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), i = lane & 31, f = lane >> 5;
   const int D = a.c.D, pieces = D / 16, group = a.Hq / a.c.H;
   const float sign = a.scale < 0.0f ? -1.0f : 1.0f;
-  int64_t left = plan.first(block + 1) - plan.first(block);
-  Start at = scratch.starts[block];
-  Rows r = rows_of(a.c, at.seq);
+  // (features past D stay zeros, and the first product with the values meets no stray NaN)
+  for (int x = 16 * tid; x < 2 * L::kBuffer; x += 16 * kThreads) *reinterpret_cast<uint4*>(lds + x) = uint4{};
+
+  // Each wave brings one block of a step: its 16-byte units `lane + 64 n` (the last
+  // one several times where there are fewer than lanes), and where they go as fp16.
+  int unit_at[kLoads], key_at[kLoads], value_at[kLoads];
+#pragma unroll
+  for (int n = 0; n < kLoads; ++n) {
+    const int y = min(lane + 64 * n, D - 1), t = y & 15;
+    unit_at[n] = 16 * y;
+    // token 8 f + 4 s + r of the block is row 8 s + 4 f + r
+    key_at[n] = L::key(16 * wave + ((t & 3) | ((t & 4) << 1) | ((t & 8) >> 1)), 2 * (y >> 4));
+    value_at[n] = L::value(y, 2 * wave);
+  }
+  int64_t left = uniform64(plan.first(block + 1) - plan.first(block));
+  const Start start = scratch.starts[block];
+  int seq = uniform(start.seq), h = uniform(start.head), tile_number = uniform(start.tile), s0 = uniform(start.step);
+  Rows r = uniform(rows_of(a.c, seq));
   int tiles = tiles_of(a, r);
   bool first_part = true;
 
   while (left > 0) {
-    const Tile tile(a, r, at.tile);
+    const Tile tile(a, r, tile_number);
     const Steps steps = tile.steps(a);
-    const int count = steps.count(), s0 = at.step, s1 = (int)min((int64_t)count, s0 + left), h = at.head;
+    const int count = steps.count(), s1 = (int)min((int64_t)count, s0 + left);
+
+    // A step's page, then its scales and bytes, then those as fp16 in a buffer: each is
+    // asked for a step before the next needs it.  Steps past the last are the last one
+    // again, so that nothing here branches.
+    const int32_t* table = a.c.table + (size_t)seq * a.c.table_width;
+    const uint32_t page_blocks = (uint32_t)a.c.H << a.c.block_shift, h_blocks = (uint32_t)h << a.c.block_shift;
+    const int in_page = (1 << a.c.block_shift) - 1, window_shift = steps.from - steps.head;
+    int page_next, page_after;       // of the blocks to be asked for next
+    uint32_t block_now, block_next;  // blocks (fewer than 2^31 in a cache) whose values, and keys, are asked for next
+    bool good;
+    uint4 kw[kLoads], vw[kLoads];
+    float ks, vs;
+    auto step_at = [&](int s) {
+      s = min(s, s1 - 1);
+      return s < steps.head ? s : s + window_shift;
+    };
+    auto page_of_step = [&](int s) { return table[min((4 * step_at(s) + wave) >> a.c.block_shift, a.c.table_width - 1)]; };
+    auto find_block = [&](int s) {
+      const int sb = 4 * step_at(s) + wave;
+      const uint32_t p = uniform(page_next);
+      good = p < (uint32_t)a.c.pages && sb >> a.c.block_shift < a.c.table_width;
+      block_next = (good ? p : 0) * page_blocks + h_blocks + (sb & in_page);
+    };
+    auto load_keys = [&]() {
+      const uint8_t* from = a.c.k + (uint64_t)block_next * (uint32_t)(16 * D);
+#pragma unroll
+      for (int n = 0; n < kLoads; ++n) kw[n] = *reinterpret_cast<const uint4*>(from + (uint32_t)unit_at[n]);
+      ks = a.c.k_scale[block_next];
+      vs = a.c.v_scale[block_next];
+      if (!good) ks = __builtin_nanf("");
+    };
+    auto load_values = [&]() {
+      const uint8_t* from = a.c.v + (uint64_t)block_now * (uint32_t)(16 * D);
+#pragma unroll
+      for (int n = 0; n < kLoads; ++n) vw[n] = *reinterpret_cast<const uint4*>(from + (uint32_t)unit_at[n]);
+    };
+    // a block that is not valid has a key scale of NaN, one that is not or that nobody
+    // sees a value scale of 0
+    auto store_scales = [&](int s, int buffer) {
+      const bool seen = kStep * step_at(s) + 16 * wave <= tile.high;
+      const float k = vs == vs ? ks : vs, v = seen && vs < __builtin_inff() ? vs : 0.0f;
+      if (lane < 2) scales[buffer][4 * lane + wave] = lane ? v : k;
+    };
+    // 8 of a thread's keys, or of its values: those as multiples of the largest value
+    // scale so far, `unit`
+    auto store_keys = [&](int buffer, int n, int half) {
+      *reinterpret_cast<h8*>(lds + buffer + (key_at[n] ^ (16 * half))) =
+          half ? halves8(kw[n].z, kw[n].w) : halves8(kw[n].x, kw[n].y);
+    };
+    auto store_values = [&](int buffer, int n, int half, _Float16 ratio) {
+      *reinterpret_cast<h8*>(lds + buffer + (value_at[n] ^ (16 * half))) =
+          half ? halves8(vw[n].z, vw[n].w, ratio) : halves8(vw[n].x, vw[n].y, ratio);
+    };
+
+    float m = -__builtin_inff(), l = 0.0f, unit = 0x1p-126f;
+    f16v o[kTiles];
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) o[t] = f16v{};
+    h8 p[kTerms][4];             // the last step's weights
+#pragma unroll
+    for (int n = 0; n < kTerms; ++n)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) p[n][u] = h8{};
+    // The products in slots: their operands from LDS are read kAhead slots before, and
+    // each slot brings a share of other work for the vector units (`beside`).
+    constexpr int kSlots = 8 * kC, kAhead = 4;
+    auto in_slots = [&](auto read, auto product, auto beside) {
+      h8 operand[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) operand[j] = read(j);
+#pragma unroll
+      for (int j = 0; j < kSlots; ++j) {
+        product(j, operand[j % kAhead]);
+        if (j + kAhead < kSlots) operand[j % kAhead] = read(j + kAhead);
+        beside(j);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    // LDS addresses: a row's chunks differ in one exclusive or, rows and buffers in the offset
+    const int key_row = L::key(i, f), value_row = L::value(i, f);
+    auto add_values = [&](int buffer, auto beside) {
+      const int base = value_row + buffer;
+      in_slots([&](int j) { return *reinterpret_cast<const h8*>(lds + (base ^ (32 * (j / kTiles))) + 4096 * (j % kTiles)); },
+               [&](int j, h8 v) {
+#pragma unroll
+                 for (int n = 0; n < kTerms; ++n)
+                   o[j % kTiles] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, p[n][j / kTiles], o[j % kTiles], 0, 0, 0);
+               },
+               beside);
+    };
+
+    page_next = page_of_step(s0);
+    page_after = page_of_step(s0 + 1);
+    find_block(s0);
+    load_keys();
+    block_now = block_next;
+    load_values();
+    page_next = page_after;
+    page_after = page_of_step(s0 + 2);
 
     // queries: features 16 c + 8 f .. of row i
-    const int row = kRows * at.tile + kWaveRows * wave + i, token = row / group;
+    const int row = kRows * tile_number + kWaveRows * wave + i, token = row / group;
     const bool in = token < r.n;
     const int pos = in ? r.len - r.n + token : -1;
     h8 q[kTerms][4 * kC];
@@ -208,133 +323,116 @@ __global__ __launch_bounds__(kThreads, kC <= 2 ? 2 : 1) void attention_tiles_ker
         }
     }
 
-    // bytes of a step: unit x of block u is 16 features of a token, or 16 tokens of a feature
-    uint4 kw[kLoads], vw[kLoads];
-    float ks[kLoads], vs[kLoads];
-    auto load = [&](int s) {
-      const int ts = steps.at(s);
+    lds_barrier();               // (the zeros, or what the last unit reads)
+    store_scales(s0, 0);
 #pragma unroll
-      for (int n = 0; n < kLoads; ++n) {
-        const int x = tid + kThreads * n, u = x / D, y = x - u * D;
-        if (u >= 4) continue;
-        const int page = page_of(a.c, at.seq, 4 * ts + u);
-        const size_t b = block_of(a.c, max(page, 0), h, 4 * ts + u);
-        kw[n] = *reinterpret_cast<const uint4*>(a.c.k + b * (16 * D) + 16 * y);
-        vw[n] = *reinterpret_cast<const uint4*>(a.c.v + b * (16 * D) + 16 * y);
-        ks[n] = page < 0 ? __builtin_nanf("") : a.c.k_scale[b];
-        vs[n] = a.c.v_scale[b];
-      }
-    };
-    auto convert = [&](int s) {
-      char* to = lds + (s & 1) * L::kBuffer;
-#pragma unroll
-      for (int n = 0; n < kLoads; ++n) {
-        const int x = tid + kThreads * n, u = x / D, y = x - u * D;
-        if (u >= 4) continue;
-        const int piece = y >> 4, t = y & 15;
-        // token 8 f + 4 s + r of the block is row 8 s + 4 f + r
-        const int key = 16 * u + ((t & 3) | ((t & 4) << 1) | ((t & 8) >> 1));
-        *reinterpret_cast<h8*>(to + L::key(key, 2 * piece)) = halves8(kw[n].x, kw[n].y);
-        *reinterpret_cast<h8*>(to + L::key(key, 2 * piece + 1)) = halves8(kw[n].z, kw[n].w);
-        *reinterpret_cast<h8*>(to + L::value(y, 2 * u)) = halves8(vw[n].x, vw[n].y);
-        *reinterpret_cast<h8*>(to + L::value(y, 2 * u + 1)) = halves8(vw[n].z, vw[n].w);
-        if (y == 0) {
-          scales[s & 1][u] = vs[n] == vs[n] ? ks[n] : __builtin_nanf("");
-          scales[s & 1][4 + u] = vs[n];
-        }
-      }
-    };
-
-    float m = -__builtin_inff(), l = 0.0f, unit = 0x1p-126f;
-    f16v o[kTiles];
-#pragma unroll
-    for (int t = 0; t < kTiles; ++t) o[t] = f16v{};
-
-    load(s0);
-    convert(s0);
-    if (s0 + 1 < s1) load(s0 + 1);
+    for (int n = 0; n < 2 * kLoads; ++n) store_keys(0, n / 2, n % 2);
+    find_block(s0 + 1);
+    load_keys();
+    block_now = block_next;
+    page_next = page_after;
+    page_after = page_of_step(s0 + 3);
     lds_barrier();
-    for (int s = s0; s < s1; ++s) {
-      if (s + 1 < s1) convert(s + 1);
-      if (s + 2 < s1) load(s + 2);
-      const char* from = lds + (s & 1) * L::kBuffer;
-      const int t0 = kStep * steps.at(s);
-      f16v sc[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        sc[e] = f16v{};
-#pragma unroll
-        for (int c = 0; c < 4 * kC; ++c)
-          if (c < pieces) {
-            const h8 k = *reinterpret_cast<const h8*>(from + L::key(32 * e + i, 2 * c + f));
-#pragma unroll
-            for (int n = 0; n < kTerms; ++n) sc[e] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[n][c], sc[e], 0, 0, 0);
-          }
-      }
-      const bool all = sees_all(a, t0, tile.low, tile.high);
-      if (!all) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-          for (int b = 0; b < 16; ++b)
-            if (!sees(a, t0 + 32 * e + 16 * (b / 8) + 8 * f + b % 8, pos)) sc[e][b] = -__builtin_inff();
-      }
-      // blocks: factor of the scores, largest score, value scale
-      float by[4], vscale[4], top = -__builtin_inff(), unit_now = unit;
+    // In step s: its scores, while the next keys and its values are turned to fp16; then
+    // its weights, while the last step's meet their values.
+    for (int s = s0, buffer = 0; s < s1; ++s, buffer ^= 1) {
+      const int here = buffer * L::kBuffer, there = L::kBuffer - here;
+      const int t0 = kStep * step_at(s);
+      float by[4], unit_now = unit;       // the factor of a block's scores
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        by[u] = factor * scales[s & 1][u];
-        vscale[u] = scales[s & 1][4 + u];
-        float best = sc[u / 2][8 * (u % 2)];
-#pragma unroll
-        for (int b = 1; b < 8; ++b) best = fmaxf(best, sc[u / 2][8 * (u % 2) + b]);
-        top = fmaxf(top, best == -__builtin_inff() ? best : best * by[u]);
-        if (t0 + 16 * u <= tile.high && vscale[u] < __builtin_inff()) unit_now = fmaxf(unit_now, vscale[u]);
+        by[u] = factor * scales[buffer][u];
+        unit_now = fmaxf(unit_now, scales[buffer][4 + u]);
       }
-      top = fmaxf(top, __shfl_xor(top, 32));
-      if (__any(top > m + kSlack) || unit_now > unit) {
-        const float now = fmaxf(m, top);
+      const _Float16 ratio = (_Float16)(scales[buffer][4 + wave] * __builtin_amdgcn_rcpf(unit_now));
+      f16v sc[2] = {f16v{}, f16v{}};
+      store_scales(s + 1, buffer ^ 1);
+      const int base = key_row + here;
+      in_slots([&](int j) { return *reinterpret_cast<const h8*>(lds + (base ^ (32 * (j / 2))) + 32 * 16 * L::kChunks * (j % 2)); },
+               [&](int j, h8 k) {
+#pragma unroll
+                 for (int n = 0; n < kTerms; ++n)
+                   sc[j % 2] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[n][j / 2], sc[j % 2], 0, 0, 0);
+               },
+               [&](int j) {
+                 if (j % 2) return;
+                 const int n = j / 8, part = j / 2 % 4;
+                 if (part < 2) store_keys(there, n, part);
+                 else store_values(here, n, part - 2, ratio);
+               });
+      load_values();
+      find_block(s + 2);
+      load_keys();
+      block_now = block_next;
+      page_next = page_after;
+      page_after = page_of_step(s + 4);
+      if (!sees_all(a, t0, tile.low, tile.high)) {
+        asm volatile("");       // (a branch, not 32 selections in every step)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          // seen tokens of a block that is not valid give NaN, hidden ones nothing: no
+          // factor of NaN, or of 0, may meet their -infinity
+          const bool bad = by[u] != by[u];
+          const int ahead = pos - (t0 + 16 * u + 8 * f);       // of the first of these tokens
+#pragma unroll
+          for (int b = 0; b < 8; ++b) {
+            const float x = sc[u / 2][8 * (u % 2) + b];
+            sc[u / 2][8 * (u % 2) + b] = ahead < b ? -__builtin_inff() : bad ? by[u] : x;
+          }
+          if (a.window > 0) {
+#pragma unroll
+            for (int b = 0; b < 8; ++b)
+              if (ahead - b >= a.window && t0 + 16 * u + 8 * f + b >= a.sinks) sc[u / 2][8 * (u % 2) + b] = -__builtin_inff();
+          }
+          by[u] = bad ? 1.0f : fmaxf(by[u], 0x1p-120f);
+        }
+      }
+      // weights under the maximum so far; where that is too low for them, or a query has
+      // seen nothing yet, again under a new one
+      float sum = 0.0f;
+      h8 next[kTerms][4];
+      auto weight = [&](int x, float base) {
+        const float e = __builtin_amdgcn_exp2f(fmaf(sc[x / 16][x % 16], by[x / 8], -base));
+        sum += e;
+        const _Float16 hi = (_Float16)e;
+        next[0][x / 8][x % 8] = hi;
+        if constexpr (kTerms == 2) next[kTerms - 1][x / 8][x % 8] = (_Float16)(e - (float)hi);
+      };
+      const float floor = above(m) - kWeightExponent;
+      add_values(there, [&](int j) {
+#pragma unroll
+        for (int x = j * 32 / kSlots; x < (j + 1) * 32 / kSlots; ++x) weight(x, floor);
+      });
+      // (no weight is larger than their sum; one of at most 2^15 stays in fp16's range)
+      if (__any(sum > 0x1p15f || (pos >= 0 && m == -__builtin_inff())) || unit_now > unit) {
+        float top = -__builtin_inff();
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          float best = sc[u / 2][8 * (u % 2)];
+#pragma unroll
+          for (int b = 1; b < 8; ++b) best = fmaxf(best, sc[u / 2][8 * (u % 2) + b]);
+          top = fmaxf(top, best * by[u]);
+        }
+        const float now = fmaxf(m, fmaxf(top, __shfl_xor(top, 32)));
         const float keep = __builtin_amdgcn_exp2f(m - above(now)), scaled = keep * unit * __builtin_amdgcn_rcpf(unit_now);
         l *= keep;
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) o[t] *= scaled;
         m = now;
         unit = unit_now;
+        sum = 0.0f;
+        const float again = above(m) - kWeightExponent;
+#pragma unroll
+        for (int x = 0; x < 32; ++x) weight(x, again);
       }
-      const float base = above(m) - kWeightExponent, inverse = __builtin_amdgcn_rcpf(unit);
-      h8 p[kTerms][4];
+      l += sum;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        // the weights times the value scale over `unit`; below 2^-40 of it they count in the sum alone
-        const float ratio = vscale[u] * inverse;
-        const bool counts = ratio >= 0x1p-40f;
-        const float from_base = counts ? base - __builtin_amdgcn_logf(ratio) : base;
-        float sum = 0.0f;
+      for (int n = 0; n < kTerms; ++n)
 #pragma unroll
-        for (int b = 0; b < 8; ++b) {
-          const float raw = sc[u / 2][8 * (u % 2) + b];
-          float e = __builtin_amdgcn_exp2f(fmaf(raw, by[u], -from_base));
-          if (!all) e = raw == -__builtin_inff() ? 0.0f : e;
-          sum += e;
-          const float v = counts ? e : 0.0f;
-          const _Float16 hi = (_Float16)v;
-          p[0][u][b] = hi;
-          if constexpr (kTerms == 2) p[kTerms - 1][u][b] = (_Float16)(v - (float)hi);
-        }
-        l += counts ? sum * __builtin_amdgcn_rcpf(ratio) : sum;
-      }
-#pragma unroll
-      for (int t = 0; t < kTiles; ++t)
-        if (2 * t < pieces) {
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const h8 v = *reinterpret_cast<const h8*>(from + L::value(32 * t + i, 2 * u + f));
-#pragma unroll
-            for (int n = 0; n < kTerms; ++n) o[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, p[n][u], o[t], 0, 0, 0);
-          }
-        }
+        for (int u = 0; u < 4; ++u) p[n][u] = next[n][u];
       lds_barrier();
     }
+    add_values(((s1 - s0 - 1) & 1) * L::kBuffer, [](int) {});
 
     l += __shfl_xor(l, 32);
     const float times = l == 0.0f ? 0.0f : unit / l;
@@ -369,15 +467,15 @@ __global__ __launch_bounds__(kThreads, kC <= 2 ? 2 : 1) void attention_tiles_ker
     }
     left -= s1 - s0;
     first_part = false;
-    at.step = 0;
-    if (++at.tile == tiles) {
-      at.tile = 0;
-      if (++at.head == a.c.H) {
-        at.head = 0;
+    s0 = 0;
+    if (++tile_number == tiles) {
+      tile_number = 0;
+      if (++h == a.c.H) {
+        h = 0;
         do {
-          ++at.seq;
-          if (at.seq >= a.c.S) break;
-          r = rows_of(a.c, at.seq);
+          ++seq;
+          if (seq >= a.c.S) break;
+          r = uniform(rows_of(a.c, seq));
           tiles = tiles_of(a, r);
         } while (tiles == 0);
       }

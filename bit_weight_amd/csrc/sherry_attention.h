@@ -14,6 +14,13 @@ constexpr float kSlack = 8.0f;           // a running maximum is kept until it i
 constexpr float kWeightExponent = 7.0f;  // weights e^(s - m) as operands are 2^7 as large: with the slack below 2^15
 constexpr float kLn2 = 0.69314718055994531f;
 
+// A value that every lane has alike, as one the compiler knows to be.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform64(int64_t v) {
+  return ((int64_t)uniform((int)(v >> 32)) << 32) | (uint32_t)uniform((int)(uint32_t)v);
+}
+__device__ __forceinline__ Rows uniform(Rows r) { return {uniform(r.row0), uniform(r.n), uniform(r.len)}; }
+
 __device__ __forceinline__ int room_of(const AttentionArgs& a) { return a.c.table_width << (a.c.block_shift + 4); }
 
 // Steps that queries at positions low .. high of a sequence look at: those of its
@@ -44,18 +51,19 @@ __device__ __forceinline__ bool sees(const AttentionArgs& a, int t, int p) {
 
 __device__ __forceinline__ float above(float m) { return m == -__builtin_inff() ? 0.0f : m; }
 
-// Four 8-bit values as fp16: 1024 + (q + 128) is 0x6400 with the byte in its low half.
-__device__ __forceinline__ void halves4(uint32_t w, h2& a, h2& b) {
-  const h2 off = {(_Float16)-1152.0f, (_Float16)-1152.0f};
+// Four 8-bit values as fp16 times r, a power of two or 0: 1024 + (q + 128) is 0x6400
+// with the byte in its low half, and one fused product and sum leaves q r.
+__device__ __forceinline__ void halves4(uint32_t w, h2 r, h2 off, h2& a, h2& b) {
   w ^= 0x80808080u;
-  a = __builtin_bit_cast(h2, __builtin_amdgcn_perm(0x64646464u, w, 0x04010400u)) + off;
-  b = __builtin_bit_cast(h2, __builtin_amdgcn_perm(0x64646464u, w, 0x04030402u)) + off;
+  a = __builtin_elementwise_fma(__builtin_bit_cast(h2, __builtin_amdgcn_perm(0x64646464u, w, 0x04010400u)), r, off);
+  b = __builtin_elementwise_fma(__builtin_bit_cast(h2, __builtin_amdgcn_perm(0x64646464u, w, 0x04030402u)), r, off);
 }
 
-__device__ __forceinline__ h8 halves8(uint32_t x, uint32_t y) {
+__device__ __forceinline__ h8 halves8(uint32_t x, uint32_t y, _Float16 r = (_Float16)1.0f) {
   h2 a, b, c, d;
-  halves4(x, a, b);
-  halves4(y, c, d);
+  const h2 times = {r, r}, off = times * h2{(_Float16)-1152.0f, (_Float16)-1152.0f};
+  halves4(x, times, off, a, b);
+  halves4(y, times, off, c, d);
   return h8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
