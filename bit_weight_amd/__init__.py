@@ -107,8 +107,9 @@ def lib() -> ctypes.CDLL:
                 "sherry_cache_write": ([vp, vp, i64, vp, i64, ci, vp, i64, vp, vp, i64, i64, vp], ci),
                 "sherry_cache_read": ([vp, vp, vp, ci, vp, i64, vp, vp, i64, i64, vp], ci),
                 "sherry_cache_attention_scratch_bytes": ([i64, i64, i64, i64, i64], sz),
+                "sherry_cache_attention_workspace_bytes": ([], sz),
                 "sherry_cache_attention": ([vp, i64, i64, vp, vp, i64, vp, vp, i64, i64, cf, i64, i64, vp, vp, ci, vp, sz,
-                                            vp], ci),
+                                            vp, sz, vp], ci),
                 "sherry_probe_read": ([vp, sz, vp, ci, ci, ci, vp], ci),
                 "sherry_probe_empty": ([vp], ci),
                 "sherry_probe_decode": ([ci, vp, ci, ci, vp], ci),
@@ -486,7 +487,7 @@ def _load_native():
             names = [n for n in dir(_binding) if not n.startswith("_") and n != "setup"]
             entries = {f"sherry_{n}": None for n in names}
             entries |= {"sherry_packed_bytes": None, "sherry_gemm_fused_workspace_bytes": None,
-                        "sherry_glu_workspace_bytes": None}
+                        "sherry_glu_workspace_bytes": None, "sherry_cache_attention_workspace_bytes": None}
             entries |= {f"sherry_{n}_scratch_bytes": None for n in names if n.endswith(("backward", "attention"))}
             _binding.setup({n: ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in entries},
                            _workspaces._bufs, _zeroed_workspace, ACTIVATIONS, _raise_status)

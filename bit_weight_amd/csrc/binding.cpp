@@ -59,6 +59,7 @@ decltype(&sherry_qk_norm_rope_backward_scratch_bytes) f_qk_norm_rope_backward_sc
 decltype(&sherry_cache_write) f_cache_write;
 decltype(&sherry_cache_read) f_cache_read;
 decltype(&sherry_cache_attention) f_cache_attention;
+decltype(&sherry_cache_attention_workspace_bytes) f_cache_attention_workspace_bytes;
 decltype(&sherry_cache_attention_scratch_bytes) f_cache_attention_scratch_bytes;
 
 struct Entry {
@@ -85,6 +86,7 @@ const Entry kEntries[] = {
     {"sherry_cache_write", &f_cache_write},
     {"sherry_cache_read", &f_cache_read},
     {"sherry_cache_attention", &f_cache_attention},
+    {"sherry_cache_attention_workspace_bytes", &f_cache_attention_workspace_bytes},
     {"sherry_cache_attention_scratch_bytes", &f_cache_attention_scratch_bytes},
 };
 
@@ -229,12 +231,13 @@ void launch(const char* name, int index, F call) {
   }
 }
 
-// The split-K workspace: the caller's tensor, none needed, or the module's.
+// The zeroed workspace: the caller's tensor, none needed, or the module's.
 struct Workspace {
   void* at = nullptr;
   size_t bytes = 0;
   at::Tensor keep;
-  Workspace(PyObject* o, size_t need, const Tokens& t) {
+  template <typename Operand>
+  Workspace(PyObject* o, size_t need, const Operand& t) {
     if (o != Py_None) {
       keep = tensor_of(o, "workspace");
       check_tensor(keep, "workspace", at::kByte, t.index);
@@ -730,11 +733,12 @@ PyObject* cache_attention(PyObject* const* a) {
   if (truth(a[12])) lse = empty({T, heads}, at::kFloat, c.device);
   const size_t bytes = f_cache_attention_scratch_bytes(T, c.S, heads, c.c.heads, c.c.dim);
   const at::Tensor scratch = empty({(int64_t)bytes}, at::kByte, c.device);
+  const Workspace ws(Py_None, f_cache_attention_workspace_bytes(), c);
   Gradients gradients("cache_attention", {a[0]}, a[11]);
   launch("sherry_cache_attention", c.index, [&](void* stream) {
     return f_cache_attention(q.data_ptr(), stride, heads, &c.c, c.table, c.table_width, c.starts, c.lens, c.S, T,
                              scale, window, sinks, y.data_ptr(), lse.defined() ? lse.data_ptr<float>() : nullptr,
-                             dtype, scratch.data_ptr(), bytes, stream);
+                             dtype, ws.at, ws.bytes, scratch.data_ptr(), bytes, stream);
   });
   gradients.mark({y, lse});
   return lse.defined() ? wrap_all({y, lse}) : wrap(y);

@@ -22,12 +22,12 @@
 namespace sherry {
 namespace {
 
-constexpr int kWaves = 4;
-constexpr int kThreads = 64 * kWaves;
 constexpr int kRows = 16;                // queries of a unit
-constexpr int kBlocks = 2 * kCUs;        // workgroups
-constexpr int kLeast = 2 * kWaves;       // steps that a workgroup takes at least
-constexpr float kWeight = 128.0f;        // 2^kWeightExponent
+
+// A workgroup's waves take its steps in turn; one workgroup a CU.  Two waves a SIMD, or
+// one where D > 128 wants the registers.
+constexpr int waves_of_kernel(int kC) { return kC <= 2 ? 8 : 4; }
+constexpr int kBlocks = kCUs;
 
 // Units of a sequence: each head's tiles of 16 rows; a row is a token and one of
 // the query heads that share the head.
@@ -40,27 +40,21 @@ __device__ __forceinline__ Steps steps_of(const AttentionArgs& a, const Rows& r)
   return Steps(a, r.len - r.n, r.len - 1);
 }
 
-__device__ __forceinline__ int64_t cost_of(const AttentionArgs& a, int i) {
-  const Rows r = rows_of(a.c, i);
-  return r.n == 0 ? 0 : (int64_t)a.c.H * tiles_of(a, r) * steps_of(a, r).count();
+// Quotients of numbers that are as a rule small: a division in 64 bits is 130 instructions.
+__device__ __forceinline__ int64_t quotient(int64_t x, int y) {
+  return (uint64_t)x >> 32 ? x / y : (int64_t)((uint32_t)x / (uint32_t)y);
 }
 
-// All units' steps, one after another, are dealt evenly: workgroup w of `used`
-// takes steps w total / used up to the next one's first.
+// All units' steps, one after another (by sequence, head and tile), are dealt evenly:
+// workgroup w takes `each` of them from step first(w) on, but at least one for each wave.
 struct Deal {
   int64_t total;
-  int used;
-  __device__ __forceinline__ explicit Deal(int64_t t) : total(t) {
-    const int64_t most = (t + kLeast - 1) / kLeast;
-    used = (int)(most < kBlocks ? most : kBlocks);
+  int each;
+  __device__ __forceinline__ Deal(int64_t t, int least) : total(t) {
+    each = (int)min(max((t + kBlocks - 1) / kBlocks, (int64_t)least), (int64_t)1 << 30);
   }
-  __device__ __forceinline__ int64_t first(int w) const { return total * w / used; }
-  // the workgroup that has step s
-  __device__ __forceinline__ int owner(int64_t s) const {
-    int w = (int)(s * used / total);
-    while (w + 1 < used && first(w + 1) <= s) ++w;
-    return w;
-  }
+  __device__ __forceinline__ int64_t first(int w) const { return (int64_t)each * w; }
+  __device__ __forceinline__ int owner(int64_t step) const { return (int)quotient(step, each); }
 };
 
 __device__ __forceinline__ float max_of_groups(float v) {
@@ -73,326 +67,413 @@ __device__ __forceinline__ float sum_of_groups(float v) {
   return v + __shfl_xor(v, 32);
 }
 
-// kC: D / 64 rounded up.  kTerms: fp16 terms of q and of the weights.
-template <int kC, int kTerms>
-struct Wave {
-  static constexpr int kTiles = 4 * kC;     // of 16 features
-  const AttentionArgs& a;
-  int lane, i, g;
-  int seq, h, pieces;
-  Rows r;
-  int pos;              // of this lane's query
-  int low, high;        // of the tile's queries
-  float factor;         // of q's power of two and the scale, for base 2
-  h8 q[kTerms][kC][2];
-  // running
-  float m, l, unit;     // maximum, this lane's part of the sum, largest value scale
-  f4 o[kTiles];         // features 16 t + 4 g + r of query i, in `unit` / kWeight
-
-  __device__ __forceinline__ Wave(const AttentionArgs& args) : a(args) {
-    lane = threadIdx.x & 63;
-    i = lane & 15;
-    g = lane >> 4;
-    pieces = a.c.D / 16;
-  }
-
-  // The queries of tile `tile`: exact as fp16 under 2^e per row, the row's largest near 2^14.
-  __device__ __forceinline__ void load_queries(int tile) {
-    const int group = a.Hq / a.c.H, row = kRows * tile + i, token = row / group;
-    const bool in = token < r.n;
-    const size_t at = (size_t)(r.row0 + (in ? token : 0)) * a.q_stride +
-                      (size_t)(h * group + (in ? row - token * group : 0)) * a.c.D;
-    const int first = r.len - r.n;
-    pos = in ? first + token : -1;
-    low = first + kRows * tile / group;
-    high = first + min((kRows * tile + kRows - 1) / group, r.n - 1);
-    f4 raw[kC][4];
-    float top = 0.0f;
-#pragma unroll
-    for (int c = 0; c < kC; ++c)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        raw[c][j] = f4{};
-        if (in && 4 * c + g < pieces) raw[c][j] = load4_as(a.q, at + 64 * c + 16 * g + 4 * j, a.c.dtype);
-#pragma unroll
-        for (int b = 0; b < 4; ++b) top = fmaxf(top, fabsf(raw[c][j][b]));
-      }
-    top = max_of_groups(top);
-    const float times = row_scale(top);
-    factor = a.scale * kLog2E / times;
-    if (r.len > room_of(a)) factor = __builtin_nanf("");     // tokens without pages
-#pragma unroll
-    for (int c = 0; c < kC; ++c)
-#pragma unroll
-      for (int half = 0; half < 2; ++half)
-#pragma unroll
-        for (int b = 0; b < 8; ++b) {
-          const float v = raw[c][2 * half + b / 4][b % 4] * times;
-          const _Float16 hi = (_Float16)v;
-          q[0][c][half][b] = hi;
-          if constexpr (kTerms == 2) q[kTerms - 1][c][half][b] = (_Float16)(v - (float)hi);
-        }
-  }
-
-  __device__ __forceinline__ void reset() {
-    m = -__builtin_inff();
-    l = 0.0f;
-    unit = 0x1p-126f;
-#pragma unroll
-    for (int t = 0; t < kTiles; ++t) o[t] = f4{};
-  }
-
-  __device__ __forceinline__ void step(int ts) {
-    // keys: lane (row 4 g' + r, group g) takes features 16 (4 c + g) .. of token 4 n + r of block g'
-    const int key_page = page_of(a.c, seq, 4 * ts + i / 4), page = page_of(a.c, seq, 4 * ts + g);
-    const size_t key_block = block_of(a.c, max(key_page, 0), h, 4 * ts + i / 4);
-    const size_t block = block_of(a.c, max(page, 0), h, 4 * ts + g);
-    const uint8_t* keys = a.c.k + key_block * (16 * a.c.D) + 16 * (i & 3);
-    const uint8_t* values = a.c.v + block * (16 * a.c.D) + 16 * i;
-    uint4 kw[4][kC], vw[kTiles];
-#pragma unroll
-    for (int n = 0; n < 4; ++n)
-#pragma unroll
-      for (int c = 0; c < kC; ++c)
-        kw[n][c] = *reinterpret_cast<const uint4*>(keys + 256 * min(4 * c + g, pieces - 1) + 64 * n);
-    float ks = a.c.k_scale[block], vs = a.c.v_scale[block];
-#pragma unroll
-    for (int t = 0; t < kTiles; ++t)
-      if (t < pieces) vw[t] = *reinterpret_cast<const uint4*>(values + 256 * t);
-    if (page < 0 || vs != vs) ks = __builtin_nanf("");      // whoever sees it gives NaN
-
-    f4 s[4];
-#pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      s[n] = f4{};
-#pragma unroll
-      for (int c = 0; c < kC; ++c) {
-        const h8 k0 = halves8(kw[n][c].x, kw[n][c].y), k1 = halves8(kw[n][c].z, kw[n][c].w);
-#pragma unroll
-        for (int t = 0; t < kTerms; ++t) {
-          s[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, q[t][c][0], s[n], 0, 0, 0);
-          s[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k1, q[t][c][1], s[n], 0, 0, 0);
-        }
-      }
-    }
-    // (the pieces past D that the keys' loads repeat meet zeros of q)
-    const float f = factor * ks;
-    const int t0 = kStep * ts;
-    const bool all = sees_all(a, t0, low, high);
-    float top = -__builtin_inff();
-#pragma unroll
-    for (int n = 0; n < 4; ++n)
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        s[n][b] *= f;
-        if (!all) {
-          const int j = t0 + 16 * g + 4 * n + b;
-          s[n][b] = sees(a, j, pos) ? s[n][b] : -__builtin_inff();
-        }
-        top = fmaxf(top, s[n][b]);
-      }
-    // (the scale of a block that is not seen may be anything)
-    const float scale_top = max_of_groups(fmaxf(unit, top > -__builtin_inff() && vs < __builtin_inff() ? vs : 0.0f));
-    top = max_of_groups(top);
-    if (__any(top > m + kSlack || scale_top > unit)) {
-      const float now = fmaxf(m, top);
-      const float keep = __builtin_amdgcn_exp2f(m - above(now));      // (0 where nothing was seen so far)
-      l *= keep;
-      const float scaled = keep * (unit / scale_top);
-#pragma unroll
-      for (int t = 0; t < kTiles; ++t) o[t] *= scaled;
-      m = now;
-      unit = scale_top;
-    }
-    const float base = above(m), w = vs * (kWeight / unit);
-    h8 p[kTerms][2];
-#pragma unroll
-    for (int n = 0; n < 4; ++n)
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const float e = __builtin_amdgcn_exp2f(s[n][b] - base);
-        l += e;
-        const float v = s[n][b] == -__builtin_inff() ? 0.0f : e * w;
-        const _Float16 hi = (_Float16)v;
-        p[0][n / 2][4 * (n % 2) + b] = hi;
-        if constexpr (kTerms == 2) p[kTerms - 1][n / 2][4 * (n % 2) + b] = (_Float16)(v - (float)hi);
-      }
-#pragma unroll
-    for (int t = 0; t < kTiles; ++t) {
-      if (t < pieces) {
-        const h8 v0 = halves8(vw[t].x, vw[t].y), v1 = halves8(vw[t].z, vw[t].w);
-#pragma unroll
-        for (int u = 0; u < kTerms; ++u) {
-          o[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, p[u][0], o[t], 0, 0, 0);
-          o[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, p[u][1], o[t], 0, 0, 0);
-        }
-      }
-    }
-  }
-};
+// Parts pass from one XCD to another, whose L2 are not one: relaxed atomics of the
+// agent's scope go past them.  (A release and an acquire at that scope write back and
+// drop the whole L2 each time: 64 sequences of 2600 to 8192 tokens took 307 us with them,
+// 131 without.)
+__device__ __forceinline__ void share(float* p, float v) { __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+__device__ __forceinline__ float shared_value(const float* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void share(float* p, f4 v) {      // (8 bytes aligned)
+  const uint4 u = __builtin_bit_cast(uint4, v);
+  uint64_t* to = reinterpret_cast<uint64_t*>(p);
+  __hip_atomic_store(to, u.x | (uint64_t)u.y << 32, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __hip_atomic_store(to + 1, u.z | (uint64_t)u.w << 32, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ f4 shared_four(const float* p) {
+  const uint64_t* from = reinterpret_cast<const uint64_t*>(p);
+  const uint64_t a = __hip_atomic_load(from, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  const uint64_t b = __hip_atomic_load(from + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return __builtin_bit_cast(f4, make_uint4((uint32_t)a, (uint32_t)(a >> 32), (uint32_t)b, (uint32_t)(b >> 32)));
+}
+// Every store of this wave has arrived before anything that follows is issued.
+__device__ __forceinline__ void all_arrived() {
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+}
 
 // A part of a unit in scratch: [16][D] of y over these steps alone, then the 16 maxima and sums.
 __host__ __device__ inline size_t part_floats(int D) { return (size_t)kRows * (D + 2); }
 
-template <int kC, int kTerms>
-__global__ __launch_bounds__(kThreads) void attention_kernel(AttentionArgs a) {
+// A workgroup's share of a unit: steps s0 .. s1 - 1 of `count`, the first of them `here` among all.
+struct Share {
+  int seq, h, tile, s0, s1, count;
+  int64_t here;
+  Rows r;
+  Steps steps;
+  __device__ __forceinline__ Share(const AttentionArgs& a, int seq_, const Rows& r_, int64_t rest, int64_t left, int64_t here_)
+      : seq(seq_), here(here_), r(r_), steps(steps_of(a, r_)) {
+    count = steps.count();
+    const int tiles = tiles_of(a, r), unit = (int)quotient(rest, count);
+    h = unit / tiles;
+    tile = unit - h * tiles;
+    s0 = (int)(rest - (int64_t)unit * count);
+    s1 = (int)min((int64_t)count, s0 + left);
+  }
+  // the unit after this one, of which `left` steps are this workgroup's (more than 0)
+  __device__ __forceinline__ void advance(const AttentionArgs& a, int64_t left) {
+    here += s1 - s0;
+    s0 = 0;
+    if (++tile == tiles_of(a, r)) {
+      tile = 0;
+      if (++h == a.c.H) {
+        h = 0;
+        do r = uniform(rows_of(a.c, ++seq));
+        while (r.n == 0);
+        steps = steps_of(a, r);
+        count = steps.count();
+      }
+    }
+    s1 = (int)min((int64_t)count, left);
+  }
+};
+
+// kC: D / 64 rounded up.  kFull: D is 64 kC.  kTerms: fp16 terms of q and of the weights.
+template <int kC, bool kFull, int kTerms>
+__global__ __launch_bounds__(64 * waves_of_kernel(kC)) void attention_kernel(AttentionArgs a) {
+  constexpr int kWaves = waves_of_kernel(kC), kThreads = 64 * kWaves;
+  constexpr int kTiles = 4 * kC;        // of 16 features
   constexpr int kPitch = 64 * kC + 4;
+  constexpr float kWeight = 128.0f;     // 2^kWeightExponent
   __shared__ float join[kWaves][kRows][kPitch];
   __shared__ float maxima[kWaves][kRows], sums[kWaves][kRows];
-  __shared__ int64_t parts[kWaves];
-  __shared__ int64_t found_rest;
-  __shared__ int found_seq;
-  const int wave = threadIdx.x >> 6, block = blockIdx.x, group = a.Hq / a.c.H;
+  __shared__ int64_t scan[kWaves], found_rest;
+  __shared__ int found_seq, is_last;
+  __shared__ Rows found_rows;
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), i = lane & 15, g = lane >> 4;
+  const int block = blockIdx.x, group = a.Hq / a.c.H, D = a.c.D, pieces = D / 16;
 
-  int64_t total = 0, before;
+  // where this workgroup's steps begin
+  int64_t total = 0, before = 0, own = 0;
+  Rows mine{};
   for (int base = 0; base < a.c.S; base += kThreads) {
-    const int i = base + threadIdx.x;
-    total += block_scan<kWaves>(i < a.c.S ? cost_of(a, i) : 0, before, parts);
+    own = 0;
+    if (base + tid < a.c.S) {
+      mine = rows_of(a.c, base + tid);
+      if (mine.n > 0) own = (int64_t)a.c.H * tiles_of(a, mine) * steps_of(a, mine).count();
+    }
+    total += block_scan<kWaves>(own, before, scan);
   }
   if (total == 0) return;
-  const Deal deal(total);
-  if (block >= deal.used) return;
+  const Deal deal(uniform64(total), kWaves);
   const int64_t begin = deal.first(block);
-  int64_t left = deal.first(block + 1) - begin, past = 0;
+  if (begin >= total) return;
+  int64_t left = min(deal.total - begin, (int64_t)deal.each), past = 0;
   for (int base = 0;; base += kThreads) {       // (begin < total, so a sequence has it)
-    const int i = base + threadIdx.x;
-    const int64_t own = i < a.c.S ? cost_of(a, i) : 0, all = block_scan<kWaves>(own, before, parts);
-    before += past;
+    int64_t all = total;
+    if (a.c.S > kThreads) {
+      own = 0;
+      if (base + tid < a.c.S) {
+        mine = rows_of(a.c, base + tid);
+        if (mine.n > 0) own = (int64_t)a.c.H * tiles_of(a, mine) * steps_of(a, mine).count();
+      }
+      all = block_scan<kWaves>(own, before, scan);
+      before += past;
+    }
     if (begin >= before && begin < before + own) {
-      found_seq = i;
+      found_seq = base + tid;
+      found_rows = mine;
       found_rest = begin - before;
     }
     past += all;
     if (past > begin) break;
   }
   __syncthreads();
-  int seq = found_seq;
-  int64_t rest = found_rest;
-
-  Wave<kC, kTerms> w(a);
+  Share now(a, uniform(found_seq), uniform(found_rows), uniform64(found_rest), left, begin);
   bool first_part = true;
-  while (left > 0) {
-    w.seq = seq;
-    w.r = rows_of(a.c, seq);
-    const Steps steps = steps_of(a, w.r);
-    const int count = steps.count(), tiles = tiles_of(a, w.r), units = w.r.n == 0 ? 0 : a.c.H * tiles;
-    for (int u = (int)(rest / count); u < units && left > 0; ++u) {
-      const int s0 = (int)(rest - (int64_t)u * count), s1 = (int)min((int64_t)count, s0 + left);
-      const int tile = u % tiles;
-      w.h = u / tiles;
-      w.load_queries(tile);
-      w.reset();
-      for (int s = s0 + wave; s < s1; s += kWaves) w.step(steps.at(s));
+
+  // A wave's next step: its pages, then its bytes, each asked for a step before it is
+  // needed, also when that is in the next unit.  Where there is none, block 0 of the
+  // cache is read, so that nothing here branches.
+  // Keys: lane (row 4 g' + r, group g) takes features 16 (4 c + g) .. of token 4 n + r of
+  // block g', so that lane (query i, group g) of the product has the 16 tokens of block
+  // g.  Values: tokens 16 g .. of feature 16 t + i.
+  int key_page, value_page;
+  uint4 kw[4][kC], vw[kTiles];
+  float ks, vs;
+  uint32_t value_block;       // (a cache has fewer than 2^31 blocks)
+  bool value_good;
+  const uint32_t page_blocks = (uint32_t)a.c.H << a.c.block_shift;
+  auto load_pages = [&](int seq, int step) {
+    const int32_t* table = a.c.table + (size_t)seq * a.c.table_width;
+    key_page = table[min((4 * step + i / 4) >> a.c.block_shift, a.c.table_width - 1)];
+    value_page = table[min((4 * step + g) >> a.c.block_shift, a.c.table_width - 1)];
+  };
+  auto load_keys = [&](bool any, int h, int step) {
+    const int kb = 4 * step + i / 4, vb = 4 * step + g, in_page = (1 << a.c.block_shift) - 1;
+    const uint32_t h_blocks = (uint32_t)h << a.c.block_shift;
+    auto good = [&](int page, int b) {
+      return any && (uint32_t)page < (uint32_t)a.c.pages && b >> a.c.block_shift < a.c.table_width;
+    };
+    value_good = good(value_page, vb);
+    value_block = value_good ? (uint32_t)value_page * page_blocks + h_blocks + (vb & in_page) : 0;
+    const uint32_t key_block = good(key_page, kb) ? (uint32_t)key_page * page_blocks + h_blocks + (kb & in_page) : 0;
+    const uint8_t* from = a.c.k + (uint64_t)key_block * (uint32_t)(16 * D) + 16 * (i & 3) + (kFull ? 256 * g : 0);
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+      for (int c = 0; c < kC; ++c)      // (pieces past D: the last one again, which meets zeros of q)
+        kw[n][c] = *reinterpret_cast<const uint4*>(from + (kFull ? 1024 * c : 256 * min(4 * c + g, pieces - 1)) + 64 * n);
+    ks = a.c.k_scale[value_block];      // (of the block whose scores this lane will have)
+    vs = a.c.v_scale[value_block];
+  };
+  auto load_values = [&]() {
+    const uint8_t* from = a.c.v + (uint64_t)value_block * (uint32_t)(16 * D) + 16 * i;
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) vw[t] = *reinterpret_cast<const uint4*>(from + 256 * (kFull ? t : min(t, pieces - 1)));
+  };
+  // The wave's steps in turn, the next unit's after this one's: sequence, head and
+  // token step of the one after s, or of the first; none: step 0 of the same.
+  struct At {
+    bool any;
+    int seq, h, step;
+  };
+  {
+    const int s = now.s0 + wave;
+    load_pages(now.seq, s < now.s1 ? now.steps.at(s) : 0);
+    load_keys(s < now.s1, now.h, s < now.s1 ? now.steps.at(s) : 0);
+  }
+  load_values();
+
+  for (;;) {
+    const Rows r = now.r;
+    const int h = now.h, tile = now.tile, s0 = now.s0, s1 = now.s1, count = now.count;
+    left -= s1 - s0;
+    Share next = now;
+    if (left > 0) next.advance(a, left);
+    else next.s0 = next.s1 = 0;
+    auto after = [&](int s) {
+      const bool same = s + kWaves < s1;
+      const int to = same ? s + kWaves : next.s0 + wave, head = same ? now.steps.head : next.steps.head,
+                from = same ? now.steps.from : next.steps.from;
+      const bool any = same || to < next.s1;
+      return At{any, same ? now.seq : next.seq, same ? h : next.h, !any ? 0 : to < head ? to : from + to - head};
+    };
+    if (s0 + wave < s1) {
+      const At x = after(s0 + wave);
+      load_pages(x.seq, x.step);
+    } else {        // (this wave has no step of this unit: what it has asked for is the next unit's first)
+      const int s = next.s0 + wave;
+      load_pages(next.seq, s < next.s1 ? next.steps.at(s) : 0);
+      load_keys(s < next.s1, next.h, s < next.s1 ? next.steps.at(s) : 0);
+      load_values();
+    }
+    {
+      // queries, exact as fp16 under 2^e per row (the row's largest near 2^13)
+      const int row = kRows * tile + i, token = row / group, position = r.len - r.n;
+      const bool in = token < r.n;
+      const int pos = in ? position + token : -1;
+      const int low = position + kRows * tile / group, high = position + min((kRows * tile + kRows - 1) / group, r.n - 1);
+      h8 q[kTerms][kC][2];
+      float factor;
+      {
+        const size_t at = (size_t)(r.row0 + (in ? token : 0)) * a.q_stride +
+                          (size_t)(h * group + (in ? row - token * group : 0)) * D;
+        RawValues<4> raw[kC];
+        float top = 0.0f;
+#pragma unroll
+        for (int c = 0; c < kC; ++c) raw[c].load(a.q, at + 16 * min(4 * c + g, pieces - 1), a.c.dtype);
+        f4 x[kC][4];
+#pragma unroll
+        for (int c = 0; c < kC; ++c)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            x[c][j] = in && 4 * c + g < pieces ? raw[c].get(j, a.c.dtype) : f4{};
+#pragma unroll
+            for (int b = 0; b < 4; ++b) top = fmaxf(top, fabsf(x[c][j][b]));
+          }
+        const float times = row_scale(max_of_groups(top));
+        factor = a.scale * kLog2E / times;
+        if (r.len > room_of(a)) factor = __builtin_nanf("");     // tokens without pages
+#pragma unroll
+        for (int c = 0; c < kC; ++c)
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int b = 0; b < 8; ++b) {
+              const float v = x[c][2 * half + b / 4][b % 4] * times;
+              const _Float16 hi = (_Float16)v;
+              q[0][c][half][b] = hi;
+              if constexpr (kTerms == 2) q[kTerms - 1][c][half][b] = (_Float16)(v - (float)hi);
+            }
+      }
+
+      // maximum, this lane's part of the sum, largest value scale so far, features
+      // 16 t + 4 g + r of query i in `unit` / kWeight
+      float m = -__builtin_inff(), l = 0.0f, unit = 0x1p-126f;
+      f4 o[kTiles];
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) o[t] = f4{};
+      for (int s = s0 + wave; s < s1; s += kWaves) {
+        const int t0 = kStep * now.steps.at(s);
+        f4 sc[4];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          sc[n] = f4{};
+#pragma unroll
+          for (int c = 0; c < kC; ++c) {
+            const h8 k0 = halves8(kw[n][c].x, kw[n][c].y), k1 = halves8(kw[n][c].z, kw[n][c].w);
+#pragma unroll
+            for (int t = 0; t < kTerms; ++t) {
+              sc[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, q[t][c][0], sc[n], 0, 0, 0);
+              sc[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k1, q[t][c][1], sc[n], 0, 0, 0);
+            }
+          }
+        }
+        const float scale_now = vs, by = factor * (value_good && vs == vs ? ks : __builtin_nanf(""));   // not valid: NaN for whoever sees it
+        const At then = after(s);
+        load_keys(then.any, then.h, then.step);
+        const At later = after(s + kWaves < s1 ? s + kWaves : s);     // (past this unit its own first step asks)
+        load_pages(later.seq, later.step);
+        float top = -__builtin_inff();
+#pragma unroll
+        for (int n = 0; n < 4; ++n) sc[n] *= by;
+        if (!sees_all(a, t0, low, high)) {
+          asm volatile("");       // (a branch, not selections in every step)
+#pragma unroll
+          for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+              if (!sees(a, t0 + 16 * g + 4 * n + b, pos)) sc[n][b] = -__builtin_inff();
+        }
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+          for (int b = 0; b < 4; ++b) top = fmaxf(top, sc[n][b]);
+        // (the scale of a block that is not seen may be anything)
+        const float scale_top = max_of_groups(fmaxf(unit, top > -__builtin_inff() && scale_now < __builtin_inff() ? scale_now : 0.0f));
+        top = max_of_groups(top);
+        if (__any(top > m + kSlack || scale_top > unit)) {
+          const float most = fmaxf(m, top);
+          const float keep = __builtin_amdgcn_exp2f(m - above(most));      // (0 where nothing was seen so far)
+          l *= keep;
+          const float scaled = keep * unit * __builtin_amdgcn_rcpf(scale_top);
+#pragma unroll
+          for (int t = 0; t < kTiles; ++t) o[t] *= scaled;
+          m = most;
+          unit = scale_top;
+        }
+        const float base = above(m), w = scale_now * kWeight * __builtin_amdgcn_rcpf(unit);
+        h8 p[kTerms][2];
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            const float e = __builtin_amdgcn_exp2f(sc[n][b] - base);
+            l += e;
+            const float v = sc[n][b] == -__builtin_inff() ? 0.0f : e * w;
+            const _Float16 hi = (_Float16)v;
+            p[0][n / 2][4 * (n % 2) + b] = hi;
+            if constexpr (kTerms == 2) p[kTerms - 1][n / 2][4 * (n % 2) + b] = (_Float16)(v - (float)hi);
+          }
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+          const h8 v0 = halves8(vw[t].x, vw[t].y), v1 = halves8(vw[t].z, vw[t].w);
+#pragma unroll
+          for (int n = 0; n < kTerms; ++n) {
+            o[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, p[n][0], o[t], 0, 0, 0);
+            o[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, p[n][1], o[t], 0, 0, 0);
+          }
+        }
+        load_values();
+      }
+
       // the waves' parts
-      const float sum = sum_of_groups(w.l);
+      l = sum_of_groups(l);
       __syncthreads();
 #pragma unroll
-      for (int t = 0; t < 4 * kC; ++t)
-        if (t < w.pieces)
-          *reinterpret_cast<f4*>(&join[wave][w.i][16 * t + 4 * w.g]) = w.o[t] * (w.unit * (1.0f / kWeight));
-      if (w.g == 0) {
-        maxima[wave][w.i] = w.m;
-        sums[wave][w.i] = sum;
+      for (int t = 0; t < kTiles; ++t)
+        *reinterpret_cast<f4*>(&join[wave][i][16 * t + 4 * g]) = o[t] * (unit * (1.0f / kWeight));
+      if (g == 0) {
+        maxima[wave][i] = m;
+        sums[wave][i] = l;
       }
       __syncthreads();
       const bool whole = s0 == 0 && s1 == count;
-      float* part = a.scratch + (size_t)(2 * block + (first_part ? 0 : 1)) * part_floats(a.c.D);
-      const int quads = a.c.D / 4;
-      for (int x = threadIdx.x; x < kRows * quads; x += kThreads) {
-        const int row = x / quads, d = 4 * (x - row * quads), line = kRows * tile + row, token = line / group;
-        float m = maxima[0][row];
+      const int quads = D / 4, rows = min(kRows, r.n * group - kRows * tile);
+      auto put = [&](int of_tile, int d, f4 y, float top, float sum) {
+        const int line = kRows * tile + of_tile, of = line / group;
+        y = sum == 0.0f ? f4{} : y / sum;
+        const size_t at = (size_t)(r.row0 + of) * a.Hq + h * group + line - of * group;
+        store4_as(a.y, at * D + d, a.c.dtype, y);
+        if (a.lse && d == 0) a.lse[at] = (top + __builtin_amdgcn_logf(sum)) * kLn2;
+      };
+      float* part = a.scratch + (size_t)(2 * block + (first_part ? 0 : 1)) * part_floats(D);
+      for (int x = tid; x < rows * quads; x += kThreads) {
+        const int line = x / quads, d = 4 * (x - line * quads);
+        float top = maxima[0][line], sum = 0.0f;
 #pragma unroll
-        for (int v = 1; v < kWaves; ++v) m = fmaxf(m, maxima[v][row]);
-        float l = 0.0f;
+        for (int v = 1; v < kWaves; ++v) top = fmaxf(top, maxima[v][line]);
         f4 y{};
 #pragma unroll
         for (int v = 0; v < kWaves; ++v) {
-          const float e = __builtin_amdgcn_exp2f(maxima[v][row] - above(m));
-          l += e * sums[v][row];
-          y += e * *reinterpret_cast<const f4*>(&join[v][row][d]);
+          const float e = __builtin_amdgcn_exp2f(maxima[v][line] - above(top));
+          sum += e * sums[v][line];
+          y += e * *reinterpret_cast<const f4*>(&join[v][line][d]);
         }
-        y = l == 0.0f ? f4{} : y / l;
         if (whole) {
-          if (token < w.r.n) {
-            const size_t at = (size_t)(w.r.row0 + token) * a.Hq + w.h * group + line - token * group;
-            store4_as(a.y, at * a.c.D + d, a.c.dtype, y);
-            if (a.lse && d == 0) a.lse[at] = (m + __builtin_amdgcn_logf(l)) * kLn2;
-          }
+          put(line, d, y, top, sum);
         } else {
-          *reinterpret_cast<f4*>(part + (size_t)row * a.c.D + d) = y;
+          share(part + (size_t)line * D + d, sum == 0.0f ? f4{} : y / sum);
           if (d == 0) {
-            part[kRows * a.c.D + row] = m;
-            part[kRows * a.c.D + kRows + row] = l;
+            share(part + kRows * D + line, top);
+            share(part + kRows * D + kRows + line, sum);
           }
         }
       }
-      left -= s1 - s0;
-      rest += s1 - s0;
+      if (!whole) {
+        // The unit's parts are in as many workgroups as its steps are dealt to; the one
+        // that is done last joins them, always in their order.  Only one unit that begins
+        // in a workgroup goes on in the next: that workgroup's counter is the unit's.
+        const int64_t unit_first = now.here - s0;
+        const int w0 = deal.owner(unit_first), w1 = deal.owner(unit_first + count - 1);
+        all_arrived();
+        __syncthreads();
+        if (tid == 0)
+          is_last = __hip_atomic_fetch_add(&a.counters[w0], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == w1 - w0;
+        __syncthreads();
+        if (is_last) {
+          if (tid == 0) __hip_atomic_store(&a.counters[w0], 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          for (int x = tid; x < rows * quads; x += kThreads) {
+            const int line = x / quads, d = 4 * (x - line * quads);
+            auto part_of = [&](int w) {
+              return a.scratch + (size_t)(2 * w + (deal.first(w) < unit_first ? 1 : 0)) * part_floats(D);
+            };
+            float top = -__builtin_inff(), sum = 0.0f;
+            for (int w = w0; w <= w1; ++w) top = fmaxf(top, shared_value(part_of(w) + kRows * D + line));
+            f4 y{};
+#pragma unroll 4
+            for (int w = w0; w <= w1; ++w) {
+              const float* from = part_of(w);
+              const float e = __builtin_amdgcn_exp2f(shared_value(from + kRows * D + line) - above(top)) *
+                              shared_value(from + kRows * D + kRows + line);
+              sum += e;
+              y += e * shared_four(from + (size_t)line * D + d);
+            }
+            put(line, d, y, top, sum);
+          }
+        }
+      }
       first_part = false;
     }
-    ++seq;
-    rest = 0;
+    if (left == 0) break;
+    now = next;
   }
 }
 
-// Joins the parts of the units that more than one workgroup had, always in the same order.
-__global__ __launch_bounds__(kThreads) void attention_join_kernel(AttentionArgs a) {
-  __shared__ int64_t parts[kWaves];
-  __shared__ int64_t found_before;
-  __shared__ int found_seq;
-  const int t = blockIdx.x, h = blockIdx.y, group = a.Hq / a.c.H;
-  if (threadIdx.x == 0) found_seq = -1;
-  int64_t total = 0, before;
-  for (int base = 0; base < a.c.S; base += kThreads) {
-    const int i = base + threadIdx.x;
-    const int64_t own = i < a.c.S ? cost_of(a, i) : 0, all = block_scan<kWaves>(own, before, parts);
-    if (own > 0) {
-      const Rows r = rows_of(a.c, i);
-      if (t >= r.row0 && t < r.row0 + r.n) {
-        found_seq = i;
-        found_before = total + before;
-      }
-    }
-    total += all;
-  }
-  __syncthreads();
-  const int seq = found_seq;
-  if (seq < 0) return;
-  const Rows r = rows_of(a.c, seq);
-  const int count = steps_of(a, r).count(), tiles = tiles_of(a, r);
-  const Deal deal(total);
-  const int quads = a.c.D / 4;
-  for (int x = threadIdx.x; x < group * quads; x += kThreads) {
-    const int head = x / quads, d = 4 * (x - head * quads), line = (t - r.row0) * group + head;
-    const int64_t first = found_before + (int64_t)(h * tiles + line / kRows) * count;
-    const int w0 = deal.owner(first), w1 = deal.owner(first + count - 1), row = line % kRows;
-    if (w0 == w1) continue;
-    float m = -__builtin_inff(), l = 0.0f;
-    for (int w = w0; w <= w1; ++w) {
-      const float* part = a.scratch + (size_t)(2 * w + (deal.first(w) < first ? 1 : 0)) * part_floats(a.c.D);
-      m = fmaxf(m, part[kRows * a.c.D + row]);
-    }
-    f4 y{};
-    for (int w = w0; w <= w1; ++w) {
-      const float* part = a.scratch + (size_t)(2 * w + (deal.first(w) < first ? 1 : 0)) * part_floats(a.c.D);
-      const float e = __builtin_amdgcn_exp2f(part[kRows * a.c.D + row] - above(m)) * part[kRows * a.c.D + kRows + row];
-      l += e;
-      y += e * *reinterpret_cast<const f4*>(part + (size_t)row * a.c.D + d);
-    }
-    y = l == 0.0f ? f4{} : y / l;
-    const size_t at = (size_t)t * a.Hq + h * group + head;
-    store4_as(a.y, at * a.c.D + d, a.c.dtype, y);
-    if (a.lse && d == 0) a.lse[at] = (m + __builtin_amdgcn_logf(l)) * kLn2;
-  }
+template <int kC, int kTerms>
+void launch_full(const AttentionArgs& a, hipStream_t stream) {
+  if (a.c.D == 64 * kC) attention_kernel<kC, true, kTerms><<<kBlocks, 64 * waves_of_kernel(kC), 0, stream>>>(a);
+  else attention_kernel<kC, false, kTerms><<<kBlocks, 64 * waves_of_kernel(kC), 0, stream>>>(a);
 }
 
 template <int kTerms>
 void launch_terms(const AttentionArgs& a, hipStream_t stream) {
   switch ((a.c.D + 63) / 64) {
-    case 1: attention_kernel<1, kTerms><<<kBlocks, kThreads, 0, stream>>>(a); break;
-    case 2: attention_kernel<2, kTerms><<<kBlocks, kThreads, 0, stream>>>(a); break;
-    case 3: attention_kernel<3, kTerms><<<kBlocks, kThreads, 0, stream>>>(a); break;
-    default: attention_kernel<4, kTerms><<<kBlocks, kThreads, 0, stream>>>(a); break;
+    case 1: return launch_full<1, kTerms>(a, stream);
+    case 2: return launch_full<2, kTerms>(a, stream);
+    case 3: return launch_full<3, kTerms>(a, stream);
+    default: return launch_full<4, kTerms>(a, stream);
   }
 }
 
@@ -406,14 +487,12 @@ size_t cache_attention_scratch_bytes(int T, int S, int Hq, int H, int D) {
   return (size_t)2 * kBlocks * part_floats(D) * sizeof(float);
 }
 
+size_t cache_attention_workspace_bytes() { return kBlocks * sizeof(int); }
+
 hipError_t launch_cache_attention(const AttentionArgs& a, hipStream_t stream, bool* partial) {
   if (tiles_pay(a.c.T, a.c.S, a.Hq, a.c.H)) return launch_attention_tiles(a, stream, partial);
   if (a.c.dtype == SHERRY_F32) launch_terms<2>(a, stream);
   else launch_terms<1>(a, stream);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  *partial = true;
-  attention_join_kernel<<<dim3(a.c.T, a.c.H), kThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 

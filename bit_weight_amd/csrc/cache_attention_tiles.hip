@@ -298,15 +298,17 @@ __global__ __launch_bounds__(kThreads, kC <= 2 ? 2 : 1) void attention_tiles_ker
       const size_t from = (size_t)(r.row0 + (in ? token : 0)) * a.q_stride +
                           (size_t)(h * group + (in ? row - token * group : 0)) * D + 8 * f;
       float top = 0.0f;
-      f4 raw[4 * kC][2];
+      RawValues<2> bytes[4 * kC];
+#pragma unroll
+      for (int c = 0; c < 4 * kC; ++c) bytes[c].load(a.q, from + 16 * min(c, pieces - 1), a.c.dtype);
+      auto value = [&](int c, int j) { return in && c < pieces ? bytes[c].get(j, a.c.dtype) : f4{}; };
 #pragma unroll
       for (int c = 0; c < 4 * kC; ++c)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          raw[c][j] = f4{};
-          if (in && c < pieces) raw[c][j] = load4_as(a.q, from + 16 * c + 4 * j, a.c.dtype);
+          const f4 x = value(c, j);
 #pragma unroll
-          for (int b = 0; b < 4; ++b) top = fmaxf(top, fabsf(raw[c][j][b]));
+          for (int b = 0; b < 4; ++b) top = fmaxf(top, fabsf(x[b]));
         }
       top = fmaxf(top, __shfl_xor(top, 32));
       const float times = row_scale(top) * sign;
@@ -315,11 +317,14 @@ __global__ __launch_bounds__(kThreads, kC <= 2 ? 2 : 1) void attention_tiles_ker
 #pragma unroll
       for (int c = 0; c < 4 * kC; ++c)
 #pragma unroll
-        for (int b = 0; b < 8; ++b) {
-          const float v = raw[c][b / 4][b % 4] * times;
-          const _Float16 hi = (_Float16)v;
-          q[0][c][b] = hi;
-          if constexpr (kTerms == 2) q[kTerms - 1][c][b] = (_Float16)(v - (float)hi);
+        for (int j = 0; j < 2; ++j) {
+          const f4 x = value(c, j) * times;
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            const _Float16 hi = (_Float16)x[b];
+            q[0][c][4 * j + b] = hi;
+            if constexpr (kTerms == 2) q[kTerms - 1][c][4 * j + b] = (_Float16)(x[b] - (float)hi);
+          }
         }
     }
 

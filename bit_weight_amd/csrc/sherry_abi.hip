@@ -1037,7 +1037,7 @@ sherry_status cache_args(const sherry_kv_cache* cache, const int32_t* table, int
   const int64_t page = cache->page_size;
   if (cache->pages < 1 || cache->pages > kMaxTokens || page < 16 || page > 1024 || (page & (page - 1)) != 0 ||
       cache->heads < 1 || cache->heads > kMaxHeads / 2 || !head_ok(cache->dim) || table_width < 1 ||
-      table_width > kMaxTokens / page || S < 1 || S > kMaxDim || T < 1 || T > kMaxDim)
+      cache->pages * cache->heads * (page / 16) >= int64_t(1) << 31 || table_width > kMaxTokens / page || S < 1 || S > kMaxDim || T < 1 || T > kMaxDim)
     return SHERRY_ERR_SHAPE;
   if (!dtype_ok(dtype)) return SHERRY_ERR_ARG;
   if (!aligned(cache->k, 16) || !aligned(cache->v, 16) || !aligned(cache->k_scale, 4) || !aligned(cache->v_scale, 4) ||
@@ -1148,6 +1148,8 @@ sherry_status sherry_cache_read(const sherry_kv_cache* cache, void* k, void* v, 
   return status_of(launch_cache_read(c, k, v, static_cast<hipStream_t>(stream)), false);
 }
 
+size_t sherry_cache_attention_workspace_bytes(void) { return cache_attention_workspace_bytes(); }
+
 size_t sherry_cache_attention_scratch_bytes(int64_t T, int64_t S, int64_t q_heads, int64_t heads, int64_t dim) {
   if (T < 1 || T > kMaxDim || S < 1 || S > kMaxDim || heads < 1 || heads > kMaxHeads / 2 || q_heads < 1 ||
       q_heads > kMaxHeads || q_heads % heads != 0 || !head_ok(dim))
@@ -1158,8 +1160,8 @@ size_t sherry_cache_attention_scratch_bytes(int64_t T, int64_t S, int64_t q_head
 sherry_status sherry_cache_attention(const void* q, int64_t q_stride, int64_t q_heads, const sherry_kv_cache* cache,
                                      const int32_t* table, int64_t table_width, const int32_t* starts,
                                      const int32_t* lens, int64_t S, int64_t T, float scale, int64_t window,
-                                     int64_t sinks, void* y, float* lse, int dtype, void* scratch,
-                                     size_t scratch_bytes, void* stream) {
+                                     int64_t sinks, void* y, float* lse, int dtype, void* workspace,
+                                     size_t workspace_bytes, void* scratch, size_t scratch_bytes, void* stream) {
   if (!q || !y) return SHERRY_ERR_NULL;
   AttentionArgs a{};
   const sherry_status s = cache_args(cache, table, table_width, starts, lens, S, T, dtype, a.c);
@@ -1168,9 +1170,10 @@ sherry_status sherry_cache_attention(const void* q, int64_t q_stride, int64_t q_
     return SHERRY_ERR_SHAPE;
   if (!std::isfinite(scale) || window < 0 || sinks < 0) return SHERRY_ERR_ARG;
   if (!aligned(q, 16) || !aligned(y, 16) || !aligned(lse, 4)) return SHERRY_ERR_ALIGN;
-  if (!scratch || scratch_bytes < sherry_cache_attention_scratch_bytes(T, S, q_heads, cache->heads, cache->dim))
+  if (!workspace || workspace_bytes < sherry_cache_attention_workspace_bytes() || !scratch ||
+      scratch_bytes < sherry_cache_attention_scratch_bytes(T, S, q_heads, cache->heads, cache->dim))
     return SHERRY_ERR_WORKSPACE;
-  if (!aligned(scratch, 256)) return SHERRY_ERR_ALIGN;
+  if (!aligned(workspace, 256) || !aligned(scratch, 256)) return SHERRY_ERR_ALIGN;
   const sherry_status d = check_device();
   if (d != SHERRY_OK) return d;
   a.q = q;
@@ -1182,6 +1185,7 @@ sherry_status sherry_cache_attention(const void* q, int64_t q_stride, int64_t q_
   a.y = y;
   a.lse = lse;
   a.scratch = static_cast<float*>(scratch);
+  a.counters = static_cast<int*>(workspace);
   bool partial = false;
   const hipError_t e = launch_cache_attention(a, static_cast<hipStream_t>(stream), &partial);
   return status_of(e, partial);

@@ -74,6 +74,27 @@ __device__ __forceinline__ float row_scale(float top) {
   return __builtin_bit_cast(float, (uint32_t)(max(up, -126) + 127) << 23);
 }
 
+// 4 n consecutive values, all asked for before one is looked at (a branch on the type
+// for each four would wait for each).
+template <int n>
+struct RawValues {
+  u4 raw[n];
+  __device__ __forceinline__ void load(const void* p, size_t at, int dtype) {
+    if (dtype == SHERRY_F32) {
+#pragma unroll
+      for (int j = 0; j < n; ++j) raw[j] = reinterpret_cast<const u4*>(static_cast<const float*>(p) + at)[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < n / 2; ++j) raw[j] = reinterpret_cast<const u4*>(static_cast<const uint16_t*>(p) + at)[j];
+    }
+  }
+  __device__ __forceinline__ f4 get(int j, int dtype) const {
+    if (dtype == SHERRY_F32) return __builtin_bit_cast(f4, raw[j]);
+    const u4 w = raw[j / 2];
+    return as_f4(j % 2 ? u4{w.z, w.w, 0u, 0u} : u4{w.x, w.y, 0u, 0u}, dtype);
+  }
+};
+
 // Long sequences' numbers across lanes.
 __device__ __forceinline__ int64_t shfl_up64(int64_t v, int d) {
   const int lo = __shfl_up((int)(uint32_t)v, d), hi = __shfl_up((int)(v >> 32), d);

@@ -241,7 +241,9 @@ struct AttentionArgs {
   void* y;                  // [T, Hq, D] of type c.dtype
   float* lse;               // [T, Hq], or nullptr
   float* scratch;
+  int* counters;            // zero, and left zero
 };
+size_t cache_attention_workspace_bytes();
 size_t cache_attention_scratch_bytes(int T, int S, int Hq, int H, int D);
 size_t attention_tiles_scratch_bytes(int S, int D);      // cache_attention_tiles.hip: many queries a sequence
 hipError_t launch_attention_tiles(const AttentionArgs& a, hipStream_t stream, bool* partial);

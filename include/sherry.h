@@ -429,7 +429,8 @@ size_t sherry_qk_norm_rope_backward_scratch_bytes(int64_t T, int64_t q_heads, in
  *   k  int8 [pages, heads, page_size / 16, dim / 16, 16 tokens, 16 features],
  *   v  int8 [pages, heads, page_size / 16, dim / 16, 16 features, 16 tokens],
  *   k_scale, v_scale  fp32 [pages, heads, page_size / 16]; value = int8 * scale.
- * k and v 16-byte aligned device pointers; the struct itself is host memory. */
+ * k and v 16-byte aligned device pointers, fewer than 2^31 blocks; the struct
+ * itself is host memory. */
 typedef struct {
   void* k;
   void* v;
@@ -482,6 +483,9 @@ sherry_status sherry_cache_read(const sherry_kv_cache* cache, void* k, void* v, 
  *   window   0: none.        sinks: looked at with a window only.
  *   y        [T, q_heads, dim] of type dtype (written), 16-byte aligned.
  *   lse      [T, q_heads] fp32 (written), or NULL.
+ *   workspace  at least sherry_cache_attention_workspace_bytes() bytes, by the
+ *            rules of sherry_workspace_bytes (zero before its first use, left
+ *            zero; one buffer may serve all calls on a stream).
  *   scratch  at least the queried bytes, any content, 256-byte aligned.
  * Products run in fp16 with fp32 sums: 16-bit queries are exact (bf16 down to
  * 2^-38 of the row's largest) and the weights e^(s - m) are rounded to 11 bits,
@@ -492,7 +496,9 @@ sherry_status sherry_cache_attention(const void* q, int64_t q_stride, int64_t q_
                                      int64_t table_width, const int32_t* starts,
                                      const int32_t* lens, int64_t S, int64_t T, float scale,
                                      int64_t window, int64_t sinks, void* y, float* lse, int dtype,
-                                     void* scratch, size_t scratch_bytes, void* stream);
+                                     void* workspace, size_t workspace_bytes, void* scratch,
+                                     size_t scratch_bytes, void* stream);
+size_t sherry_cache_attention_workspace_bytes(void);
 size_t sherry_cache_attention_scratch_bytes(int64_t T, int64_t S, int64_t q_heads, int64_t heads,
                                             int64_t dim);
 
