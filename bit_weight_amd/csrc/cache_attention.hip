@@ -45,17 +45,28 @@ __device__ __forceinline__ int64_t quotient(int64_t x, int y) {
   return (uint64_t)x >> 32 ? x / y : (int64_t)((uint32_t)x / (uint32_t)y);
 }
 
-// All units' steps, one after another (by sequence, head and tile), are dealt evenly:
-// workgroup w takes `each` of them from step first(w) on, but at least one for each wave.
+// A unit's steps are cut into equal pieces of at most `most` steps: kShort where that
+// gives every piece a workgroup of its own; 1 where a workgroup has many steps (kMany of
+// them), so that the shares are even; else kLong, so that short units are not cut (into
+// even shares 64 sequences of 125 to 500 tokens took 32 us, 19.5 in pieces; 16 windows of
+// 4096 tokens in pieces 27.7 us, 21.4 in even shares).  All pieces, one after another
+// (by sequence, head and tile), are dealt evenly: workgroup w takes `each` of them from
+// piece first(w) on; those of one unit it takes together.
+constexpr int kShort = 8, kLong = 16, kMany = 24;
 struct Deal {
   int64_t total;
   int each;
-  __device__ __forceinline__ Deal(int64_t t, int least) : total(t) {
-    each = (int)min(max((t + kBlocks - 1) / kBlocks, (int64_t)least), (int64_t)1 << 30);
+  __device__ __forceinline__ explicit Deal(int64_t t) : total(t) {
+    each = (int)min((t + kBlocks - 1) / kBlocks, (int64_t)1 << 30);
   }
   __device__ __forceinline__ int64_t first(int w) const { return (int64_t)each * w; }
-  __device__ __forceinline__ int owner(int64_t step) const { return (int)quotient(step, each); }
+  __device__ __forceinline__ int owner(int64_t piece) const { return (int)quotient(piece, each); }
 };
+__device__ __forceinline__ int pieces_of(int steps, int most) { return (steps + most - 1) / most; }
+
+__device__ __forceinline__ int64_t pieces_of(const AttentionArgs& a, const Rows& r, int most) {
+  return r.n > 0 ? (int64_t)a.c.H * tiles_of(a, r) * pieces_of(steps_of(a, r).count(), most) : 0;
+}
 
 __device__ __forceinline__ float max_of_groups(float v) {
   v = fmaxf(v, __shfl_xor(v, 16));
@@ -95,25 +106,30 @@ __device__ __forceinline__ void all_arrived() {
 // A part of a unit in scratch: [16][D] of y over these steps alone, then the 16 maxima and sums.
 __host__ __device__ inline size_t part_floats(int D) { return (size_t)kRows * (D + 2); }
 
-// A workgroup's share of a unit: steps s0 .. s1 - 1 of `count`, the first of them `here` among all.
+// A workgroup's share of a unit: pieces p0 .. p1 - 1 of `pieces`, steps s0 .. s1 - 1.
 struct Share {
-  int seq, h, tile, s0, s1, count;
-  int64_t here;
+  int seq, h, tile, p0, p1, pieces, s0, s1;
   Rows r;
   Steps steps;
-  __device__ __forceinline__ Share(const AttentionArgs& a, int seq_, const Rows& r_, int64_t rest, int64_t left, int64_t here_)
-      : seq(seq_), here(here_), r(r_), steps(steps_of(a, r_)) {
-    count = steps.count();
-    const int tiles = tiles_of(a, r), unit = (int)quotient(rest, count);
+  __device__ __forceinline__ void cut(int64_t left) {
+    const int count = steps.count(), each = count / pieces, more = count - each * pieces;
+    p1 = (int)min((int64_t)pieces, p0 + left);
+    s0 = each * p0 + min(p0, more);
+    s1 = each * p1 + min(p1, more);
+  }
+  // `rest` of the sequence's pieces come before, `left` are this workgroup's from there on
+  __device__ __forceinline__ Share(const AttentionArgs& a, int seq_, const Rows& r_, int64_t rest, int64_t left, int most)
+      : seq(seq_), r(r_), steps(steps_of(a, r_)) {
+    pieces = pieces_of(steps.count(), most);
+    const int tiles = tiles_of(a, r), unit = (int)quotient(rest, pieces);
     h = unit / tiles;
     tile = unit - h * tiles;
-    s0 = (int)(rest - (int64_t)unit * count);
-    s1 = (int)min((int64_t)count, s0 + left);
+    p0 = (int)(rest - (int64_t)unit * pieces);
+    cut(left);
   }
-  // the unit after this one, of which `left` steps are this workgroup's (more than 0)
-  __device__ __forceinline__ void advance(const AttentionArgs& a, int64_t left) {
-    here += s1 - s0;
-    s0 = 0;
+  // the unit after this one, of which `left` pieces are this workgroup's (more than 0)
+  __device__ __forceinline__ void advance(const AttentionArgs& a, int64_t left, int most) {
+    p0 = 0;
     if (++tile == tiles_of(a, r)) {
       tile = 0;
       if (++h == a.c.H) {
@@ -121,10 +137,10 @@ struct Share {
         do r = uniform(rows_of(a.c, ++seq));
         while (r.n == 0);
         steps = steps_of(a, r);
-        count = steps.count();
+        pieces = pieces_of(steps.count(), most);
       }
     }
-    s1 = (int)min((int64_t)count, left);
+    cut(left);
   }
 };
 
@@ -143,43 +159,74 @@ __global__ __launch_bounds__(64 * waves_of_kernel(kC)) void attention_kernel(Att
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), i = lane & 15, g = lane >> 4;
   const int block = blockIdx.x, group = a.Hq / a.c.H, D = a.c.D, pieces = D / 16;
 
-  // where this workgroup's steps begin
+  // Where this workgroup's pieces begin: up to 64 sequences a lane each, in every wave;
+  // more of them a thread each, 64 kWaves at a time.
   int64_t total = 0, before = 0, own = 0;
+  int most = kShort;         // steps of a piece
   Rows mine{};
-  for (int base = 0; base < a.c.S; base += kThreads) {
-    own = 0;
-    if (base + tid < a.c.S) {
-      mine = rows_of(a.c, base + tid);
-      if (mine.n > 0) own = (int64_t)a.c.H * tiles_of(a, mine) * steps_of(a, mine).count();
+  auto look_at = [&](int seq) {
+    mine = {};
+    if (seq < a.c.S) mine = rows_of(a.c, seq);
+    own = pieces_of(a, mine, most);
+  };
+  const bool few = a.c.S <= 64;
+  if (few) look_at(lane);
+  for (;;) {
+    if (few) {
+      own = pieces_of(a, mine, most);
+      int64_t sum = own;
+#pragma unroll
+      for (int d = 1; d < 64; d *= 2) {
+        const int64_t v = shfl_up64(sum, d);
+        if (lane >= d) sum += v;
+      }
+      before = sum - own;
+      total = ((int64_t)__builtin_amdgcn_readlane((int)(sum >> 32), 63) << 32) | (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)sum, 63);
+    } else {
+      total = 0;
+      for (int base = 0; base < a.c.S; base += kThreads) {
+        look_at(base + tid);
+        total += block_scan<kWaves>(own, before, scan);
+      }
+      total = uniform64(total);
     }
-    total += block_scan<kWaves>(own, before, scan);
+    if (most == kLong || (most == kShort ? total <= kBlocks : total >= kMany * kBlocks)) break;
+    most = most == kShort ? 1 : kLong;
   }
   if (total == 0) return;
-  const Deal deal(uniform64(total), kWaves);
+  const Deal deal(total);
   const int64_t begin = deal.first(block);
   if (begin >= total) return;
-  int64_t left = min(deal.total - begin, (int64_t)deal.each), past = 0;
-  for (int base = 0;; base += kThreads) {       // (begin < total, so a sequence has it)
-    int64_t all = total;
-    if (a.c.S > kThreads) {
-      own = 0;
-      if (base + tid < a.c.S) {
-        mine = rows_of(a.c, base + tid);
-        if (mine.n > 0) own = (int64_t)a.c.H * tiles_of(a, mine) * steps_of(a, mine).count();
-      }
-      all = block_scan<kWaves>(own, before, scan);
+  int64_t left = min(total - begin, (int64_t)deal.each);
+  int first_seq;
+  int64_t first_rest;
+  Rows first_rows;
+  if (few) {
+    const int at = __ffsll((unsigned long long)__ballot(begin >= before && begin < before + own)) - 1;
+    first_seq = at;
+    first_rows = {__builtin_amdgcn_readlane(mine.row0, at), __builtin_amdgcn_readlane(mine.n, at), __builtin_amdgcn_readlane(mine.len, at)};
+    first_rest = begin - (((int64_t)__builtin_amdgcn_readlane((int)(before >> 32), at) << 32) |
+                          (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)before, at));
+  } else {
+    int64_t past = 0;
+    for (int base = 0; past <= begin; base += kThreads) {       // (begin < total, so a sequence has it)
+      look_at(base + tid);
+      const int64_t all = block_scan<kWaves>(own, before, scan);
       before += past;
+      if (begin >= before && begin < before + own) {
+        found_seq = base + tid;
+        found_rows = mine;
+        found_rest = begin - before;
+      }
+      past += all;
     }
-    if (begin >= before && begin < before + own) {
-      found_seq = base + tid;
-      found_rows = mine;
-      found_rest = begin - before;
-    }
-    past += all;
-    if (past > begin) break;
+    __syncthreads();
+    first_seq = uniform(found_seq);
+    first_rows = uniform(found_rows);
+    first_rest = uniform64(found_rest);
   }
-  __syncthreads();
-  Share now(a, uniform(found_seq), uniform(found_rows), uniform64(found_rest), left, begin);
+  Share now(a, first_seq, first_rows, first_rest, left, most);
+  int64_t here = begin;        // the share's first piece
   bool first_part = true;
 
   // A wave's next step: its pages, then its bytes, each asked for a step before it is
@@ -237,10 +284,10 @@ __global__ __launch_bounds__(64 * waves_of_kernel(kC)) void attention_kernel(Att
 
   for (;;) {
     const Rows r = now.r;
-    const int h = now.h, tile = now.tile, s0 = now.s0, s1 = now.s1, count = now.count;
-    left -= s1 - s0;
+    const int h = now.h, tile = now.tile, s0 = now.s0, s1 = now.s1;
+    left -= now.p1 - now.p0;
     Share next = now;
-    if (left > 0) next.advance(a, left);
+    if (left > 0) next.advance(a, left, most);
     else next.s0 = next.s1 = 0;
     auto after = [&](int s) {
       const bool same = s + kWaves < s1;
@@ -344,13 +391,13 @@ __global__ __launch_bounds__(64 * waves_of_kernel(kC)) void attention_kernel(Att
         const float scale_top = max_of_groups(fmaxf(unit, top > -__builtin_inff() && scale_now < __builtin_inff() ? scale_now : 0.0f));
         top = max_of_groups(top);
         if (__any(top > m + kSlack || scale_top > unit)) {
-          const float most = fmaxf(m, top);
-          const float keep = __builtin_amdgcn_exp2f(m - above(most));      // (0 where nothing was seen so far)
+          const float peak = fmaxf(m, top);
+          const float keep = __builtin_amdgcn_exp2f(m - above(peak));      // (0 where nothing was seen so far)
           l *= keep;
           const float scaled = keep * unit * __builtin_amdgcn_rcpf(scale_top);
 #pragma unroll
           for (int t = 0; t < kTiles; ++t) o[t] *= scaled;
-          m = most;
+          m = peak;
           unit = scale_top;
         }
         const float base = above(m), w = scale_now * kWeight * __builtin_amdgcn_rcpf(unit);
@@ -389,7 +436,7 @@ __global__ __launch_bounds__(64 * waves_of_kernel(kC)) void attention_kernel(Att
         sums[wave][i] = l;
       }
       __syncthreads();
-      const bool whole = s0 == 0 && s1 == count;
+      const bool whole = now.p0 == 0 && now.p1 == now.pieces;
       const int quads = D / 4, rows = min(kRows, r.n * group - kRows * tile);
       auto put = [&](int of_tile, int d, f4 y, float top, float sum) {
         const int line = kRows * tile + of_tile, of = line / group;
@@ -422,11 +469,11 @@ __global__ __launch_bounds__(64 * waves_of_kernel(kC)) void attention_kernel(Att
         }
       }
       if (!whole) {
-        // The unit's parts are in as many workgroups as its steps are dealt to; the one
+        // The unit's parts are in as many workgroups as its pieces are dealt to; the one
         // that is done last joins them, always in their order.  Only one unit that begins
         // in a workgroup goes on in the next: that workgroup's counter is the unit's.
-        const int64_t unit_first = now.here - s0;
-        const int w0 = deal.owner(unit_first), w1 = deal.owner(unit_first + count - 1);
+        const int64_t unit_first = here - now.p0;
+        const int w0 = deal.owner(unit_first), w1 = deal.owner(unit_first + now.pieces - 1);
         all_arrived();
         __syncthreads();
         if (tid == 0)
@@ -434,29 +481,71 @@ __global__ __launch_bounds__(64 * waves_of_kernel(kC)) void attention_kernel(Att
         __syncthreads();
         if (is_last) {
           if (tid == 0) __hip_atomic_store(&a.counters[w0], 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-          for (int x = tid; x < rows * quads; x += kThreads) {
+          auto part_of = [&](int w) {
+            return a.scratch + (size_t)(2 * w + (deal.first(w) < unit_first ? 1 : 0)) * part_floats(D);
+          };
+          // the threads share the parts too (each a trip to memory), eight asked for at once
+          const int outputs = rows * quads, sharers = max(1, min(kWaves, kThreads / outputs));
+          for (int base = 0; base < outputs; base += kThreads) {
+            const int sharer = sharers > 1 ? tid / outputs : 0, x = base + tid - sharer * outputs;
+            const bool has = sharer < sharers && x < outputs;
             const int line = x / quads, d = 4 * (x - line * quads);
-            auto part_of = [&](int w) {
-              return a.scratch + (size_t)(2 * w + (deal.first(w) < unit_first ? 1 : 0)) * part_floats(D);
-            };
             float top = -__builtin_inff(), sum = 0.0f;
-            for (int w = w0; w <= w1; ++w) top = fmaxf(top, shared_value(part_of(w) + kRows * D + line));
             f4 y{};
-#pragma unroll 4
-            for (int w = w0; w <= w1; ++w) {
-              const float* from = part_of(w);
-              const float e = __builtin_amdgcn_exp2f(shared_value(from + kRows * D + line) - above(top)) *
-                              shared_value(from + kRows * D + kRows + line);
-              sum += e;
-              y += e * shared_four(from + (size_t)line * D + d);
+            for (int w = w0 + sharer; has && w <= w1; w += 8 * sharers) {
+              float tops[8], sums_of[8];
+              f4 ys[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const float* from = part_of(min(w + k * sharers, w1));
+                tops[k] = shared_value(from + kRows * D + line);
+                sums_of[k] = shared_value(from + kRows * D + kRows + line);
+                ys[k] = shared_four(from + (size_t)line * D + d);
+              }
+              float peak = top;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) peak = fmaxf(peak, w + k * sharers <= w1 ? tops[k] : top);
+              const float keep = __builtin_amdgcn_exp2f(top - above(peak));
+              sum *= keep;
+              y *= keep;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const float e = w + k * sharers <= w1 ? __builtin_amdgcn_exp2f(tops[k] - above(peak)) * sums_of[k] : 0.0f;
+                sum += e;
+                y += w + k * sharers <= w1 ? e * ys[k] : f4{};
+              }
+              top = peak;
             }
-            put(line, d, y, top, sum);
+            if (sharers > 1) {
+              if (has) {
+                *reinterpret_cast<f4*>(&join[sharer][line][d]) = y;
+                if (d == 0) {
+                  maxima[sharer][line] = top;
+                  sums[sharer][line] = sum;
+                }
+              }
+              __syncthreads();
+              if (sharer == 0 && has) {
+                float peak = top;
+                for (int v = 1; v < sharers; ++v) peak = fmaxf(peak, maxima[v][line]);
+                sum = 0.0f;
+                y = f4{};
+                for (int v = 0; v < sharers; ++v) {
+                  const float e = __builtin_amdgcn_exp2f(maxima[v][line] - above(peak));
+                  sum += e * sums[v][line];
+                  y += e * *reinterpret_cast<const f4*>(&join[v][line][d]);
+                }
+                top = peak;
+              }
+            }
+            if (sharer == 0 && has) put(line, d, y, top, sum);
           }
         }
       }
       first_part = false;
     }
     if (left == 0) break;
+    here += now.p1 - now.p0;
     now = next;
   }
 }
