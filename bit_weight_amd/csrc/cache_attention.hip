@@ -40,11 +40,6 @@ __device__ __forceinline__ Steps steps_of(const AttentionArgs& a, const Rows& r)
   return Steps(a, r.len - r.n, r.len - 1);
 }
 
-// Quotients of numbers that are as a rule small: a division in 64 bits is 130 instructions.
-__device__ __forceinline__ int64_t quotient(int64_t x, int y) {
-  return (uint64_t)x >> 32 ? x / y : (int64_t)((uint32_t)x / (uint32_t)y);
-}
-
 // A unit's steps are cut into equal pieces of at most `most` steps: kShort where that
 // gives every piece a workgroup of its own; 1 where a workgroup has many steps (kMany of
 // them), so that the shares are even; else kLong, so that short units are not cut (into

@@ -56,7 +56,7 @@ struct Plan {
   int64_t total;
   int used;
   int pad;
-  __device__ __forceinline__ int64_t first(int w) const { return total * w / used; }
+  __device__ __forceinline__ int64_t first(int w) const { return quotient(total * w, used); }
 };
 
 // In scratch: the plan, where each workgroup begins, each sequence's steps (up to
@@ -79,8 +79,9 @@ struct Scratch {
 // One workgroup: steps of each sequence (a wave a sequence, its lanes taking the
 // tiles in turn), their running sum, and each workgroup's beginning.
 __global__ __launch_bounds__(kPlanThreads) void attention_plan_kernel(AttentionArgs a, int blocks) {
-  __shared__ int64_t parts[kPlanThreads / 64];
+  __shared__ int64_t parts[kPlanThreads / 64], near[kPlanThreads + 1];
   const Scratch s(a.scratch, blocks, a.c.S);
+  int64_t* before = a.c.S <= kPlanThreads ? near : s.before;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   for (int i = wave; i < a.c.S; i += kPlanThreads / 64) {
     const Rows r = rows_of(a.c, i);
@@ -89,20 +90,20 @@ __global__ __launch_bounds__(kPlanThreads) void attention_plan_kernel(AttentionA
     for (int t = lane; t < tiles; t += 64) sum += Tile(a, r, t).steps(a).count();
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) sum += ((int64_t)__shfl_xor((int)(sum >> 32), d) << 32) + (uint32_t)__shfl_xor((int)(uint32_t)sum, d);
-    if (lane == 0) s.before[i + 1] = sum * a.c.H;
+    if (lane == 0) before[i + 1] = sum * a.c.H;
   }
   __threadfence_block();
   __syncthreads();
   int64_t total = 0;
   for (int base = 0; base < a.c.S; base += kPlanThreads) {
     const int i = base + threadIdx.x;
-    const int64_t own = i < a.c.S ? s.before[i + 1] : 0;
-    int64_t before;
-    const int64_t all = block_scan<kPlanThreads / 64>(own, before, parts);
-    if (i < a.c.S) s.before[i + 1] = total + before + own;
+    const int64_t own = i < a.c.S ? before[i + 1] : 0;
+    int64_t earlier;
+    const int64_t all = block_scan<kPlanThreads / 64>(own, earlier, parts);
+    if (i < a.c.S) before[i + 1] = total + earlier + own;
     total += all;
   }
-  if (threadIdx.x == 0) s.before[0] = 0;
+  if (threadIdx.x == 0) before[0] = 0;
   __threadfence_block();
   __syncthreads();
   Plan plan{total, 0, 0};
@@ -114,18 +115,25 @@ __global__ __launch_bounds__(kPlanThreads) void attention_plan_kernel(AttentionA
     int lo = 0, hi = a.c.S - 1;      // the last sequence whose steps begin at or before `at`
     while (lo < hi) {
       const int mid = (lo + hi + 1) / 2;
-      if (s.before[mid] <= at) lo = mid;
+      if (before[mid] <= at) lo = mid;
       else hi = mid - 1;
     }
     const Rows r = rows_of(a.c, lo);
-    const int64_t each = (s.before[lo + 1] - s.before[lo]) / a.c.H;
-    int64_t rest = at - s.before[lo];
+    const int64_t each = (before[lo + 1] - before[lo]) / a.c.H;
+    int64_t rest = at - before[lo];
     Start b{lo, (int)(rest / each), 0, 0};
     rest -= b.head * each;
+    // tiles one after another, their first and last queries as Tile has them, with no division
+    const int group = a.Hq / a.c.H, first = r.len - r.n, whole = kRows / group, over = kRows % group;
+    int low = 0, low_over = 0, high = (kRows - 1) / group, high_over = (kRows - 1) % group;
     for (;; ++b.tile) {
-      const int count = Tile(a, r, b.tile).steps(a).count();
+      const int count = Steps(a, first + low, first + min(high, r.n - 1)).count();
       if (rest < count) break;
       rest -= count;
+      low += whole;
+      high += whole;
+      if ((low_over += over) >= group) low_over -= group, ++low;
+      if ((high_over += over) >= group) high_over -= group, ++high;
     }
     b.step = (int)rest;
     s.starts[w] = b;

@@ -39,6 +39,11 @@ struct Steps {
   __device__ __forceinline__ int at(int s) const { return s < head ? s : from + s - head; }
 };
 
+// Quotients of numbers that are as a rule small: a division in 64 bits is 130 instructions.
+__device__ __forceinline__ int64_t quotient(int64_t x, int y) {
+  return (uint64_t)x >> 32 ? x / y : (int64_t)((uint32_t)x / (uint32_t)y);
+}
+
 // Whether every query at low .. high sees every token of a step, and whether the
 // one at p sees token t.
 __device__ __forceinline__ bool sees_all(const AttentionArgs& a, int t0, int low, int high) {
