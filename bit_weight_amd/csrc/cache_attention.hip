@@ -24,10 +24,14 @@ namespace {
 
 constexpr int kRows = 16;                // queries of a unit
 
-// A workgroup's waves take its steps in turn; one workgroup a CU.  Two waves a SIMD, or
-// one where D > 128 wants the registers.
-constexpr int waves_of_kernel(int kC) { return kC <= 2 ? 8 : 4; }
-constexpr int kBlocks = kCUs;
+// A workgroup's waves take its steps in turn.  Two workgroups a CU, or one where D > 128
+// wants the registers: a unit is short beside its beginning and end, which are mostly
+// waits, and one workgroup's run under the other's steps (one of eight waves a CU: 256
+// sequences of up to 100 tokens 50 us, 34 so).
+constexpr int kWaves = 4;
+constexpr int kThreads = 64 * kWaves;
+constexpr int kBlocks = 2 * kCUs;
+constexpr int blocks_of_kernel(int kC) { return kC <= 2 ? kBlocks : kBlocks / 2; }
 
 // Units of a sequence: each head's tiles of 16 rows; a row is a token and one of
 // the query heads that share the head.
@@ -35,32 +39,43 @@ __device__ __forceinline__ int tiles_of(const AttentionArgs& a, const Rows& r) {
   return (r.n * (a.Hq / a.c.H) + kRows - 1) / kRows;
 }
 
-// All of a sequence's units look at the same steps.
-__device__ __forceinline__ Steps steps_of(const AttentionArgs& a, const Rows& r) {
-  return Steps(a, r.len - r.n, r.len - 1);
+// What a unit looks at.
+__device__ __forceinline__ Steps steps_of(const AttentionArgs& a, const Rows& r, int tile) {
+  const int group = a.Hq / a.c.H, first = r.len - r.n;
+  const bool begins = tile == 0, ends = kRows * (tile + 1) >= r.n * group;       // (no division where all is one unit)
+  return Steps(a, begins ? first : first + kRows * tile / group, ends ? r.len - 1 : first + (kRows * tile + kRows - 1) / group);
 }
 
-// A unit's steps are cut into equal pieces of at most `most` steps: kShort where that
-// gives every piece a workgroup of its own; 1 where a workgroup has many steps (kMany of
-// them), so that the shares are even; else kLong, so that short units are not cut (into
-// even shares 64 sequences of 125 to 500 tokens took 32 us, 19.5 in pieces; 16 windows of
-// 4096 tokens in pieces 27.7 us, 21.4 in even shares).  All pieces, one after another
-// (by sequence, head and tile), are dealt evenly: workgroup w takes `each` of them from
-// piece first(w) on; those of one unit it takes together.
-constexpr int kShort = 8, kLong = 16, kMany = 24;
+// A unit's steps are cut into equal pieces of at most `most` steps, but no more than
+// kParts of them (as many as its sequence's last unit, which looks at the most but for
+// one):
+//   kShort, and units of up to kMiddle not at all, where half of the workgroups get one;
+//   kMiddle where every piece has a workgroup of its own;
+//   1 where a workgroup has kMany steps or more, so that the shares are even;
+//   as many as a workgroup has on average where that gives every piece one of its own;
+//   else kLong, so that short units are not cut.
+// (One sequence of 1000 tokens: 12.6 us in pieces of 8, 11.0 of 4; of 16000: 21 us in 63
+// parts, 15.8 in 31; 64 of 125 to 500 tokens: 32 us in even shares, 16 in pieces; 16
+// windows of 4096 tokens: 32 us in pieces of 16, 24 of the average.)  All pieces, one
+// after another (by sequence, head and tile), are dealt evenly: workgroup w takes `each`
+// of them from piece first(w) on; those of one unit it takes together.
+constexpr int kShort = 4, kMiddle = 8, kLong = 16, kMany = 24, kParts = 32;
 struct Deal {
   int64_t total;
   int each;
-  __device__ __forceinline__ explicit Deal(int64_t t) : total(t) {
-    each = (int)min((t + kBlocks - 1) / kBlocks, (int64_t)1 << 30);
+  __device__ __forceinline__ explicit Deal(int64_t t, int blocks) : total(t) {
+    each = (int)min(quotient(t + blocks - 1, blocks), (int64_t)1 << 30);
   }
   __device__ __forceinline__ int64_t first(int w) const { return (int64_t)each * w; }
   __device__ __forceinline__ int owner(int64_t piece) const { return (int)quotient(piece, each); }
 };
-__device__ __forceinline__ int pieces_of(int steps, int most) { return (steps + most - 1) / most; }
+__device__ __forceinline__ int pieces_of(int steps, int most) {
+  if (most == kShort && steps <= kMiddle) return 1;
+  return most == 1 ? steps : min((steps + most - 1) / most, kParts);
+}
 
 __device__ __forceinline__ int64_t pieces_of(const AttentionArgs& a, const Rows& r, int most) {
-  return r.n > 0 ? (int64_t)a.c.H * tiles_of(a, r) * pieces_of(steps_of(a, r).count(), most) : 0;
+  return r.n > 0 ? (int64_t)a.c.H * tiles_of(a, r) * pieces_of(steps_of(a, r, tiles_of(a, r) - 1).count(), most) : 0;
 }
 
 __device__ __forceinline__ float max_of_groups(float v) {
@@ -114,35 +129,37 @@ struct Share {
   }
   // `rest` of the sequence's pieces come before, `left` are this workgroup's from there on
   __device__ __forceinline__ Share(const AttentionArgs& a, int seq_, const Rows& r_, int64_t rest, int64_t left, int most)
-      : seq(seq_), r(r_), steps(steps_of(a, r_)) {
+      : seq(seq_), r(r_), steps(steps_of(a, r_, tiles_of(a, r_) - 1)) {
     pieces = pieces_of(steps.count(), most);
     const int tiles = tiles_of(a, r), unit = (int)quotient(rest, pieces);
     h = unit / tiles;
     tile = unit - h * tiles;
+    steps = steps_of(a, r, tile);
     p0 = (int)(rest - (int64_t)unit * pieces);
     cut(left);
   }
   // the unit after this one, of which `left` pieces are this workgroup's (more than 0)
   __device__ __forceinline__ void advance(const AttentionArgs& a, int64_t left, int most) {
     p0 = 0;
-    if (++tile == tiles_of(a, r)) {
+    const int tiles = tiles_of(a, r);
+    if (++tile == tiles) {
       tile = 0;
       if (++h == a.c.H) {
         h = 0;
         do r = uniform(rows_of(a.c, ++seq));
         while (r.n == 0);
-        steps = steps_of(a, r);
-        pieces = pieces_of(steps.count(), most);
+        pieces = pieces_of(steps_of(a, r, tiles_of(a, r) - 1).count(), most);
       }
     }
+    steps = steps_of(a, r, tile);
     cut(left);
   }
 };
 
 // kC: D / 64 rounded up.  kFull: D is 64 kC.  kTerms: fp16 terms of q and of the weights.
 template <int kC, bool kFull, int kTerms>
-__global__ __launch_bounds__(64 * waves_of_kernel(kC)) void attention_kernel(AttentionArgs a) {
-  constexpr int kWaves = waves_of_kernel(kC), kThreads = 64 * kWaves;
+__global__ __launch_bounds__(kThreads, kC <= 2 ? 2 : 1) void attention_kernel(AttentionArgs a) {
+  constexpr int kGrid = blocks_of_kernel(kC);
   constexpr int kTiles = 4 * kC;        // of 16 features
   constexpr int kPitch = 64 * kC + 4;
   constexpr float kWeight = 128.0f;     // 2^kWeightExponent
@@ -156,15 +173,15 @@ __global__ __launch_bounds__(64 * waves_of_kernel(kC)) void attention_kernel(Att
 
   // Where this workgroup's pieces begin: up to 64 sequences a lane each, in every wave;
   // more of them a thread each, 64 kWaves at a time.
+  const bool few = a.c.S <= 64;
   int64_t total = 0, before = 0, own = 0;
-  int most = kShort;         // steps of a piece
+  int round = few ? 0 : 2, most = few ? kShort : 1;      // (steps of a piece)
   Rows mine{};
   auto look_at = [&](int seq) {
     mine = {};
     if (seq < a.c.S) mine = rows_of(a.c, seq);
     own = pieces_of(a, mine, most);
   };
-  const bool few = a.c.S <= 64;
   if (few) look_at(lane);
   for (;;) {
     if (few) {
@@ -185,11 +202,12 @@ __global__ __launch_bounds__(64 * waves_of_kernel(kC)) void attention_kernel(Att
       }
       total = uniform64(total);
     }
-    if (most == kLong || (most == kShort ? total <= kBlocks : total >= kMany * kBlocks)) break;
-    most = most == kShort ? 1 : kLong;
+    if (round == 4 || (round == 2 ? total >= kMany * kGrid : total <= (round == 0 ? kGrid / 2 : kGrid))) break;
+    most = round == 0 ? kMiddle : round == 1 ? 1 : round == 2 ? max(kMiddle, (int)quotient(total, kGrid) + 1) : kLong;
+    ++round;
   }
   if (total == 0) return;
-  const Deal deal(total);
+  const Deal deal(total, kGrid);
   const int64_t begin = deal.first(block);
   if (begin >= total) return;
   int64_t left = min(total - begin, (int64_t)deal.each);
@@ -547,8 +565,8 @@ __global__ __launch_bounds__(64 * waves_of_kernel(kC)) void attention_kernel(Att
 
 template <int kC, int kTerms>
 void launch_full(const AttentionArgs& a, hipStream_t stream) {
-  if (a.c.D == 64 * kC) attention_kernel<kC, true, kTerms><<<kBlocks, 64 * waves_of_kernel(kC), 0, stream>>>(a);
-  else attention_kernel<kC, false, kTerms><<<kBlocks, 64 * waves_of_kernel(kC), 0, stream>>>(a);
+  if (a.c.D == 64 * kC) attention_kernel<kC, true, kTerms><<<blocks_of_kernel(kC), kThreads, 0, stream>>>(a);
+  else attention_kernel<kC, false, kTerms><<<blocks_of_kernel(kC), kThreads, 0, stream>>>(a);
 }
 
 template <int kTerms>
@@ -563,18 +581,30 @@ void launch_terms(const AttentionArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-// Many rows a sequence: the kernel that shares a step's keys and values between 128 rows.
-static bool tiles_pay(int T, int S, int Hq, int H) { return (int64_t)T * (Hq / H) >= 64 * (int64_t)S; }
+// Whether the kernel that shares a step's keys and values between 128 rows pays: where a
+// sequence has 64 rows or more, and the steps of 16 rows that all of them take are many
+// (counted with the longest sequence that the table has room for, or the window: the host
+// knows no lengths).  Beside 16-row units its own start, deal and join take 40 us: prompts
+// of 361 tokens behind 1750, 32 heads of 128 in fp32 (35000 steps), 105 us here, 100 there;
+// 173 behind 5300, 12 heads (21000): 54 and 64.
+constexpr int64_t kTilesPay = 32000;
+static bool tiles_pay(const AttentionArgs& a) {
+  const int64_t T = a.c.T, S = a.c.S, group = a.Hq / a.c.H;
+  if (T * group < 64 * S) return false;
+  int64_t seen = (int64_t)a.c.table_width << (a.c.block_shift + 4);
+  if (a.window > 0) seen = std::min<int64_t>(seen, (int64_t)a.window + a.sinks);
+  return T * a.Hq / 16 * (seen / kStep + 1) >= kTilesPay;
+}
 
 size_t cache_attention_scratch_bytes(int T, int S, int Hq, int H, int D) {
-  if (tiles_pay(T, S, Hq, H)) return attention_tiles_scratch_bytes(S, D);
-  return (size_t)2 * kBlocks * part_floats(D) * sizeof(float);
+  const size_t rows = (size_t)2 * kBlocks * part_floats(D) * sizeof(float);
+  return (int64_t)T * (Hq / H) >= 64 * (int64_t)S ? std::max(rows, attention_tiles_scratch_bytes(S, D)) : rows;
 }
 
 size_t cache_attention_workspace_bytes() { return kBlocks * sizeof(int); }
 
 hipError_t launch_cache_attention(const AttentionArgs& a, hipStream_t stream, bool* partial) {
-  if (tiles_pay(a.c.T, a.c.S, a.Hq, a.c.H)) return launch_attention_tiles(a, stream, partial);
+  if (tiles_pay(a)) return launch_attention_tiles(a, stream, partial);
   if (a.c.dtype == SHERRY_F32) launch_terms<2>(a, stream);
   else launch_terms<1>(a, stream);
   return hipGetLastError();

@@ -25,7 +25,7 @@ constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kWaveRows = 32;
 constexpr int kRows = kWaves * kWaveRows;
-constexpr int kLeast = 8;                // steps that a workgroup takes at least
+constexpr int kLeast = 4;                // steps that a workgroup takes at least
 constexpr int kPlanThreads = 1024;
 
 constexpr int blocks_of_kernel(int kC) { return kC <= 2 ? 2 * kCUs : kCUs; }
@@ -520,13 +520,34 @@ __global__ __launch_bounds__(kThreads) void attention_tiles_join_kernel(Attentio
   for (int x = threadIdx.x; x < per * quads; x += kThreads) {
     const int line = line0 + x / quads, d = 4 * (x % quads), row = kRows * next.tile + line, token = row / group;
     if (line >= kRows || token >= r.n) continue;
+    // four parts asked for at a time, the last one again where there are fewer
     float m = -__builtin_inff(), l = 0.0f;
-    for (int n = 0; n < parts; ++n) m = fmaxf(m, part(n)[kRows * D + line]);
     f4 y{};
-    for (int n = 0; n < parts; ++n) {
-      const float e = __builtin_amdgcn_exp2f(part(n)[kRows * D + line] - above(m));
-      l += e;
-      y += e * *reinterpret_cast<const f4*>(part(n) + (size_t)line * D + d);
+    for (int n0 = 0; n0 < parts; n0 += 4) {
+      float lse[4];
+      f4 v[4];
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const float* from = part(min(n0 + n, parts - 1));
+        lse[n] = from[kRows * D + line];
+        v[n] = *reinterpret_cast<const f4*>(from + (size_t)line * D + d);
+      }
+      float now = m;
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        if (n0 + n >= parts) lse[n] = -__builtin_inff();
+        now = fmaxf(now, lse[n]);
+      }
+      const float keep = __builtin_amdgcn_exp2f(m - above(now));
+      l *= keep;
+      y *= keep;
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const float e = n0 + n < parts ? __builtin_amdgcn_exp2f(lse[n] - above(now)) : 0.0f;
+        l += e;
+        y += n0 + n < parts ? e * v[n] : f4{};
+      }
+      m = now;
     }
     y = l == 0.0f ? f4{} : y / l;
     const size_t to = (size_t)(r.row0 + token) * a.Hq + next.head * group + row - token * group;
@@ -568,7 +589,7 @@ hipError_t launch_attention_tiles(const AttentionArgs& a, hipStream_t stream, bo
   *partial = true;
   e = a.c.dtype == SHERRY_F32 ? launch_terms<2>(a, stream) : launch_terms<1>(a, stream);
   if (e != hipSuccess) return e;
-  attention_tiles_join_kernel<<<dim3(blocks, 4), kThreads, 0, stream>>>(a, blocks);
+  attention_tiles_join_kernel<<<dim3(blocks, 8), kThreads, 0, stream>>>(a, blocks);
   return hipGetLastError();
 }
 

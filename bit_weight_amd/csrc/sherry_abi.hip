@@ -995,6 +995,11 @@ bool head_ok(int64_t dim) { return dim >= 16 && dim <= 256 && dim % 16 == 0; }
 // Rows of `width` values, 16 bytes aligned each.
 bool rows_ok(int64_t stride, int64_t width) { return stride >= width && stride % 8 == 0 && stride <= kMaxTokens; }
 
+bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + b_bytes && y < x + a_bytes;
+}
+
 // What the forward and the backward of the head norms share.
 sherry_status head_norm_args(const void* x, int64_t x_stride, const float* q_weight, const float* k_weight, float eps,
                              int norm, const double* freqs, int64_t rotary_dim, int interleaved,
@@ -1170,6 +1175,8 @@ sherry_status sherry_cache_attention(const void* q, int64_t q_stride, int64_t q_
     return SHERRY_ERR_SHAPE;
   if (!std::isfinite(scale) || window < 0 || sinks < 0) return SHERRY_ERR_ARG;
   if (!aligned(q, 16) || !aligned(y, 16) || !aligned(lse, 4)) return SHERRY_ERR_ALIGN;
+  const size_t size = dtype == SHERRY_F32 ? 4 : 2;
+  if (overlap(y, size * T * q_heads * cache->dim, q, size * ((T - 1) * q_stride + q_heads * cache->dim))) return SHERRY_ERR_ARG;
   if (!workspace || workspace_bytes < sherry_cache_attention_workspace_bytes() || !scratch ||
       scratch_bytes < sherry_cache_attention_scratch_bytes(T, S, q_heads, cache->heads, cache->dim))
     return SHERRY_ERR_WORKSPACE;

@@ -481,7 +481,8 @@ sherry_status sherry_cache_read(const sherry_kv_cache* cache, void* k, void* v, 
  * gives y = 0 and lse = -infinity.
  *   q        rows of q_heads * dim values;  q_heads a multiple of heads.
  *   window   0: none.        sinks: looked at with a window only.
- *   y        [T, q_heads, dim] of type dtype (written), 16-byte aligned.
+ *   y        [T, q_heads, dim] of type dtype (written), 16-byte aligned; it
+ *            overlaps no input (over q: SHERRY_ERR_ARG).
  *   lse      [T, q_heads] fp32 (written), or NULL.
  *   workspace  at least sherry_cache_attention_workspace_bytes() bytes, by the
  *            rules of sherry_workspace_bytes (zero before its first use, left
