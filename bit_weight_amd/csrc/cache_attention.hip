@@ -17,6 +17,10 @@
 // largest one so far (a power of two too) times 2^7.  One fp16 term of each
 // for 16-bit queries (q is exact, the weights off by 2^-12), a high and a low
 // one for fp32 queries (2^-23).
+//
+// Measured: 64 sequences of up to 8192 tokens, one query each, 32 heads over 8 of 128 in
+// bf16: 133 us for 680 MB (5.1 TB/s, what a copy reaches); one of 1000 tokens 11.0 us, all
+// of it launch, the chain page -> keys -> values -> parts -> join.
 #include "sherry_attention.h"
 
 namespace sherry {

@@ -14,6 +14,13 @@
 // with the values from the same lane.  A block's key scale is part of its scores'
 // factor, its value scale (over the largest so far, a power of two) part of its
 // weights' exponent, and taken out of their sum again.
+//
+// Measured: pieces of up to 1024 tokens of 4 prompts over up to 6000, 32 heads over 8 of
+// 128 in bf16, 2.2e11 operations, in 296 us of which the deal is 9 and the join of parts
+// 20 (0.73 PFLOP/s; the library's fp16 product reaches 1.52).  The main kernel's matrix
+// units are busy 36 % of the time, the vector units 49 % (8-bit values to fp16,
+// exponentials, masks), LDS 38 %: no unit is full, waits and the phases' unevenness are
+// the rest.  Tiles of 64 rows: 448 us.
 #include "sherry_attention.h"
 
 namespace sherry {
