@@ -579,7 +579,7 @@ PyObject* qk_norm_rope(PyObject* const* a) {
     fail(PyExc_RuntimeError, "x must hold (q_heads + k_heads) * dim values a row, at most 1024 heads of 256");
   const bool interleaved = truth(a[10]);
   const at::Tensor q = empty({s.T, hq, dim}, s.type, s.device), k = empty({s.T, hk, dim}, s.type, s.device);
-  Gradients gradients("qk_norm_rope", {a[0], a[6], a[7]});
+  Gradients gradients("qk_norm_rope", {a[0], a[2], a[6], a[7]});
   launch("sherry_qk_norm_rope", s.index, [&](void* stream) {
     return f_qk_norm_rope(s.x, s.stride, s.wq, s.wk, s.eps, s.norm, s.freqs, s.rotary, interleaved, s.positions,
                           q.data_ptr(), k.data_ptr(), s.dtype, s.T, hq, hk, dim, stream);
@@ -619,7 +619,7 @@ PyObject* qk_norm_rope_backward(PyObject* const* a) {
     dwk = empty({dim}, at::kFloat, s.device);
     scratch = empty({(int64_t)bytes}, at::kByte, s.device);
   }
-  Gradients gradients("qk_norm_rope_backward", {a[0], a[1], a[2], a[5], a[6]}, a[10]);
+  Gradients gradients("qk_norm_rope_backward", {a[0], a[1], a[2], a[4], a[5], a[6]}, a[10]);
   launch("sherry_qk_norm_rope_backward", s.index, [&](void* stream) {
     return f_qk_norm_rope_backward(dq.data_ptr(), dk.data_ptr(), s.x, s.stride, s.wq, s.wk, s.eps, s.norm, s.freqs,
                                    s.rotary, interleaved, s.positions, dx.data_ptr(), stride,
@@ -685,7 +685,9 @@ PyObject* cache_write(PyObject* const* a) {
   const int64_t T = k.size(0);
   const int64_t ks = heads_of(k, "k", k.scalar_type(), c.index, T, c.c.heads, c.c.dim);
   const int64_t vs = heads_of(v, "v", k.scalar_type(), c.index, T, c.c.heads, c.c.dim);
-  if (c10::GradMode::is_enabled() && (k.requires_grad() || v.requires_grad()))
+  bool graded = k.requires_grad() || v.requires_grad();
+  for (int i : {2, 3}) graded |= tensor_of(a[i], "cache").requires_grad();
+  if (c10::GradMode::is_enabled() && graded)
     fail(PyExc_RuntimeError, "cache_write cannot carry gradients, but a tensor requires one: call it in torch.no_grad()");
   launch("sherry_cache_write", c.index, [&](void* stream) {
     return f_cache_write(&c.c, k.data_ptr(), ks, v.data_ptr(), vs, dtype, c.table, c.table_width, c.starts, c.lens,
@@ -702,10 +704,12 @@ PyObject* cache_read(PyObject* const* a) {
   const int dtype = dtype_of(type);
   if (T < 1 || T > (1 << 20)) fail(PyExc_RuntimeError, "tokens must be from 1 to 2^20, got %lld", (long long)T);
   const at::Tensor k = empty({T, c.c.heads, c.c.dim}, type, c.device), v = empty({T, c.c.heads, c.c.dim}, type, c.device);
+  Gradients gradients("cache_read", {a[2], a[3]});
   launch("sherry_cache_read", c.index, [&](void* stream) {
     return f_cache_read(&c.c, k.data_ptr(), v.data_ptr(), dtype, c.table, c.table_width, c.starts, c.lens, c.S, T,
                         stream);
   });
+  gradients.mark({k, v});
   return wrap_all({k, v});
 }
 
@@ -734,7 +738,7 @@ PyObject* cache_attention(PyObject* const* a) {
   const size_t bytes = f_cache_attention_scratch_bytes(T, c.S, heads, c.c.heads, c.c.dim);
   const at::Tensor scratch = empty({(int64_t)bytes}, at::kByte, c.device);
   const Workspace ws(Py_None, f_cache_attention_workspace_bytes(), c);
-  Gradients gradients("cache_attention", {a[0]}, a[11]);
+  Gradients gradients("cache_attention", {a[0], a[3], a[4]}, a[11]);
   launch("sherry_cache_attention", c.index, [&](void* stream) {
     return f_cache_attention(q.data_ptr(), stride, heads, &c.c, c.table, c.table_width, c.starts, c.lens, c.S, T,
                              scale, window, sinks, y.data_ptr(), lse.defined() ? lse.data_ptr<float>() : nullptr,

@@ -297,11 +297,15 @@ def test_gradients_are_not_lost_silently():
     starts = i32(0, T)
     cases = {
         "qk_norm_rope": [lambda f: bw.qk_norm_rope(f(x), pos, fr, Hq, Hk, D, wq, wk),
+                         lambda f: bw.qk_norm_rope(x, pos, f(fr), Hq, Hk, D, wq, wk),
                          lambda f: bw.qk_norm_rope(x, pos, fr, Hq, Hk, D, f(wq), wk),
                          lambda f: bw.qk_norm_rope(x, pos, fr, Hq, Hk, D, wq, f(wk))],
         "qk_norm_rope_backward": [lambda f: bw.qk_norm_rope_backward(f(q), k, x, pos, fr, wq, wk),
                                   lambda f: bw.qk_norm_rope_backward(q, k, f(x), pos, fr, wq, wk)],
-        "cache_attention": [lambda f: bw.cache_attention(f(q), cache, table, starts, tl, lse=True)],
+        "cache_attention": [lambda f: bw.cache_attention(f(q), cache, table, starts, tl, lse=True),
+                            lambda f: bw.cache_attention(q, cache._replace(k_scale=f(cache.k_scale)), table, starts, tl, lse=True),
+                            lambda f: bw.cache_attention(q, cache._replace(v_scale=f(cache.v_scale)), table, starts, tl, lse=True)],
+        "cache_read": [lambda f: bw.cache_read(cache._replace(v_scale=f(cache.v_scale)), table, starts, tl, T)],
     }
     for name, calls in cases.items():
         for call in calls:
