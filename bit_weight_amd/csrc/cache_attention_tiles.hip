@@ -232,17 +232,19 @@ __global__ __launch_bounds__(kThreads, kC <= 2 ? 2 : 1) void attention_tiles_ker
       for (int n = 0; n < kLoads; ++n) kw[n] = *reinterpret_cast<const uint4*>(from + (uint32_t)unit_at[n]);
       ks = a.c.k_scale[block_next];
       vs = a.c.v_scale[block_next];
-      if (!good) ks = __builtin_nanf("");
+      if (!good) ks = __builtin_nanf(""), vs = 0.0f;
     };
     auto load_values = [&]() {
       const uint8_t* from = a.c.v + (uint64_t)block_now * (uint32_t)(16 * D);
 #pragma unroll
       for (int n = 0; n < kLoads; ++n) vw[n] = *reinterpret_cast<const uint4*>(from + (uint32_t)unit_at[n]);
     };
-    // a block that is not valid has a key scale of NaN, one that is not or that nobody
-    // sees a value scale of 0
+    // a block that is not valid has a key scale of NaN; one that is not, that is not finite
+    // or that no query of the tile sees (all of it after the last one, or before the first
+    // one's window and behind the first tokens) a value scale of 0
     auto store_scales = [&](int s, int buffer) {
-      const bool seen = kStep * step_at(s) + 16 * wave <= tile.high;
+      const int first = kStep * step_at(s) + 16 * wave;
+      const bool seen = first <= tile.high && (a.window == 0 || tile.low - (first + 15) < a.window || first < a.sinks);
       const float k = vs == vs ? ks : vs, v = seen && vs < __builtin_inff() ? vs : 0.0f;
       if (lane < 2) scales[buffer][4 * lane + wave] = lane ? v : k;
     };
