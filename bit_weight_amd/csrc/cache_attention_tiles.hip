@@ -12,8 +12,9 @@
 // scores of one query.  Keys lie in LDS with the rows of a 16-token block dealt so
 // that these are tokens 8 f .. 8 f + 7 of two blocks: the operand of the product
 // with the values from the same lane.  A block's key scale is part of its scores'
-// factor, its value scale (over the largest so far, a power of two) part of its
-// weights' exponent, and taken out of their sum again.
+// factor.  Its value scale, over the largest that the query has seen so far (a power of
+// two), goes into the query's weights and not into the values, which all queries share:
+// no result depends on the scale of tokens that its query does not see.
 //
 // Measured: pieces of up to 1024 tokens of 4 prompts over up to 6000, 32 heads over 8 of
 // 128 in bf16, 2.2e11 operations, in 296 us of which the deal is 9 and the join of parts
@@ -239,26 +240,24 @@ __global__ __launch_bounds__(kThreads, kC <= 2 ? 2 : 1) void attention_tiles_ker
 #pragma unroll
       for (int n = 0; n < kLoads; ++n) vw[n] = *reinterpret_cast<const uint4*>(from + (uint32_t)unit_at[n]);
     };
-    // a block that is not valid has a key scale of NaN; one that is not, that is not finite
-    // or that no query of the tile sees (all of it after the last one, or before the first
-    // one's window and behind the first tokens) a value scale of 0
-    auto store_scales = [&](int s, int buffer) {
-      const int first = kStep * step_at(s) + 16 * wave;
-      const bool seen = first <= tile.high && (a.window == 0 || tile.low - (first + 15) < a.window || first < a.sinks);
-      const float k = vs == vs ? ks : vs, v = seen && vs < __builtin_inff() ? vs : 0.0f;
+    // a block that is not valid has a key scale of NaN; one that is not or whose scale is
+    // not finite a value scale of 0
+    auto store_scales = [&](int buffer) {
+      const float k = vs == vs ? ks : vs, v = vs < __builtin_inff() ? vs : 0.0f;
       if (lane < 2) scales[buffer][4 * lane + wave] = lane ? v : k;
     };
-    // 8 of a thread's keys, or of its values: those as multiples of the largest value
-    // scale so far, `unit`
+    // 8 of a thread's keys, or of its values
     auto store_keys = [&](int buffer, int n, int half) {
       *reinterpret_cast<h8*>(lds + buffer + (key_at[n] ^ (16 * half))) =
           half ? halves8(kw[n].z, kw[n].w) : halves8(kw[n].x, kw[n].y);
     };
-    auto store_values = [&](int buffer, int n, int half, _Float16 ratio) {
+    auto store_values = [&](int buffer, int n, int half) {
       *reinterpret_cast<h8*>(lds + buffer + (value_at[n] ^ (16 * half))) =
-          half ? halves8(vw[n].z, vw[n].w, ratio) : halves8(vw[n].x, vw[n].y, ratio);
+          half ? halves8(vw[n].z, vw[n].w) : halves8(vw[n].x, vw[n].y);
     };
 
+    // maximum, this lane's part of the sum, largest value scale that the query has seen,
+    // features of the output in `unit`
     float m = -__builtin_inff(), l = 0.0f, unit = 0x1p-126f;
     f16v o[kTiles];
 #pragma unroll
@@ -346,7 +345,7 @@ __global__ __launch_bounds__(kThreads, kC <= 2 ? 2 : 1) void attention_tiles_ker
     }
 
     lds_barrier();               // (the zeros, or what the last unit reads)
-    store_scales(s0, 0);
+    store_scales(0);
 #pragma unroll
     for (int n = 0; n < 2 * kLoads; ++n) store_keys(0, n / 2, n % 2);
     find_block(s0 + 1);
@@ -360,15 +359,14 @@ __global__ __launch_bounds__(kThreads, kC <= 2 ? 2 : 1) void attention_tiles_ker
     for (int s = s0, buffer = 0; s < s1; ++s, buffer ^= 1) {
       const int here = buffer * L::kBuffer, there = L::kBuffer - here;
       const int t0 = kStep * step_at(s);
-      float by[4], unit_now = unit;       // the factor of a block's scores
+      float by[4], value_scale[4];        // a block's; by: the factor of its scores
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         by[u] = factor * scales[buffer][u];
-        unit_now = fmaxf(unit_now, scales[buffer][4 + u]);
+        value_scale[u] = scales[buffer][4 + u];
       }
-      const _Float16 ratio = (_Float16)(scales[buffer][4 + wave] * __builtin_amdgcn_rcpf(unit_now));
       f16v sc[2] = {f16v{}, f16v{}};
-      store_scales(s + 1, buffer ^ 1);
+      store_scales(buffer ^ 1);
       const int base = key_row + here;
       in_slots([&](int j) { return *reinterpret_cast<const h8*>(lds + (base ^ (32 * (j / 2))) + 32 * 16 * L::kChunks * (j % 2)); },
                [&](int j, h8 k) {
@@ -380,7 +378,7 @@ __global__ __launch_bounds__(kThreads, kC <= 2 ? 2 : 1) void attention_tiles_ker
                  if (j % 2) return;
                  const int n = j / 8, part = j / 2 % 4;
                  if (part < 2) store_keys(there, n, part);
-                 else store_values(here, n, part - 2, ratio);
+                 else store_values(here, n, part - 2);
                });
       load_values();
       find_block(s + 2);
@@ -388,7 +386,11 @@ __global__ __launch_bounds__(kThreads, kC <= 2 ? 2 : 1) void attention_tiles_ker
       block_now = block_next;
       page_next = page_after;
       page_after = page_of_step(s + 4);
-      if (!sees_all(a, t0, tile.low, tile.high)) {
+      float unit_now = unit;
+      if (sees_all(a, t0, tile.low, tile.high)) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) unit_now = fmaxf(unit_now, value_scale[u]);
+      } else {
         asm volatile("");       // (a branch, not 32 selections in every step)
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
@@ -396,6 +398,9 @@ __global__ __launch_bounds__(kThreads, kC <= 2 ? 2 : 1) void attention_tiles_ker
           // factor of NaN, or of 0, may meet their -infinity
           const bool bad = by[u] != by[u];
           const int ahead = pos - (t0 + 16 * u + 8 * f);       // of the first of these tokens
+          const int behind = pos - (t0 + 16 * u);              // of the block's first
+          if (behind >= 0 && (a.window == 0 || behind - 15 < a.window || t0 + 16 * u < a.sinks))
+            unit_now = fmaxf(unit_now, value_scale[u]);
 #pragma unroll
           for (int b = 0; b < 8; ++b) {
             const float x = sc[u / 2][8 * (u % 2) + b];
@@ -411,22 +416,29 @@ __global__ __launch_bounds__(kThreads, kC <= 2 ? 2 : 1) void attention_tiles_ker
       }
       // weights under the maximum so far; where that is too low for them, or a query has
       // seen nothing yet, again under a new one
-      float sum = 0.0f;
+      float sum = 0.0f, ratio[4];
       h8 next[kTerms][4];
+      // (a block that the query does not see may have any scale: its weights are 0)
+      auto ratios = [&](float of) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) ratio[u] = fminf(value_scale[u] * __builtin_amdgcn_rcpf(of), 1.0f);
+      };
       auto weight = [&](int x, float base) {
         const float e = __builtin_amdgcn_exp2f(fmaf(sc[x / 16][x % 16], by[x / 8], -base));
         sum += e;
-        const _Float16 hi = (_Float16)e;
+        const float v = e * ratio[x / 8];
+        const _Float16 hi = (_Float16)v;
         next[0][x / 8][x % 8] = hi;
-        if constexpr (kTerms == 2) next[kTerms - 1][x / 8][x % 8] = (_Float16)(e - (float)hi);
+        if constexpr (kTerms == 2) next[kTerms - 1][x / 8][x % 8] = (_Float16)(v - (float)hi);
       };
+      ratios(unit);
       const float floor = above(m) - kWeightExponent;
       add_values(there, [&](int j) {
 #pragma unroll
         for (int x = j * 32 / kSlots; x < (j + 1) * 32 / kSlots; ++x) weight(x, floor);
       });
       // (no weight is larger than their sum; one of at most 2^15 stays in fp16's range)
-      if (__any(sum > 0x1p15f || (pos >= 0 && m == -__builtin_inff())) || unit_now > unit) {
+      if (__any(sum > 0x1p15f || (pos >= 0 && m == -__builtin_inff()) || unit_now > unit)) {
         float top = -__builtin_inff();
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
@@ -443,6 +455,7 @@ __global__ __launch_bounds__(kThreads, kC <= 2 ? 2 : 1) void attention_tiles_ker
         m = now;
         unit = unit_now;
         sum = 0.0f;
+        ratios(unit);
         const float again = above(m) - kWeightExponent;
 #pragma unroll
         for (int x = 0; x < 32; ++x) weight(x, again);

@@ -56,19 +56,18 @@ __device__ __forceinline__ bool sees(const AttentionArgs& a, int t, int p) {
 
 __device__ __forceinline__ float above(float m) { return m == -__builtin_inff() ? 0.0f : m; }
 
-// Four 8-bit values as fp16 times r, a power of two or 0: 1024 + (q + 128) is 0x6400
-// with the byte in its low half, and one fused product and sum leaves q r.
-__device__ __forceinline__ void halves4(uint32_t w, h2 r, h2 off, h2& a, h2& b) {
+// Four 8-bit values as fp16: 1024 + (q + 128) is 0x6400 with the byte in its low half.
+__device__ __forceinline__ void halves4(uint32_t w, h2& a, h2& b) {
+  const h2 off = {(_Float16)-1152.0f, (_Float16)-1152.0f};
   w ^= 0x80808080u;
-  a = __builtin_elementwise_fma(__builtin_bit_cast(h2, __builtin_amdgcn_perm(0x64646464u, w, 0x04010400u)), r, off);
-  b = __builtin_elementwise_fma(__builtin_bit_cast(h2, __builtin_amdgcn_perm(0x64646464u, w, 0x04030402u)), r, off);
+  a = __builtin_bit_cast(h2, __builtin_amdgcn_perm(0x64646464u, w, 0x04010400u)) + off;
+  b = __builtin_bit_cast(h2, __builtin_amdgcn_perm(0x64646464u, w, 0x04030402u)) + off;
 }
 
-__device__ __forceinline__ h8 halves8(uint32_t x, uint32_t y, _Float16 r = (_Float16)1.0f) {
+__device__ __forceinline__ h8 halves8(uint32_t x, uint32_t y) {
   h2 a, b, c, d;
-  const h2 times = {r, r}, off = times * h2{(_Float16)-1152.0f, (_Float16)-1152.0f};
-  halves4(x, times, off, a, b);
-  halves4(y, times, off, c, d);
+  halves4(x, a, b);
+  halves4(y, c, d);
   return h8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 

@@ -490,9 +490,9 @@ sherry_status sherry_cache_read(const sherry_kv_cache* cache, void* k, void* v, 
  *   scratch  at least the queried bytes, any content, 256-byte aligned.
  * Products run in fp16 with fp32 sums: 16-bit queries are exact (bf16 down to
  * 2^-38 of the row's largest) and the weights e^(s - m) are rounded to 11 bits,
- * fp32 queries and their weights to 22; weights times scales below 2^-31 of the
- * largest are lost, with many queries also what a block's values hold below 2^-24
- * of the largest value scale so far.  Value scales are taken to be powers of two,
+ * fp32 queries and their weights to 22; weights times value scales below 2^-31 of
+ * the largest weight times the largest scale that the query sees are lost (what it
+ * does not see has no part in this).  Value scales are taken to be powers of two,
  * as cache_write leaves them.  The sums run in a fixed order: equal calls give equal
  * bits (a row's bits may differ with the other rows of a call, which decide how the
  * work is split).  table_width * page_size is taken as the longest sequence's length

@@ -8,7 +8,7 @@ import attention_reference as ref
 import bit_weight_amd as bw
 from test_attention_edges_gpu import i32
 from test_attention_gpu import check, scales_of, sequences
-from test_attention_tiles_gpu import STEPS
+from test_attention_tiles_gpu import STEPS, wide  # noqa: F401 (a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -99,3 +99,57 @@ def test_blocks_before_every_window(kernel, new, Hq, H, t):
     y, lse = bw.cache_attention(q.cuda(), cache, table, i32(0, new), tl, window=window, lse=True)
     small = [j for j in range(new) if (n - new + j) % 64 >= 48 + window][-12:]
     check_rows(q, y, lse, k, v, scales_of(cache, table, 0, n, 16), window, 0, [*small, new - 1], Hq - 1)
+
+
+@pytest.mark.parametrize("t", list(ref.TYPES))
+@pytest.mark.parametrize("blocks", [[0, 1, 0, 0], [0, 0, 0, 1], [1, 0, 1, 0], [0, 0, 0, 0, 1, 0, 0, 1, 0]])
+@pytest.mark.parametrize("D,Hq,H", [(64, 4, 1), (128, 2, 2), (256, 3, 1)])
+def test_tokens_after_the_query(wide, D, Hq, H, blocks, t):  # noqa: F811
+    """Prompts without history whose blocks are small or large: no query depends on
+    the scale of tokens after it, in the tiles and in the 16-row kernel."""
+    dtype, far = ref.TYPES[t], FAR[t]
+    cache, table, tl, (k, v) = written([far[b] for b in blocks], H, D, 61)
+    n = 16 * len(blocks)
+    units = scales_of(cache, table, 0, n, 16)
+    q = torch.randn(n, Hq, D, generator=ref.gen(63)).to(dtype)
+    want, want_lse = ref.attention(q, k, v, D ** -0.5, None, 0, dtype, units)
+    y, lse = bw.cache_attention(q.cuda(), cache, table, i32(0, n), tl, lse=True)
+    assert wide
+    check("y", y, *want)
+    check("lse", lse, *want_lse)
+    few = 16 * H // Hq      # queries of a unit of 16 rows
+    for at in (0, 16, n - few):
+        y, lse = bw.cache_attention(q[at:at + few].cuda(), cache, table, i32(0, few), i32(at + few), lse=True)
+        check("y", y, want[0][at:at + few], want[1][at:at + few])
+        check("lse", lse, want_lse[0][at:at + few], want_lse[1][at:at + few])
+
+
+@pytest.mark.parametrize("t", list(ref.TYPES))
+@pytest.mark.parametrize("sinks", [0, 3, 16, 21])
+def test_windows_of_a_tile(sinks, t):
+    """Tiles of eight tokens: some of their windows see a large block, the others only
+    a small one; first tokens are small."""
+    low, high = FAR[t]
+    dtype, Hq, H, D, window, new = ref.TYPES[t], 1024, 64, 16, 5, 1000
+    assert new * Hq // 16 * ((window + sinks) // 64 + 1) >= STEPS
+    cache, table, tl, (k, v) = written([low, low] + [high, low] * 31, H, D, 71)
+    n = 64 * 16
+    q = torch.randn(new, Hq, D, generator=ref.gen(73)).to(dtype)
+    y, lse = bw.cache_attention(q.cuda(), cache, table, i32(0, new), tl, window=window, sinks=sinks, lse=True)
+    units = scales_of(cache, table, 0, n, 16)
+    for head in (0, 700):
+        check_rows(q, y, lse, k, v, units, window, sinks, list(range(0, 40)) + list(range(500, 540)) + [new - 1], head)
+
+
+@pytest.mark.parametrize("t", ["bf16", "fp32"])
+@pytest.mark.parametrize("blocks", [[0, 1, 0, 0] * 16, [0] * 40 + [1] + [0] * 23])
+def test_tokens_after_the_query_in_parts(wide, blocks, t):  # noqa: F811
+    """Queries of a longer prompt, whose steps several workgroups share."""
+    dtype, far, D, Hq = ref.TYPES[t], FAR[t], 64, 2
+    cache, table, tl, (k, v) = written([far[b] for b in blocks], 1, D, 81)
+    n = 16 * len(blocks)
+    q = torch.randn(n, Hq, D, generator=ref.gen(83)).to(dtype)
+    y, lse = bw.cache_attention(q.cuda(), cache, table, i32(0, n), tl, lse=True)
+    assert wide
+    rows = [0, 1, 15, 16, 17, 40, 100, 320, 639, 640, 641, 655, 656, n - 1]
+    check_rows(q, y, lse, k, v, scales_of(cache, table, 0, n, 16), None, 0, rows, 1)
