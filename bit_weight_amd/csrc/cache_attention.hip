@@ -348,7 +348,6 @@ __global__ __launch_bounds__(kThreads, kC <= 2 ? 2 : 1) void attention_kernel(At
           }
         const float times = row_scale(max_of_groups(top));
         factor = a.scale * kLog2E / times;
-        if (r.len > room_of(a)) factor = __builtin_nanf("");     // tokens without pages
 #pragma unroll
         for (int c = 0; c < kC; ++c)
 #pragma unroll
@@ -362,9 +361,10 @@ __global__ __launch_bounds__(kThreads, kC <= 2 ? 2 : 1) void attention_kernel(At
             }
       }
 
-      // maximum, this lane's part of the sum, largest value scale so far, features
-      // 16 t + 4 g + r of query i in `unit` / kWeight
-      float m = -__builtin_inff(), l = 0.0f, unit = 0x1p-126f;
+      // maximum, this lane's part of the sum (NaN for all of a sequence longer than its
+      // table, also where a window hides what the table has room for), largest value scale
+      // so far, features 16 t + 4 g + r of query i in `unit` / kWeight
+      float m = -__builtin_inff(), l = r.len > room_of(a) ? __builtin_nanf("") : 0.0f, unit = 0x1p-126f;
       f4 o[kTiles];
 #pragma unroll
       for (int t = 0; t < kTiles; ++t) o[t] = f4{};

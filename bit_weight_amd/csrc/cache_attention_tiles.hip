@@ -256,9 +256,10 @@ __global__ __launch_bounds__(kThreads, kC <= 2 ? 2 : 1) void attention_tiles_ker
           half ? halves8(vw[n].z, vw[n].w) : halves8(vw[n].x, vw[n].y);
     };
 
-    // maximum, this lane's part of the sum, largest value scale that the query has seen,
-    // features of the output in `unit`
-    float m = -__builtin_inff(), l = 0.0f, unit = 0x1p-126f;
+    // maximum, this lane's part of the sum (NaN for all of a sequence longer than its
+    // table, also where a window hides what the table has room for), largest value scale
+    // that the query has seen, features of the output in `unit`
+    float m = -__builtin_inff(), l = r.len > room_of(a) ? __builtin_nanf("") : 0.0f, unit = 0x1p-126f;
     f16v o[kTiles];
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) o[t] = f16v{};
@@ -329,7 +330,6 @@ __global__ __launch_bounds__(kThreads, kC <= 2 ? 2 : 1) void attention_tiles_ker
       top = fmaxf(top, __shfl_xor(top, 32));
       const float times = row_scale(top) * sign;
       factor = a.scale * kLog2E / times;        // (positive: the sign is in q)
-      if (r.len > room_of(a)) factor = __builtin_nanf("");
 #pragma unroll
       for (int c = 0; c < 4 * kC; ++c)
 #pragma unroll

@@ -29,7 +29,7 @@ struct Steps {
   int head, from, to;
   __device__ __forceinline__ Steps(const AttentionArgs& a, int low, int high) {
     head = from = 0;
-    to = min(max(high, 0), room_of(a) - 1) / kStep + 1;     // (what has no page gives NaN, once)
+    to = min(max(high, 0), room_of(a) - 1) / kStep + 1;     // (a sequence longer than its table gives NaN whatever it looks at)
     if (a.window > 0) {
       from = min(max(low - a.window + 1, 0) / kStep, to - 1);
       head = min((a.sinks + kStep - 1) / kStep, from);
