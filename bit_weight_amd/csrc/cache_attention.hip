@@ -14,9 +14,11 @@
 //
 // 8-bit values are exact in fp16, so the products run on fp16 operands with fp32
 // sums: q under a power of two per row, e^(s - m) times the value scale over the
-// largest one so far (a power of two too) times 2^7.  One fp16 term of each
-// for 16-bit queries (q is exact, the weights off by 2^-12), a high and a low
-// one for fp32 queries (2^-23).
+// largest one so far (a power of two too) times 2^7.  A 16-bit q is exact in one
+// fp16 term, an fp32 one takes a high and a low one (2^-23).  A weight's rounding comes
+// to y as that of the values would: one term (2^-12) for bf16, whose own rounding of 2^-9
+// hides it (the error's mean square grows by 1 %), two for fp16, where one made the error
+// 1.2 to 1.4 times that of the last rounding, and for fp32.
 //
 // Measured: 64 sequences of up to 8192 tokens, one query each, 32 heads over 8 of 128 in
 // bf16: 133 us for 680 MB (5.1 TB/s, what a copy reaches); one of 1000 tokens 11.0 us, all
@@ -160,8 +162,8 @@ struct Share {
   }
 };
 
-// kC: D / 64 rounded up.  kFull: D is 64 kC.  kTerms: fp16 terms of q and of the weights.
-template <int kC, bool kFull, int kTerms>
+// kC: D / 64 rounded up.  kFull: D is 64 kC.  kTerms, kWeights: fp16 terms of q and of the weights.
+template <int kC, bool kFull, int kTerms, int kWeights>
 __global__ __launch_bounds__(kThreads, kC <= 2 ? 2 : 1) void attention_kernel(AttentionArgs a) {
   constexpr int kGrid = blocks_of_kernel(kC);
   constexpr int kTiles = 4 * kC;        // of 16 features
@@ -418,7 +420,7 @@ __global__ __launch_bounds__(kThreads, kC <= 2 ? 2 : 1) void attention_kernel(At
           unit = scale_top;
         }
         const float base = above(m), w = scale_now * kWeight * __builtin_amdgcn_rcpf(unit);
-        h8 p[kTerms][2];
+        h8 p[kWeights][2];
 #pragma unroll
         for (int n = 0; n < 4; ++n)
 #pragma unroll
@@ -428,13 +430,13 @@ __global__ __launch_bounds__(kThreads, kC <= 2 ? 2 : 1) void attention_kernel(At
             const float v = sc[n][b] == -__builtin_inff() ? 0.0f : e * w;
             const _Float16 hi = (_Float16)v;
             p[0][n / 2][4 * (n % 2) + b] = hi;
-            if constexpr (kTerms == 2) p[kTerms - 1][n / 2][4 * (n % 2) + b] = (_Float16)(v - (float)hi);
+            if constexpr (kWeights == 2) p[kWeights - 1][n / 2][4 * (n % 2) + b] = (_Float16)(v - (float)hi);
           }
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) {
           const h8 v0 = halves8(vw[t].x, vw[t].y), v1 = halves8(vw[t].z, vw[t].w);
 #pragma unroll
-          for (int n = 0; n < kTerms; ++n) {
+          for (int n = 0; n < kWeights; ++n) {
             o[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, p[n][0], o[t], 0, 0, 0);
             o[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, p[n][1], o[t], 0, 0, 0);
           }
@@ -567,19 +569,19 @@ __global__ __launch_bounds__(kThreads, kC <= 2 ? 2 : 1) void attention_kernel(At
   }
 }
 
-template <int kC, int kTerms>
+template <int kC, int kTerms, int kWeights>
 void launch_full(const AttentionArgs& a, hipStream_t stream) {
-  if (a.c.D == 64 * kC) attention_kernel<kC, true, kTerms><<<blocks_of_kernel(kC), kThreads, 0, stream>>>(a);
-  else attention_kernel<kC, false, kTerms><<<blocks_of_kernel(kC), kThreads, 0, stream>>>(a);
+  if (a.c.D == 64 * kC) attention_kernel<kC, true, kTerms, kWeights><<<blocks_of_kernel(kC), kThreads, 0, stream>>>(a);
+  else attention_kernel<kC, false, kTerms, kWeights><<<blocks_of_kernel(kC), kThreads, 0, stream>>>(a);
 }
 
-template <int kTerms>
+template <int kTerms, int kWeights>
 void launch_terms(const AttentionArgs& a, hipStream_t stream) {
   switch ((a.c.D + 63) / 64) {
-    case 1: return launch_full<1, kTerms>(a, stream);
-    case 2: return launch_full<2, kTerms>(a, stream);
-    case 3: return launch_full<3, kTerms>(a, stream);
-    default: return launch_full<4, kTerms>(a, stream);
+    case 1: return launch_full<1, kTerms, kWeights>(a, stream);
+    case 2: return launch_full<2, kTerms, kWeights>(a, stream);
+    case 3: return launch_full<3, kTerms, kWeights>(a, stream);
+    default: return launch_full<4, kTerms, kWeights>(a, stream);
   }
 }
 
@@ -609,8 +611,9 @@ size_t cache_attention_workspace_bytes() { return kBlocks * sizeof(int); }
 
 hipError_t launch_cache_attention(const AttentionArgs& a, hipStream_t stream, bool* partial) {
   if (tiles_pay(a)) return launch_attention_tiles(a, stream, partial);
-  if (a.c.dtype == SHERRY_F32) launch_terms<2>(a, stream);
-  else launch_terms<1>(a, stream);
+  if (a.c.dtype == SHERRY_F32) launch_terms<2, 2>(a, stream);
+  else if (a.c.dtype == SHERRY_F16) launch_terms<1, 2>(a, stream);
+  else launch_terms<1, 1>(a, stream);
   return hipGetLastError();
 }
 

@@ -163,8 +163,8 @@ struct Layout {
   static __device__ __forceinline__ int value(int row, int chunk) { return kKeys + 16 * (8 * row + (chunk ^ ((row >> 1) & 7))); }
 };
 
-// kTerms: fp16 terms of q and of the weights.
-template <int kC, int kTerms>
+// kTerms, kWeights: fp16 terms of q and of the weights.
+template <int kC, int kTerms, int kWeights>
 __global__ __launch_bounds__(kThreads, kC <= 2 ? 2 : 1) void attention_tiles_kernel(AttentionArgs a, int blocks) {
   using L = Layout<kC>;
   constexpr int kTiles = 2 * kC;          // of 32 features
@@ -263,9 +263,9 @@ __global__ __launch_bounds__(kThreads, kC <= 2 ? 2 : 1) void attention_tiles_ker
     f16v o[kTiles];
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) o[t] = f16v{};
-    h8 p[kTerms][4];             // the last step's weights
+    h8 p[kWeights][4];           // the last step's weights
 #pragma unroll
-    for (int n = 0; n < kTerms; ++n)
+    for (int n = 0; n < kWeights; ++n)
 #pragma unroll
       for (int u = 0; u < 4; ++u) p[n][u] = h8{};
     // The products in slots: their operands from LDS are read kAhead slots before, and
@@ -290,7 +290,7 @@ __global__ __launch_bounds__(kThreads, kC <= 2 ? 2 : 1) void attention_tiles_ker
       in_slots([&](int j) { return *reinterpret_cast<const h8*>(lds + (base ^ (32 * (j / kTiles))) + 4096 * (j % kTiles)); },
                [&](int j, h8 v) {
 #pragma unroll
-                 for (int n = 0; n < kTerms; ++n)
+                 for (int n = 0; n < kWeights; ++n)
                    o[j % kTiles] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, p[n][j / kTiles], o[j % kTiles], 0, 0, 0);
                },
                beside);
@@ -417,7 +417,7 @@ __global__ __launch_bounds__(kThreads, kC <= 2 ? 2 : 1) void attention_tiles_ker
       // weights under the maximum so far; where that is too low for them, or a query has
       // seen nothing yet, again under a new one
       float sum = 0.0f, ratio[4];
-      h8 next[kTerms][4];
+      h8 next[kWeights][4];
       // (a block that the query does not see may have any scale: its weights are 0)
       auto ratios = [&](float of) {
 #pragma unroll
@@ -429,7 +429,7 @@ __global__ __launch_bounds__(kThreads, kC <= 2 ? 2 : 1) void attention_tiles_ker
         const float v = e * ratio[x / 8];
         const _Float16 hi = (_Float16)v;
         next[0][x / 8][x % 8] = hi;
-        if constexpr (kTerms == 2) next[kTerms - 1][x / 8][x % 8] = (_Float16)(v - (float)hi);
+        if constexpr (kWeights == 2) next[kWeights - 1][x / 8][x % 8] = (_Float16)(v - (float)hi);
       };
       ratios(unit);
       const float floor = above(m) - kWeightExponent;
@@ -462,7 +462,7 @@ __global__ __launch_bounds__(kThreads, kC <= 2 ? 2 : 1) void attention_tiles_ker
       }
       l += sum;
 #pragma unroll
-      for (int n = 0; n < kTerms; ++n)
+      for (int n = 0; n < kWeights; ++n)
 #pragma unroll
         for (int u = 0; u < 4; ++u) p[n][u] = next[n][u];
       lds_barrier();
@@ -578,20 +578,20 @@ __global__ __launch_bounds__(kThreads) void attention_tiles_join_kernel(Attentio
   }
 }
 
-template <int kC, int kTerms>
+template <int kC, int kTerms, int kWeights>
 hipError_t launch_tiles(const AttentionArgs& a, hipStream_t stream) {
   constexpr int blocks = blocks_of_kernel(kC);
-  attention_tiles_kernel<kC, kTerms><<<blocks, kThreads, 0, stream>>>(a, blocks);
+  attention_tiles_kernel<kC, kTerms, kWeights><<<blocks, kThreads, 0, stream>>>(a, blocks);
   return hipGetLastError();
 }
 
-template <int kTerms>
+template <int kTerms, int kWeights>
 hipError_t launch_terms(const AttentionArgs& a, hipStream_t stream) {
   switch ((a.c.D + 63) / 64) {
-    case 1: return launch_tiles<1, kTerms>(a, stream);
-    case 2: return launch_tiles<2, kTerms>(a, stream);
-    case 3: return launch_tiles<3, kTerms>(a, stream);
-    default: return launch_tiles<4, kTerms>(a, stream);
+    case 1: return launch_tiles<1, kTerms, kWeights>(a, stream);
+    case 2: return launch_tiles<2, kTerms, kWeights>(a, stream);
+    case 3: return launch_tiles<3, kTerms, kWeights>(a, stream);
+    default: return launch_tiles<4, kTerms, kWeights>(a, stream);
   }
 }
 
@@ -609,7 +609,9 @@ hipError_t launch_attention_tiles(const AttentionArgs& a, hipStream_t stream, bo
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   *partial = true;
-  e = a.c.dtype == SHERRY_F32 ? launch_terms<2>(a, stream) : launch_terms<1>(a, stream);
+  e = a.c.dtype == SHERRY_F32   ? launch_terms<2, 2>(a, stream)
+      : a.c.dtype == SHERRY_F16 ? launch_terms<1, 2>(a, stream)
+                                : launch_terms<1, 1>(a, stream);
   if (e != hipSuccess) return e;
   attention_tiles_join_kernel<<<dim3(blocks, 8), kThreads, 0, stream>>>(a, blocks);
   return hipGetLastError();

@@ -489,8 +489,8 @@ sherry_status sherry_cache_read(const sherry_kv_cache* cache, void* k, void* v, 
  *            zero; one buffer may serve all calls on a stream).
  *   scratch  at least the queried bytes, any content, 256-byte aligned.
  * Products run in fp16 with fp32 sums: 16-bit queries are exact (bf16 down to
- * 2^-38 of the row's largest) and the weights e^(s - m) are rounded to 11 bits,
- * fp32 queries and their weights to 22; weights times value scales below 2^-31 of
+ * 2^-38 of the row's largest) and fp32 queries are rounded to 22 bits; the weights
+ * e^(s - m) are rounded to 11 bits for bf16, to 22 for fp16 and fp32; weights times value scales below 2^-31 of
  * the largest weight times the largest scale that the query sees are lost (what it
  * does not see has no part in this).  Value scales are taken to be powers of two,
  * as cache_write leaves them.  The sums run in a fixed order: equal calls give equal
