@@ -50,3 +50,49 @@ def test_rounding_of_fp16(wide, n, D, tiles):  # noqa: F811
     error = (got.double() - want).square().mean().sqrt()
     rounding = (want.half().double() - want).square().mean().sqrt()
     assert rounding <= error * 1.0000001 and error <= 1.05 * rounding, float(error / rounding)
+
+
+@pytest.mark.parametrize("tiles", [False, True])
+@pytest.mark.parametrize("seed", range(4))
+def test_two_terms_of_fp32(wide, seed, tiles):  # noqa: F811
+    """A few tokens of weights near the largest above thousands of small ones, in fp32.
+    Queries have one feature that is not 0, of few bits, so that a score is one exact
+    product: times the scale's factor, and less the maximum, 4 U of |s| + |m|, U = 2^-24.
+    Weights: 2^-22 and 4 U; the sums (the weights' and the products') 2 U for each of up
+    to n terms would be the worst order's: lanes and steps of 64 make it 2 (n / 64 + 64) U;
+    fp16's last step: half of 2^-24 under weights that are 2^7 as large as the maximum's
+    at least: 2^-32 a token, times the largest value.  The join's: 16 U.  (One term alone
+    would miss this bound by three to six times.)"""
+    n, D, H, Hq, page = 4000, 64, 1, 4, 16
+    new = 64 if tiles else 4
+    g = ref.gen(140 + seed)
+    cache, table, tl, _ = filled([n], page, H, D, 141)
+    k = torch.zeros(n, H, D)
+    k[:, 0, 0] = 0.25 * torch.randint(-16, 16, (n,), generator=g)      # in 8 bits without a rounding
+    peaks = torch.randperm(n - new, generator=g)[:6]
+    k[:, 0, 1] = -8.0
+    k[peaks, 0, 1] = 0.0
+    v = torch.randint(64, 128, (n, H, D), generator=g) * (2.0 * torch.randint(0, 2, (n, H, D), generator=g) - 1)
+    bw.cache_write(cache, k.cuda(), v.cuda(), table, i32(0, n), tl)
+    rk, rv = bw.cache_read(cache, table, i32(0, n), tl, n)
+    assert torch.equal(rk.cpu(), k) and torch.equal(rv.cpu(), v)
+    q = torch.zeros(new, Hq, D)
+    q[:, :, 0] = 0.125 * torch.randint(-3, 4, (new, Hq), generator=g)
+    q[:, :, 1] = 2.0      # 16 of e lower where it is no peak
+    got = bw.cache_attention(q.cuda(), cache, table, i32(0, new), tl, scale=1.0).double().cpu()
+    assert bool(wide) == tiles
+    s = torch.einsum("thd,lgd->thl", q.double(), k.double())      # exact, and so is the difference below
+    hidden = torch.arange(n)[None, :] > n - new + torch.arange(new)[:, None]
+    s = s.masked_fill(hidden[:, None], -torch.inf)
+    m = s.amax(-1, keepdim=True)
+    e = torch.exp(s - m)
+    total = e.sum(-1, keepdim=True)
+    w, av = e / total, v[:, 0].double()
+    want = w @ av
+    U = ref.U
+    each = torch.where(w > 0, 2.0 ** -22 + (4 + 4 * (s.abs() + m.abs()).nan_to_num(0.0, 0.0, 0.0)) * U, 0.0)      # relative, of a weight
+    sums = (2 * (n / 64 + 64) + 16) * U
+    bound = (w * each) @ av.abs() + ((w * each).sum(-1, keepdim=True) + 2 * sums) * (w @ av.abs()) \
+        + n * 2.0 ** -32 * 127 / total + want.abs() * U
+    off = (got - want).abs()
+    assert float((off / bound).max()) <= 1, float((off / bound).max())
