@@ -13,6 +13,7 @@
 
 #include <ATen/ATen.h>
 #include <ATen/hip/EmptyTensor.h>
+#include <c10/core/AutogradState.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/core/GradMode.h>
 #include <c10/hip/HIPFunctions.h>
@@ -266,6 +267,15 @@ struct Workspace {
   }
 };
 
+// Forward mode: the operators have no such derivatives.  A tensor that carries a tangent
+// is refused, as torch's functions without one do, unless forward mode is off (as in the
+// forward of a torch.autograd.Function with a jvp of its own); it does not go by the grad
+// mode.
+void refuse_tangent(const char* name, const at::Tensor& t) {
+  if (t._fw_grad(/*level=*/0).defined() && c10::AutogradState::get_tls_state().get_fw_grad_mode())
+    fail(PyExc_NotImplementedError, "bit_weight_amd.%s has no forward-mode derivative, but a tensor carries a tangent", name);
+}
+
 // Autograd: the operators have backward passes of their own and no grad_fn.
 // Where one of the tensors requires a gradient the outputs are made to say
 // so, and a backward pass through them fails by the operator's name instead
@@ -274,6 +284,9 @@ struct Workspace {
 class Gradients {
  public:
   Gradients(const char* name, std::initializer_list<PyObject*> inputs, PyObject* out = Py_None) : name_(name) {
+    for (PyObject* o : inputs)
+      if (o != Py_None) refuse_tangent(name, THPVariable_Unpack(o));
+    if (out != Py_None) refuse_tangent(name, THPVariable_Unpack(out));
     if (!c10::GradMode::is_enabled()) return;
     for (PyObject* o : inputs)
       if (o != Py_None && THPVariable_Unpack(o).requires_grad())
@@ -687,6 +700,7 @@ PyObject* cache_write(PyObject* const* a) {
   const int64_t vs = heads_of(v, "v", k.scalar_type(), c.index, T, c.c.heads, c.c.dim);
   bool graded = k.requires_grad() || v.requires_grad();
   for (int i : {2, 3}) graded |= tensor_of(a[i], "cache").requires_grad();
+  for (int i : {2, 3, 4, 5}) refuse_tangent("cache_write", tensor_of(a[i], "cache"));
   if (c10::GradMode::is_enabled() && graded)
     fail(PyExc_RuntimeError, "cache_write cannot carry gradients, but a tensor requires one: call it in torch.no_grad()");
   launch("sherry_cache_write", c.index, [&](void* stream) {
