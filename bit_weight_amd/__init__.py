@@ -601,7 +601,8 @@ def qk_norm_rope_backward(dq: torch.Tensor, dk: torch.Tensor, x: torch.Tensor, p
     """Gradients of qk_norm_rope from dq, dk and its inputs -> (dx, dq_weight fp32
     [dim], dk_weight fp32 [dim]; both None with norm=False).  dx is
     [T, (q_heads + k_heads) dim], or out, whose rows may be longer (the rest is
-    left as it was, for the values' gradient); out may be x."""
+    left as it was, for the values' gradient); out may be x, but no other part of
+    it or of another input."""
     return (_native or _load_native()).qk_norm_rope_backward(dq, dk, x, positions, freqs, q_weight, k_weight, eps, norm,
                                                              interleaved, out)
 

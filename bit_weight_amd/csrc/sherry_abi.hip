@@ -1000,6 +1000,26 @@ bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
   return x < y + b_bytes && y < x + a_bytes;
 }
 
+// Whether one of T rows of `row` bytes, `stride` apart, meets the n bytes at b.
+bool rows_meet(const void* a, int64_t T, int64_t stride, int64_t row, const void* b, int64_t n) {
+  const int64_t x = (int64_t)reinterpret_cast<uintptr_t>(a), y = (int64_t)reinterpret_cast<uintptr_t>(b);
+  const int64_t i = y < x + row ? 0 : (y - x - row) / stride + 1;      // the first row that ends behind y
+  return i < T && x + i * stride < y + n;
+}
+
+// Whether a row of a meets another row of b than its own, or a part of its own (rows of
+// different strides: any of b's or what lies between them).
+bool rows_cross(const void* a, int64_t a_stride, const void* b, int64_t b_stride, int64_t T, int64_t row) {
+  if (T > 1 && a_stride != b_stride) return rows_meet(a, T, a_stride, row, b, (T - 1) * b_stride + row);
+  const int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(a) - reinterpret_cast<uintptr_t>(b));
+  if (d == 0) return false;
+  // row i of a begins d + (i - j) stride behind row j of b: within a row's length for the
+  // nearest two i - j?
+  int64_t k = -(d / a_stride), r = d % a_stride;
+  if (r < 0) r += a_stride, ++k;
+  return (r < row && k < T && -k < T) || (a_stride - r < row && k - 1 < T && 1 - k < T);
+}
+
 // What the forward and the backward of the head norms share.
 sherry_status head_norm_args(const void* x, int64_t x_stride, const float* q_weight, const float* k_weight, float eps,
                              int norm, const double* freqs, int64_t rotary_dim, int interleaved,
@@ -1111,6 +1131,13 @@ sherry_status sherry_qk_norm_rope_backward(const void* dq, const void* dk, const
       return SHERRY_ERR_WORKSPACE;
     if (!aligned(scratch, 256)) return SHERRY_ERR_ALIGN;
   }
+  // dx over what other rows' gradients are still to be read from
+  const int64_t size = dtype == SHERRY_F32 ? 4 : 2, row = (q_heads + k_heads) * dim * size;
+  auto meets = [&](const void* p, int64_t bytes) { return p && rows_meet(dx, T, dx_stride * size, row, p, bytes); };
+  if (meets(dq, T * q_heads * dim * size) || meets(dk, T * k_heads * dim * size) || meets(q_weight, dim * 4) ||
+      meets(k_weight, dim * 4) || meets(freqs, rotary_dim * 4) || meets(positions, T * 4) ||
+      (norm && rows_cross(dx, dx_stride * size, x, x_stride * size, T, row)))
+    return SHERRY_ERR_ARG;
   const sherry_status d = check_device();
   if (d != SHERRY_OK) return d;
   g.dx = dx;

@@ -408,7 +408,7 @@ sherry_status sherry_qk_norm_rope(const void* x, int64_t x_stride, const float* 
  *   dq [T, q_heads, dim], dk [T, k_heads, dim].
  *   dx       the first (q_heads + k_heads) * dim values of rows dx_stride
  *            apart (written; what follows them is left as it was); may be x
- *            with the same stride, overlaps no input otherwise.
+ *            with the same stride, overlaps no input otherwise (SHERRY_ERR_ARG).
  *   dq_weight, dk_weight  [dim] fp32 (written), each may be NULL; NULL without
  *            the norm (x and scratch may be NULL then too).
  *   scratch  at least the queried bytes, any content, 256-byte aligned.
