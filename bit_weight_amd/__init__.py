@@ -613,7 +613,8 @@ def cache_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, table: torch.T
     product) into the cache: rows starts[i] .. starts[i+1] - 1 are the last of the
     lens[i] tokens of sequence i, whose pages are table[i] (all int32).  Each
     block of 16 tokens and head has one power of two as its scale, which grows
-    with its tokens.  Returns the cache."""
+    with its tokens and stays when they are written over (refused drafts), unless
+    the block is written again from its first position.  Returns the cache."""
     (_native or _load_native()).cache_write(*cache, k, v, table, starts, lens)
     return cache
 

@@ -460,7 +460,10 @@ typedef struct {
  * is not finite makes its block's scale NaN, and so the block's values.
  * A block is written by one sequence of a call only, and a block's first
  * position first; earlier positions may be written again (drafts that were
- * refused), later ones are then forgotten. */
+ * refused): values at later ones are then never looked at, but the block's scale
+ * stays what they made it.  A large draft leaves the block's other tokens, and
+ * those written after it, as coarse as its scale; one that is not finite leaves
+ * them NaN.  Writing the block again from its first position makes the scale anew. */
 sherry_status sherry_cache_write(const sherry_kv_cache* cache, const void* k, int64_t k_stride,
                                  const void* v, int64_t v_stride, int dtype, const int32_t* table,
                                  int64_t table_width, const int32_t* starts, const int32_t* lens,
