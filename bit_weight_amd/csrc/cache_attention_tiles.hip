@@ -423,8 +423,8 @@ __global__ __launch_bounds__(kThreads, kC <= 2 ? 2 : 1) void attention_tiles_ker
 #pragma unroll
         for (int u = 0; u < 4; ++u) ratio[u] = fminf(value_scale[u] * __builtin_amdgcn_rcpf(of), 1.0f);
       };
-      auto weight = [&](int x, float base) {
-        const float e = __builtin_amdgcn_exp2f(fmaf(sc[x / 16][x % 16], by[x / 8], -base));
+      auto weight = [&](int x, float exponent) {
+        const float e = __builtin_amdgcn_exp2f(exponent);
         sum += e;
         const float v = e * ratio[x / 8];
         const _Float16 hi = (_Float16)v;
@@ -435,7 +435,8 @@ __global__ __launch_bounds__(kThreads, kC <= 2 ? 2 : 1) void attention_tiles_ker
       const float floor = above(m) - kWeightExponent;
       add_values(there, [&](int j) {
 #pragma unroll
-        for (int x = j * 32 / kSlots; x < (j + 1) * 32 / kSlots; ++x) weight(x, floor);
+        for (int x = j * 32 / kSlots; x < (j + 1) * 32 / kSlots; ++x)
+          weight(x, fmaf(sc[x / 16][x % 16], by[x / 8], -floor));
       });
       // (no weight is larger than their sum; one of at most 2^15 stays in fp16's range)
       if (__any(sum > 0x1p15f || (pos >= 0 && m == -__builtin_inff()) || unit_now > unit)) {
@@ -456,9 +457,15 @@ __global__ __launch_bounds__(kThreads, kC <= 2 ? 2 : 1) void attention_tiles_ker
         unit = unit_now;
         sum = 0.0f;
         ratios(unit);
+        // (the products rounded as the maximum is: a fused one would leave half a step of
+        // the score, which from 2^28 on is more than a weight's exponent has room for)
         const float again = above(m) - kWeightExponent;
 #pragma unroll
-        for (int x = 0; x < 32; ++x) weight(x, again);
+        for (int x = 0; x < 32; ++x) {
+#pragma clang fp contract(off)
+          const float score = sc[x / 16][x % 16] * by[x / 8];
+          weight(x, score - again);
+        }
       }
       l += sum;
 #pragma unroll
