@@ -89,6 +89,8 @@ __device__ __forceinline__ float max_of_groups(float v) {
   return fmaxf(v, __shfl_xor(v, 32));
 }
 
+__device__ __forceinline__ float inverse(float sum) { return sum == 0.0f ? 0.0f : 1.0f / sum; }      // (of weights: none, y is 0)
+
 __device__ __forceinline__ float sum_of_groups(float v) {
   v += __shfl_xor(v, 16);
   return v + __shfl_xor(v, 32);
@@ -419,7 +421,7 @@ __global__ __launch_bounds__(kThreads, kC <= 2 ? 2 : 1) void attention_kernel(At
           m = peak;
           unit = scale_top;
         }
-        const float base = above(m), w = scale_now * kWeight * __builtin_amdgcn_rcpf(unit);
+        const float base = above(m), w = kWeight * (scale_now * __builtin_amdgcn_rcpf(unit));
         h8 p[kWeights][2];
 #pragma unroll
         for (int n = 0; n < 4; ++n)
@@ -444,12 +446,13 @@ __global__ __launch_bounds__(kThreads, kC <= 2 ? 2 : 1) void attention_kernel(At
         load_values();
       }
 
-      // the waves' parts
+      // the waves' parts, each a mean of values: sums of them might pass fp32's range
       l = sum_of_groups(l);
+      const float times = inverse(kWeight * l);
       __syncthreads();
 #pragma unroll
       for (int t = 0; t < kTiles; ++t)
-        *reinterpret_cast<f4*>(&join[wave][i][16 * t + 4 * g]) = o[t] * (unit * (1.0f / kWeight));
+        *reinterpret_cast<f4*>(&join[wave][i][16 * t + 4 * g]) = o[t] * times * unit;
       if (g == 0) {
         maxima[wave][i] = m;
         sums[wave][i] = l;
@@ -457,9 +460,24 @@ __global__ __launch_bounds__(kThreads, kC <= 2 ? 2 : 1) void attention_kernel(At
       __syncthreads();
       const bool whole = now.p0 == 0 && now.p1 == now.pieces;
       const int quads = D / 4, rows = min(kRows, r.n * group - kRows * tile);
+      // of the first `count` of `join`, a line's four features; their maximum and sum
+      auto mean_of = [&](int count, int line, int d, float& top, float& sum) {
+        float e[kWaves];
+        top = maxima[0][line];
+        sum = 0.0f;
+#pragma unroll
+        for (int v = 1; v < kWaves; ++v) top = fmaxf(top, v < count ? maxima[v][line] : top);
+#pragma unroll
+        for (int v = 0; v < kWaves; ++v)
+          sum += e[v] = v < count ? __builtin_amdgcn_exp2f(maxima[v][line] - above(top)) * sums[v][line] : 0.0f;
+        const float times = inverse(sum);
+        f4 y{};
+#pragma unroll
+        for (int v = 0; v < kWaves; ++v) y += v < count ? e[v] * times * *reinterpret_cast<const f4*>(&join[v][line][d]) : f4{};
+        return y;
+      };
       auto put = [&](int of_tile, int d, f4 y, float top, float sum) {
         const int line = kRows * tile + of_tile, of = line / group;
-        y = sum == 0.0f ? f4{} : y / sum;
         const size_t at = (size_t)(r.row0 + of) * a.Hq + h * group + line - of * group;
         store4_as(a.y, at * D + d, a.c.dtype, y);
         if (a.lse && d == 0) a.lse[at] = (top + __builtin_amdgcn_logf(sum)) * kLn2;
@@ -467,20 +485,12 @@ __global__ __launch_bounds__(kThreads, kC <= 2 ? 2 : 1) void attention_kernel(At
       float* part = a.scratch + (size_t)(2 * block + (first_part ? 0 : 1)) * part_floats(D);
       for (int x = tid; x < rows * quads; x += kThreads) {
         const int line = x / quads, d = 4 * (x - line * quads);
-        float top = maxima[0][line], sum = 0.0f;
-#pragma unroll
-        for (int v = 1; v < kWaves; ++v) top = fmaxf(top, maxima[v][line]);
-        f4 y{};
-#pragma unroll
-        for (int v = 0; v < kWaves; ++v) {
-          const float e = __builtin_amdgcn_exp2f(maxima[v][line] - above(top));
-          sum += e * sums[v][line];
-          y += e * *reinterpret_cast<const f4*>(&join[v][line][d]);
-        }
+        float top, sum;
+        const f4 y = mean_of(kWaves, line, d, top, sum);
         if (whole) {
           put(line, d, y, top, sum);
         } else {
-          share(part + (size_t)line * D + d, sum == 0.0f ? f4{} : y / sum);
+          share(part + (size_t)line * D + d, y);
           if (d == 0) {
             share(part + kRows * D + line, top);
             share(part + kRows * D + kRows + line, sum);
@@ -524,15 +534,16 @@ __global__ __launch_bounds__(kThreads, kC <= 2 ? 2 : 1) void attention_kernel(At
               float peak = top;
 #pragma unroll
               for (int k = 0; k < 8; ++k) peak = fmaxf(peak, w + k * sharers <= w1 ? tops[k] : top);
-              const float keep = __builtin_amdgcn_exp2f(top - above(peak));
-              sum *= keep;
-              y *= keep;
+              const float had = sum * __builtin_amdgcn_exp2f(top - above(peak));
+              float e[8];
+              sum = had;
 #pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const float e = w + k * sharers <= w1 ? __builtin_amdgcn_exp2f(tops[k] - above(peak)) * sums_of[k] : 0.0f;
-                sum += e;
-                y += w + k * sharers <= w1 ? e * ys[k] : f4{};
-              }
+              for (int k = 0; k < 8; ++k)
+                sum += e[k] = w + k * sharers <= w1 ? __builtin_amdgcn_exp2f(tops[k] - above(peak)) * sums_of[k] : 0.0f;
+              const float times = inverse(sum);
+              y *= had * times;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) y += w + k * sharers <= w1 ? e[k] * times * ys[k] : f4{};
               top = peak;
             }
             if (sharers > 1) {
@@ -544,18 +555,7 @@ __global__ __launch_bounds__(kThreads, kC <= 2 ? 2 : 1) void attention_kernel(At
                 }
               }
               __syncthreads();
-              if (sharer == 0 && has) {
-                float peak = top;
-                for (int v = 1; v < sharers; ++v) peak = fmaxf(peak, maxima[v][line]);
-                sum = 0.0f;
-                y = f4{};
-                for (int v = 0; v < sharers; ++v) {
-                  const float e = __builtin_amdgcn_exp2f(maxima[v][line] - above(peak));
-                  sum += e * sums[v][line];
-                  y += e * *reinterpret_cast<const f4*>(&join[v][line][d]);
-                }
-                top = peak;
-              }
+              if (sharer == 0 && has) y = mean_of(sharers, line, d, top, sum);
             }
             if (sharer == 0 && has) put(line, d, y, top, sum);
           }

@@ -567,18 +567,17 @@ __global__ __launch_bounds__(kThreads) void attention_tiles_join_kernel(Attentio
         if (n0 + n >= parts) lse[n] = -__builtin_inff();
         now = fmaxf(now, lse[n]);
       }
-      const float keep = __builtin_amdgcn_exp2f(m - above(now));
-      l *= keep;
-      y *= keep;
+      const float had = l * __builtin_amdgcn_exp2f(m - above(now));
+      float e[4];
+      l = had;
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const float e = n0 + n < parts ? __builtin_amdgcn_exp2f(lse[n] - above(now)) : 0.0f;
-        l += e;
-        y += n0 + n < parts ? e * v[n] : f4{};
-      }
+      for (int n = 0; n < 4; ++n) l += e[n] = n0 + n < parts ? __builtin_amdgcn_exp2f(lse[n] - above(now)) : 0.0f;
+      const float times = l == 0.0f ? 0.0f : 1.0f / l;      // (a mean throughout: a sum of values might pass fp32's range)
+      y *= had * times;
+#pragma unroll
+      for (int n = 0; n < 4; ++n) y += n0 + n < parts ? e[n] * times * v[n] : f4{};
       m = now;
     }
-    y = l == 0.0f ? f4{} : y / l;
     const size_t to = (size_t)(r.row0 + token) * a.Hq + next.head * group + row - token * group;
     store4_as(a.y, to * D + d, a.c.dtype, y);
     if (a.lse && d == 0) a.lse[to] = (m + __builtin_amdgcn_logf(l)) * kLn2;
