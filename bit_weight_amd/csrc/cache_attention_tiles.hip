@@ -477,7 +477,7 @@ __global__ __launch_bounds__(kThreads, kC <= 2 ? 2 : 1) void attention_tiles_ker
     add_values(((s1 - s0 - 1) & 1) * L::kBuffer, [](int) {});
 
     l += __shfl_xor(l, 32);
-    const float times = l == 0.0f ? 0.0f : unit / l;
+    const float times = l == 0.0f ? 0.0f : 1.0f / l;      // (and then `unit`: their product may be subnormal)
     const bool whole = s0 == 0 && s1 == count;
     const float lse2 = m - kWeightExponent + __builtin_amdgcn_logf(l);
     if (whole) {
@@ -489,7 +489,7 @@ __global__ __launch_bounds__(kThreads, kC <= 2 ? 2 : 1) void attention_tiles_ker
           for (int b = 0; b < 4; ++b) {
             const int d = 32 * t + 8 * b + 4 * f;
             if (d < D)
-              store4_as(a.y, to * D + d, a.c.dtype, f4{o[t][4 * b], o[t][4 * b + 1], o[t][4 * b + 2], o[t][4 * b + 3]} * times);
+              store4_as(a.y, to * D + d, a.c.dtype, f4{o[t][4 * b], o[t][4 * b + 1], o[t][4 * b + 2], o[t][4 * b + 3]} * times * unit);
           }
         if (a.lse && f == 0) a.lse[to] = lse2 * kLn2;
       }
@@ -503,7 +503,7 @@ __global__ __launch_bounds__(kThreads, kC <= 2 ? 2 : 1) void attention_tiles_ker
           const int d = 32 * t + 8 * b + 4 * f;
           if (d < D)
             *reinterpret_cast<f4*>(part + (size_t)line * D + d) =
-                f4{o[t][4 * b], o[t][4 * b + 1], o[t][4 * b + 2], o[t][4 * b + 3]} * times;
+                f4{o[t][4 * b], o[t][4 * b + 1], o[t][4 * b + 2], o[t][4 * b + 3]} * times * unit;
         }
       if (f == 0) part[kRows * D + line] = lse2;
     }

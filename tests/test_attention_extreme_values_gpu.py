@@ -28,7 +28,7 @@ SIZES = {"unit": (3, 40), "parts": (2, 6000), "tiles": (100, 100), "tiles in par
 @pytest.mark.parametrize("t", ["fp32", "bf16"])
 @pytest.mark.parametrize("D,Hq", [(64, 2), (128, 1), (256, 1)])
 @pytest.mark.parametrize("kind", list(SIZES))
-@pytest.mark.parametrize("size", [2.0 ** 127, 2.0 ** 118])
+@pytest.mark.parametrize("size", [2.0 ** 127, 2.0 ** 118, 2.0 ** -115, 2.0 ** -120, 2.0 ** -130])
 def test_ends_of_the_range(wide, size, kind, D, Hq, t):  # noqa: F811
     """Values of one sign from `size` to 1.9 times that: their scales are 2^121 down to
     2^-126, the smallest."""
