@@ -622,7 +622,8 @@ def cache_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, table: torch.T
 def cache_read(cache: KVCache, table: torch.Tensor, starts: torch.Tensor, lens: torch.Tensor, tokens: int,
                dtype: torch.dtype = torch.float32):
     """The last starts[i+1] - starts[i] tokens of each sequence back as `dtype` ->
-    (k, v), each [tokens, heads, dim]."""
+    (k, v), each [tokens, heads, dim].  Rows of no sequence (from starts[-1] on) are
+    not written: they hold whatever the memory did."""
     return (_native or _load_native()).cache_read(*cache, table, starts, lens, tokens, dtype)
 
 
@@ -634,5 +635,6 @@ def cache_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, starts
     [T, q_heads, dim] of q's type, or (y, lse fp32 [T, q_heads]) with `lse`.
     scale is 1 / sqrt(dim) unless given.  With a window a query sees its last
     `window` tokens and the first `sinks` ones.  starts, lens and table are as
-    cache_write's."""
+    cache_write's.  Rows of no sequence (from starts[-1] on) are not written: in `out`
+    they stay as they were, in new tensors they hold whatever the memory did."""
     return (_native or _load_native()).cache_attention(q, *cache, table, starts, lens, scale, window, sinks, out, lse)

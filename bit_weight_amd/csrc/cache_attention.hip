@@ -57,14 +57,17 @@ __device__ __forceinline__ Steps steps_of(const AttentionArgs& a, const Rows& r,
 // one):
 //   kShort, and units of up to kMiddle not at all, where half of the workgroups get one;
 //   kMiddle where every piece has a workgroup of its own;
-//   1 where a workgroup has kMany steps or more, so that the shares are even;
+//   1 where a workgroup has kMany steps or more;
 //   as many as a workgroup has on average where that gives every piece one of its own;
 //   else kLong, so that short units are not cut.
 // (One sequence of 1000 tokens: 12.6 us in pieces of 8, 11.0 of 4; of 16000: 21 us in 63
 // parts, 15.8 in 31; 64 of 125 to 500 tokens: 32 us in even shares, 16 in pieces; 16
 // windows of 4096 tokens: 32 us in pieces of 16, 24 of the average.)  All pieces, one
 // after another (by sequence, head and tile), are dealt evenly: workgroup w takes `each`
-// of them from piece first(w) on; those of one unit it takes together.
+// of them from piece first(w) on; those of one unit it takes together.  Even are the
+// pieces: a causal prompt's earlier units have its last one's number of them and fewer
+// steps, so that the workgroups of a prompt without history have from none to twice
+// the average.
 constexpr int kShort = 4, kMiddle = 8, kLong = 16, kMany = 24, kParts = 32;
 struct Deal {
   int64_t total;
@@ -587,12 +590,15 @@ void launch_terms(const AttentionArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-// Whether the kernel that shares a step's keys and values between 128 rows pays: where a
-// sequence has 64 rows or more, and the steps of 16 rows that all of them take are many
-// (counted with the longest sequence that the table has room for, or the window: the host
-// knows no lengths).  Beside 16-row units its own start, deal and join take 40 us: prompts
-// of 361 tokens behind 1750, 32 heads of 128 in fp32 (35000 steps), 105 us here, 100 there;
-// 173 behind 5300, 12 heads (21000): 54 and 64.
+// Whether the kernel that shares a step's keys and values between 128 rows pays: where
+// sequences have 64 rows or more on average, and the steps of 16 rows that all of them take
+// are many (counted with the longest sequence that the table has room for, or the window:
+// the host knows no lengths).  One kernel takes all sequences of a call: a prompt among
+// many single tokens (4000 tokens among 299: 1060 us, apart 280 and 167) goes to 16-row
+// units with them.  Beside those the tiles' own start, deal and join take 40 us.  Prompts
+// behind 1700 tokens, 32 heads over 8 of 128, in units and in tiles, us: of 361 (24000
+// steps) 57 and 75 in bf16, 63 and 104 in fp32; of 460 (31000) 67 and 74, 74 and 101; of
+// 600 (43000) 82 and 83, 94 and 118; of 800 (64000) 106 and 85, 120 and 125.
 constexpr int64_t kTilesPay = 32000;
 static bool tiles_pay(const AttentionArgs& a) {
   const int64_t T = a.c.T, S = a.c.S, group = a.Hq / a.c.H;

@@ -17,11 +17,13 @@
 // no result depends on the scale of tokens that its query does not see.
 //
 // Measured: pieces of up to 1024 tokens of 4 prompts over up to 6000, 32 heads over 8 of
-// 128 in bf16, 2.2e11 operations, in 296 us of which the deal is 9 and the join of parts
-// 20 (0.73 PFLOP/s; the library's fp16 product reaches 1.52).  The main kernel's matrix
-// units are busy 36 % of the time, the vector units 49 % (8-bit values to fp16,
-// exponentials, masks), LDS 38 %: no unit is full, waits and the phases' unevenness are
-// the rest.  Tiles of 64 rows: 448 us.
+// 128 in bf16, 2.2e11 operations, in 308 us of which the deal is 9 and the join of parts
+// 19 (0.70 PFLOP/s; the library's fp16 product reaches 1.52).  The main kernel's matrix
+// units are busy 34 % of the time, the vector units 52 % (8-bit values to fp16,
+// exponentials, masks), LDS 36 %: no unit is full, waits and the phases' unevenness are
+// the rest.  Value scales in the weights instead of the values cost 8 us of it.  Two terms
+// of the weights (fp16): 397 us, of q too (fp32, where 72 registers spill): 570.  Tiles of
+// 64 rows: 448 us.
 #include "sherry_attention.h"
 
 namespace sherry {

@@ -14,11 +14,14 @@
 // tokens, turned in registers, and LDS brings the 16 tokens of a feature together
 // (4 features 80 bytes apart, so that 64 lanes' words lie in different banks).
 //
-// Both are bound by memory: all loads of an item are asked for before the first is used,
-// and arrays of loaded bytes are ext_vector types (as HIP's uint4 they became stack
-// arrays, which went through LDS: 102 instead of 82 us).  Measured with 8 heads of 128 in
-// bf16: 64000 tokens read in 82 us (4.8 TB/s), 6800 tokens of 5 sequences written in 17.7, one token of
-// 64 sequences written in 6.6.
+// All loads of an item are asked for before the first is used, and arrays of loaded bytes
+// are ext_vector types (as HIP's uint4 they became stack arrays, which went through LDS:
+// 102 instead of 82 us).  Reading is bound by memory.  Writing is not: its waves wait 54 %
+// of their time, for a chain (lengths, table, rows, maximum, store) with nothing under it
+// where a wave has one or two items.  Measured with 8 heads of 128 in bf16: 64000 tokens
+// read in 82 us (4.8 TB/s), 6800 tokens of 5 sequences written in 16.6 (2.5 TB/s), one
+// token of 64 sequences written in 5.3, of 1024 in 31.5, of 4096 in 198 (every wave looks
+// for its block among all sequences).
 #include "sherry_cache.h"
 
 namespace sherry {

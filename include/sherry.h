@@ -457,7 +457,8 @@ typedef struct {
  * and q = rint(x / 2^e), half to even.  Where a block has earlier tokens (the
  * position of the first new one is no multiple of 16) its scale can only grow,
  * and the earlier values are rounded again, rint(q * old / new).  A value that
- * is not finite makes its block's scale NaN, and so the block's values.
+ * is not finite makes its block's scale NaN, and so the block's values.  One past
+ * 127 * 2^121 (1.98 * 2^127) is 64 * 2^122, infinity in fp32.
  * A block is written by one sequence of a call only, and a block's first
  * position first; earlier positions may be written again (drafts that were
  * refused): values at later ones are then never looked at, but the block's scale
@@ -498,8 +499,10 @@ sherry_status sherry_cache_read(const sherry_kv_cache* cache, void* k, void* v, 
  * does not see has no part in this).  Value scales are taken to be powers of two,
  * as cache_write leaves them.  The sums run in a fixed order: equal calls give equal
  * bits (a row's bits may differ with the other rows of a call, which decide how the
- * work is split).  table_width * page_size is taken as the longest sequence's length
- * where the kernel is chosen: a table no wider than needed helps short prompts. */
+ * work is split).  One kernel takes all sequences of a call, chosen by T * q_heads /
+ * (heads * S), the rows a key head has on average of a sequence, and table_width * page_size as the longest sequence's length: a
+ * table no wider than needed helps short prompts, and a long prompt among very many
+ * single tokens is faster in a call of its own. */
 sherry_status sherry_cache_attention(const void* q, int64_t q_stride, int64_t q_heads,
                                      const sherry_kv_cache* cache, const int32_t* table,
                                      int64_t table_width, const int32_t* starts,
