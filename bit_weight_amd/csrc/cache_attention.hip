@@ -15,10 +15,10 @@
 // 8-bit values are exact in fp16, so the products run on fp16 operands with fp32
 // sums: q under a power of two per row, e^(s - m) times the value scale over the
 // largest one so far (a power of two too) times 2^7.  A 16-bit q is exact in one
-// fp16 term, an fp32 one takes a high and a low one (2^-23).  A weight's rounding comes
-// to y as that of the values would: one term (2^-12) for bf16, whose own rounding of 2^-9
-// hides it (the error's mean square grows by 1 %), two for fp16, where one made the error
-// 1.2 to 1.4 times that of the last rounding, and for fp32.
+// fp16 term, an fp32 one takes a high and a low one (2^-22).  A weight's rounding comes
+// to y as that of the values would: one term (half a step: 2^-11) for bf16, whose own
+// half step of 2^-8 hides it (the error's mean square grows by up to 1.4 %), two for fp16,
+// where one made the error 1.2 to 1.4 times that of the last rounding, and for fp32 (2^-22).
 //
 // Measured: 64 sequences of up to 8192 tokens, one query each, 32 heads over 8 of 128 in
 // bf16: 133 us for 680 MB (5.1 TB/s, what a copy reaches); one of 1000 tokens 11.0 us, all
